@@ -252,6 +252,49 @@ embla_status embla_sparse_decode_e4m3(const embla_shape *shape, const void *q,
                                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Decode of a batch whose sequences share a prefix (one system prompt, one document): the
+ * prefix's keys are held once, [Hkv, prefix_stride, D], and read once for the whole batch;
+ * sequence b's context is those prefix_len keys followed by the shape->ctx_len keys of its own
+ * cache.  Key j of a sequence is prefix row j for j < prefix_len, else row j - prefix_len of its
+ * own planes.
+ *   shape      ctx_len = own keys per sequence (0 is allowed; the current token is the last
+ *              one), cache_stride of the own caches
+ *   prefix_len >= 0; prefix_stride >= prefix_len: rows between the prefix's planes.
+ *              prefix_len + ctx_len <= 2^31 - 257
+ *   k_prefix, v_prefix  bf16 [Hkv, prefix_stride, D] (not read, and NULL is allowed, when
+ *              prefix_len is 0; the same for the own caches when ctx_len is 0)
+ *
+ * embla_full_decode_shared: embla_full_decode on those contexts.
+ *   q, alpha, c, eps, out, n_surv   as for embla_full_decode (out + n_surv over prefix and own)
+ *   sel_scores fp32 [B, Hkv, score_stride] or NULL, score_stride >= prefix_len + ctx_len:
+ *              sigma_j of all prefix_len + ctx_len keys; entries past them are not written
+ *   sel_hist   uint32 [B, Hkv, 2048], required iff sel_scores != NULL
+ *   workspace  embla_full_decode_shared_workspace_size bytes, 16-byte aligned
+ * The selection is embla_select_topk on a shape whose ctx_len is prefix_len + ctx_len and whose
+ * cache_stride is score_stride.  A key of weight zero contributes nothing, whatever its value
+ * row holds; a call that meets an infinite or NaN value row gives those sums by a slow path.
+ * A NaN score (a key or query row holding NaN, an all-zero row with eps == 0) weighs nothing.
+ *
+ * embla_sparse_decode_shared: embla_sparse_decode on those contexts.
+ *   idx, idx_stride, count   as for embla_sparse_decode, indices in [0, prefix_len + ctx_len)
+ *   q, tau, out              as for embla_sparse_decode
+ */
+size_t embla_full_decode_shared_workspace_size(const embla_shape *shape, int64_t prefix_len);
+embla_status embla_full_decode_shared(const embla_shape *shape, int64_t prefix_len,
+                                      int64_t prefix_stride, const void *q, const void *k_prefix,
+                                      const void *v_prefix, const void *k_cache,
+                                      const void *v_cache, float alpha, float c, float eps,
+                                      float *out, int32_t *n_surv, float *sel_scores,
+                                      int64_t score_stride, uint32_t *sel_hist, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+embla_status embla_sparse_decode_shared(const embla_shape *shape, int64_t prefix_len,
+                                        int64_t prefix_stride, const void *q, const void *k_prefix,
+                                        const void *v_prefix, const void *k_cache,
+                                        const void *v_cache, const int32_t *idx,
+                                        int32_t idx_stride, const int32_t *count, float tau,
+                                        float *out, void *stream);
+
+/*
  * Selection per query head — the other reading of which score the selection ranks
  * ("Three kinds of attention", Sparse: "the 1,024 keys that layer scored highest" under
  * grouped queries): every query head h ranks the keys by its own score s_hj and keeps its
@@ -371,6 +414,40 @@ embla_status embla_append_kv_e4m3(const embla_shape *shape, int64_t pos, const u
                                   const float *k_scale_rows, const uint8_t *v_code_rows,
                                   const float *v_scale_rows, uint8_t *k_codes, float *k_scales,
                                   uint8_t *v_codes, float *v_scales, void *stream);
+
+/*
+ * Rows quantised as they are written — "KV bridge, KV reuse, and prefill": the caches at 8
+ * bits.  The n_new tokens' bf16 K and V rows become rows pos .. pos + n_new - 1 of every
+ * (b, g) plane of the 8-bit caches (the format of embla_full_decode_e4m3); no other row is
+ * touched.  One token per sequence (a decode step) or a whole prompt.
+ *   k_rows, v_rows     bf16 [B, Hkv, n_new, D]
+ *   k_codes, v_codes   uint8 [B, Hkv, cache_stride, D];  k_scales, v_scales fp32 [B, Hkv, cache_stride]
+ *   pos, n_new         >= 0, pos + n_new <= cache_stride; shape->ctx_len is not used
+ * With a = the largest finite |x_d| of a row: scale = a / 448 (fp32; 1 for a row without a
+ * finite value other than 0) and code_d = the E4M3 value nearest to the exact quotient
+ * 448 x_d / a (ties to even), so scale * decode(code_d) is within 2^-4 |x_d| + 2^-10 scale of
+ * x_d.  An infinite or NaN x_d becomes the NaN code and leaves the row's other elements
+ * as they are.  B * Hkv * n_new above 2^31 - 1 is EMBLA_ERR_UNSUPPORTED.
+ */
+embla_status embla_quantize_kv_e4m3(const embla_shape *shape, int64_t pos, int64_t n_new,
+                                    const void *k_rows, const void *v_rows, uint8_t *k_codes,
+                                    float *k_scales, uint8_t *v_codes, float *v_scales,
+                                    void *stream);
+
+/*
+ * Rows of the 8-bit caches read back: rows pos .. pos + n_rows - 1 of every plane as bf16
+ * (the product scale * decode(code) in fp32, rounded to the nearest bf16), into the first
+ * n_rows rows of planes rows_stride rows apart: a packed array (rows_stride = n_rows), or the
+ * front of a bf16 cache for the calls that take one (a prompt's prefill behind older
+ * tokens, the prefix of embla_full_decode_shared).  Rows n_rows .. rows_stride - 1 of the
+ * planes are not written.
+ *   k_rows, v_rows     bf16 [B, Hkv, rows_stride, D], rows_stride >= n_rows
+ *   codes, scales      as for embla_quantize_kv_e4m3; shape->ctx_len is not used
+ */
+embla_status embla_dequantize_kv_e4m3(const embla_shape *shape, int64_t pos, int64_t n_rows,
+                                      const uint8_t *k_codes, const float *k_scales,
+                                      const uint8_t *v_codes, const float *v_scales, void *k_rows,
+                                      void *v_rows, int64_t rows_stride, void *stream);
 
 /*
  * V-read accounting — "The Architecture of Embla 1", "Skipping V": a value row

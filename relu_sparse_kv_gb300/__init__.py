@@ -103,6 +103,14 @@ def library() -> ctypes.CDLL:
                                                                 vp, vp, vp, vp, vp]),
             "embla_append_kv": (ctypes.c_int, [P, i64, vp, vp, vp, vp, vp]),
             "embla_append_kv_e4m3": (ctypes.c_int, [P, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "embla_full_decode_shared_workspace_size": (sz, [P, i64]),
+            "embla_full_decode_shared": (ctypes.c_int, [P, i64, i64, vp, vp, vp, vp, vp, f32, f32,
+                                                        f32, vp, vp, vp, i64, vp, vp, sz, vp]),
+            "embla_sparse_decode_shared": (ctypes.c_int, [P, i64, i64, vp, vp, vp, vp, vp, vp, i32,
+                                                          vp, f32, vp, vp]),
+            "embla_quantize_kv_e4m3": (ctypes.c_int, [P, i64, i64, vp, vp, vp, vp, vp, vp, vp]),
+            "embla_dequantize_kv_e4m3": (ctypes.c_int, [P, i64, i64, vp, vp, vp, vp, vp, vp, i64,
+                                                        vp]),
             "embla_full_decode_select_workspace_size": (sz, [P, i32, i32]),
             "embla_full_decode_select": (ctypes.c_int, [P, vp, vp, vp, f32, f32, f32, vp, vp, vp,
                                                         vp, i32, i32, vp, i32, vp, vp, sz, vp]),
@@ -295,6 +303,46 @@ def embla_append_kv_e4m3(shape: Shape, pos: int, k_code_rows, k_scale_rows, v_co
     _call("embla_append_kv_e4m3", ctypes.byref(shape.c()), pos, _ptr(k_code_rows),
           _ptr(k_scale_rows), _ptr(v_code_rows), _ptr(v_scale_rows), _ptr(k_codes),
           _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _stream(stream))
+
+
+def _check_codes(shape: Shape, k_codes, k_scales, v_codes, v_scales):
+    B, Hkv, D, ncap = shape.batch, shape.n_kv_heads, shape.head_dim, shape.cache_stride
+    _check(k_codes, torch.uint8, (B, Hkv, ncap, D), "k_codes")
+    _check(v_codes, torch.uint8, (B, Hkv, ncap, D), "v_codes")
+    _check(k_scales, torch.float32, (B, Hkv, ncap), "k_scales")
+    _check(v_scales, torch.float32, (B, Hkv, ncap), "v_scales")
+
+
+def _check_rows(shape: Shape, k_rows, v_rows) -> int:
+    """k_rows and v_rows are bf16 [B, Hkv, T, D]; returns T."""
+    _check(k_rows, torch.bfloat16, None, "k_rows")
+    if k_rows.dim() != 4:
+        raise ValueError("k_rows must be [B, Hkv, T, D]")
+    want = (shape.batch, shape.n_kv_heads, k_rows.shape[2], shape.head_dim)
+    _check(k_rows, torch.bfloat16, want, "k_rows")
+    _check(v_rows, torch.bfloat16, want, "v_rows")
+    return want[2]
+
+
+def embla_quantize_kv_e4m3(shape: Shape, pos: int, k_rows, v_rows, k_codes, k_scales, v_codes,
+                           v_scales, stream=None):
+    """Quantise T tokens' K and V rows (bf16 [B, Hkv, T, D]) into rows pos .. pos + T - 1 of the
+    8-bit caches (codes uint8 [B, Hkv, cache_stride, D], scales float32 [B, Hkv, cache_stride])."""
+    T = _check_rows(shape, k_rows, v_rows)
+    _check_codes(shape, k_codes, k_scales, v_codes, v_scales)
+    _call("embla_quantize_kv_e4m3", ctypes.byref(shape.c()), pos, T, _ptr(k_rows), _ptr(v_rows),
+          _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _stream(stream))
+
+
+def embla_dequantize_kv_e4m3(shape: Shape, pos: int, k_codes, k_scales, v_codes, v_scales, k_rows,
+                             v_rows, n_rows: int | None = None, stream=None):
+    """Read rows pos .. pos + n_rows - 1 of the 8-bit caches back as bf16 into the first n_rows
+    rows of k_rows and v_rows (bf16 [B, Hkv, T, D], T >= n_rows; n_rows defaults to T)."""
+    T = _check_rows(shape, k_rows, v_rows)
+    _check_codes(shape, k_codes, k_scales, v_codes, v_scales)
+    _call("embla_dequantize_kv_e4m3", ctypes.byref(shape.c()), pos, T if n_rows is None else n_rows,
+          _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_rows), _ptr(v_rows),
+          T, _stream(stream))
 
 
 def embla_full_decode_select_workspace_size(shape: Shape, topk: int = 1024, recent: int = 128) -> int:
@@ -499,6 +547,65 @@ def embla_sparse_decode_per_head(shape: Shape, q, k_cache, v_cache, idx, count, 
     _call("embla_sparse_decode_per_head", ctypes.byref(shape.c()), _ptr(q), _ptr(k_cache),
           _ptr(v_cache), _ptr(idx), idx.shape[2], _ptr(count), tau, _ptr(out), _ptr(ws),
           ws.numel() * ws.element_size(), _stream(stream))
+
+
+def embla_full_decode_shared_workspace_size(shape: Shape, prefix_len: int) -> int:
+    return library().embla_full_decode_shared_workspace_size(ctypes.byref(shape.c()), prefix_len)
+
+
+def _check_shared_caches(shape: Shape, prefix_len: int, k_prefix, v_prefix, k_cache, v_cache) -> int:
+    """k_prefix and v_prefix are bf16 [Hkv, prefix_stride, D] holding prefix_len rows at least;
+    returns prefix_stride."""
+    B, Hkv, D, ncap = shape.batch, shape.n_kv_heads, shape.head_dim, shape.cache_stride
+    _check(k_prefix, torch.bfloat16, None, "k_prefix")
+    if k_prefix.dim() != 3 or prefix_len > k_prefix.shape[1]:
+        raise ValueError("k_prefix must be [Hkv, prefix_stride, D], prefix_stride >= prefix_len")
+    want = (Hkv, k_prefix.shape[1], D)
+    _check(k_prefix, torch.bfloat16, want, "k_prefix")
+    _check(v_prefix, torch.bfloat16, want, "v_prefix")
+    _check(k_cache, torch.bfloat16, (B, Hkv, ncap, D), "k_cache")
+    _check(v_cache, torch.bfloat16, (B, Hkv, ncap, D), "v_cache")
+    return want[1]
+
+
+def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefix, k_cache, v_cache,
+                             out, n_surv, sel_scores=None, sel_hist=None, alpha: float = 1.0,
+                             c: float = 1.0, eps: float = 1e-6, workspace=None, stream=None):
+    """embla_full_decode of sequences that share their first prefix_len keys (k_prefix, v_prefix
+    bf16 [Hkv, prefix_stride, D]) and go on with shape.ctx_len keys of their own caches;
+    sel_scores fp32 [B, Hkv, score_stride] holds the scores of prefix and own keys, and
+    embla_select_topk takes it with Shape(..., ctx_len=prefix_len + shape.ctx_len,
+    cache_stride=score_stride)."""
+    B, Hq, Hkv, D = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
+    _check(q, torch.bfloat16, (B, Hq, D), "q")
+    pstride = _check_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)
+    _check(out, torch.float32, (B, Hq, D), "out")
+    _check(n_surv, torch.int32, (B, Hkv), "n_surv")
+    _check(sel_scores, torch.float32, None, "sel_scores", allow_none=True)
+    if sel_scores is not None and (sel_scores.dim() != 3 or tuple(sel_scores.shape[:2]) != (B, Hkv)):
+        raise ValueError("sel_scores must be [B, Hkv, score_stride]")
+    _check(sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist", allow_none=True)
+    ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), workspace, q.device)
+    _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, pstride, _ptr(q),
+          _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), alpha, c, eps, _ptr(out),
+          _ptr(n_surv), _ptr(sel_scores), 0 if sel_scores is None else sel_scores.shape[2],
+          _ptr(sel_hist), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+
+
+def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefix, k_cache, v_cache,
+                               idx, count, out, tau: float | None = None, stream=None):
+    """embla_sparse_decode of sequences that share a prefix (as for embla_full_decode_shared):
+    an index below prefix_len is a row of the prefix, any other one row idx - prefix_len of the
+    sequence's own cache."""
+    B, Hq, Hkv, D = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
+    _check(q, torch.bfloat16, (B, Hq, D), "q")
+    pstride = _check_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)
+    _check_select_outputs(shape, idx, count)
+    _check(out, torch.float32, (B, Hq, D), "out")
+    tau = D ** -0.5 if tau is None else tau
+    _call("embla_sparse_decode_shared", ctypes.byref(shape.c()), prefix_len, pstride, _ptr(q),
+          _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), _ptr(idx), idx.shape[2],
+          _ptr(count), tau, _ptr(out), _stream(stream))
 
 
 def embla_window_decode(shape: Shape, q, k_win, v_win, pos: int, out, window: int = 128,

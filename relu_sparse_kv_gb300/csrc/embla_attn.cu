@@ -154,6 +154,24 @@ bool encode_planes(CUtensorMap *map, const void *base, uint64_t rows, uint64_t p
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D bf16 map of q [batch][Hkv][G][128], boxes of {64 columns, G heads, 1 KV head, 128 / G
+// sequences}: 128 query rows of one KV head, sequence by sequence; sequences past the batch
+// read as zeros.
+bool encode_query_block(CUtensorMap *map, const void *q, int batch, int Hq, int Hkv) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int G = Hq / Hkv;
+  const cuuint64_t row = kHeadDim * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(G),
+                              static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[3] = {row, row * static_cast<cuuint64_t>(G), row * static_cast<cuuint64_t>(Hq)};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(G), 1u, static_cast<cuuint32_t>(128 / G)};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool finite(float x) { return x == x && x - x == 0.0f; }
@@ -172,6 +190,18 @@ embla_status check_shape(const embla_shape *s, int *G, bool ctx_checks) {
   if (s->head_dim != kHeadDim) return EMBLA_ERR_UNSUPPORTED;
   if (*G != 4 && *G != 8) return EMBLA_ERR_UNSUPPORTED;
   return EMBLA_OK;
+}
+
+// A shared prefix of `len` keys and the shape's own keys make a context of fewer than 2^31 keys
+// (with room for a tile past its end).
+bool prefix_fits(const embla_shape *s, int64_t len) {
+  return len >= 0 && len <= INT32_MAX - 256 - s->ctx_len;
+}
+
+// Rows pos .. pos + count - 1 lie in the cache's planes.
+bool rows_in_cache(const embla_shape *s, int64_t pos, int64_t count) {
+  return s->cache_stride >= 0 && pos >= 0 && count >= 0 && pos <= s->cache_stride &&
+         count <= s->cache_stride - pos;
 }
 
 embla_status cuda_status(cudaError_t e) { return e == cudaSuccess ? EMBLA_OK : EMBLA_ERR_CUDA; }
@@ -614,6 +644,136 @@ embla_status embla_prefill(const embla_shape *shape, int64_t n_new, const void *
                                     static_cast<cudaStream_t>(stream)));
 }
 
+size_t embla_full_decode_shared_workspace_size(const embla_shape *shape, int64_t prefix_len) {
+  int G = 0;
+  if (check_shape(shape, &G, true) != EMBLA_OK || !prefix_fits(shape, prefix_len)) return 0;
+  const int sms = sm_count_of(current_device());
+  if (sms <= 0) return 0;
+  return shared_workspace_bytes(
+      shared_split(shape->batch, shape->n_kv_heads, G, prefix_len, shape->ctx_len, sms));
+}
+
+embla_status embla_full_decode_shared(const embla_shape *shape, int64_t prefix_len,
+                                      int64_t prefix_stride, const void *q, const void *k_prefix,
+                                      const void *v_prefix, const void *k_cache,
+                                      const void *v_cache, float alpha, float c, float eps,
+                                      float *out, int32_t *n_surv, float *sel_scores,
+                                      int64_t score_stride, uint32_t *sel_hist, void *workspace,
+                                      size_t workspace_bytes, void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, true);
+  if (st != EMBLA_OK) return st;
+  if (!prefix_fits(shape, prefix_len) || prefix_stride < prefix_len) return EMBLA_ERR_INVALID_ARG;
+  if (!(finite(alpha) && alpha > 0.0f) || !(finite(c) && c >= 0.0f) ||
+      !(finite(eps) && eps >= 0.0f))
+    return EMBLA_ERR_INVALID_ARG;
+  const int64_t units = static_cast<int64_t>(shape->batch) * shape->n_kv_heads;
+  const int64_t n = shape->ctx_len;
+  if (units == 0) return EMBLA_OK;
+  if (!q || !out || !n_surv || (prefix_len > 0 && (!k_prefix || !v_prefix)) ||
+      (n > 0 && (!k_cache || !v_cache)) || (prefix_len + n > 0 && !workspace))
+    return EMBLA_ERR_INVALID_ARG;
+  if ((sel_scores == nullptr) != (sel_hist == nullptr)) return EMBLA_ERR_INVALID_ARG;
+  if (sel_scores && score_stride < prefix_len + n) return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(out) || !aligned16(n_surv) || !aligned16(sel_scores) ||
+      !aligned16(sel_hist) || !aligned16(workspace))
+    return EMBLA_ERR_INVALID_ARG;
+  // TMA plane coordinates and the second kernel's grid are 32-bit
+  if (units * G > INT32_MAX / 2) return EMBLA_ERR_UNSUPPORTED;
+  const int sms = sm_count_of(current_device());
+  if (sms <= 0) return EMBLA_ERR_CUDA;
+  const SharedSplit sp = shared_split(shape->batch, shape->n_kv_heads, G, prefix_len, n, sms);
+  if (workspace_bytes < shared_workspace_bytes(sp)) return EMBLA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (sp.ctas() == 0) {
+    // no keys: every output is 0, nothing survives, the histogram is empty
+    if (sel_hist)
+      st = cuda_status(cudaMemsetAsync(sel_hist, 0, static_cast<size_t>(units) * kHistBins * 4, s));
+    if (st == EMBLA_OK)
+      st = cuda_status(cudaMemsetAsync(out, 0, static_cast<size_t>(units) * G * kHeadDim * 4, s));
+    if (st == EMBLA_OK) st = cuda_status(cudaMemsetAsync(n_surv, 0, static_cast<size_t>(units) * 4, s));
+    return st;
+  }
+  uint32_t *flags = flags_ptr();
+  if (!flags) return EMBLA_ERR_CUDA;
+  // Planes of the prefix and of the own caches; a side without keys has no tiles, and its maps
+  // stand in for nothing.
+  CUtensorMap tm_q, tm_kp, tm_vp, tm_ko, tm_vo;
+  const uint64_t planes = static_cast<uint64_t>(shape->n_kv_heads);
+  if (prefix_len > 0 &&
+      (!encode_planes(&tm_kp, k_prefix, static_cast<uint64_t>(prefix_len),
+                      static_cast<uint64_t>(prefix_stride), planes) ||
+       !encode_planes(&tm_vp, v_prefix, static_cast<uint64_t>(prefix_len),
+                      static_cast<uint64_t>(prefix_stride), planes)))
+    return EMBLA_ERR_CUDA;
+  if (n > 0 && (!encode_planes(&tm_ko, k_cache, static_cast<uint64_t>(n),
+                               static_cast<uint64_t>(shape->cache_stride), static_cast<uint64_t>(units)) ||
+                !encode_planes(&tm_vo, v_cache, static_cast<uint64_t>(n),
+                               static_cast<uint64_t>(shape->cache_stride), static_cast<uint64_t>(units))))
+    return EMBLA_ERR_CUDA;
+  if (n == 0) tm_ko = tm_kp, tm_vo = tm_vp;
+  if (prefix_len == 0) tm_kp = tm_ko, tm_vp = tm_vo;
+  if (!encode_query_block(&tm_q, q, shape->batch, shape->n_q_heads, shape->n_kv_heads)) return EMBLA_ERR_CUDA;
+  SharedCall a = {};
+  a.tm_q = &tm_q;
+  a.tm_kp = &tm_kp;
+  a.tm_vp = &tm_vp;
+  a.tm_ko = &tm_ko;
+  a.tm_vo = &tm_vo;
+  a.q = q;
+  a.k_prefix = k_prefix;
+  a.v_prefix = v_prefix;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.prefix_stride = prefix_stride;
+  a.cache_stride = shape->cache_stride;
+  a.sel_scores = sel_scores;
+  a.sel_hist = sel_hist;
+  a.score_stride = score_stride;
+  a.workspace = workspace;
+  a.out = out;
+  a.n_surv = n_surv;
+  a.flags = flags;
+  a.alpha = alpha;
+  a.c = c;
+  a.eps = eps;
+  a.sm_count = sms;
+  return cuda_status(launch_shared_decode(a, sp, s));
+}
+
+embla_status embla_sparse_decode_shared(const embla_shape *shape, int64_t prefix_len,
+                                        int64_t prefix_stride, const void *q, const void *k_prefix,
+                                        const void *v_prefix, const void *k_cache,
+                                        const void *v_cache, const int32_t *idx,
+                                        int32_t idx_stride, const int32_t *count, float tau,
+                                        float *out, void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, true);
+  if (st != EMBLA_OK) return st;
+  if (!prefix_fits(shape, prefix_len) || prefix_stride < prefix_len) return EMBLA_ERR_INVALID_ARG;
+  if (!finite(tau) || idx_stride < 0) return EMBLA_ERR_INVALID_ARG;
+  const int64_t units = static_cast<int64_t>(shape->batch) * shape->n_kv_heads;
+  if (units == 0) return EMBLA_OK;
+  if (!q || !idx || !count || !out || (prefix_len > 0 && (!k_prefix || !v_prefix)) ||
+      (shape->ctx_len > 0 && (!k_cache || !v_cache)))
+    return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(idx) || !aligned16(count) || !aligned16(out))
+    return EMBLA_ERR_INVALID_ARG;
+  if (units > INT32_MAX / 8) return EMBLA_ERR_UNSUPPORTED;  // the grid, in clusters of 8
+  uint32_t *flags = flags_ptr();
+  if (!flags) return EMBLA_ERR_CUDA;
+  const int sms = sm_count_of(current_device());
+  if (sms <= 0) return EMBLA_ERR_CUDA;
+  const SharedRows prefix = {k_prefix, v_prefix, prefix_len, prefix_stride};
+  return cuda_status(launch_sparse_decode(G, false, shape->n_q_heads, q, k_cache, v_cache, nullptr,
+                                          nullptr, idx, idx_stride, count, units,
+                                          shape->n_kv_heads, prefix_len + shape->ctx_len,
+                                          shape->cache_stride, tau, out, nullptr, flags, sms,
+                                          static_cast<cudaStream_t>(stream), &prefix));
+}
+
 size_t embla_relu2_mlp_workspace_size(int64_t d, int64_t f) {
   const int sms = sm_count_of(current_device());
   if (sms <= 0 || d < 1 || f < 1) return 0;
@@ -717,6 +877,52 @@ embla_status embla_append_kv_e4m3(const embla_shape *shape, int64_t pos, const u
       {reinterpret_cast<const uint8_t *>(k_scale_rows), reinterpret_cast<uint8_t *>(k_scales), 4, ncap, 0},
       {reinterpret_cast<const uint8_t *>(v_scale_rows), reinterpret_cast<uint8_t *>(v_scales), 4, ncap, 0}};
   return cuda_status(launch_append_rows(jobs, 4, units, pos, static_cast<cudaStream_t>(stream)));
+}
+
+embla_status embla_quantize_kv_e4m3(const embla_shape *shape, int64_t pos, int64_t n_new,
+                                    const void *k_rows, const void *v_rows, uint8_t *k_codes,
+                                    float *k_scales, uint8_t *v_codes, float *v_scales,
+                                    void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, false);
+  if (st != EMBLA_OK) return st;
+  if (!rows_in_cache(shape, pos, n_new)) return EMBLA_ERR_INVALID_ARG;
+  const int64_t units = static_cast<int64_t>(shape->batch) * shape->n_kv_heads;
+  if (units == 0 || n_new == 0) return EMBLA_OK;
+  if (!k_rows || !v_rows || !k_codes || !k_scales || !v_codes || !v_scales)
+    return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(k_rows) || !aligned16(v_rows) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      !aligned16(k_scales) || !aligned16(v_scales))
+    return EMBLA_ERR_INVALID_ARG;
+  if (n_new > INT32_MAX / units) return EMBLA_ERR_UNSUPPORTED;
+  const QuantizeParams p = {
+      {{static_cast<const uint16_t *>(k_rows), k_codes, k_scales},
+       {static_cast<const uint16_t *>(v_rows), v_codes, v_scales}},
+      units * n_new, n_new, shape->cache_stride, pos};
+  return cuda_status(launch_quantize_rows(p, static_cast<cudaStream_t>(stream)));
+}
+
+embla_status embla_dequantize_kv_e4m3(const embla_shape *shape, int64_t pos, int64_t n_rows,
+                                      const uint8_t *k_codes, const float *k_scales,
+                                      const uint8_t *v_codes, const float *v_scales, void *k_rows,
+                                      void *v_rows, int64_t rows_stride, void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, false);
+  if (st != EMBLA_OK) return st;
+  if (!rows_in_cache(shape, pos, n_rows) || rows_stride < n_rows) return EMBLA_ERR_INVALID_ARG;
+  const int64_t units = static_cast<int64_t>(shape->batch) * shape->n_kv_heads;
+  if (units == 0 || n_rows == 0) return EMBLA_OK;
+  if (!k_rows || !v_rows || !k_codes || !k_scales || !v_codes || !v_scales)
+    return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(k_rows) || !aligned16(v_rows) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      !aligned16(k_scales) || !aligned16(v_scales))
+    return EMBLA_ERR_INVALID_ARG;
+  if (n_rows > INT32_MAX / units) return EMBLA_ERR_UNSUPPORTED;
+  const DequantizeParams p = {
+      {{k_codes, k_scales, static_cast<uint16_t *>(k_rows)},
+       {v_codes, v_scales, static_cast<uint16_t *>(v_rows)}},
+      units * n_rows, n_rows, shape->cache_stride, pos, rows_stride};
+  return cuda_status(launch_dequantize_rows(p, static_cast<cudaStream_t>(stream)));
 }
 
 embla_status embla_self_test_wait_limit(uint32_t limit_us, int arrive, void *stream) {

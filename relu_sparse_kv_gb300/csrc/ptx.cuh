@@ -135,6 +135,16 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
+// 4-D tiled TMA load.
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
 // Same, with an L2 cache policy (createpolicy result).
 __device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *map, uint64_t *bar,
                                                  int32_t x, int32_t y, uint64_t policy) {
@@ -485,6 +495,30 @@ __device__ __forceinline__ void sq_acc_bf16x2(uint32_t w, float &a, float &b) {
       "fma.rn.f32.bf16 %1, hi, hi, %1;\n\t}"
       : "+f"(a), "+f"(b)
       : "r"(w));
+}
+
+// Sum of squares of row r of a 128 x 128 bf16 tile in shared memory (two 64-column boxes in the
+// 128-byte swizzle).  Pieces are taken in an order rotated by row, so neighbouring rows read
+// different banks; a sum of squares does not care which columns a piece holds.
+__device__ __forceinline__ float row_square_sum(const uint8_t *tile, int box_bytes, int r) {
+  float a[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int pc = (c ^ (r & 7)) * 16;
+    const uint4 x0 = *reinterpret_cast<const uint4 *>(tile + r * 128 + pc);
+    const uint4 x1 = *reinterpret_cast<const uint4 *>(tile + box_bytes + r * 128 + pc);
+    sq_acc_bf16x2(x0.x, a[0], a[1]);
+    sq_acc_bf16x2(x0.y, a[2], a[3]);
+    sq_acc_bf16x2(x0.z, a[4], a[5]);
+    sq_acc_bf16x2(x0.w, a[6], a[7]);
+    sq_acc_bf16x2(x1.x, a[0], a[1]);
+    sq_acc_bf16x2(x1.y, a[2], a[3]);
+    sq_acc_bf16x2(x1.z, a[4], a[5]);
+    sq_acc_bf16x2(x1.w, a[6], a[7]);
+  }
+  return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
 }
 
 // 8-bit E4M3 codes (OCP FP8: bias 7, no infinities, S.1111.111 NaN).  Every E4M3 value is

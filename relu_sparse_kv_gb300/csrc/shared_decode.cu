@@ -1,0 +1,755 @@
+// Full-layer (ReLU^2) decode of a batch whose sequences share one prefix: the prefix's keys
+// are held once and read once for the whole batch, each sequence's own keys follow them.
+//
+// Source: "The Architecture of Embla 1", "Sevren Sparse Attention learns to be sparse" and
+// "Three kinds of attention" (the weights, the normaliser and the score the selection ranks
+// are those of the full-layer decode).  With q^, k^ the RMS-normalised rows and
+// s' = q^ . k^, a query head's weights are w' = max(s', 0)^2 and
+//   out = sum_j w'_j v_j / (c / alpha^2 + sum_j w'_j)
+// over the prefix's keys and the sequence's own: sums over keys add, so pieces of the key
+// axis give partial sums (records) that a second kernel adds in a fixed order.
+//
+// One KV head's queries of 128 / G sequences make one 128-row operand, so every key tile is
+// a dense product for all of them:
+//   S  = Q K^T   (M 128 query rows x N 128 keys, fp32 in tensor memory)
+//   O += P V     (P = w' as two bf16 matrices hi + lo, about 17 bits of weight, in tensor
+//                memory over S; V as the cached rows lie)
+// A tile of a sequence's own keys runs through the same operands with every other sequence's
+// weights zero.  The value tile is read whole: a prefix key is dead for all of 128 rows far
+// too rarely to skip (0.95^128).
+//
+// Bound by HBM up to one row block (64 KB of K and V per tile at the SM's share of the
+// bandwidth takes longer than its products); the grid is one CTA per SM, shared out over the
+// row blocks so that the CTAs of different row blocks walk the same prefix tiles at the same
+// time (read from HBM once).
+//
+// Warp roles: 0 TMA producer (rings of 3 K and 3 V tiles); 1 issuer of S; 2-9 epilogue, one
+// thread per (query row, half of the tile's keys); 10 issuer of P V; 11-14 key norms, one
+// thread per key.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace embla {
+namespace {
+
+constexpr int kRows = 128;               // query rows of a row block
+constexpr int kRing = 3;                 // K, V, key-norm stages and S/P buffers
+constexpr int kEpiWarps = 8;
+constexpr int kNormWarps = 4;
+constexpr int kWarpPV = 2 + kEpiWarps;
+constexpr int kWarpNorm = kWarpPV + 1;
+constexpr int kSThreads = (kWarpNorm + kNormWarps) * 32;
+constexpr int kBox = 128 * 128;          // one [128 rows][64 bf16] box, 16 KB
+constexpr int kTileB = 2 * kBox;         // a 128 x 128 bf16 tile
+constexpr int kOffQ = 0;
+constexpr int kOffK = kOffQ + kTileB;
+constexpr int kOffV = kOffK + kRing * kTileB;
+constexpr int kOffRK = kOffV + kRing * kTileB;
+constexpr int kOffBar = kOffRK + kRing * kRows * 4;
+constexpr int kNBars = 1 + 7 * kRing + 3;
+constexpr int kOffMisc = kOffBar + kNBars * 8;
+constexpr int kSSmem = kOffMisc + 16 + 1024;  // + room to align the base to 1024
+static_assert(kSSmem <= 227 * 1024, "shared memory per CTA");
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
+constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) MN-major
+constexpr int kColO = kRing * 128, kTmemCols = 512;
+
+// A record: the numerators of 128 rows, each row's denominator and each sequence's
+// survivor count for either half of the tiles' keys.
+constexpr int kRecNum = kRows * kHeadDim;
+constexpr int kRecDen = 2 * kRows;
+constexpr int kRecCnt = 2 * 32;
+constexpr int kRecWords = kRecNum + kRecDen + kRecCnt;
+static_assert(kRecWords % 8 == 0, "records keep 32-byte alignment");
+
+struct SharedParams {
+  SharedSplit sp;
+  float *rec;
+  uint32_t *flags;
+  float *sel;              // [B, Hkv, score_stride] or null
+  uint32_t *hist;          // [B, Hkv, 2048] or null; zeroed here
+  int64_t score_stride;
+  int32_t vec_prefix, vec_own;  // score rows of prefix / own tiles start on 32 bytes
+  float alpha, eps;
+};
+
+__device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+// A CTA's part of the work: pieces of row block rb's tile list, and the stretch (the part of
+// it inside one KV head's list) at hand.
+struct Walk {
+  int rb, nb;           // the row block, its sequences
+  int64_t gt;           // tiles per KV head
+  int64_t t, end;       // the next tile, the piece's end
+  int64_t piece;
+  int g;                // stretch: KV head, tiles [t0, t1) of its list
+  int64_t t0, t1;
+  __device__ Walk(const SharedSplit &sp, int cta) {
+    rb = sp.block_of_cta(cta);
+    piece = cta - static_cast<int64_t>(rb) * sp.ctas_full;
+    nb = sp.sequences(rb);
+    gt = sp.group_tiles(rb);
+    const int64_t T = gt * sp.Hkv, Q = sp.pieces(rb);
+    t = split_piece_start(piece, T, Q);
+    end = split_piece_start(piece + 1, T, Q);
+  }
+  __device__ bool next() {
+    if (t >= end) return false;
+    g = static_cast<int>(t / gt);
+    t0 = t - g * gt;
+    const int64_t left = end - t;
+    t1 = gt - t0 < left ? gt : t0 + left;
+    t += t1 - t0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void give_up(volatile int *abort_flag, uint32_t *flags) {
+  *abort_flag = 1;
+  atomicOr(flags, kFlagWaitTimeout);
+}
+
+// The maximum of each of 32 values over the G lanes of a sequence: lane h of the group ends
+// with values h * 32 / G .. (reduce-scatter; NaN gives way to numbers).
+template <int G>
+__device__ __forceinline__ void group_max(float (&v)[32], int lane) {
+  static_assert(G == 4 || G == 8, "query heads per KV head");
+#pragma unroll
+  for (int o = G / 2, half = 16; o >= 1; o >>= 1, half >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int k = 0; k < half; ++k) {
+      const float send = upper ? v[k] : v[k + half];
+      const float keep = upper ? v[k + half] : v[k];
+      v[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+}
+
+template <int G>
+__global__ void __launch_bounds__(kSThreads, 1)
+    shared_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
+                         const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ko,
+                         const __grid_constant__ CUtensorMap tm_vo, const SharedParams p) {
+  constexpr int kSeqs = kRows / G;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *sQ = smem + kOffQ;
+  uint8_t *sK = smem + kOffK;
+  uint8_t *sV = smem + kOffV;
+  float *sRK = reinterpret_cast<float *>(smem + kOffRK);
+  uint64_t *qfull = reinterpret_cast<uint64_t *>(smem + kOffBar);
+  // A K stage is free once its tile's S is done (sfull) and its norms are taken (rkfull), a V
+  // stage once its P V is done (pvdone).
+  uint64_t *kfull = qfull + 1;
+  uint64_t *rkfull = kfull + kRing, *rkempty = rkfull + kRing;
+  uint64_t *vfull = rkempty + kRing;
+  uint64_t *sfull = vfull + kRing;
+  uint64_t *pfull = sfull + kRing;
+  uint64_t *pvdone = pfull + kRing;
+  uint64_t *ofull = pvdone + kRing;  // a stretch's P V all done
+  uint64_t *qempty = ofull + 1;      // its query rows no longer needed
+  uint64_t *ofree = qempty + 1;      // its O read out of tensor memory
+  uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
+  uint32_t *s_tmem = misc;
+  volatile int *s_abort = reinterpret_cast<volatile int *>(misc + 1);
+  volatile int *s_issued = reinterpret_cast<volatile int *>(misc + 2);   // tile loads issued
+  volatile int *s_qissued = reinterpret_cast<volatile int *>(misc + 3);  // query loads issued
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SharedSplit &sp = p.sp;
+
+  if (warp == 0) {
+    if (lane < kRing) {
+      mbar_init(&kfull[lane], 1);
+      mbar_init(&rkfull[lane], kNormWarps);
+      mbar_init(&rkempty[lane], kEpiWarps);
+      mbar_init(&vfull[lane], 1);
+      mbar_init(&sfull[lane], 1);
+      mbar_init(&pfull[lane], kEpiWarps);
+      mbar_init(&pvdone[lane], 1);
+    }
+    if (lane == 0) {
+      mbar_init(qfull, 1);
+      mbar_init(ofull, 1);
+      mbar_init(qempty, 1 + kEpiWarps);  // the S issuer's commit + every epilogue warp
+      mbar_init(ofree, kEpiWarps);
+      *s_abort = 0;
+      *s_issued = 0;
+      *s_qissued = 0;
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  // Every role walks the CTA's stretches in the same order, and their tiles through the rings
+  // by a running tile count i: stage i % kRing, phase (i / kRing) & 1.  Stretch k's query and
+  // output barriers take phase k & 1.
+  Walk w(sp, static_cast<int>(blockIdx.x));
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      for (int k = 0; ok && w.next(); ++k) {
+        if (k > 0 && !mbar_wait(qempty, (k - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(qfull, kTileB);
+        tma_load_4d(sQ, &tm_q, qfull, 0, 0, w.g, w.rb * kSeqs);
+        tma_load_4d(sQ + kBox, &tm_q, qfull, 64, 0, w.g, w.rb * kSeqs);
+        *s_qissued = k + 1;
+        for (int64_t t = w.t0; t < w.t1; ++t, ++i) {
+          const int s = i % kRing;
+          const uint32_t ph = ((i / kRing) - 1) & 1;
+          const bool own = t >= sp.tp;
+          const int64_t x = t - sp.tp;
+          const int row = static_cast<int>((own ? x % sp.ts : t) * kTileKeys);
+          const int plane = own ? static_cast<int>((w.rb * kSeqs + x / sp.ts) * sp.Hkv + w.g) : w.g;
+          const CUtensorMap *mk = own ? &tm_ko : &tm_kp, *mv = own ? &tm_vo : &tm_vp;
+          if (i >= kRing && !(mbar_wait(&sfull[s], ph) && mbar_wait(&rkfull[s], ph))) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&kfull[s], kTileB);
+          tma_load_3d(sK + s * kTileB, mk, &kfull[s], 0, row, plane);
+          tma_load_3d(sK + s * kTileB + kBox, mk, &kfull[s], 64, row, plane);
+          if (i >= kRing && !mbar_wait(&pvdone[s], ph)) {
+            *s_issued = 2 * i + 1;
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&vfull[s], kTileB);
+          tma_load_3d(sV + s * kTileB, mv, &vfull[s], 0, row, plane);
+          tma_load_3d(sV + s * kTileB + kBox, mv, &vfull[s], 64, row, plane);
+          *s_issued = 2 * i + 2;
+        }
+      }
+      if (!ok) give_up(s_abort, p.flags);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ S issuer
+    if (lane == 0) {
+      const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
+      const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
+      int i = 0;
+      bool ok = true;
+      for (int k = 0; ok && w.next(); ++k) {
+        ok = !*s_abort && mbar_wait(qfull, k & 1);
+        for (int64_t t = w.t0; ok && t < w.t1; ++t, ++i) {
+          const int s = i % kRing;
+          ok = mbar_wait(&kfull[s], (i / kRing) & 1) &&
+               (i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1));
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // dims 16kk..16kk+15: 32 bytes into a 128-byte row; dims 64.. start the second box
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
+            tc_mma_bf16(tmem + s * 128, qdesc + off, kdesc + static_cast<uint64_t>((s * kTileB) >> 4) + off,
+                        kIdescS, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&sfull[s]);
+        }
+        if (ok) tc_commit(qempty);
+      }
+      if (!ok) give_up(s_abort, p.flags);
+    }
+    __syncwarp();
+  } else if (warp == kWarpPV) {
+    // ------------------------------------------------------------------ P V issuer
+    if (lane == 0) {
+      int i = 0, done = 0;
+      bool ok = true;
+      for (int k = 0; ok && w.next(); ++k) {
+        ok = !*s_abort && (k == 0 || mbar_wait(ofree, (k - 1) & 1));
+        for (int64_t t = w.t0; ok && t < w.t1; ++t, ++i) {
+          const int s = i % kRing;
+          ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[s], (i / kRing) & 1);
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // keys 16kk..16kk+15: in their group of 32 columns hi takes the first 16, lo the rest
+            const uint32_t a_hi = tmem + s * 128 + (kk >> 1) * 32 + (kk & 1) * 8;
+            const uint64_t vd = smem_desc_sw128_mn(smem_u32(sV + s * kTileB + kk * 2048), kBox);
+            tc_mma_bf16_tmem_a(tmem + kColO, a_hi, vd, kIdescPV, (t > w.t0 || kk > 0) ? 1u : 0u);
+            tc_mma_bf16_tmem_a(tmem + kColO, a_hi + 16, vd, kIdescPV, 1u);
+          }
+          tc_commit(&pvdone[s]);
+        }
+        if (ok) {
+          tc_commit(ofull);
+          done = k + 1;
+        }
+      }
+      if (!ok) give_up(s_abort, p.flags);
+      // every MMA of this thread has completed before the tensor memory is released
+      if (done > 0) mbar_wait(ofull, (done - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpNorm) {
+    // ------------------------------------------------------------------ key norms
+    const int r = (warp - kWarpNorm) * 32 + lane;  // this thread's key of every tile
+    int i = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      for (int64_t t = w.t0; ok && t < w.t1; ++t, ++i) {
+        const int s = i % kRing;
+        ok = mbar_wait(&kfull[s], (i / kRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const float rk = rsqrtf(row_square_sum(sK + s * kTileB, kBox, r) * (1.0f / kHeadDim) + p.eps);
+        ok = i < kRing || mbar_wait(&rkempty[s], ((i / kRing) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        sRK[s * kRows + r] = rk;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rkfull[s]);
+      }
+    }
+    if (!ok && lane == 0) give_up(s_abort, p.flags);
+    // the counts of the selection's bins, added up by the next kernel, start at zero
+    if (p.hist != nullptr) {
+      uint4 *h = reinterpret_cast<uint4 *>(p.hist);
+      const int64_t n4 = static_cast<int64_t>(sp.B) * sp.Hkv * (kHistBins / 4);
+      for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRows + r; e < n4; e += static_cast<int64_t>(gridDim.x) * kRows)
+        h[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;          // the tensor-memory lanes this warp may read
+    const int half = (warp - 2) >> 2;      // keys 64 half .. of each tile
+    const int r = quarter * 32 + lane;     // query row: sequence r / G of the block, head r % G
+    const int seq = r / G, h = r % G;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    int i = 0;
+    bool ok = true;
+    for (int k = 0; ok && w.next(); ++k) {
+      ok = !*s_abort && mbar_wait(qfull, k & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const float ss = row_square_sum(sQ, kBox, r);
+      const float rq = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
+      {
+        // the query rows are read: every lane's sum depends on them
+        const float used = __shfl_sync(0xffffffffu, ss, 0) + __shfl_sync(0xffffffffu, ss, 31);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_after(qempty, used);
+      }
+      const bool valid = seq < w.nb;
+      float *scores = nullptr;  // this row's (sequence, KV head)
+      if (p.sel != nullptr && valid)
+        scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride;
+      float den[2] = {0.0f, 0.0f};
+      int live = 0;  // keys of this lane's share with a group maximum above zero
+      for (int64_t t = w.t0; t < w.t1; ++t, ++i) {
+        const int s = i % kRing;
+        ok = mbar_wait(&sfull[s], (i / kRing) & 1) && mbar_wait(&rkfull[s], (i / kRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const bool own = t >= sp.tp;
+        const int64_t x = t - sp.tp;
+        const int owner = own ? static_cast<int>(x / sp.ts) : 0;
+        const int64_t kt = own ? x % sp.ts : t;
+        const bool mine = valid && (!own || seq == owner);
+        const float rqm = mine ? rq : 0.0f;  // another sequence's keys weigh nothing here
+        // keys of the tile that exist; the first one's place in the score row
+        const int64_t rest = (own ? sp.n : sp.P) - kt * kTileKeys;
+        const int64_t j0 = (own ? sp.P : 0) + kt * kTileKeys;
+        const bool vec = rest >= kTileKeys && (own ? p.vec_own : p.vec_prefix);
+#pragma unroll
+        for (int c0 = 0; c0 < 2; ++c0) {
+          const int col = half * 64 + c0 * 32;
+          const uint32_t cols = tmem + lane_base + s * 128 + col;
+          uint32_t acc[32];
+          tmem_load_x32(cols, acc);
+          tmem_wait_ld(acc);
+          const float *rkp = sRK + s * kRows + col;
+          float v[32];
+          uint32_t pw[32];  // the weights: 16 columns of hi, 16 of lo
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 rk = *reinterpret_cast<const float2 *>(rkp + c);
+            v[c] = __uint_as_float(acc[c]);
+            v[c + 1] = __uint_as_float(acc[c + 1]);
+            mul2(v[c], v[c + 1], rk.x, rk.y);
+            mul2(v[c], v[c + 1], rqm, rqm);
+            float w0 = fmaxf(v[c], 0.0f), w1 = fmaxf(v[c + 1], 0.0f);
+            mul2(w0, w1, w0, w1);
+            den[0] += w0;
+            den[1] += w1;
+            const uint32_t hi = pack_bf16x2(w0, w1);
+            pw[c >> 1] = hi;
+            pw[16 + (c >> 1)] = pack_bf16x2(w0 - bf16lo(hi), w1 - bf16hi(hi));
+          }
+          tmem_store_x32(cols, pw);
+          group_max<G>(v, lane);
+          constexpr int kMine = 32 / G;  // keys this lane holds the maximum of
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) live += v[c] > 0.0f ? 1 : 0;
+          if (scores != nullptr && mine) {
+            const int first = col + h * kMine;
+            float *dst = scores + j0 + first;
+            if (vec) {
+              if constexpr (G == 4)
+                st_global_v8(dst, p.alpha * v[0], p.alpha * v[1], p.alpha * v[2], p.alpha * v[3],
+                             p.alpha * v[4], p.alpha * v[5], p.alpha * v[6], p.alpha * v[7]);
+              else
+                *reinterpret_cast<float4 *>(dst) =
+                    make_float4(p.alpha * v[0], p.alpha * v[1], p.alpha * v[2], p.alpha * v[3]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < kMine; ++c)
+                if (first + c < rest) dst[c] = p.alpha * v[c];
+            }
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();  // P is read by the tensor cores
+        // every lane's weight sums depend on all of its key-norm reads
+        const float used = __shfl_sync(0xffffffffu, den[0], 0) + __shfl_sync(0xffffffffu, den[1], 31);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&pfull[s]);
+          mbar_arrive_after(&rkempty[s], used);
+        }
+      }
+      if (!ok) break;
+      ok = mbar_wait(ofull, k & 1) && !*s_abort;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after_sync();
+      uint32_t o[64];
+      tmem_load_x32(tmem + lane_base + kColO + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+      tmem_load_x32(tmem + lane_base + kColO + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+      tmem_wait_ld(o);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree);  // the next stretch's P V may overwrite O
+      // The record: every row when the stretch holds prefix tiles, else the rows of the
+      // sequences whose tiles it holds.
+      const int first_seq = w.t0 < sp.tp ? 0 : static_cast<int>((w.t0 - sp.tp) / sp.ts);
+      const int last_seq = w.t0 < sp.tp ? w.nb - 1 : static_cast<int>((w.t1 - 1 - sp.tp) / sp.ts);
+#pragma unroll
+      for (int m = 1; m < G; m <<= 1) live += __shfl_xor_sync(0xffffffffu, live, m);
+      if (seq >= first_seq && seq <= last_seq) {
+        float *rec = p.rec + sp.slot(w.rb, w.piece, w.g) * kRecWords;
+        float *dst = rec + r * kHeadDim + half * 64;
+#pragma unroll
+        for (int c = 0; c < 64; c += 8)
+          st_global_v8(dst + c, __uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
+                       __uint_as_float(o[c + 3]), __uint_as_float(o[c + 4]), __uint_as_float(o[c + 5]),
+                       __uint_as_float(o[c + 6]), __uint_as_float(o[c + 7]));
+        rec[kRecNum + half * kRows + r] = den[0] + den[1];
+        if (h == 0) reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + half * 32 + seq] = live;
+      }
+    }
+    if (!ok && lane == 0) give_up(s_abort, p.flags);
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0 && *s_abort) {
+    // No copy may still be landing in shared memory when the CTA leaves.  Without an abort
+    // every copy issued was waited for by the role that used it; after one, wait (bounded)
+    // for the last armed phase of every barrier that a copy completes.
+    const int qi = *s_qissued;
+    if (qi > 0) mbar_wait(qfull, (qi - 1) & 1);
+    const int issued = *s_issued;  // 2 per key tile: K, V
+    const int nk = (issued + 1) / 2, nv = issued / 2;
+    for (int s = 0; s < kRing; ++s) {
+      int uses = nk > s ? (nk - 1 - s) / kRing + 1 : 0;
+      if (uses) mbar_wait(&kfull[s], (uses - 1) & 1);
+      uses = nv > s ? (nv - 1 - s) / kRing + 1 : 0;
+      if (uses) mbar_wait(&vfull[s], (uses - 1) & 1);
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------------------- finish
+
+constexpr int kFThreads = 256;
+constexpr int kFWarps = kFThreads / 32;
+
+struct FinishParams {
+  SharedSplit sp;
+  const float *rec;
+  const uint16_t *q;
+  const uint16_t *kp, *vp, *ko, *vo;
+  int64_t prefix_stride, cache_stride;
+  const float *sel;
+  uint32_t *hist;
+  int64_t score_stride;
+  int32_t hist_ctas, hist_splits;  // CTAs of the histogram part; per (sequence, KV head)
+  float *out;
+  int32_t *n_surv;
+  float alpha, c, eps;
+};
+
+// A row whose sums are not finite, term by term: the products of a whole value tile give NaN
+// where a weight of zero meets a value that is infinite or NaN, and a key of weight zero (or
+// another sequence's key) contributes nothing here.  One pass over all keys per row: slow,
+// and only for inputs that hold such values.
+__device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int hq, float *s_q, float *s_w,
+                                              float *s_sum) {
+  const SharedSplit &sp = p.sp;
+  const int g = hq / sp.G, tid = threadIdx.x;
+  if (tid < kHeadDim)
+    s_q[tid] = __uint_as_float(static_cast<uint32_t>(p.q[(static_cast<int64_t>(b) * sp.G * sp.Hkv + hq) * kHeadDim + tid]) << 16);
+  __syncthreads();
+  float qs = 0.0f;
+  for (int d = 0; d < kHeadDim; ++d) qs = fmaf(s_q[d], s_q[d], qs);
+  const float rq = rsqrtf(qs * (1.0f / kHeadDim) + p.eps);
+  const int64_t N = sp.P + sp.n;
+  const int64_t unit = static_cast<int64_t>(b) * sp.Hkv + g;
+  float num = 0.0f, den = 0.0f;  // thread d < 128: dimension d
+  for (int64_t j0 = 0; j0 < N; j0 += kFThreads) {
+    const int64_t j = j0 + tid;
+    float w = 0.0f;
+    if (j < N) {
+      const uint16_t *kr = j < sp.P ? p.kp + (g * p.prefix_stride + j) * kHeadDim
+                                    : p.ko + (unit * p.cache_stride + j - sp.P) * kHeadDim;
+      float dot = 0.0f, k0 = 0.0f, k1 = 0.0f;
+      for (int d = 0; d < kHeadDim; d += 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(kr + d);
+        dot = fmaf(s_q[d], bf16lo(x), dot);
+        dot = fmaf(s_q[d + 1], bf16hi(x), dot);
+        sq_acc_bf16x2(x, k0, k1);
+      }
+      w = fmaxf(dot * rsqrtf((k0 + k1) * (1.0f / kHeadDim) + p.eps) * rq, 0.0f);
+      w *= w;
+    }
+    s_w[tid] = w;
+    __syncthreads();
+    if (tid < kHeadDim) {
+      float a = 0.0f, z = 0.0f;
+      const int m = N - j0 < kFThreads ? static_cast<int>(N - j0) : kFThreads;
+      for (int i = 0; i < m; ++i) {
+        const float wi = s_w[i];
+        if (wi == 0.0f) continue;
+        const int64_t ji = j0 + i;
+        const uint16_t *vr = ji < sp.P ? p.vp + (g * p.prefix_stride + ji) * kHeadDim
+                                       : p.vo + (unit * p.cache_stride + ji - sp.P) * kHeadDim;
+        a = fmaf(wi, __uint_as_float(static_cast<uint32_t>(vr[tid]) << 16), a);
+        z += wi;
+      }
+      num += a;
+      den += z;
+    }
+    __syncthreads();
+  }
+  if (tid < kHeadDim) {
+    s_sum[tid] = num;
+    if (tid == 0) s_sum[kHeadDim] = den;
+  }
+  __syncthreads();
+}
+
+// One launch, two kinds of CTA: the first hist_ctas count the selection's bins of a part of a
+// unit's scores; the others finish one query head's output each from its records.
+__global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishParams p) {
+  __shared__ __align__(16) uint32_t s_mem[kHistBins];
+  const SharedSplit &sp = p.sp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) < p.hist_ctas) {
+    for (int e = threadIdx.x; e < kHistBins; e += kFThreads) s_mem[e] = 0u;
+    __syncthreads();
+    pdl_wait_primary();  // the scores are complete
+    pdl_launch_dependents();
+    const int64_t u = blockIdx.x / p.hist_splits, part = blockIdx.x % p.hist_splits;
+    const int64_t N = sp.P + sp.n;
+    const int64_t a = N * part / p.hist_splits, e = N * (part + 1) / p.hist_splits;
+    const float *su = p.sel + u * p.score_stride;
+    for (int64_t j = a + threadIdx.x; j < e; j += kFThreads) atomicAdd(&s_mem[order_key(su[j]) >> 21], 1u);
+    __syncthreads();
+    for (int k = threadIdx.x; k < kHistBins; k += kFThreads)
+      if (s_mem[k] != 0u) atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
+    return;
+  }
+  pdl_wait_primary();  // the records are complete
+  pdl_launch_dependents();
+  const int row = static_cast<int>(blockIdx.x) - p.hist_ctas;
+  const int Hq = sp.G * sp.Hkv;
+  const int b = row / Hq, hq = row % Hq, g = hq / sp.G;
+  const int seqs = kRows / sp.G;
+  const int rb = b / seqs, seq = b % seqs, r = seq * sp.G + hq % sp.G;
+  // the pieces whose record holds this row: those with prefix tiles of this KV head, then
+  // those with own tiles of this sequence
+  const int64_t gt = sp.group_tiles(rb), T = gt * sp.Hkv, Q = sp.pieces(rb), base = g * gt;
+  int64_t qa = 0, qb = -1, qc = 0, qd = -1;
+  if (sp.tp > 0) {
+    qa = split_piece_of_tile(base, T, Q);
+    qb = split_piece_of_tile(base + sp.tp - 1, T, Q);
+  }
+  if (sp.ts > 0) {
+    const int64_t own = base + sp.tp + static_cast<int64_t>(seq) * sp.ts;
+    qc = split_piece_of_tile(own, T, Q);
+    qd = split_piece_of_tile(own + sp.ts - 1, T, Q);
+    if (qc <= qb) qc = qb + 1;
+  }
+  const int n1 = static_cast<int>(qb - qa + 1), nrec = n1 + static_cast<int>(qd >= qc ? qd - qc + 1 : 0);
+  auto record = [&](int i) {
+    return p.rec + sp.slot(rb, i < n1 ? qa + i : qc + (i - n1), g) * kRecWords;
+  };
+  // each warp adds every eighth record, lane l dims 4l .. 4l + 3; then the warps in order
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float den = 0.0f;
+  int live = 0;
+#pragma unroll 4
+  for (int i = warp; i < nrec; i += kFWarps) {
+    const float *rec = record(i);
+    const float4 x = *reinterpret_cast<const float4 *>(rec + r * kHeadDim + 4 * lane);
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+    if (lane < 2) {
+      den += rec[kRecNum + lane * kRows + r];
+      live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
+    }
+  }
+  float *s_acc = reinterpret_cast<float *>(s_mem);            // [8 warps][128]
+  float *s_den = s_acc + kFWarps * kHeadDim;                  // [8][2]
+  int *s_live = reinterpret_cast<int *>(s_den + 2 * kFWarps);  // [8][2]
+  *reinterpret_cast<float4 *>(s_acc + warp * kHeadDim + 4 * lane) = acc;
+  if (lane < 2) {
+    s_den[warp * 2 + lane] = den;
+    s_live[warp * 2 + lane] = live;
+  }
+  __syncthreads();
+  float num = 0.0f, dsum = 0.0f;
+  int nlive = 0;
+  if (threadIdx.x < kHeadDim) {
+#pragma unroll
+    for (int k = 0; k < kFWarps; ++k) num += s_acc[k * kHeadDim + threadIdx.x];
+#pragma unroll
+    for (int k = 0; k < 2 * kFWarps; ++k) {
+      dsum += s_den[k];
+      nlive += s_live[k];
+    }
+  }
+  const bool bad = !(fabsf(num) <= 3.402823466e38f);
+  if (__syncthreads_or(bad)) {
+    float *s_sum = reinterpret_cast<float *>(s_mem);  // [129]
+    row_term_by_term(p, b, hq, s_sum + 256, s_sum + 512, s_sum);
+    num = s_sum[threadIdx.x < kHeadDim ? threadIdx.x : 0];
+    dsum = s_sum[kHeadDim];
+  }
+  if (threadIdx.x < kHeadDim) {
+    const float z = p.c / p.alpha / p.alpha + dsum;
+    p.out[static_cast<int64_t>(row) * kHeadDim + threadIdx.x] = z != 0.0f ? num / z : 0.0f;
+    if (threadIdx.x == 0 && hq % sp.G == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
+  }
+}
+
+}  // namespace
+
+SharedSplit shared_split(int B, int Hkv, int G, int64_t P, int64_t n, int sm_count) {
+  SharedSplit sp = {};
+  sp.P = P;
+  sp.n = n;
+  sp.B = B;
+  sp.Hkv = Hkv;
+  sp.G = G;
+  sp.tp = (P + kTileKeys - 1) / kTileKeys;
+  sp.ts = (n + kTileKeys - 1) / kTileKeys;
+  const int seqs = kRows / G;
+  sp.blocks = (B + seqs - 1) / seqs;
+  if (sp.blocks == 0 || sp.tp + sp.ts == 0) return sp;
+  // CTAs per row block in proportion to its tiles: as many as fit the SMs, one at least
+  const int64_t full = sp.group_tiles(0) * Hkv, last = sp.group_tiles(sp.blocks - 1) * Hkv;
+  int64_t cf = sm_count / (sp.blocks > 1 ? sp.blocks - 1 : 1);
+  if (cf > full) cf = full;
+  int64_t cl = 1;
+  for (; cf >= 1; --cf) {
+    cl = (cf * last + full - 1) / full;
+    if (cl > last) cl = last;
+    if ((sp.blocks - 1) * cf + cl <= sm_count) break;
+  }
+  if (cf < 1) {
+    cf = 1;
+    cl = 1;
+  }
+  sp.ctas_full = static_cast<int32_t>(cf);
+  sp.ctas_last = static_cast<int32_t>(cl);
+  return sp;
+}
+
+size_t shared_workspace_bytes(const SharedSplit &sp) {
+  if (sp.ctas() == 0) return 0;
+  // + room to align the records to 32 bytes
+  return static_cast<size_t>(sp.slot(sp.blocks, 0, 0)) * kRecWords * 4 + 16;
+}
+
+cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cudaStream_t stream) {
+  SharedParams p;
+  p.sp = sp;
+  p.rec = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(a.workspace) + 31u) & ~uintptr_t{31});
+  p.flags = a.flags;
+  p.sel = a.sel_scores;
+  p.hist = a.sel_hist;
+  p.score_stride = a.score_stride;
+  const bool rows32 = (reinterpret_cast<uintptr_t>(a.sel_scores) & 31u) == 0 && a.score_stride % 8 == 0;
+  p.vec_prefix = rows32;
+  p.vec_own = rows32 && sp.P % 8 == 0;
+  p.alpha = a.alpha;
+  p.eps = a.eps;
+  auto kernel = sp.G == 4 ? shared_decode_kernel<4> : shared_decode_kernel<8>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(sp.ctas())), dim3(kSThreads), static_cast<size_t>(kSSmem),
+                 stream, 0u, *a.tm_q, *a.tm_kp, *a.tm_vp, *a.tm_ko, *a.tm_vo, p);
+  if (e != cudaSuccess) return e;
+  FinishParams f;
+  f.sp = sp;
+  f.rec = p.rec;
+  f.q = static_cast<const uint16_t *>(a.q);
+  f.kp = static_cast<const uint16_t *>(a.k_prefix);
+  f.vp = static_cast<const uint16_t *>(a.v_prefix);
+  f.ko = static_cast<const uint16_t *>(a.k_cache);
+  f.vo = static_cast<const uint16_t *>(a.v_cache);
+  f.prefix_stride = a.prefix_stride;
+  f.cache_stride = a.cache_stride;
+  f.sel = a.sel_scores;
+  f.hist = a.sel_hist;
+  f.score_stride = a.score_stride;
+  const int64_t units = static_cast<int64_t>(sp.B) * sp.Hkv;
+  // parts of a unit's scores: enough CTAs for the SMs, 4096 keys a part at least
+  int64_t splits = (2 * static_cast<int64_t>(a.sm_count) + units - 1) / units;
+  const int64_t most = (sp.P + sp.n + 4095) / 4096;
+  f.hist_splits = static_cast<int32_t>(splits < most ? splits : most);
+  f.hist_ctas = a.sel_hist != nullptr ? static_cast<int32_t>(units * f.hist_splits) : 0;
+  f.out = a.out;
+  f.n_surv = a.n_surv;
+  f.alpha = a.alpha;
+  f.c = a.c;
+  f.eps = a.eps;
+  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(f.hist_ctas + units * sp.G)), dim3(kFThreads),
+                    0, stream, 0u, f);
+}
+
+}  // namespace embla

@@ -317,6 +317,10 @@ struct SparseParams {
   // cache plane of unit u: u itself, or for a selection per query head (one unit per
   // (sequence, query head)) (u / Hq) * Hkv + (u % Hq) / Gq
   int per_head, Hq, Hkv, Gq;
+  // shared-prefix variant: rows below plen lie in the prefix's planes (one per KV head,
+  // pstride rows apart), row j >= plen is row j - plen of the unit's own cache
+  const uint8_t *Kp, *Vp;
+  int64_t plen, pstride;
   __device__ int64_t plane(int64_t u) const {
     return per_head ? (u / Hq) * Hkv + (u % Hq) / Gq : u;
   }
@@ -405,7 +409,7 @@ __device__ __forceinline__ void sp_combine(SpMerge<G, W> &mg, int rank, int64_t 
   cluster_wait();  // and they are done reading this one's
 }
 
-template <int G, int CL, int W = kSpWarps>
+template <int G, int CL, int W = kSpWarps, bool SHARED = false>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(W * 32, W <= kSpWarps ? 2 : 1)
     sparse_decode_kernel(const SparseParams p) {
   pdl_wait_primary();  // the selection and the query are complete
@@ -430,6 +434,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(W * 32, W <= kSpWar
   cnt = cnt < 0 ? 0 : (cnt > p.idx_stride ? p.idx_stride : cnt);
   const uint8_t *Ku = p.K + p.plane(u) * p.ncap * kRowBytes;
   const uint8_t *Vu = p.V + p.plane(u) * p.ncap * kRowBytes;
+  const int64_t prow0 = SHARED ? (u % p.Hkv) * p.pstride : 0;  // the prefix plane's first row
   const float tau2 = p.tau * kLog2e;
   uint8_t *sK = smem + warp * kSpStage;
   uint8_t *sV = sK + kSpBlock * kRowBytes;
@@ -470,9 +475,17 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(W * 32, W <= kSpWar
       const int r = 2 * k + (lane >> 4);
       const int64_t jr = __shfl_sync(0xffffffffu, j, r);
       const uint32_t nbytes = jr >= 0 ? 16u : 0u;
-      const int64_t off = (jr >= 0 ? jr : 0) * kRowBytes + piece * 16;
-      cp_async16_zfill(sK + sp_piece(r, piece), Ku + off, nbytes);
-      cp_async16_zfill(sV + sp_piece(r, piece), Vu + off, nbytes);
+      if constexpr (SHARED) {
+        const bool pre = jr < p.plen;  // absent rows count as prefix rows and are not read
+        const int64_t own = jr - p.plen;
+        const int64_t off = (jr < 0 ? 0 : pre ? prow0 + jr : own) * kRowBytes + piece * 16;
+        cp_async16_zfill(sK + sp_piece(r, piece), (pre ? p.Kp : Ku) + off, nbytes);
+        cp_async16_zfill(sV + sp_piece(r, piece), (pre ? p.Vp : Vu) + off, nbytes);
+      } else {
+        const int64_t off = (jr >= 0 ? jr : 0) * kRowBytes + piece * 16;
+        cp_async16_zfill(sK + sp_piece(r, piece), Ku + off, nbytes);
+        cp_async16_zfill(sV + sp_piece(r, piece), Vu + off, nbytes);
+      }
     }
     cp_async_wait_all();
     __syncwarp();
@@ -850,38 +863,32 @@ cudaError_t launch_sparse_t(void (*kernel)(SparseParams), dim3 grid, const Spars
   return launch_pdl(kernel, grid, dim3(W * 32), bytes, stream, 0u, p);
 }
 
-template <int G>
+template <int G, bool SHARED = false>
 cudaError_t launch_sparse_g(dim3 grid, const SparseParams &p, cudaStream_t stream) {
   if (p.wide) {
     // the wide variant (bf16 caches, clusters of up to 4)
     if (p.ks != nullptr) return cudaErrorInvalidValue;
     if (p.cl == 4)
-      return launch_sparse_t<false, kSpWideWarps>(sparse_decode_kernel<G, 4, kSpWideWarps>, grid, p, stream);
+      return launch_sparse_t<false, kSpWideWarps>(sparse_decode_kernel<G, 4, kSpWideWarps, SHARED>, grid, p, stream);
     if (p.cl == 2)
-      return launch_sparse_t<false, kSpWideWarps>(sparse_decode_kernel<G, 2, kSpWideWarps>, grid, p, stream);
+      return launch_sparse_t<false, kSpWideWarps>(sparse_decode_kernel<G, 2, kSpWideWarps, SHARED>, grid, p, stream);
     return cudaErrorInvalidValue;
   }
-  if constexpr (G == 1) {
-    switch (p.cl) {
-      case 8: return launch_sparse_t<false>(sparse_decode_kernel<1, 8>, grid, p, stream);
-      case 4: return launch_sparse_t<false>(sparse_decode_kernel<1, 4>, grid, p, stream);
-      case 2: return launch_sparse_t<false>(sparse_decode_kernel<1, 2>, grid, p, stream);
-      default: return launch_sparse_t<false>(sparse_decode_kernel<1, 1>, grid, p, stream);
-    }
-  }
-  if (p.ks != nullptr) {
-    switch (p.cl) {
-      case 8: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 8>, grid, p, stream);
-      case 4: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 4>, grid, p, stream);
-      case 2: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 2>, grid, p, stream);
-      default: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 1>, grid, p, stream);
+  if constexpr (G > 1 && !SHARED) {
+    if (p.ks != nullptr) {
+      switch (p.cl) {
+        case 8: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 8>, grid, p, stream);
+        case 4: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 4>, grid, p, stream);
+        case 2: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 2>, grid, p, stream);
+        default: return launch_sparse_t<true>(sparse_decode_e4m3_kernel<G, 1>, grid, p, stream);
+      }
     }
   }
   switch (p.cl) {
-    case 8: return launch_sparse_t<false>(sparse_decode_kernel<G, 8>, grid, p, stream);
-    case 4: return launch_sparse_t<false>(sparse_decode_kernel<G, 4>, grid, p, stream);
-    case 2: return launch_sparse_t<false>(sparse_decode_kernel<G, 2>, grid, p, stream);
-    default: return launch_sparse_t<false>(sparse_decode_kernel<G, 1>, grid, p, stream);
+    case 8: return launch_sparse_t<false>(sparse_decode_kernel<G, 8, kSpWarps, SHARED>, grid, p, stream);
+    case 4: return launch_sparse_t<false>(sparse_decode_kernel<G, 4, kSpWarps, SHARED>, grid, p, stream);
+    case 2: return launch_sparse_t<false>(sparse_decode_kernel<G, 2, kSpWarps, SHARED>, grid, p, stream);
+    default: return launch_sparse_t<false>(sparse_decode_kernel<G, 1, kSpWarps, SHARED>, grid, p, stream);
   }
 }
 
@@ -899,11 +906,11 @@ cudaError_t launch_sparse_decode(int G, bool per_head, int Hq, const void *q, co
                                  const float *k_scales, const float *v_scales, const int32_t *idx, int idx_stride, const int32_t *count,
                                  int64_t units, int Hkv, int64_t n, int64_t ncap, float tau,
                                  float *out, void *workspace, uint32_t *flags, int sm_count,
-                                 cudaStream_t stream) {
+                                 cudaStream_t stream, const SharedRows *prefix) {
   (void)Hkv;
   (void)workspace;
   if (units == 0) return cudaSuccess;
-  SparseParams p;
+  SparseParams p = {};
   p.q = static_cast<const uint16_t *>(q);
   p.K = static_cast<const uint8_t *>(k_cache);
   p.V = static_cast<const uint8_t *>(v_cache);
@@ -940,6 +947,17 @@ cudaError_t launch_sparse_decode(int G, bool per_head, int Hq, const void *q, co
   p.Hkv = Hkv;
   p.Gq = Hq / Hkv;
   const dim3 grid(static_cast<unsigned>(units * cl));
+  if (prefix != nullptr) {
+    // rows from two places: one unit per (sequence, KV head), bf16 caches
+    if (per_head || k_scales != nullptr) return cudaErrorInvalidValue;
+    p.Kp = static_cast<const uint8_t *>(prefix->k);
+    p.Vp = static_cast<const uint8_t *>(prefix->v);
+    p.plen = prefix->len;
+    p.pstride = prefix->stride;
+    if (G == 4) return launch_sparse_g<4, true>(grid, p, stream);
+    if (G == 8) return launch_sparse_g<8, true>(grid, p, stream);
+    return cudaErrorInvalidValue;
+  }
   if (per_head) {
     // one query head per unit (its own rows); 8-bit caches are not built for this variant
     if (k_scales != nullptr) return cudaErrorInvalidValue;
