@@ -21,6 +21,7 @@ Tensors (torch, on the current CUDA device, C-contiguous):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -59,6 +60,11 @@ class Shape:
     def c(self) -> _Shape:
         return _Shape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.ctx_len,
                       self.cache_stride)
+
+    @functools.cached_property
+    def ref(self):
+        """The shape as the C calls take it (they read it only)."""
+        return ctypes.byref(self.c())
 
     @property
     def units(self) -> int:
@@ -143,8 +149,9 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(t, dtype, shape, name, allow_none=False):
@@ -160,6 +167,19 @@ def _check(t, dtype, shape, name, allow_none=False):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_here(*tensors):
+    """Each of (tensor, dtype, shape, name) as _check has it, and on the current device: the
+    kernels launch there."""
+    dev = -1 if tensors[0][0] is None else tensors[0][0].get_device()
+    for t, dtype, shape, name in tensors:
+        if not (t is not None and t.dtype is dtype and dev >= 0 and t.get_device() == dev
+                and t.shape == shape and t.is_contiguous()):
+            _check(t, dtype, shape, name)
+            raise ValueError(f"{name} is on {t.device}, other tensors of the call are not")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the call's tensors are on cuda:{dev}, which is not the current device")
 
 
 def _call(name, *args):
@@ -305,44 +325,37 @@ def embla_append_kv_e4m3(shape: Shape, pos: int, k_code_rows, k_scale_rows, v_co
           _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _stream(stream))
 
 
-def _check_codes(shape: Shape, k_codes, k_scales, v_codes, v_scales):
+def _check_rows_and_codes(shape: Shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales) -> int:
+    """Rows bf16 [B, Hkv, T, D] and 8-bit caches; returns T."""
     B, Hkv, D, ncap = shape.batch, shape.n_kv_heads, shape.head_dim, shape.cache_stride
-    _check(k_codes, torch.uint8, (B, Hkv, ncap, D), "k_codes")
-    _check(v_codes, torch.uint8, (B, Hkv, ncap, D), "v_codes")
-    _check(k_scales, torch.float32, (B, Hkv, ncap), "k_scales")
-    _check(v_scales, torch.float32, (B, Hkv, ncap), "v_scales")
-
-
-def _check_rows(shape: Shape, k_rows, v_rows) -> int:
-    """k_rows and v_rows are bf16 [B, Hkv, T, D]; returns T."""
-    _check(k_rows, torch.bfloat16, None, "k_rows")
-    if k_rows.dim() != 4:
+    if k_rows is None or k_rows.dim() != 4:
         raise ValueError("k_rows must be [B, Hkv, T, D]")
-    want = (shape.batch, shape.n_kv_heads, k_rows.shape[2], shape.head_dim)
-    _check(k_rows, torch.bfloat16, want, "k_rows")
-    _check(v_rows, torch.bfloat16, want, "v_rows")
-    return want[2]
+    T = k_rows.shape[2]
+    rows, codes, scales = (B, Hkv, T, D), (B, Hkv, ncap, D), (B, Hkv, ncap)
+    _check_here((k_rows, torch.bfloat16, rows, "k_rows"), (v_rows, torch.bfloat16, rows, "v_rows"),
+                (k_codes, torch.uint8, codes, "k_codes"), (k_scales, torch.float32, scales, "k_scales"),
+                (v_codes, torch.uint8, codes, "v_codes"), (v_scales, torch.float32, scales, "v_scales"))
+    return T
 
 
 def embla_quantize_kv_e4m3(shape: Shape, pos: int, k_rows, v_rows, k_codes, k_scales, v_codes,
                            v_scales, stream=None):
     """Quantise T tokens' K and V rows (bf16 [B, Hkv, T, D]) into rows pos .. pos + T - 1 of the
     8-bit caches (codes uint8 [B, Hkv, cache_stride, D], scales float32 [B, Hkv, cache_stride])."""
-    T = _check_rows(shape, k_rows, v_rows)
-    _check_codes(shape, k_codes, k_scales, v_codes, v_scales)
-    _call("embla_quantize_kv_e4m3", ctypes.byref(shape.c()), pos, T, _ptr(k_rows), _ptr(v_rows),
-          _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _stream(stream))
+    T = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
+    _call("embla_quantize_kv_e4m3", shape.ref, pos, T, k_rows.data_ptr(), v_rows.data_ptr(),
+          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+          _stream(stream))
 
 
 def embla_dequantize_kv_e4m3(shape: Shape, pos: int, k_codes, k_scales, v_codes, v_scales, k_rows,
                              v_rows, n_rows: int | None = None, stream=None):
     """Read rows pos .. pos + n_rows - 1 of the 8-bit caches back as bf16 into the first n_rows
     rows of k_rows and v_rows (bf16 [B, Hkv, T, D], T >= n_rows; n_rows defaults to T)."""
-    T = _check_rows(shape, k_rows, v_rows)
-    _check_codes(shape, k_codes, k_scales, v_codes, v_scales)
-    _call("embla_dequantize_kv_e4m3", ctypes.byref(shape.c()), pos, T if n_rows is None else n_rows,
-          _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_rows), _ptr(v_rows),
-          T, _stream(stream))
+    T = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
+    _call("embla_dequantize_kv_e4m3", shape.ref, pos, T if n_rows is None else n_rows,
+          k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+          k_rows.data_ptr(), v_rows.data_ptr(), T, _stream(stream))
 
 
 def embla_full_decode_select_workspace_size(shape: Shape, topk: int = 1024, recent: int = 128) -> int:
@@ -550,22 +563,18 @@ def embla_sparse_decode_per_head(shape: Shape, q, k_cache, v_cache, idx, count, 
 
 
 def embla_full_decode_shared_workspace_size(shape: Shape, prefix_len: int) -> int:
-    return library().embla_full_decode_shared_workspace_size(ctypes.byref(shape.c()), prefix_len)
+    return library().embla_full_decode_shared_workspace_size(shape.ref, prefix_len)
 
 
-def _check_shared_caches(shape: Shape, prefix_len: int, k_prefix, v_prefix, k_cache, v_cache) -> int:
-    """k_prefix and v_prefix are bf16 [Hkv, prefix_stride, D] holding prefix_len rows at least;
-    returns prefix_stride."""
-    B, Hkv, D, ncap = shape.batch, shape.n_kv_heads, shape.head_dim, shape.cache_stride
-    _check(k_prefix, torch.bfloat16, None, "k_prefix")
-    if k_prefix.dim() != 3 or prefix_len > k_prefix.shape[1]:
+def _shared_caches(shape: Shape, prefix_len: int, k_prefix, v_prefix, k_cache, v_cache):
+    """The checks of k_prefix and v_prefix (bf16 [Hkv, prefix_stride, D] holding prefix_len rows at
+    least) and of the own caches."""
+    if k_prefix is None or k_prefix.dim() != 3 or prefix_len > k_prefix.shape[1]:
         raise ValueError("k_prefix must be [Hkv, prefix_stride, D], prefix_stride >= prefix_len")
-    want = (Hkv, k_prefix.shape[1], D)
-    _check(k_prefix, torch.bfloat16, want, "k_prefix")
-    _check(v_prefix, torch.bfloat16, want, "v_prefix")
-    _check(k_cache, torch.bfloat16, (B, Hkv, ncap, D), "k_cache")
-    _check(v_cache, torch.bfloat16, (B, Hkv, ncap, D), "v_cache")
-    return want[1]
+    pre = (shape.n_kv_heads, k_prefix.shape[1], shape.head_dim)
+    own = (shape.batch, shape.n_kv_heads, shape.cache_stride, shape.head_dim)
+    return ((k_prefix, torch.bfloat16, pre, "k_prefix"), (v_prefix, torch.bfloat16, pre, "v_prefix"),
+            (k_cache, torch.bfloat16, own, "k_cache"), (v_cache, torch.bfloat16, own, "v_cache"))
 
 
 def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefix, k_cache, v_cache,
@@ -576,20 +585,27 @@ def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefi
     sel_scores fp32 [B, Hkv, score_stride] holds the scores of prefix and own keys, and
     embla_select_topk takes it with Shape(..., ctx_len=prefix_len + shape.ctx_len,
     cache_stride=score_stride)."""
-    B, Hq, Hkv, D = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
-    _check(q, torch.bfloat16, (B, Hq, D), "q")
-    pstride = _check_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)
-    _check(out, torch.float32, (B, Hq, D), "out")
-    _check(n_surv, torch.int32, (B, Hkv), "n_surv")
-    _check(sel_scores, torch.float32, None, "sel_scores", allow_none=True)
-    if sel_scores is not None and (sel_scores.dim() != 3 or tuple(sel_scores.shape[:2]) != (B, Hkv)):
-        raise ValueError("sel_scores must be [B, Hkv, score_stride]")
-    _check(sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist", allow_none=True)
-    ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), workspace, q.device)
-    _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, pstride, _ptr(q),
-          _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), alpha, c, eps, _ptr(out),
-          _ptr(n_surv), _ptr(sel_scores), 0 if sel_scores is None else sel_scores.shape[2],
-          _ptr(sel_hist), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    B, Hkv = shape.batch, shape.n_kv_heads
+    heads = (B, shape.n_q_heads, shape.head_dim)
+    _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
+                (n_surv, torch.int32, (B, Hkv), "n_surv"),
+                *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
+    score_stride = 0
+    if sel_scores is not None:
+        if sel_scores.dim() != 3:
+            raise ValueError("sel_scores must be [B, Hkv, score_stride]")
+        score_stride = sel_scores.shape[2]
+        _check_here((sel_scores, torch.float32, (B, Hkv, score_stride), "sel_scores"))
+    if sel_hist is not None:
+        _check_here((sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist"))
+    # a workspace of the caller's is checked against the size by the C call
+    ws = workspace
+    if ws is None:
+        ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device)
+    _call("embla_full_decode_shared", shape.ref, prefix_len, k_prefix.shape[1], q.data_ptr(),
+          k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), alpha, c,
+          eps, out.data_ptr(), n_surv.data_ptr(), _ptr(sel_scores), score_stride, _ptr(sel_hist),
+          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
 
 
 def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefix, k_cache, v_cache,
@@ -597,15 +613,18 @@ def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_pre
     """embla_sparse_decode of sequences that share a prefix (as for embla_full_decode_shared):
     an index below prefix_len is a row of the prefix, any other one row idx - prefix_len of the
     sequence's own cache."""
-    B, Hq, Hkv, D = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
-    _check(q, torch.bfloat16, (B, Hq, D), "q")
-    pstride = _check_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)
-    _check_select_outputs(shape, idx, count)
-    _check(out, torch.float32, (B, Hq, D), "out")
-    tau = D ** -0.5 if tau is None else tau
-    _call("embla_sparse_decode_shared", ctypes.byref(shape.c()), prefix_len, pstride, _ptr(q),
-          _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), _ptr(idx), idx.shape[2],
-          _ptr(count), tau, _ptr(out), _stream(stream))
+    B, Hkv = shape.batch, shape.n_kv_heads
+    heads = (B, shape.n_q_heads, shape.head_dim)
+    if idx is None or idx.dim() != 3:
+        raise ValueError("idx must be [B, Hkv, idx_stride]")
+    idx_stride = idx.shape[2]
+    _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
+                (idx, torch.int32, (B, Hkv, idx_stride), "idx"), (count, torch.int32, (B, Hkv), "count"),
+                *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
+    _call("embla_sparse_decode_shared", shape.ref, prefix_len, k_prefix.shape[1], q.data_ptr(),
+          k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          idx.data_ptr(), idx_stride, count.data_ptr(),
+          shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream))
 
 
 def embla_window_decode(shape: Shape, q, k_win, v_win, pos: int, out, window: int = 128,

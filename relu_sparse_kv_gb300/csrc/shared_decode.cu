@@ -23,9 +23,9 @@
 // row blocks so that the CTAs of different row blocks walk the same prefix tiles at the same
 // time (read from HBM once).
 //
-// Warp roles: 0 TMA producer (rings of 3 K and 3 V tiles); 1 issuer of S; 2-9 epilogue, one
-// thread per (query row, half of the tile's keys); 10 issuer of P V; 11-14 key norms, one
-// thread per key.
+// Warp roles: 0 TMA producer (rings of 3 K and 3 V tiles); 1 issuer of S; 2 issuer of P V;
+// 4-7 key norms, one thread per key; 8-23 epilogue, one thread per (query row, quarter of the
+// tile's keys).
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -34,11 +34,15 @@ namespace {
 
 constexpr int kRows = 128;               // query rows of a row block
 constexpr int kRing = 3;                 // K, V, key-norm stages and S/P buffers
-constexpr int kEpiWarps = 8;
+constexpr int kWarpPV = 2;
+constexpr int kWarpNorm = 4;             // first of the key-norm warps
 constexpr int kNormWarps = 4;
-constexpr int kWarpPV = 2 + kEpiWarps;
-constexpr int kWarpNorm = kWarpPV + 1;
-constexpr int kSThreads = (kWarpNorm + kNormWarps) * 32;
+constexpr int kWarpEpi = kWarpNorm + kNormWarps;
+constexpr int kEpiWarps = 16;
+constexpr int kParts = kEpiWarps / 4;    // epilogue threads per query row
+constexpr int kPartCols = 128 / kParts;  // keys of a tile per epilogue thread
+static_assert(kPartCols == 32, "a thread's keys are one group of P columns");
+constexpr int kSThreads = (kWarpEpi + kEpiWarps) * 32;
 constexpr int kBox = 128 * 128;          // one [128 rows][64 bf16] box, 16 KB
 constexpr int kTileB = 2 * kBox;         // a 128 x 128 bf16 tile
 constexpr int kOffQ = 0;
@@ -55,10 +59,10 @@ constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) M
 constexpr int kColO = kRing * 128, kTmemCols = 512;
 
 // A record: the numerators of 128 rows, each row's denominator and each sequence's
-// survivor count for either half of the tiles' keys.
+// survivor count for each quarter of the tiles' keys.
 constexpr int kRecNum = kRows * kHeadDim;
-constexpr int kRecDen = 2 * kRows;
-constexpr int kRecCnt = 2 * 32;
+constexpr int kRecDen = kParts * kRows;
+constexpr int kRecCnt = kParts * 32;
 constexpr int kRecWords = kRecNum + kRecDen + kRecCnt;
 static_assert(kRecWords % 8 == 0, "records keep 32-byte alignment");
 
@@ -73,11 +77,22 @@ struct SharedParams {
   float alpha, eps;
 };
 
+// Two fp32 lanes at once, each rounded as the scalar operation would be.
 __device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
   asm("{\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%0, %1};\n\t"
       "mov.b64 y, {%2, %3};\n\t"
       "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+__device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\t"
       "mov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
@@ -90,8 +105,8 @@ struct Walk {
   int64_t gt;           // tiles per KV head
   int64_t t, end;       // the next tile, the piece's end
   int64_t piece;
-  int g;                // stretch: KV head, tiles [t0, t1) of its list
-  int64_t t0, t1;
+  int g;                // stretch: KV head, tiles [t0, t1) of its list (below 2^30)
+  int t0, t1;
   __device__ Walk(const SharedSplit &sp, int cta) {
     rb = sp.block_of_cta(cta);
     piece = cta - static_cast<int64_t>(rb) * sp.ctas_full;
@@ -104,9 +119,9 @@ struct Walk {
   __device__ bool next() {
     if (t >= end) return false;
     g = static_cast<int>(t / gt);
-    t0 = t - g * gt;
+    t0 = static_cast<int>(t - g * gt);
     const int64_t left = end - t;
-    t1 = gt - t0 < left ? gt : t0 + left;
+    t1 = static_cast<int>(gt - t0 < left ? gt : t0 + left);
     t += t1 - t0;
     return true;
   }
@@ -166,6 +181,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SharedSplit &sp = p.sp;
+  const int tp = static_cast<int>(sp.tp), ts = static_cast<int>(sp.ts);  // prefix, own tiles
 
   if (warp == 0) {
     if (lane < kRing) {
@@ -217,13 +233,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
         tma_load_4d(sQ, &tm_q, qfull, 0, 0, w.g, w.rb * kSeqs);
         tma_load_4d(sQ + kBox, &tm_q, qfull, 64, 0, w.g, w.rb * kSeqs);
         *s_qissued = k + 1;
-        for (int64_t t = w.t0; t < w.t1; ++t, ++i) {
+        for (int t = w.t0; t < w.t1; ++t, ++i) {
           const int s = i % kRing;
           const uint32_t ph = ((i / kRing) - 1) & 1;
-          const bool own = t >= sp.tp;
-          const int64_t x = t - sp.tp;
-          const int row = static_cast<int>((own ? x % sp.ts : t) * kTileKeys);
-          const int plane = own ? static_cast<int>((w.rb * kSeqs + x / sp.ts) * sp.Hkv + w.g) : w.g;
+          const bool own = t >= tp;
+          const int x = t - tp;
+          const int row = (own ? x % ts : t) * kTileKeys;
+          const int plane = own ? (w.rb * kSeqs + x / ts) * sp.Hkv + w.g : w.g;
           const CUtensorMap *mk = own ? &tm_ko : &tm_kp, *mv = own ? &tm_vo : &tm_vp;
           if (i >= kRing && !(mbar_wait(&sfull[s], ph) && mbar_wait(&rkfull[s], ph))) {
             ok = false;
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       bool ok = true;
       for (int k = 0; ok && w.next(); ++k) {
         ok = !*s_abort && mbar_wait(qfull, k & 1);
-        for (int64_t t = w.t0; ok && t < w.t1; ++t, ++i) {
+        for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
           const int s = i % kRing;
           ok = mbar_wait(&kfull[s], (i / kRing) & 1) &&
                (i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1));
@@ -282,7 +298,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       bool ok = true;
       for (int k = 0; ok && w.next(); ++k) {
         ok = !*s_abort && (k == 0 || mbar_wait(ofree, (k - 1) & 1));
-        for (int64_t t = w.t0; ok && t < w.t1; ++t, ++i) {
+        for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
           const int s = i % kRing;
           ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[s], (i / kRing) & 1);
           if (!ok) break;
@@ -307,13 +323,15 @@ __global__ void __launch_bounds__(kSThreads, 1)
       if (done > 0) mbar_wait(ofull, (done - 1) & 1);
     }
     __syncwarp();
-  } else if (warp >= kWarpNorm) {
+  } else if (warp == kWarpPV + 1) {
+    // no role: fills the warpgroup of single-thread roles
+  } else if (warp < kWarpEpi) {
     // ------------------------------------------------------------------ key norms
     const int r = (warp - kWarpNorm) * 32 + lane;  // this thread's key of every tile
     int i = 0;
     bool ok = true;
     while (ok && w.next()) {
-      for (int64_t t = w.t0; ok && t < w.t1; ++t, ++i) {
+      for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
         ok = mbar_wait(&kfull[s], (i / kRing) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -337,11 +355,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;          // the tensor-memory lanes this warp may read
-    const int half = (warp - 2) >> 2;      // keys 64 half .. of each tile
-    const int r = quarter * 32 + lane;     // query row: sequence r / G of the block, head r % G
+    const int quarter = warp & 3;            // the tensor-memory lanes this warp may read
+    const int part = (warp - kWarpEpi) >> 2;  // keys 32 part .. of each tile
+    const int r = quarter * 32 + lane;       // query row: sequence r / G of the block, head r % G
     const int seq = r / G, h = r % G;
+    constexpr int kMine = kPartCols / G;  // keys this lane ends up with the group maximum of
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t part_col = static_cast<uint32_t>(part * kPartCols);
     int i = 0;
     bool ok = true;
     for (int k = 0; ok && w.next(); ++k) {
@@ -357,61 +377,75 @@ __global__ void __launch_bounds__(kSThreads, 1)
         if (lane == 0) mbar_arrive_after(qempty, used);
       }
       const bool valid = seq < w.nb;
-      float *scores = nullptr;  // this row's (sequence, KV head)
+      const bool some = quarter * (32 / G) < w.nb;  // this warp has valid rows
+      float *scores = nullptr;  // this row's (sequence, KV head), at this lane's first key
       if (p.sel != nullptr && valid)
-        scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride;
+        scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride + part_col +
+                 h * kMine;
       float den[2] = {0.0f, 0.0f};
       int live = 0;  // keys of this lane's share with a group maximum above zero
-      for (int64_t t = w.t0; t < w.t1; ++t, ++i) {
+      for (int t = w.t0; t < w.t1; ++t, ++i) {
         const int s = i % kRing;
         ok = mbar_wait(&sfull[s], (i / kRing) & 1) && mbar_wait(&rkfull[s], (i / kRing) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc_fence_after_sync();
-        const bool own = t >= sp.tp;
-        const int64_t x = t - sp.tp;
-        const int owner = own ? static_cast<int>(x / sp.ts) : 0;
-        const int64_t kt = own ? x % sp.ts : t;
-        const bool mine = valid && (!own || seq == owner);
-        const float rqm = mine ? rq : 0.0f;  // another sequence's keys weigh nothing here
-        // keys of the tile that exist; the first one's place in the score row
-        const int64_t rest = (own ? sp.n : sp.P) - kt * kTileKeys;
-        const int64_t j0 = (own ? sp.P : 0) + kt * kTileKeys;
-        const bool vec = rest >= kTileKeys && (own ? p.vec_own : p.vec_prefix);
-#pragma unroll
-        for (int c0 = 0; c0 < 2; ++c0) {
-          const int col = half * 64 + c0 * 32;
-          const uint32_t cols = tmem + lane_base + s * 128 + col;
-          uint32_t acc[32];
+        const bool own = t >= tp;
+        const int x = t - tp;
+        const int owner = own ? x / ts : seq;
+        const uint32_t cols = tmem + lane_base + s * 128 + part_col;
+        float used = 0.0f;
+        if (!own ? some : owner / (32 / G) == quarter) {
+          tc_fence_after_sync();
+          uint32_t acc[kPartCols];
           tmem_load_x32(cols, acc);
           tmem_wait_ld(acc);
-          const float *rkp = sRK + s * kRows + col;
-          float v[32];
-          uint32_t pw[32];  // the weights: 16 columns of hi, 16 of lo
+          const float rqm = seq == owner ? rq : 0.0f;  // another sequence's keys weigh nothing here
+          const float4 *rkp = reinterpret_cast<const float4 *>(sRK + s * kRows + part_col);
+          float v[kPartCols];  // s' of this row and these keys
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 rk = *reinterpret_cast<const float2 *>(rkp + c);
+          for (int c = 0; c < kPartCols; c += 4) {
+            const float4 rk = rkp[c / 4];
             v[c] = __uint_as_float(acc[c]);
             v[c + 1] = __uint_as_float(acc[c + 1]);
+            v[c + 2] = __uint_as_float(acc[c + 2]);
+            v[c + 3] = __uint_as_float(acc[c + 3]);
             mul2(v[c], v[c + 1], rk.x, rk.y);
+            mul2(v[c + 2], v[c + 3], rk.z, rk.w);
             mul2(v[c], v[c + 1], rqm, rqm);
-            float w0 = fmaxf(v[c], 0.0f), w1 = fmaxf(v[c + 1], 0.0f);
-            mul2(w0, w1, w0, w1);
-            den[0] += w0;
-            den[1] += w1;
-            const uint32_t hi = pack_bf16x2(w0, w1);
-            pw[c >> 1] = hi;
-            pw[16 + (c >> 1)] = pack_bf16x2(w0 - bf16lo(hi), w1 - bf16hi(hi));
+            mul2(v[c + 2], v[c + 3], rqm, rqm);
           }
-          tmem_store_x32(cols, pw);
+          // the weights over the scores' columns: 16 columns of hi, then 16 of lo
+#pragma unroll
+          for (int c0 = 0; c0 < kPartCols; c0 += 16) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              float w0 = fmaxf(v[c0 + c], 0.0f), w1 = fmaxf(v[c0 + c + 1], 0.0f);
+              mul2(w0, w1, w0, w1);
+              add2(den[0], den[1], w0, w1);
+              hi[c >> 1] = pack_bf16x2(w0, w1);
+              lo[c >> 1] = pack_bf16x2(w0 - bf16lo(hi[c >> 1]), w1 - bf16hi(hi[c >> 1]));
+            }
+            tmem_store_x8(cols + c0 / 2, hi);
+            tmem_store_x8(cols + 16 + c0 / 2, lo);
+          }
+          used = __shfl_sync(0xffffffffu, den[0], 0) + __shfl_sync(0xffffffffu, den[1], 31);
+          tmem_wait_st();
+          tc_fence_before_sync();  // P is read by the tensor cores
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&pfull[s]);
+            mbar_arrive_after(&rkempty[s], used);  // every lane's sums depend on its norm reads
+          }
           group_max<G>(v, lane);
-          constexpr int kMine = 32 / G;  // keys this lane holds the maximum of
 #pragma unroll
           for (int c = 0; c < kMine; ++c) live += v[c] > 0.0f ? 1 : 0;
-          if (scores != nullptr && mine) {
-            const int first = col + h * kMine;
-            float *dst = scores + j0 + first;
-            if (vec) {
+          if (scores != nullptr && seq == owner) {
+            // the tile's first key in the score row, and how many keys it has
+            const int64_t kt = own ? x - owner * ts : t;
+            const int64_t rest = (own ? sp.n : sp.P) - kt * kTileKeys;
+            float *dst = scores + (own ? sp.P : 0) + kt * kTileKeys;
+            if (rest >= kTileKeys && (own ? p.vec_own : p.vec_prefix)) {
               if constexpr (G == 4)
                 st_global_v8(dst, p.alpha * v[0], p.alpha * v[1], p.alpha * v[2], p.alpha * v[3],
                              p.alpha * v[4], p.alpha * v[5], p.alpha * v[6], p.alpha * v[7]);
@@ -419,20 +453,28 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 *reinterpret_cast<float4 *>(dst) =
                     make_float4(p.alpha * v[0], p.alpha * v[1], p.alpha * v[2], p.alpha * v[3]);
             } else {
+              const int64_t room = rest - static_cast<int>(part_col) - h * kMine;
 #pragma unroll
               for (int c = 0; c < kMine; ++c)
-                if (first + c < rest) dst[c] = p.alpha * v[c];
+                if (c < room) dst[c] = p.alpha * v[c];
             }
           }
-        }
-        tmem_wait_st();
-        tc_fence_before_sync();  // P is read by the tensor cores
-        // every lane's weight sums depend on all of its key-norm reads
-        const float used = __shfl_sync(0xffffffffu, den[0], 0) + __shfl_sync(0xffffffffu, den[1], 31);
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&pfull[s]);
-          mbar_arrive_after(&rkempty[s], used);
+        } else {
+          // no row of this warp reads the tile: zero weights for rows that other tiles count
+          // for (rows past the batch hold anything, no other row sees them)
+          if (some) {
+            tc_fence_after_sync();
+            const uint32_t zero[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            tmem_store_x16(cols, zero);
+            tmem_store_x16(cols + 16, zero);
+            tmem_wait_st();
+            tc_fence_before_sync();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&pfull[s]);
+            mbar_arrive(&rkempty[s]);
+          }
         }
       }
       if (!ok) break;
@@ -440,29 +482,28 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after_sync();
-      uint32_t o[64];
-      tmem_load_x32(tmem + lane_base + kColO + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-      tmem_load_x32(tmem + lane_base + kColO + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+      uint32_t o[kPartCols];
+      tmem_load_x32(tmem + lane_base + kColO + part_col, o);
       tmem_wait_ld(o);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree);  // the next stretch's P V may overwrite O
       // The record: every row when the stretch holds prefix tiles, else the rows of the
       // sequences whose tiles it holds.
-      const int first_seq = w.t0 < sp.tp ? 0 : static_cast<int>((w.t0 - sp.tp) / sp.ts);
-      const int last_seq = w.t0 < sp.tp ? w.nb - 1 : static_cast<int>((w.t1 - 1 - sp.tp) / sp.ts);
+      const int first_seq = w.t0 < tp ? 0 : (w.t0 - tp) / ts;
+      const int last_seq = w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
 #pragma unroll
       for (int m = 1; m < G; m <<= 1) live += __shfl_xor_sync(0xffffffffu, live, m);
       if (seq >= first_seq && seq <= last_seq) {
         float *rec = p.rec + sp.slot(w.rb, w.piece, w.g) * kRecWords;
-        float *dst = rec + r * kHeadDim + half * 64;
+        float *dst = rec + r * kHeadDim + part_col;
 #pragma unroll
-        for (int c = 0; c < 64; c += 8)
+        for (int c = 0; c < kPartCols; c += 8)
           st_global_v8(dst + c, __uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
                        __uint_as_float(o[c + 3]), __uint_as_float(o[c + 4]), __uint_as_float(o[c + 5]),
                        __uint_as_float(o[c + 6]), __uint_as_float(o[c + 7]));
-        rec[kRecNum + half * kRows + r] = den[0] + den[1];
-        if (h == 0) reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + half * 32 + seq] = live;
+        rec[kRecNum + part * kRows + r] = den[0] + den[1];
+        if (h == 0) reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + part * 32 + seq] = live;
       }
     }
     if (!ok && lane == 0) give_up(s_abort, p.flags);
@@ -494,6 +535,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
 constexpr int kFThreads = 256;
 constexpr int kFWarps = kFThreads / 32;
+constexpr int kHistKeys = 4096;  // scores a histogram CTA counts
 
 struct FinishParams {
   SharedSplit sp;
@@ -505,6 +547,7 @@ struct FinishParams {
   uint32_t *hist;
   int64_t score_stride;
   int32_t hist_ctas, hist_splits;  // CTAs of the histogram part; per (sequence, KV head)
+  int32_t hist_vec;                // score rows start on 16 bytes
   float *out;
   int32_t *n_surv;
   float alpha, c, eps;
@@ -580,11 +623,28 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     __syncthreads();
     pdl_wait_primary();  // the scores are complete
     pdl_launch_dependents();
-    const int64_t u = blockIdx.x / p.hist_splits, part = blockIdx.x % p.hist_splits;
-    const int64_t N = sp.P + sp.n;
-    const int64_t a = N * part / p.hist_splits, e = N * (part + 1) / p.hist_splits;
-    const float *su = p.sel + u * p.score_stride;
-    for (int64_t j = a + threadIdx.x; j < e; j += kFThreads) atomicAdd(&s_mem[order_key(su[j]) >> 21], 1u);
+    const int64_t u = blockIdx.x / p.hist_splits;
+    const int64_t N = sp.P + sp.n, a = (blockIdx.x % p.hist_splits) * static_cast<int64_t>(kHistKeys);
+    const int m = static_cast<int>(N - a < kHistKeys ? N - a : kHistKeys);
+    const float *su = p.sel + u * p.score_stride + a;
+    auto count = [&](float x) { atomicAdd(&s_mem[order_key(x) >> 21], 1u); };
+    if (p.hist_vec) {
+      const float4 *s4 = reinterpret_cast<const float4 *>(su);
+      constexpr int kLoads = 4;  // in flight per thread
+      const int m4 = m / 4;
+      for (int e = threadIdx.x; e < m4; e += kLoads * kFThreads) {
+        float4 x[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+          if (e + k * kFThreads < m4) x[k] = s4[e + k * kFThreads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+          if (e + k * kFThreads < m4) count(x[k].x), count(x[k].y), count(x[k].z), count(x[k].w);
+      }
+      if (static_cast<int>(threadIdx.x) < m % 4) count(su[m4 * 4 + threadIdx.x]);
+    } else {
+      for (int e = threadIdx.x; e < m; e += kFThreads) count(su[e]);
+    }
     __syncthreads();
     for (int k = threadIdx.x; k < kHistBins; k += kFThreads)
       if (s_mem[k] != 0u) atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
@@ -627,18 +687,18 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     acc.y += x.y;
     acc.z += x.z;
     acc.w += x.w;
-    if (lane < 2) {
+    if (lane < kParts) {
       den += rec[kRecNum + lane * kRows + r];
       live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
     }
   }
   float *s_acc = reinterpret_cast<float *>(s_mem);            // [8 warps][128]
-  float *s_den = s_acc + kFWarps * kHeadDim;                  // [8][2]
-  int *s_live = reinterpret_cast<int *>(s_den + 2 * kFWarps);  // [8][2]
+  float *s_den = s_acc + kFWarps * kHeadDim;                       // [8][kParts]
+  int *s_live = reinterpret_cast<int *>(s_den + kParts * kFWarps);  // [8][kParts]
   *reinterpret_cast<float4 *>(s_acc + warp * kHeadDim + 4 * lane) = acc;
-  if (lane < 2) {
-    s_den[warp * 2 + lane] = den;
-    s_live[warp * 2 + lane] = live;
+  if (lane < kParts) {
+    s_den[warp * kParts + lane] = den;
+    s_live[warp * kParts + lane] = live;
   }
   __syncthreads();
   float num = 0.0f, dsum = 0.0f;
@@ -647,7 +707,7 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
 #pragma unroll
     for (int k = 0; k < kFWarps; ++k) num += s_acc[k * kHeadDim + threadIdx.x];
 #pragma unroll
-    for (int k = 0; k < 2 * kFWarps; ++k) {
+    for (int k = 0; k < kParts * kFWarps; ++k) {
       dsum += s_den[k];
       nlive += s_live[k];
     }
@@ -738,11 +798,11 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.hist = a.sel_hist;
   f.score_stride = a.score_stride;
   const int64_t units = static_cast<int64_t>(sp.B) * sp.Hkv;
-  // parts of a unit's scores: enough CTAs for the SMs, 4096 keys a part at least
-  int64_t splits = (2 * static_cast<int64_t>(a.sm_count) + units - 1) / units;
-  const int64_t most = (sp.P + sp.n + 4095) / 4096;
-  f.hist_splits = static_cast<int32_t>(splits < most ? splits : most);
-  f.hist_ctas = a.sel_hist != nullptr ? static_cast<int32_t>(units * f.hist_splits) : 0;
+  f.hist_splits = static_cast<int32_t>((sp.P + sp.n + kHistKeys - 1) / kHistKeys);
+  const int64_t hist_ctas = a.sel_hist != nullptr ? units * f.hist_splits : 0;
+  if (hist_ctas + units * sp.G > INT32_MAX) return cudaErrorInvalidValue;
+  f.hist_ctas = static_cast<int32_t>(hist_ctas);
+  f.hist_vec = a.score_stride % 4 == 0;
   f.out = a.out;
   f.n_surv = a.n_surv;
   f.alpha = a.alpha;
