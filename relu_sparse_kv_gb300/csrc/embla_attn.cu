@@ -684,6 +684,7 @@ embla_status embla_full_decode_shared(const embla_shape *shape, int64_t prefix_l
   const int sms = sm_count_of(current_device());
   if (sms <= 0) return EMBLA_ERR_CUDA;
   const SharedSplit sp = shared_split(shape->batch, shape->n_kv_heads, G, prefix_len, n, sms);
+  if (!sp.fits()) return EMBLA_ERR_UNSUPPORTED;
   if (workspace_bytes < shared_workspace_bytes(sp)) return EMBLA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sp.ctas() == 0) {

@@ -187,7 +187,8 @@ cudaError_t launch_prefill(const CUtensorMap &tm_q, const CUtensorMap &tm_k, con
 // 128-key tiles, the prefix's tp tiles and then each of its sequences' ts own tiles, and the
 // lists of the KV heads follow one another.  Each row block's list is cut into as many equal
 // pieces as it gets CTAs; the record of the stretch of KV head g inside piece q lives in
-// slot(rb, q, g).
+// slot(rb, q, g).  Tiles times pieces of a row block stay below 2^32 (fits()), so the device
+// splits in 32 bits.
 struct SharedSplit {
   int64_t P, n;
   int64_t tp, ts;
@@ -206,6 +207,13 @@ struct SharedSplit {
   __host__ __device__ int block_of_cta(int cta) const {
     const int rb = ctas_full > 0 ? cta / ctas_full : 0;
     return rb < blocks - 1 ? rb : blocks - 1;
+  }
+  __host__ __device__ bool fits() const {
+    return blocks == 0 || group_tiles(0) * Hkv * (ctas_full > ctas_last ? ctas_full : ctas_last) <= INT32_MAX;
+  }
+  __host__ __device__ uint32_t piece_start(uint32_t q, uint32_t T, uint32_t Q) const { return q * T / Q; }
+  __host__ __device__ uint32_t piece_of_tile(uint32_t t, uint32_t T, uint32_t Q) const {
+    return ((t + 1) * Q - 1) / T;
   }
   __host__ __device__ int64_t slot(int rb, int64_t piece, int g) const {
     return static_cast<int64_t>(rb) * (ctas_full + Hkv) + piece + g;

@@ -101,26 +101,25 @@ __device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1) {
 // A CTA's part of the work: pieces of row block rb's tile list, and the stretch (the part of
 // it inside one KV head's list) at hand.
 struct Walk {
-  int rb, nb;           // the row block, its sequences
-  int64_t gt;           // tiles per KV head
-  int64_t t, end;       // the next tile, the piece's end
-  int64_t piece;
-  int g;                // stretch: KV head, tiles [t0, t1) of its list (below 2^30)
-  int t0, t1;
+  int rb, nb;        // the row block, its sequences
+  uint32_t gt;       // tiles per KV head
+  uint32_t t, end;   // the next tile, the piece's end
+  int piece;
+  int g, t0, t1;     // stretch: KV head, tiles [t0, t1) of its list
   __device__ Walk(const SharedSplit &sp, int cta) {
     rb = sp.block_of_cta(cta);
-    piece = cta - static_cast<int64_t>(rb) * sp.ctas_full;
+    piece = cta - rb * sp.ctas_full;
     nb = sp.sequences(rb);
-    gt = sp.group_tiles(rb);
-    const int64_t T = gt * sp.Hkv, Q = sp.pieces(rb);
-    t = split_piece_start(piece, T, Q);
-    end = split_piece_start(piece + 1, T, Q);
+    gt = static_cast<uint32_t>(sp.group_tiles(rb));
+    const uint32_t T = gt * sp.Hkv, Q = static_cast<uint32_t>(sp.pieces(rb));
+    t = sp.piece_start(piece, T, Q);
+    end = sp.piece_start(piece + 1, T, Q);
   }
   __device__ bool next() {
     if (t >= end) return false;
     g = static_cast<int>(t / gt);
     t0 = static_cast<int>(t - g * gt);
-    const int64_t left = end - t;
+    const uint32_t left = end - t;
     t1 = static_cast<int>(gt - t0 < left ? gt : t0 + left);
     t += t1 - t0;
     return true;
@@ -208,6 +207,14 @@ __global__ void __launch_bounds__(kSThreads, 1)
     tmem_alloc(s_tmem, kTmemCols);
     tmem_relinquish();
   }
+  if (threadIdx.x == (kWarpPV + 1) * 32) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kp);
+    tma_prefetch_desc(&tm_vp);
+    tma_prefetch_desc(&tm_ko);
+    tma_prefetch_desc(&tm_vo);
+  }
+  Walk w(sp, static_cast<int>(blockIdx.x));
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -218,7 +225,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
   // Every role walks the CTA's stretches in the same order, and their tiles through the rings
   // by a running tile count i: stage i % kRing, phase (i / kRing) & 1.  Stretch k's query and
   // output barriers take phase k & 1.
-  Walk w(sp, static_cast<int>(blockIdx.x));
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -264,19 +270,21 @@ __global__ void __launch_bounds__(kSThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S issuer
-    if (lane == 0) {
-      const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
-      const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
-      int i = 0;
-      bool ok = true;
-      for (int k = 0; ok && w.next(); ++k) {
-        ok = !*s_abort && mbar_wait(qfull, k & 1);
-        for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
-          const int s = i % kRing;
-          ok = mbar_wait(&kfull[s], (i / kRing) & 1) &&
-               (i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1));
-          if (!ok) break;
-          tc_fence_after_sync();
+    // The warp walks together and one lane issues (elect_one).
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
+    const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
+    int i = 0;
+    bool ok = true;
+    for (int k = 0; ok && w.next(); ++k) {
+      ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(qfull, k & 1));
+      for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
+        const int s = i % kRing;
+        ok = mbar_wait(&kfull[s], (i / kRing) & 1) &&
+             (i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // dims 16kk..16kk+15: 32 bytes into a 128-byte row; dims 64.. start the second box
@@ -286,42 +294,47 @@ __global__ void __launch_bounds__(kSThreads, 1)
           }
           tc_commit(&sfull[s]);
         }
-        if (ok) tc_commit(qempty);
+        __syncwarp();
       }
-      if (!ok) give_up(s_abort, p.flags);
+      if (ok && elect_one()) tc_commit(qempty);
+      __syncwarp();
     }
-    __syncwarp();
+    if (!ok && lane == 0) give_up(s_abort, p.flags);
   } else if (warp == kWarpPV) {
     // ------------------------------------------------------------------ P V issuer
-    if (lane == 0) {
-      int i = 0, done = 0;
-      bool ok = true;
-      for (int k = 0; ok && w.next(); ++k) {
-        ok = !*s_abort && (k == 0 || mbar_wait(ofree, (k - 1) & 1));
-        for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
-          const int s = i % kRing;
-          ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[s], (i / kRing) & 1);
-          if (!ok) break;
-          tc_fence_after_sync();
+    const uint64_t vdesc = smem_desc_sw128_mn(smem_u32(sV), kBox);
+    int i = 0, done = 0;
+    bool ok = true;
+    for (int k = 0; ok && w.next(); ++k) {
+      ok = __all_sync(0xffffffffu, !*s_abort && (k == 0 || mbar_wait(ofree, (k - 1) & 1)));
+      for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
+        const int s = i % kRing;
+        ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[s], (i / kRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // keys 16kk..16kk+15: in their group of 32 columns hi takes the first 16, lo the rest
             const uint32_t a_hi = tmem + s * 128 + (kk >> 1) * 32 + (kk & 1) * 8;
-            const uint64_t vd = smem_desc_sw128_mn(smem_u32(sV + s * kTileB + kk * 2048), kBox);
+            const uint64_t vd = vdesc + static_cast<uint64_t>((s * kTileB + kk * 2048) >> 4);
             tc_mma_bf16_tmem_a(tmem + kColO, a_hi, vd, kIdescPV, (t > w.t0 || kk > 0) ? 1u : 0u);
             tc_mma_bf16_tmem_a(tmem + kColO, a_hi + 16, vd, kIdescPV, 1u);
           }
           tc_commit(&pvdone[s]);
         }
-        if (ok) {
-          tc_commit(ofull);
-          done = k + 1;
-        }
+        __syncwarp();
       }
-      if (!ok) give_up(s_abort, p.flags);
-      // every MMA of this thread has completed before the tensor memory is released
-      if (done > 0) mbar_wait(ofull, (done - 1) & 1);
+      if (ok) {
+        if (elect_one()) tc_commit(ofull);
+        __syncwarp();
+        done = k + 1;
+      }
     }
+    if (!ok && lane == 0) give_up(s_abort, p.flags);
+    // every MMA of this warp has completed before the tensor memory is released
+    if (done > 0) mbar_wait(ofull, (done - 1) & 1);
     __syncwarp();
   } else if (warp == kWarpPV + 1) {
     // no role: fills the warpgroup of single-thread roles
@@ -535,7 +548,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
 constexpr int kFThreads = 256;
 constexpr int kFWarps = kFThreads / 32;
-constexpr int kHistKeys = 4096;  // scores a histogram CTA counts
 
 struct FinishParams {
   SharedSplit sp;
@@ -547,6 +559,7 @@ struct FinishParams {
   uint32_t *hist;
   int64_t score_stride;
   int32_t hist_ctas, hist_splits;  // CTAs of the histogram part; per (sequence, KV head)
+  int32_t hist_keys;               // scores a histogram CTA counts
   int32_t hist_vec;                // score rows start on 16 bytes
   float *out;
   int32_t *n_surv;
@@ -624,8 +637,8 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     pdl_wait_primary();  // the scores are complete
     pdl_launch_dependents();
     const int64_t u = blockIdx.x / p.hist_splits;
-    const int64_t N = sp.P + sp.n, a = (blockIdx.x % p.hist_splits) * static_cast<int64_t>(kHistKeys);
-    const int m = static_cast<int>(N - a < kHistKeys ? N - a : kHistKeys);
+    const int64_t N = sp.P + sp.n, a = (blockIdx.x % p.hist_splits) * static_cast<int64_t>(p.hist_keys);
+    const int m = static_cast<int>(N - a < p.hist_keys ? N - a : p.hist_keys);
     const float *su = p.sel + u * p.score_stride + a;
     auto count = [&](float x) { atomicAdd(&s_mem[order_key(x) >> 21], 1u); };
     if (p.hist_vec) {
@@ -659,19 +672,20 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
   const int rb = b / seqs, seq = b % seqs, r = seq * sp.G + hq % sp.G;
   // the pieces whose record holds this row: those with prefix tiles of this KV head, then
   // those with own tiles of this sequence
-  const int64_t gt = sp.group_tiles(rb), T = gt * sp.Hkv, Q = sp.pieces(rb), base = g * gt;
-  int64_t qa = 0, qb = -1, qc = 0, qd = -1;
+  const uint32_t gt = static_cast<uint32_t>(sp.group_tiles(rb)), T = gt * sp.Hkv;
+  const uint32_t Q = static_cast<uint32_t>(sp.pieces(rb)), base = g * gt;
+  int qa = 0, qb = -1, qc = 0, qd = -1;
   if (sp.tp > 0) {
-    qa = split_piece_of_tile(base, T, Q);
-    qb = split_piece_of_tile(base + sp.tp - 1, T, Q);
+    qa = static_cast<int>(sp.piece_of_tile(base, T, Q));
+    qb = static_cast<int>(sp.piece_of_tile(base + static_cast<uint32_t>(sp.tp) - 1, T, Q));
   }
   if (sp.ts > 0) {
-    const int64_t own = base + sp.tp + static_cast<int64_t>(seq) * sp.ts;
-    qc = split_piece_of_tile(own, T, Q);
-    qd = split_piece_of_tile(own + sp.ts - 1, T, Q);
+    const uint32_t own = base + static_cast<uint32_t>(sp.tp + seq * sp.ts);
+    qc = static_cast<int>(sp.piece_of_tile(own, T, Q));
+    qd = static_cast<int>(sp.piece_of_tile(own + static_cast<uint32_t>(sp.ts) - 1, T, Q));
     if (qc <= qb) qc = qb + 1;
   }
-  const int n1 = static_cast<int>(qb - qa + 1), nrec = n1 + static_cast<int>(qd >= qc ? qd - qc + 1 : 0);
+  const int n1 = qb - qa + 1, nrec = n1 + (qd >= qc ? qd - qc + 1 : 0);
   auto record = [&](int i) {
     return p.rec + sp.slot(rb, i < n1 ? qa + i : qc + (i - n1), g) * kRecWords;
   };
@@ -798,7 +812,10 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.hist = a.sel_hist;
   f.score_stride = a.score_stride;
   const int64_t units = static_cast<int64_t>(sp.B) * sp.Hkv;
-  f.hist_splits = static_cast<int32_t>((sp.P + sp.n + kHistKeys - 1) / kHistKeys);
+  // scores per histogram CTA: six CTAs to an SM, 2,048 to 16,384 scores each
+  const int64_t N = sp.P + sp.n, share = (units * N / (6 * a.sm_count) + 1023) / 1024 * 1024;
+  f.hist_keys = static_cast<int32_t>(share < 2048 ? 2048 : share > 16384 ? 16384 : share);
+  f.hist_splits = static_cast<int32_t>((N + f.hist_keys - 1) / f.hist_keys);
   const int64_t hist_ctas = a.sel_hist != nullptr ? units * f.hist_splits : 0;
   if (hist_ctas + units * sp.G > INT32_MAX) return cudaErrorInvalidValue;
   f.hist_ctas = static_cast<int32_t>(hist_ctas);

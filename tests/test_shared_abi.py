@@ -162,6 +162,7 @@ int main() {
                 continue;
               }
               if (sp.ctas() < sp.blocks || (sp.ctas() > sms && sp.ctas() > sp.blocks)) return 2;
+              if (!sp.fits()) return 12;
               const long slots = sp.slot(sp.blocks, 0, 0);
               std::vector<char> used(slots, 0);
               std::vector<long> cta_of;  // (row block, piece) by CTA
@@ -174,7 +175,7 @@ int main() {
                 for (long q = 0; q < Q; ++q) {
                   const long cta = (long)rb * sp.ctas_full + q;
                   if (cta >= sp.ctas() || sp.block_of_cta(cta) != rb) return 4;
-                  const long b = split_piece_start(q, T, Q), e = split_piece_start(q + 1, T, Q);
+                  const long b = sp.piece_start(q, T, Q), e = sp.piece_start(q + 1, T, Q);
                   if (b != covered || e <= b) return 5;
                   covered = e;
                   for (long g = b / gt; g <= (e - 1) / gt; ++g) {
@@ -182,7 +183,7 @@ int main() {
                     if (s < 0 || s >= slots || used[s]) return 6;
                     used[s] = 1;
                   }
-                  if (split_piece_of_tile(b, T, Q) != q || split_piece_of_tile(e - 1, T, Q) != q) return 7;
+                  if (sp.piece_of_tile(b, T, Q) != q || sp.piece_of_tile(e - 1, T, Q) != q) return 7;
                 }
                 if (covered != T) return 8;
               }
