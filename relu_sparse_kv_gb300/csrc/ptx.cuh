@@ -452,9 +452,23 @@ __device__ __forceinline__ void tmem_store_x32(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+// 16 lanes x 32 consecutive 32-bit columns in the fragment layout of the warp MMAs: register
+// 4j + 2i + e of lane l holds lane l / 4 + 8i of the 16, column 8j + 2(l % 4) + e.
+__device__ __forceinline__ void tmem_load_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// 16 lanes x 16 consecutive 32-bit columns from registers: register 2j + i of lane l goes to
+// lane l / 4 + 8i of the 16, column 4j + l % 4.
+__device__ __forceinline__ void tmem_store_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
@@ -517,16 +531,27 @@ __device__ __forceinline__ void sq_acc_bf16x2(uint32_t w, float &a, float &b) {
       : "r"(w));
 }
 
-// Sum of squares of row r of a 128 x 128 bf16 tile in shared memory (two 64-column boxes in the
-// 128-byte swizzle).  Pieces are taken in an order rotated by row, so neighbouring rows read
-// different banks; a sum of squares does not care which columns a piece holds.
-__device__ __forceinline__ float row_square_sum(const uint8_t *tile, int box_bytes, int r) {
+// a - lo(w), b - hi(w) for the two bf16 values packed in w (each one rounding in fp32).
+__device__ __forceinline__ void sub_bf16x2(uint32_t w, float &a, float &b) {
+  asm("{\n\t.reg .b16 lo, hi, m;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "mov.b16 m, 0xBF80;\n\t"
+      "fma.rn.f32.bf16 %0, lo, m, %0;\n\t"
+      "fma.rn.f32.bf16 %1, hi, m, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
+}
+
+// Sum of squares of row r of a 128 x 128 bf16 tile in shared memory (two 64-column boxes of
+// 128-byte rows).  Pieces are taken in an order that `turn` (0 .. 7) rotates, so lanes with
+// different turns read different banks; the sum does not care which columns a piece holds.
+__device__ __forceinline__ float row_square_sum(const uint8_t *tile, int box_bytes, int r, int turn) {
   float a[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[i] = 0.0f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const int pc = (c ^ (r & 7)) * 16;
+    const int pc = (c ^ turn) * 16;
     const uint4 x0 = *reinterpret_cast<const uint4 *>(tile + r * 128 + pc);
     const uint4 x1 = *reinterpret_cast<const uint4 *>(tile + box_bytes + r * 128 + pc);
     sq_acc_bf16x2(x0.x, a[0], a[1]);

@@ -24,8 +24,12 @@
 // time (read from HBM once).
 //
 // Warp roles: 0 TMA producer (rings of 3 K and 3 V tiles); 1 issuer of S; 2 issuer of P V;
-// 4-7 key norms, one thread per key; 8-23 epilogue, one thread per (query row, quarter of the
-// tile's keys).
+// 4-7 key norms, one thread per key; 8-23 epilogue, each a quarter of the query rows and of the
+// tile's keys.  The epilogue reads S in the fragment layout of the warp MMAs, where a thread
+// holds rows l, l + 8, l + 16 and l + 24 of its quarter, and the query rows lie in the block so
+// that those are heads of one sequence: the group maximum that the selection ranks is taken
+// within a thread (over lanes it cost two and a half instructions per score on the pipe that
+// bound the epilogue).
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -73,7 +77,7 @@ struct SharedParams {
   float *sel;              // [B, Hkv, score_stride] or null
   uint32_t *hist;          // [B, Hkv, 2048] or null; zeroed here
   int64_t score_stride;
-  int32_t vec_prefix, vec_own;  // score rows of prefix / own tiles start on 32 bytes
+  int32_t pair_prefix, pair_own;  // score rows of prefix / own tiles start on 8 bytes
   float alpha, eps;
 };
 
@@ -131,22 +135,18 @@ __device__ __forceinline__ void give_up(volatile int *abort_flag, uint32_t *flag
   atomicOr(flags, kFlagWaitTimeout);
 }
 
-// The maximum of each of 32 values over the G lanes of a sequence: lane h of the group ends
-// with values h * 32 / G .. (reduce-scatter; NaN gives way to numbers).
+// Row of the block that holds head h of sequence seq: a quarter of 32 rows holds 32 / G
+// sequences; head h lies in the quarter's eight rows number h / (G / 4), where a sequence has
+// G / 4 rows.
 template <int G>
-__device__ __forceinline__ void group_max(float (&v)[32], int lane) {
-  static_assert(G == 4 || G == 8, "query heads per KV head");
-#pragma unroll
-  for (int o = G / 2, half = 16; o >= 1; o >>= 1, half >>= 1) {
-    const bool upper = (lane & o) != 0;
-#pragma unroll
-    for (int k = 0; k < half; ++k) {
-      const float send = upper ? v[k] : v[k + half];
-      const float keep = upper ? v[k + half] : v[k];
-      v[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
-    }
-  }
+__host__ __device__ constexpr int block_row(int seq, int h) {
+  constexpr int kSeqsQ = 32 / G, kHeads8 = G / 4;
+  return seq / kSeqsQ * 32 + h / kHeads8 * 8 + seq % kSeqsQ * kHeads8 + h % kHeads8;
 }
+
+// Weights are carried as (s' / 128)^2: |s'| <= 128 (two rows of mean square 1), so the clamp of
+// a saturating product is the maximum with 0.
+constexpr float kWeightScale = 128.0f * 128.0f;
 
 template <int G>
 __global__ void __launch_bounds__(kSThreads, 1)
@@ -236,8 +236,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
           break;
         }
         mbar_arrive_expect_tx(qfull, kTileB);
-        tma_load_4d(sQ, &tm_q, qfull, 0, 0, w.g, w.rb * kSeqs);
-        tma_load_4d(sQ + kBox, &tm_q, qfull, 64, 0, w.g, w.rb * kSeqs);
+        for (int e = 0; e < 16; ++e) {  // eight rows at a time (block_row)
+          const int head = e % 4 * (G / 4), seq = w.rb * kSeqs + e / 4 * (32 / G);
+          tma_load_4d(sQ + e * 1024, &tm_q, qfull, 0, head, w.g, seq);
+          tma_load_4d(sQ + kBox + e * 1024, &tm_q, qfull, 64, head, w.g, seq);
+        }
         *s_qissued = k + 1;
         for (int t = w.t0; t < w.t1; ++t, ++i) {
           const int s = i % kRing;
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         ok = mbar_wait(&kfull[s], (i / kRing) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const float rk = rsqrtf(row_square_sum(sK + s * kTileB, kBox, r) * (1.0f / kHeadDim) + p.eps);
+        const float rk = rsqrtf(row_square_sum(sK + s * kTileB, kBox, r, r & 7) * (1.0f / kHeadDim) + p.eps);
         ok = i < kRing || mbar_wait(&rkempty[s], ((i / kRing) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -370,33 +373,41 @@ __global__ void __launch_bounds__(kSThreads, 1)
     // ------------------------------------------------------------------ epilogue
     const int quarter = warp & 3;            // the tensor-memory lanes this warp may read
     const int part = (warp - kWarpEpi) >> 2;  // keys 32 part .. of each tile
-    const int r = quarter * 32 + lane;       // query row: sequence r / G of the block, head r % G
-    const int seq = r / G, h = r % G;
-    constexpr int kMine = kPartCols / G;  // keys this lane ends up with the group maximum of
+    const int q4 = lane & 3;                 // columns 8j + 2 q4, + 1 of those
+    constexpr int kSeqsQ = 32 / G;           // sequences of a quarter
+    const int seq = quarter * kSeqsQ + (lane >> 2) / (G / 4);  // this thread's sequence
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t part_col = static_cast<uint32_t>(part * kPartCols);
+    // this lane's key of each pair of scores (groups of 8 end up split over two lanes)
+    const int odd = G == 8 ? (lane >> 2) & 1 : 0;
     int i = 0;
     bool ok = true;
     for (int k = 0; ok && w.next(); ++k) {
       ok = !*s_abort && mbar_wait(qfull, k & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const float ss = row_square_sum(sQ, kBox, r);
-      const float rq = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
+      // 1 / rms of the thread's four rows: each lane takes one of its four lanes' rows
+      float rq[4];
       {
+        const float ss = row_square_sum(sQ, kBox, quarter * 32 + (lane >> 2) + 8 * q4, (lane & 3) * 2 + ((lane >> 2) & 1));
+        const float mine = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) rq[m] = __shfl_sync(0xffffffffu, mine, (lane & ~3) | m);
         // the query rows are read: every lane's sum depends on them
         const float used = __shfl_sync(0xffffffffu, ss, 0) + __shfl_sync(0xffffffffu, ss, 31);
         __syncwarp();
         if (lane == 0) mbar_arrive_after(qempty, used);
       }
       const bool valid = seq < w.nb;
-      const bool some = quarter * (32 / G) < w.nb;  // this warp has valid rows
-      float *scores = nullptr;  // this row's (sequence, KV head), at this lane's first key
+      const bool some = quarter * kSeqsQ < w.nb;  // this warp has valid rows
+      float *scores = nullptr;  // this thread's (sequence, KV head), at its first key
       if (p.sel != nullptr && valid)
         scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride + part_col +
-                 h * kMine;
-      float den[2] = {0.0f, 0.0f};
-      int live = 0;  // keys of this lane's share with a group maximum above zero
+                 2 * q4 + odd;
+      float den[4][2];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
+      int live = 0;  // keys of this thread's share with a group maximum above zero
       for (int t = w.t0; t < w.t1; ++t, ++i) {
         const int s = i % kRing;
         ok = mbar_wait(&sfull[s], (i / kRing) & 1) && mbar_wait(&rkfull[s], (i / kRing) & 1);
@@ -406,43 +417,44 @@ __global__ void __launch_bounds__(kSThreads, 1)
         const int x = t - tp;
         const int owner = own ? x / ts : seq;
         const uint32_t cols = tmem + lane_base + s * 128 + part_col;
-        float used = 0.0f;
-        if (!own ? some : owner / (32 / G) == quarter) {
+        if (!own ? some : owner / kSeqsQ == quarter) {
           tc_fence_after_sync();
-          uint32_t acc[kPartCols];
-          tmem_load_x32(cols, acc);
-          tmem_wait_ld(acc);
-          const float rqm = seq == owner ? rq : 0.0f;  // another sequence's keys weigh nothing here
-          const float4 *rkp = reinterpret_cast<const float4 *>(sRK + s * kRows + part_col);
-          float v[kPartCols];  // s' of this row and these keys
+          uint32_t acc[2][16];  // rows l / 4 (+ 8), then those + 16
+          tmem_load_16x256b_x4(cols, acc[0]);
+          tmem_load_16x256b_x4(cols + (16u << 16), acc[1]);
+          tmem_wait_ld(acc[0]);
+          tmem_wait_ld(acc[1]);
+          const float on = seq == owner ? 1.0f : 0.0f;  // another sequence's keys weigh nothing here
+          const float *rkp = sRK + s * kRows + part_col + 2 * q4;
+          float top[8];  // the group's maximum (of this thread's four heads) for its 8 keys
+          uint32_t hi[2][8], lo[2][8];
 #pragma unroll
-          for (int c = 0; c < kPartCols; c += 4) {
-            const float4 rk = rkp[c / 4];
-            v[c] = __uint_as_float(acc[c]);
-            v[c + 1] = __uint_as_float(acc[c + 1]);
-            v[c + 2] = __uint_as_float(acc[c + 2]);
-            v[c + 3] = __uint_as_float(acc[c + 3]);
-            mul2(v[c], v[c + 1], rk.x, rk.y);
-            mul2(v[c + 2], v[c + 3], rk.z, rk.w);
-            mul2(v[c], v[c + 1], rqm, rqm);
-            mul2(v[c + 2], v[c + 3], rqm, rqm);
-          }
-          // the weights over the scores' columns: 16 columns of hi, then 16 of lo
+          for (int j = 0; j < 4; ++j) {
+            const float2 rk = *reinterpret_cast<const float2 *>(rkp + 8 * j);
 #pragma unroll
-          for (int c0 = 0; c0 < kPartCols; c0 += 16) {
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-              float w0 = fmaxf(v[c0 + c], 0.0f), w1 = fmaxf(v[c0 + c + 1], 0.0f);
+            for (int m = 0; m < 4; ++m) {
+              float v0 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1)]);
+              float v1 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1) + 1]);
+              mul2(v0, v1, rk.x, rk.y);
+              mul2(v0, v1, rq[m], rq[m]);
+              top[2 * j] = m == 0 ? v0 : fmaxf(top[2 * j], v0);
+              top[2 * j + 1] = m == 0 ? v1 : fmaxf(top[2 * j + 1], v1);
+              const float f = on * (1.0f / 128.0f);
+              float w0 = __saturatef(v0 * f), w1 = __saturatef(v1 * f);
               mul2(w0, w1, w0, w1);
-              add2(den[0], den[1], w0, w1);
-              hi[c >> 1] = pack_bf16x2(w0, w1);
-              lo[c >> 1] = pack_bf16x2(w0 - bf16lo(hi[c >> 1]), w1 - bf16hi(hi[c >> 1]));
+              add2(den[m][0], den[m][1], w0, w1);
+              // the weights over the scores' columns: 16 columns of hi, then 16 of lo
+              const uint32_t b = pack_bf16x2(w0, w1);
+              sub_bf16x2(b, w0, w1);
+              hi[m >> 1][2 * j + (m & 1)] = b;
+              lo[m >> 1][2 * j + (m & 1)] = pack_bf16x2(w0, w1);
             }
-            tmem_store_x8(cols + c0 / 2, hi);
-            tmem_store_x8(cols + 16 + c0 / 2, lo);
           }
-          used = __shfl_sync(0xffffffffu, den[0], 0) + __shfl_sync(0xffffffffu, den[1], 31);
+          tmem_store_16x128b_x4(cols, hi[0]);
+          tmem_store_16x128b_x4(cols + 16, lo[0]);
+          tmem_store_16x128b_x4(cols + (16u << 16), hi[1]);
+          tmem_store_16x128b_x4(cols + (16u << 16) + 16, lo[1]);
+          const float used = __shfl_sync(0xffffffffu, den[0][0], 0) + __shfl_sync(0xffffffffu, den[0][1], 31);
           tmem_wait_st();
           tc_fence_before_sync();  // P is read by the tensor cores
           __syncwarp();
@@ -450,26 +462,41 @@ __global__ void __launch_bounds__(kSThreads, 1)
             mbar_arrive(&pfull[s]);
             mbar_arrive_after(&rkempty[s], used);  // every lane's sums depend on its norm reads
           }
-          group_max<G>(v, lane);
+          if constexpr (G == 8) {
+            // the other four heads are the lane's across: each keeps one key of every pair
 #pragma unroll
-          for (int c = 0; c < kMine; ++c) live += v[c] > 0.0f ? 1 : 0;
+            for (int j = 0; j < 4; ++j) {
+              const float give = odd ? top[2 * j] : top[2 * j + 1];
+              const float keep = odd ? top[2 * j + 1] : top[2 * j];
+              top[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+            }
+          }
+          constexpr int kEach = G == 8 ? 1 : 2;  // keys of every 8 that this thread keeps
+          if (seq == owner) {
+#pragma unroll
+            for (int c = 0; c < 4 * kEach; ++c) live += top[c] > 0.0f ? 1 : 0;
+          }
           if (scores != nullptr && seq == owner) {
             // the tile's first key in the score row, and how many keys it has
             const int64_t kt = own ? x - owner * ts : t;
             const int64_t rest = (own ? sp.n : sp.P) - kt * kTileKeys;
             float *dst = scores + (own ? sp.P : 0) + kt * kTileKeys;
-            if (rest >= kTileKeys && (own ? p.vec_own : p.vec_prefix)) {
-              if constexpr (G == 4)
-                st_global_v8(dst, p.alpha * v[0], p.alpha * v[1], p.alpha * v[2], p.alpha * v[3],
-                             p.alpha * v[4], p.alpha * v[5], p.alpha * v[6], p.alpha * v[7]);
-              else
-                *reinterpret_cast<float4 *>(dst) =
-                    make_float4(p.alpha * v[0], p.alpha * v[1], p.alpha * v[2], p.alpha * v[3]);
-            } else {
-              const int64_t room = rest - static_cast<int>(part_col) - h * kMine;
+            if (rest >= kTileKeys && (G == 8 || (own ? p.pair_own : p.pair_prefix))) {
 #pragma unroll
-              for (int c = 0; c < kMine; ++c)
-                if (c < room) dst[c] = p.alpha * v[c];
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (G == 8)
+                  dst[8 * j] = p.alpha * top[j];
+                else
+                  *reinterpret_cast<float2 *>(dst + 8 * j) =
+                      make_float2(p.alpha * top[2 * j], p.alpha * top[2 * j + 1]);
+              }
+            } else {
+              const int64_t room = rest - static_cast<int>(part_col) - 2 * q4 - odd;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                  if (8 * j + e < room) dst[8 * j + e] = p.alpha * top[kEach * j + e];
             }
           }
         } else {
@@ -505,18 +532,33 @@ __global__ void __launch_bounds__(kSThreads, 1)
       // sequences whose tiles it holds.
       const int first_seq = w.t0 < tp ? 0 : (w.t0 - tp) / ts;
       const int last_seq = w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
+      // this thread's sequence's count and its four rows' weight sums, over the lanes that share
+      // them
+      live += __shfl_xor_sync(0xffffffffu, live, 1);
+      live += __shfl_xor_sync(0xffffffffu, live, 2);
+      if constexpr (G == 8) live += __shfl_xor_sync(0xffffffffu, live, 4);
+      float dsum = 0.0f;
 #pragma unroll
-      for (int m = 1; m < G; m <<= 1) live += __shfl_xor_sync(0xffffffffu, live, m);
+      for (int m = 0; m < 4; ++m) {
+        float d = den[m][0] + den[m][1];
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        d += __shfl_xor_sync(0xffffffffu, d, 2);
+        if (m == q4) dsum = d;
+      }
+      float *rec = p.rec + sp.slot(w.rb, w.piece, w.g) * kRecWords;
       if (seq >= first_seq && seq <= last_seq) {
-        float *rec = p.rec + sp.slot(w.rb, w.piece, w.g) * kRecWords;
-        float *dst = rec + r * kHeadDim + part_col;
+        rec[kRecNum + part * kRows + quarter * 32 + (lane >> 2) + 8 * q4] = dsum;
+        if (q4 == 0 && odd == 0) reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + part * 32 + seq] = live;
+      }
+      // the numerators: lane l holds row l of the quarter, of sequence
+      const int row_seq = quarter * kSeqsQ + (lane & 7) / (G / 4);
+      if (row_seq >= first_seq && row_seq <= last_seq) {
+        float *dst = rec + (quarter * 32 + lane) * kHeadDim + part_col;
 #pragma unroll
         for (int c = 0; c < kPartCols; c += 8)
           st_global_v8(dst + c, __uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
                        __uint_as_float(o[c + 3]), __uint_as_float(o[c + 4]), __uint_as_float(o[c + 5]),
                        __uint_as_float(o[c + 6]), __uint_as_float(o[c + 7]));
-        rec[kRecNum + part * kRows + r] = den[0] + den[1];
-        if (h == 0) reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + part * 32 + seq] = live;
       }
     }
     if (!ok && lane == 0) give_up(s_abort, p.flags);
@@ -669,7 +711,8 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
   const int Hq = sp.G * sp.Hkv;
   const int b = row / Hq, hq = row % Hq, g = hq / sp.G;
   const int seqs = kRows / sp.G;
-  const int rb = b / seqs, seq = b % seqs, r = seq * sp.G + hq % sp.G;
+  const int rb = b / seqs, seq = b % seqs, h = hq % sp.G;
+  const int r = sp.G == 4 ? block_row<4>(seq, h) : block_row<8>(seq, h);
   // the pieces whose record holds this row: those with prefix tiles of this KV head, then
   // those with own tiles of this sequence
   const uint32_t gt = static_cast<uint32_t>(sp.group_tiles(rb)), T = gt * sp.Hkv;
@@ -726,6 +769,8 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
       nlive += s_live[k];
     }
   }
+  num *= kWeightScale;
+  dsum *= kWeightScale;
   const bool bad = !(fabsf(num) <= 3.402823466e38f);
   if (__syncthreads_or(bad)) {
     float *s_sum = reinterpret_cast<float *>(s_mem);  // [129]
@@ -787,9 +832,8 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   p.sel = a.sel_scores;
   p.hist = a.sel_hist;
   p.score_stride = a.score_stride;
-  const bool rows32 = (reinterpret_cast<uintptr_t>(a.sel_scores) & 31u) == 0 && a.score_stride % 8 == 0;
-  p.vec_prefix = rows32;
-  p.vec_own = rows32 && sp.P % 8 == 0;
+  p.pair_prefix = a.score_stride % 2 == 0;
+  p.pair_own = p.pair_prefix && sp.P % 2 == 0;
   p.alpha = a.alpha;
   p.eps = a.eps;
   auto kernel = sp.G == 4 ? shared_decode_kernel<4> : shared_decode_kernel<8>;
