@@ -23,8 +23,8 @@
 // row blocks so that the CTAs of different row blocks walk the same prefix tiles at the same
 // time (read from HBM once).
 //
-// Warp roles: 0 TMA producer (rings of 3 K and 3 V tiles); 1 issuer of S; 2 issuer of P V;
-// 4-7 key norms, one thread per key; 8-23 epilogue, each a quarter of the query rows and of the
+// Warp roles: 0 TMA producer of K (a ring of 3 tiles); 1 issuer of S; 2 issuer of P V; 3 TMA
+// producer of the query rows and of V (a ring of 3: its waits do not hold up K); 4-7 key norms, one thread per key; 8-23 epilogue, each a quarter of the query rows and of the
 // tile's keys.  The epilogue reads S in the fragment layout of the warp MMAs, where a thread
 // holds rows l, l + 8, l + 16 and l + 24 of its quarter, and the query rows lie in the block so
 // that those are heads of one sequence: the group maximum that the selection ranks is taken
@@ -33,12 +33,16 @@
 #include "internal.h"
 #include "ptx.cuh"
 
+#ifndef EMBLA_GROUPS
+#define EMBLA_GROUPS 2
+#endif
 namespace embla {
 namespace {
 
 constexpr int kRows = 128;               // query rows of a row block
 constexpr int kRing = 3;                 // K, V, key-norm stages and S/P buffers
 constexpr int kWarpPV = 2;
+constexpr int kWarpV = 3;
 constexpr int kWarpNorm = 4;             // first of the key-norm warps
 constexpr int kNormWarps = 4;
 constexpr int kWarpEpi = kWarpNorm + kNormWarps;
@@ -56,7 +60,7 @@ constexpr int kOffRK = kOffV + kRing * kTileB;
 constexpr int kOffBar = kOffRK + kRing * kRows * 4;
 constexpr int kNBars = 1 + 7 * kRing + 3;
 constexpr int kOffMisc = kOffBar + kNBars * 8;
-constexpr int kSSmem = kOffMisc + 16 + 1024;  // + room to align the base to 1024
+constexpr int kSSmem = kOffMisc + 32 + 1024;  // + room to align the base to 1024
 static_assert(kSSmem <= 227 * 1024, "shared memory per CTA");
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) MN-major
@@ -77,6 +81,7 @@ struct SharedParams {
   float *sel;              // [B, Hkv, score_stride] or null
   uint32_t *hist;          // [B, Hkv, 2048] or null; zeroed here
   int64_t score_stride;
+  int32_t groups;          // epilogue groups, 1 or 2: two take alternate tiles
   int32_t pair_prefix, pair_own;  // score rows of prefix / own tiles start on 8 bytes
   float alpha, eps;
 };
@@ -175,8 +180,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
   uint32_t *s_tmem = misc;
   volatile int *s_abort = reinterpret_cast<volatile int *>(misc + 1);
-  volatile int *s_issued = reinterpret_cast<volatile int *>(misc + 2);   // tile loads issued
-  volatile int *s_qissued = reinterpret_cast<volatile int *>(misc + 3);  // query loads issued
+  volatile int *s_kissued = reinterpret_cast<volatile int *>(misc + 2);  // K tile loads issued
+  volatile int *s_vissued = reinterpret_cast<volatile int *>(misc + 3);  // V tile loads issued
+  volatile int *s_qissued = reinterpret_cast<volatile int *>(misc + 4);  // query loads issued
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SharedSplit &sp = p.sp;
@@ -186,10 +192,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
     if (lane < kRing) {
       mbar_init(&kfull[lane], 1);
       mbar_init(&rkfull[lane], kNormWarps);
-      mbar_init(&rkempty[lane], kEpiWarps);
+      mbar_init(&rkempty[lane], kEpiWarps / p.groups);
       mbar_init(&vfull[lane], 1);
       mbar_init(&sfull[lane], 1);
-      mbar_init(&pfull[lane], kEpiWarps);
+      mbar_init(&pfull[lane], kEpiWarps / p.groups);
       mbar_init(&pvdone[lane], 1);
     }
     if (lane == 0) {
@@ -198,7 +204,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
       mbar_init(qempty, 1 + kEpiWarps);  // the S issuer's commit + every epilogue warp
       mbar_init(ofree, kEpiWarps);
       *s_abort = 0;
-      *s_issued = 0;
+      *s_kissued = 0;
+      *s_vissued = 0;
       *s_qissued = 0;
     }
     fence_barrier_init();
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     tmem_alloc(s_tmem, kTmemCols);
     tmem_relinquish();
   }
-  if (threadIdx.x == (kWarpPV + 1) * 32) {
+  if (threadIdx.x == kWarpV * 32) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_kp);
     tma_prefetch_desc(&tm_vp);
@@ -225,8 +232,40 @@ __global__ void __launch_bounds__(kSThreads, 1)
   // Every role walks the CTA's stretches in the same order, and their tiles through the rings
   // by a running tile count i: stage i % kRing, phase (i / kRing) & 1.  Stretch k's query and
   // output barriers take phase k & 1.
+  // where tile t of the walk's stretch lies: the maps, the plane and the row
+  auto place = [&](int t, int &plane, int &row) {
+    const bool own = t >= tp;
+    const int x = t - tp;
+    row = (own ? x % ts : t) * kTileKeys;
+    plane = own ? (w.rb * kSeqs + x / ts) * sp.Hkv + w.g : w.g;
+    return own;
+  };
   if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
+    // ------------------------------------------------------------------ K producer
+    if (lane == 0) {
+      int i = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        for (int t = w.t0; t < w.t1; ++t, ++i) {
+          const int s = i % kRing;
+          const uint32_t ph = ((i / kRing) - 1) & 1;
+          int plane, row;
+          const CUtensorMap *map = place(t, plane, row) ? &tm_ko : &tm_kp;
+          if (i >= kRing && !(mbar_wait(&sfull[s], ph) && mbar_wait(&rkfull[s], ph))) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&kfull[s], kTileB);
+          tma_load_3d(sK + s * kTileB, map, &kfull[s], 0, row, plane);
+          tma_load_3d(sK + s * kTileB + kBox, map, &kfull[s], 64, row, plane);
+          *s_kissued = i + 1;
+        }
+      }
+      if (!ok) give_up(s_abort, p.flags);
+    }
+    __syncwarp();
+  } else if (warp == kWarpV) {
+    // ------------------------------------------------------------------ query and V producer
     if (lane == 0) {
       int i = 0;
       bool ok = true;
@@ -236,6 +275,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           break;
         }
         mbar_arrive_expect_tx(qfull, kTileB);
+#pragma unroll 1
         for (int e = 0; e < 16; ++e) {  // eight rows at a time (block_row)
           const int head = e % 4 * (G / 4), seq = w.rb * kSeqs + e / 4 * (32 / G);
           tma_load_4d(sQ + e * 1024, &tm_q, qfull, 0, head, w.g, seq);
@@ -244,28 +284,16 @@ __global__ void __launch_bounds__(kSThreads, 1)
         *s_qissued = k + 1;
         for (int t = w.t0; t < w.t1; ++t, ++i) {
           const int s = i % kRing;
-          const uint32_t ph = ((i / kRing) - 1) & 1;
-          const bool own = t >= tp;
-          const int x = t - tp;
-          const int row = (own ? x % ts : t) * kTileKeys;
-          const int plane = own ? (w.rb * kSeqs + x / ts) * sp.Hkv + w.g : w.g;
-          const CUtensorMap *mk = own ? &tm_ko : &tm_kp, *mv = own ? &tm_vo : &tm_vp;
-          if (i >= kRing && !(mbar_wait(&sfull[s], ph) && mbar_wait(&rkfull[s], ph))) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&kfull[s], kTileB);
-          tma_load_3d(sK + s * kTileB, mk, &kfull[s], 0, row, plane);
-          tma_load_3d(sK + s * kTileB + kBox, mk, &kfull[s], 64, row, plane);
-          if (i >= kRing && !mbar_wait(&pvdone[s], ph)) {
-            *s_issued = 2 * i + 1;
+          int plane, row;
+          const CUtensorMap *map = place(t, plane, row) ? &tm_vo : &tm_vp;
+          if (i >= kRing && !mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&vfull[s], kTileB);
-          tma_load_3d(sV + s * kTileB, mv, &vfull[s], 0, row, plane);
-          tma_load_3d(sV + s * kTileB + kBox, mv, &vfull[s], 64, row, plane);
-          *s_issued = 2 * i + 2;
+          tma_load_3d(sV + s * kTileB, map, &vfull[s], 0, row, plane);
+          tma_load_3d(sV + s * kTileB + kBox, map, &vfull[s], 64, row, plane);
+          *s_vissued = i + 1;
         }
       }
       if (!ok) give_up(s_abort, p.flags);
@@ -319,11 +347,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            // keys 16kk..16kk+15: in their group of 32 columns hi takes the first 16, lo the rest
-            const uint32_t a_hi = tmem + s * 128 + (kk >> 1) * 32 + (kk & 1) * 8;
+            // keys 16kk..16kk+15: in their group of 16 columns hi takes the first 8, lo the rest
+            const uint32_t a_hi = tmem + s * 128 + kk * 16;
             const uint64_t vd = vdesc + static_cast<uint64_t>((s * kTileB + kk * 2048) >> 4);
             tc_mma_bf16_tmem_a(tmem + kColO, a_hi, vd, kIdescPV, (t > w.t0 || kk > 0) ? 1u : 0u);
-            tc_mma_bf16_tmem_a(tmem + kColO, a_hi + 16, vd, kIdescPV, 1u);
+            tc_mma_bf16_tmem_a(tmem + kColO, a_hi + 8, vd, kIdescPV, 1u);
           }
           tc_commit(&pvdone[s]);
         }
@@ -339,8 +367,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
     // every MMA of this warp has completed before the tensor memory is released
     if (done > 0) mbar_wait(ofull, (done - 1) & 1);
     __syncwarp();
-  } else if (warp == kWarpPV + 1) {
-    // no role: fills the warpgroup of single-thread roles
   } else if (warp < kWarpEpi) {
     // ------------------------------------------------------------------ key norms
     const int r = (warp - kWarpNorm) * 32 + lane;  // this thread's key of every tile
@@ -372,7 +398,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
   } else {
     // ------------------------------------------------------------------ epilogue
     const int quarter = warp & 3;            // the tensor-memory lanes this warp may read
-    const int part = (warp - kWarpEpi) >> 2;  // keys 32 part .. of each tile
+    // Four warps read each quarter.  In one group, each takes 32 of every tile's keys; in two,
+    // two warps take every other tile, 64 keys each.
+    const int part = (warp - kWarpEpi) >> 2;
+    const int group = p.groups == 2 ? part >> 1 : 0;
+    const int first_part = p.groups == 2 ? (part & 1) * 2 : part;
     const int q4 = lane & 3;                 // columns 8j + 2 q4, + 1 of those
     constexpr int kSeqsQ = 32 / G;           // sequences of a quarter
     const int seq = quarter * kSeqsQ + (lane >> 2) / (G / 4);  // this thread's sequence
@@ -402,13 +432,14 @@ __global__ void __launch_bounds__(kSThreads, 1)
       const bool some = quarter * kSeqsQ < w.nb;  // this warp has valid rows
       float *scores = nullptr;  // this thread's (sequence, KV head), at its first key
       if (p.sel != nullptr && valid)
-        scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride + part_col +
-                 2 * q4 + odd;
+        scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride + 2 * q4 +
+                 odd;
       float den[4][2];
 #pragma unroll
       for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
       int live = 0;  // keys of this thread's share with a group maximum above zero
       for (int t = w.t0; t < w.t1; ++t, ++i) {
+        if (p.groups == 2 && (i & 1) != group) continue;
         const int s = i % kRing;
         ok = mbar_wait(&sfull[s], (i / kRing) & 1) && mbar_wait(&rkfull[s], (i / kRing) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -416,44 +447,91 @@ __global__ void __launch_bounds__(kSThreads, 1)
         const bool own = t >= tp;
         const int x = t - tp;
         const int owner = own ? x / ts : seq;
-        const uint32_t cols = tmem + lane_base + s * 128 + part_col;
         if (!own ? some : owner / kSeqsQ == quarter) {
           tc_fence_after_sync();
-          uint32_t acc[2][16];  // rows l / 4 (+ 8), then those + 16
-          tmem_load_16x256b_x4(cols, acc[0]);
-          tmem_load_16x256b_x4(cols + (16u << 16), acc[1]);
-          tmem_wait_ld(acc[0]);
-          tmem_wait_ld(acc[1]);
-          const float on = seq == owner ? 1.0f : 0.0f;  // another sequence's keys weigh nothing here
-          const float *rkp = sRK + s * kRows + part_col + 2 * q4;
-          float top[8];  // the group's maximum (of this thread's four heads) for its 8 keys
-          uint32_t hi[2][8], lo[2][8];
+          // another sequence's keys weigh nothing here
+          const float f = seq == owner ? 1.0f / 128.0f : 0.0f;
+          // the tile's first key in the score row, and how many keys it has
+          const int kt = own ? x - owner * ts : t;
+          const int rest = static_cast<int>(own ? sp.n : sp.P) - kt * kTileKeys;
+          const bool store = scores != nullptr && seq == owner;
+          const bool pairs = rest >= kTileKeys && (G == 8 || (own ? p.pair_own : p.pair_prefix));
+          float *dst = scores + (own ? sp.P : 0) + static_cast<int64_t>(kt) * kTileKeys;
+          const uint32_t stage = tmem + lane_base + s * 128;
+          const float *rkp = sRK + s * kRows + 2 * q4;
+          // Sixteen keys: weights, P, the group's maxima and their scores.
+          auto keys16 = [&](const uint32_t (&acc)[2][8], int col) {
+            float top[4];  // the maximum over this thread's four heads for its four keys
+            uint32_t hi[2][4], lo[2][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 rk = *reinterpret_cast<const float2 *>(rkp + 8 * j);
+            for (int j = 0; j < 2; ++j) {
+              const float2 rk = *reinterpret_cast<const float2 *>(rkp + col + 8 * j);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              float v0 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1)]);
-              float v1 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1) + 1]);
-              mul2(v0, v1, rk.x, rk.y);
-              mul2(v0, v1, rq[m], rq[m]);
-              top[2 * j] = m == 0 ? v0 : fmaxf(top[2 * j], v0);
-              top[2 * j + 1] = m == 0 ? v1 : fmaxf(top[2 * j + 1], v1);
-              const float f = on * (1.0f / 128.0f);
-              float w0 = __saturatef(v0 * f), w1 = __saturatef(v1 * f);
-              mul2(w0, w1, w0, w1);
-              add2(den[m][0], den[m][1], w0, w1);
-              // the weights over the scores' columns: 16 columns of hi, then 16 of lo
-              const uint32_t b = pack_bf16x2(w0, w1);
-              sub_bf16x2(b, w0, w1);
-              hi[m >> 1][2 * j + (m & 1)] = b;
-              lo[m >> 1][2 * j + (m & 1)] = pack_bf16x2(w0, w1);
+              for (int m = 0; m < 4; ++m) {
+                float v0 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1)]);
+                float v1 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1) + 1]);
+                mul2(v0, v1, rk.x, rk.y);
+                mul2(v0, v1, rq[m], rq[m]);
+                top[2 * j] = m == 0 ? v0 : fmaxf(top[2 * j], v0);
+                top[2 * j + 1] = m == 0 ? v1 : fmaxf(top[2 * j + 1], v1);
+                float w0 = __saturatef(v0 * f), w1 = __saturatef(v1 * f);
+                mul2(w0, w1, w0, w1);
+                add2(den[m][0], den[m][1], w0, w1);
+                // the weights over the scores' columns: 8 columns of hi, then 8 of lo
+                const uint32_t b = pack_bf16x2(w0, w1);
+                sub_bf16x2(b, w0, w1);
+                hi[m >> 1][2 * j + (m & 1)] = b;
+                lo[m >> 1][2 * j + (m & 1)] = pack_bf16x2(w0, w1);
+              }
             }
+            tmem_store_16x128b_x2(stage + col, hi[0]);
+            tmem_store_16x128b_x2(stage + col + 8, lo[0]);
+            tmem_store_16x128b_x2(stage + col + (16u << 16), hi[1]);
+            tmem_store_16x128b_x2(stage + col + (16u << 16) + 8, lo[1]);
+            if constexpr (G == 8) {
+              // the other four heads are the lane's across: each keeps one key of every pair
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float give = odd ? top[2 * j] : top[2 * j + 1];
+                const float keep = odd ? top[2 * j + 1] : top[2 * j];
+                top[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+              }
+            }
+            constexpr int kEach = G == 8 ? 1 : 2;  // keys of every 8 that this thread keeps
+            if (seq == owner) {
+#pragma unroll
+              for (int e = 0; e < 2 * kEach; ++e) live += top[e] > 0.0f ? 1 : 0;
+            }
+            if (store) {
+              if (pairs) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  if constexpr (G == 8)
+                    dst[col + 8 * j] = p.alpha * top[j];
+                  else
+                    *reinterpret_cast<float2 *>(dst + col + 8 * j) =
+                        make_float2(p.alpha * top[2 * j], p.alpha * top[2 * j + 1]);
+                }
+              } else {
+                const int room = rest - col - 2 * q4 - odd;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                  for (int e = 0; e < kEach; ++e)
+                    if (8 * j + e < room) dst[col + 8 * j + e] = p.alpha * top[kEach * j + e];
+              }
+            }
+          };
+#pragma unroll 1
+          for (int c = 0; c < 2 * p.groups; ++c) {
+            const int col = first_part * kPartCols + c * 16;
+            uint32_t acc[2][8];  // rows l / 4 (+ 8), then those + 16
+            tmem_load_16x256b_x2(stage + col, acc[0]);
+            tmem_load_16x256b_x2(stage + col + (16u << 16), acc[1]);
+            tmem_wait_ld(acc[0]);
+            tmem_wait_ld(acc[1]);
+            keys16(acc, col);
           }
-          tmem_store_16x128b_x4(cols, hi[0]);
-          tmem_store_16x128b_x4(cols + 16, lo[0]);
-          tmem_store_16x128b_x4(cols + (16u << 16), hi[1]);
-          tmem_store_16x128b_x4(cols + (16u << 16) + 16, lo[1]);
           const float used = __shfl_sync(0xffffffffu, den[0][0], 0) + __shfl_sync(0xffffffffu, den[0][1], 31);
           tmem_wait_st();
           tc_fence_before_sync();  // P is read by the tensor cores
@@ -462,51 +540,14 @@ __global__ void __launch_bounds__(kSThreads, 1)
             mbar_arrive(&pfull[s]);
             mbar_arrive_after(&rkempty[s], used);  // every lane's sums depend on its norm reads
           }
-          if constexpr (G == 8) {
-            // the other four heads are the lane's across: each keeps one key of every pair
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float give = odd ? top[2 * j] : top[2 * j + 1];
-              const float keep = odd ? top[2 * j + 1] : top[2 * j];
-              top[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4));
-            }
-          }
-          constexpr int kEach = G == 8 ? 1 : 2;  // keys of every 8 that this thread keeps
-          if (seq == owner) {
-#pragma unroll
-            for (int c = 0; c < 4 * kEach; ++c) live += top[c] > 0.0f ? 1 : 0;
-          }
-          if (scores != nullptr && seq == owner) {
-            // the tile's first key in the score row, and how many keys it has
-            const int64_t kt = own ? x - owner * ts : t;
-            const int64_t rest = (own ? sp.n : sp.P) - kt * kTileKeys;
-            float *dst = scores + (own ? sp.P : 0) + kt * kTileKeys;
-            if (rest >= kTileKeys && (G == 8 || (own ? p.pair_own : p.pair_prefix))) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if constexpr (G == 8)
-                  dst[8 * j] = p.alpha * top[j];
-                else
-                  *reinterpret_cast<float2 *>(dst + 8 * j) =
-                      make_float2(p.alpha * top[2 * j], p.alpha * top[2 * j + 1]);
-              }
-            } else {
-              const int64_t room = rest - static_cast<int>(part_col) - 2 * q4 - odd;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < kEach; ++e)
-                  if (8 * j + e < room) dst[8 * j + e] = p.alpha * top[kEach * j + e];
-            }
-          }
         } else {
           // no row of this warp reads the tile: zero weights for rows that other tiles count
           // for (rows past the batch hold anything, no other row sees them)
           if (some) {
             tc_fence_after_sync();
             const uint32_t zero[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            tmem_store_x16(cols, zero);
-            tmem_store_x16(cols + 16, zero);
+            for (int c = 0; c < 2 * p.groups; ++c)
+              tmem_store_x16(tmem + lane_base + s * 128 + first_part * kPartCols + 16 * c, zero);
             tmem_wait_st();
             tc_fence_before_sync();
           }
@@ -571,8 +612,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     // for the last armed phase of every barrier that a copy completes.
     const int qi = *s_qissued;
     if (qi > 0) mbar_wait(qfull, (qi - 1) & 1);
-    const int issued = *s_issued;  // 2 per key tile: K, V
-    const int nk = (issued + 1) / 2, nv = issued / 2;
+    const int nk = *s_kissued, nv = *s_vissued;
     for (int s = 0; s < kRing; ++s) {
       int uses = nk > s ? (nk - 1 - s) / kRing + 1 : 0;
       if (uses) mbar_wait(&kfull[s], (uses - 1) & 1);
@@ -832,6 +872,7 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   p.sel = a.sel_scores;
   p.hist = a.sel_hist;
   p.score_stride = a.score_stride;
+  p.groups = EMBLA_GROUPS;
   p.pair_prefix = a.score_stride % 2 == 0;
   p.pair_own = p.pair_prefix && sp.P % 2 == 0;
   p.alpha = a.alpha;
