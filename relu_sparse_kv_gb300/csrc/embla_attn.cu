@@ -154,19 +154,19 @@ bool encode_planes(CUtensorMap *map, const void *base, uint64_t rows, uint64_t p
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 4-D bf16 map of q [batch][Hkv][G][128], boxes of {64 columns, G / 4 heads, 1 KV head, 32 / G
-// sequences}: eight query rows of one KV head; sequences past the batch read as zeros.
+// 5-D bf16 map of q [batch][Hkv][4][G / 4][128] with the batch inside the groups of G / 4 heads,
+// boxes of {64 columns, G / 4 heads, 32 / G sequences, 4 groups, 1 KV head}: 32 query rows of one
+// KV head, in the order of the decode's row blocks; sequences past the batch read as zeros.
 bool encode_query_block(CUtensorMap *map, const void *q, int batch, int Hq, int Hkv) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const int G = Hq / Hkv;
-  const cuuint64_t row = kHeadDim * 2;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(G),
-                              static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(batch)};
-  const cuuint64_t strides[3] = {row, row * static_cast<cuuint64_t>(G), row * static_cast<cuuint64_t>(Hq)};
-  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(G / 4), 1u, static_cast<cuuint32_t>(32 / G)};
-  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+  const cuuint64_t row = kHeadDim * 2, G = static_cast<cuuint64_t>(Hq / Hkv);
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(kHeadDim), G / 4, static_cast<cuuint64_t>(batch), 4u,
+                              static_cast<cuuint64_t>(Hkv)};
+  const cuuint64_t strides[4] = {row, row * static_cast<cuuint64_t>(Hq), row * (G / 4), row * G};
+  const cuuint32_t box[5] = {64u, static_cast<cuuint32_t>(G / 4), static_cast<cuuint32_t>(32 / G), 4u, 1u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(q), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -58,7 +58,7 @@ constexpr int kOffK = kOffQ + kTileB;
 constexpr int kOffV = kOffK + kRing * kTileB;
 constexpr int kOffRK = kOffV + kRing * kTileB;
 constexpr int kOffBar = kOffRK + kRing * kRows * 4;
-constexpr int kNBars = 1 + 7 * kRing + 3;
+constexpr int kNBars = 1 + 5 * kRing + 3;
 constexpr int kOffMisc = kOffBar + kNBars * 8;
 constexpr int kSSmem = kOffMisc + 32 + 1024;  // + room to align the base to 1024
 static_assert(kSSmem <= 227 * 1024, "shared memory per CTA");
@@ -166,14 +166,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
   uint8_t *sV = smem + kOffV;
   float *sRK = reinterpret_cast<float *>(smem + kOffRK);
   uint64_t *qfull = reinterpret_cast<uint64_t *>(smem + kOffBar);
-  // A K stage is free once its tile's S is done (sfull) and its norms are taken (rkfull), a V
-  // stage once its P V is done (pvdone).
   uint64_t *kfull = qfull + 1;
-  uint64_t *rkfull = kfull + kRing, *rkempty = rkfull + kRing;
-  uint64_t *vfull = rkempty + kRing;
-  uint64_t *sfull = vfull + kRing;
+  uint64_t *vfull = kfull + kRing;
+  uint64_t *sfull = vfull + kRing;   // S done and the key norms taken: the K stage is free
   uint64_t *pfull = sfull + kRing;
-  uint64_t *pvdone = pfull + kRing;
+  uint64_t *pvdone = pfull + kRing;  // P V done: the V stage, S/P buffer and norms are free
   uint64_t *ofull = pvdone + kRing;  // a stretch's P V all done
   uint64_t *qempty = ofull + 1;      // its query rows no longer needed
   uint64_t *ofree = qempty + 1;      // its O read out of tensor memory
@@ -191,10 +188,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
   if (warp == 0) {
     if (lane < kRing) {
       mbar_init(&kfull[lane], 1);
-      mbar_init(&rkfull[lane], kNormWarps);
-      mbar_init(&rkempty[lane], kEpiWarps / p.groups);
       mbar_init(&vfull[lane], 1);
-      mbar_init(&sfull[lane], 1);
+      mbar_init(&sfull[lane], 1 + kNormWarps);  // the S issuer's commit and the norms
       mbar_init(&pfull[lane], kEpiWarps / p.groups);
       mbar_init(&pvdone[lane], 1);
     }
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           const uint32_t ph = ((i / kRing) - 1) & 1;
           int plane, row;
           const CUtensorMap *map = place(t, plane, row) ? &tm_ko : &tm_kp;
-          if (i >= kRing && !(mbar_wait(&sfull[s], ph) && mbar_wait(&rkfull[s], ph))) {
+          if (i >= kRing && !mbar_wait(&sfull[s], ph)) {
             ok = false;
             break;
           }
@@ -275,11 +270,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
           break;
         }
         mbar_arrive_expect_tx(qfull, kTileB);
-#pragma unroll 1
-        for (int e = 0; e < 16; ++e) {  // eight rows at a time (block_row)
-          const int head = e % 4 * (G / 4), seq = w.rb * kSeqs + e / 4 * (32 / G);
-          tma_load_4d(sQ + e * 1024, &tm_q, qfull, 0, head, w.g, seq);
-          tma_load_4d(sQ + kBox + e * 1024, &tm_q, qfull, 64, head, w.g, seq);
+        for (int e = 0; e < 4; ++e) {  // a quarter of the rows at a time (block_row)
+          const int seq = w.rb * kSeqs + e * (32 / G);
+          tma_load_5d(sQ + e * 4096, &tm_q, qfull, 0, 0, seq, 0, w.g);
+          tma_load_5d(sQ + kBox + e * 4096, &tm_q, qfull, 64, 0, seq, 0, w.g);
         }
         *s_qissued = k + 1;
         for (int t = w.t0; t < w.t1; ++t, ++i) {
@@ -379,12 +373,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const float rk = rsqrtf(row_square_sum(sK + s * kTileB, kBox, r, r & 7) * (1.0f / kHeadDim) + p.eps);
-        ok = i < kRing || mbar_wait(&rkempty[s], ((i / kRing) - 1) & 1);
+        ok = i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         sRK[s * kRows + r] = rk;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&rkfull[s]);
+        if (lane == 0) mbar_arrive(&sfull[s]);
       }
     }
     if (!ok && lane == 0) give_up(s_abort, p.flags);
@@ -438,11 +432,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll
       for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
       int live = 0;  // keys of this thread's share with a group maximum above zero
-      for (int t = w.t0; t < w.t1; ++t, ++i) {
-        if (p.groups == 2 && (i & 1) != group) continue;
-        const int s = i % kRing;
-        ok = mbar_wait(&sfull[s], (i / kRing) & 1) && mbar_wait(&rkfull[s], (i / kRing) & 1);
-        ok = __all_sync(0xffffffffu, ok);
+      // this group's tiles: every groups-th of the running count
+      const int skip = (group - i) & (p.groups - 1);
+      for (int t = w.t0 + skip, it = i + skip; t < w.t1; t += p.groups, it += p.groups) {
+        const int s = it % kRing;
+        ok = mbar_wait(&sfull[s], (it / kRing) & 1);
         if (!ok) break;
         const bool own = t >= tp;
         const int x = t - tp;
@@ -532,14 +526,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
             tmem_wait_ld(acc[1]);
             keys16(acc, col);
           }
-          const float used = __shfl_sync(0xffffffffu, den[0][0], 0) + __shfl_sync(0xffffffffu, den[0][1], 31);
           tmem_wait_st();
           tc_fence_before_sync();  // P is read by the tensor cores
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&pfull[s]);
-            mbar_arrive_after(&rkempty[s], used);  // every lane's sums depend on its norm reads
-          }
+          if (lane == 0) mbar_arrive(&pfull[s]);
         } else {
           // no row of this warp reads the tile: zero weights for rows that other tiles count
           // for (rows past the batch hold anything, no other row sees them)
@@ -552,12 +542,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
             tc_fence_before_sync();
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&pfull[s]);
-            mbar_arrive(&rkempty[s]);
-          }
+          if (lane == 0) mbar_arrive(&pfull[s]);
         }
       }
+      i += w.t1 - w.t0;
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ok = mbar_wait(ofull, k & 1) && !*s_abort;
       ok = __all_sync(0xffffffffu, ok);
