@@ -30,6 +30,8 @@
 // that those are heads of one sequence: the group maximum that the selection ranks is taken
 // within a thread (over lanes it cost two and a half instructions per score on the pipe that
 // bound the epilogue).
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -453,35 +455,36 @@ __global__ void __launch_bounds__(kSThreads, 1)
           float *dst = scores + (own ? sp.P : 0) + static_cast<int64_t>(kt) * kTileKeys;
           const uint32_t stage = tmem + lane_base + s * 128;
           const float *rkp = sRK + s * kRows + 2 * q4;
-          // Sixteen keys: weights, P, the group's maxima and their scores.
-          auto keys16 = [&](const uint32_t (&acc)[2][8], int col) {
-            float top[4];  // the maximum over this thread's four heads for its four keys
-            uint32_t hi[2][4], lo[2][4];
+          float top[4];  // the maximum over this thread's four heads for its four of 16 keys
+          // Sixteen keys of rows l / 4 + 16 side and + 8: weights, P, the maximum so far.
+          auto rows16 = [&](const uint32_t (&acc)[8], int col, auto which) {
+            constexpr int side = decltype(which)::value;
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float2 rk = *reinterpret_cast<const float2 *>(rkp + col + 8 * j);
 #pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                float v0 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1)]);
-                float v1 = __uint_as_float(acc[m >> 1][4 * j + 2 * (m & 1) + 1]);
+              for (int m = 0; m < 2; ++m) {
+                float v0 = __uint_as_float(acc[4 * j + 2 * m]), v1 = __uint_as_float(acc[4 * j + 2 * m + 1]);
                 mul2(v0, v1, rk.x, rk.y);
-                mul2(v0, v1, rq[m], rq[m]);
-                top[2 * j] = m == 0 ? v0 : fmaxf(top[2 * j], v0);
-                top[2 * j + 1] = m == 0 ? v1 : fmaxf(top[2 * j + 1], v1);
+                mul2(v0, v1, rq[2 * side + m], rq[2 * side + m]);
+                top[2 * j] = side == 0 && m == 0 ? v0 : fmaxf(top[2 * j], v0);
+                top[2 * j + 1] = side == 0 && m == 0 ? v1 : fmaxf(top[2 * j + 1], v1);
                 float w0 = __saturatef(v0 * f), w1 = __saturatef(v1 * f);
                 mul2(w0, w1, w0, w1);
-                add2(den[m][0], den[m][1], w0, w1);
+                add2(den[2 * side + m][0], den[2 * side + m][1], w0, w1);
                 // the weights over the scores' columns: 8 columns of hi, then 8 of lo
                 const uint32_t b = pack_bf16x2(w0, w1);
                 sub_bf16x2(b, w0, w1);
-                hi[m >> 1][2 * j + (m & 1)] = b;
-                lo[m >> 1][2 * j + (m & 1)] = pack_bf16x2(w0, w1);
+                hi[2 * j + m] = b;
+                lo[2 * j + m] = pack_bf16x2(w0, w1);
               }
             }
-            tmem_store_16x128b_x2(stage + col, hi[0]);
-            tmem_store_16x128b_x2(stage + col + 8, lo[0]);
-            tmem_store_16x128b_x2(stage + col + (16u << 16), hi[1]);
-            tmem_store_16x128b_x2(stage + col + (16u << 16) + 8, lo[1]);
+            tmem_store_16x128b_x2(stage + col + (side * 16u << 16), hi);
+            tmem_store_16x128b_x2(stage + col + (side * 16u << 16) + 8, lo);
+          };
+          // Those keys' maxima over the whole group: counted and written out.
+          auto group_scores = [&](int col) {
             if constexpr (G == 8) {
               // the other four heads are the lane's across: each keeps one key of every pair
 #pragma unroll
@@ -516,15 +519,19 @@ __global__ void __launch_bounds__(kSThreads, 1)
               }
             }
           };
+          // each load is on its way while the rows before it are worked on
+          uint32_t a[8], b[8];
+          const int col0 = first_part * kPartCols, col1 = col0 + p.groups * kPartCols;
+          tmem_load_16x256b_x2(stage + col0, a);
 #pragma unroll 1
-          for (int c = 0; c < 2 * p.groups; ++c) {
-            const int col = first_part * kPartCols + c * 16;
-            uint32_t acc[2][8];  // rows l / 4 (+ 8), then those + 16
-            tmem_load_16x256b_x2(stage + col, acc[0]);
-            tmem_load_16x256b_x2(stage + col + (16u << 16), acc[1]);
-            tmem_wait_ld(acc[0]);
-            tmem_wait_ld(acc[1]);
-            keys16(acc, col);
+          for (int col = col0; col < col1; col += 16) {
+            tmem_wait_ld(a);
+            tmem_load_16x256b_x2(stage + col + (16u << 16), b);
+            rows16(a, col, std::integral_constant<int, 0>{});
+            tmem_wait_ld(b);
+            if (col + 16 < col1) tmem_load_16x256b_x2(stage + col + 16, a);
+            rows16(b, col, std::integral_constant<int, 1>{});
+            group_scores(col);
           }
           tmem_wait_st();
           tc_fence_before_sync();  // P is read by the tensor cores
