@@ -486,6 +486,25 @@ __device__ __forceinline__ void st_global_v8(float *dst, float a0, float a1, flo
                : "memory");
 }
 
+// Two floats (dst 8-byte aligned) or one to global memory where `on` holds: a predicated store, no
+// branch.
+__device__ __forceinline__ void st_global_v2_if(bool on, float *dst, float a0, float a1) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "@p st.global.v2.f32 [%0], {%1, %2};\n\t}" ::"l"(dst),
+      "f"(a0), "f"(a1), "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+__device__ __forceinline__ void st_global_if(bool on, float *dst, float a) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p st.global.f32 [%0], %1;\n\t}" ::"l"(dst),
+      "f"(a), "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_store_x1(uint32_t taddr, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
 }

@@ -81,7 +81,8 @@ struct SharedParams {
   float *rec;
   uint32_t *flags;
   float *sel;              // [B, Hkv, score_stride] or null
-  uint32_t *hist;          // [B, Hkv, 2048] or null; zeroed here
+  uint32_t *hist;          // [B, Hkv, 2048], zeroed here, and so are the survivor counts (with scores)
+  int32_t *n_surv;
   int64_t score_stride;
   int32_t groups;          // epilogue groups, 1 or 2: two take alternate tiles
   int32_t pair_prefix, pair_own;  // score rows of prefix / own tiles start on 8 bytes
@@ -155,7 +156,9 @@ __host__ __device__ constexpr int block_row(int seq, int h) {
 // a saturating product is the maximum with 0.
 constexpr float kWeightScale = 128.0f * 128.0f;
 
-template <int G>
+// SCORES: every key's group maximum is written out (and the survivors are counted from those by
+// the next kernel, as the histogram is); without, the survivors are counted here.
+template <int G, bool SCORES>
 __global__ void __launch_bounds__(kSThreads, 1)
     shared_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kp,
                          const __grid_constant__ CUtensorMap tm_vp, const __grid_constant__ CUtensorMap tm_ko,
@@ -384,12 +387,15 @@ __global__ void __launch_bounds__(kSThreads, 1)
       }
     }
     if (!ok && lane == 0) give_up(s_abort, p.flags);
-    // the counts of the selection's bins, added up by the next kernel, start at zero
-    if (p.hist != nullptr) {
+    // the counts that the next kernel adds up start at zero
+    if constexpr (SCORES) {
       uint4 *h = reinterpret_cast<uint4 *>(p.hist);
       const int64_t n4 = static_cast<int64_t>(sp.B) * sp.Hkv * (kHistBins / 4);
       for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRows + r; e < n4; e += static_cast<int64_t>(gridDim.x) * kRows)
         h[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRows + r; e < static_cast<int64_t>(sp.B) * sp.Hkv;
+           e += static_cast<int64_t>(gridDim.x) * kRows)
+        p.n_surv[e] = 0;
     }
   } else {
     // ------------------------------------------------------------------ epilogue
@@ -426,10 +432,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
       }
       const bool valid = seq < w.nb;
       const bool some = quarter * kSeqsQ < w.nb;  // this warp has valid rows
-      float *scores = nullptr;  // this thread's (sequence, KV head), at its first key
-      if (p.sel != nullptr && valid)
-        scores = p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) * p.score_stride + 2 * q4 +
-                 odd;
+      // this thread's (sequence, KV head)'s scores, at its first key
+      float *scores = SCORES && valid ? p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) *
+                                                    p.score_stride + 2 * q4 + odd
+                                      : nullptr;
       float den[4][2];
 #pragma unroll
       for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
@@ -450,19 +456,19 @@ __global__ void __launch_bounds__(kSThreads, 1)
           // the tile's first key in the score row, and how many keys it has
           const int kt = own ? x - owner * ts : t;
           const int rest = static_cast<int>(own ? sp.n : sp.P) - kt * kTileKeys;
-          const bool store = scores != nullptr && seq == owner;
+          const bool reads = valid && seq == owner;
           const bool pairs = rest >= kTileKeys && (G == 8 || (own ? p.pair_own : p.pair_prefix));
           float *dst = scores + (own ? sp.P : 0) + static_cast<int64_t>(kt) * kTileKeys;
           const uint32_t stage = tmem + lane_base + s * 128;
           const float *rkp = sRK + s * kRows + 2 * q4;
           float top[4];  // the maximum over this thread's four heads for its four of 16 keys
           // Sixteen keys of rows l / 4 + 16 side and + 8: weights, P, the maximum so far.
-          auto rows16 = [&](const uint32_t (&acc)[8], int col, auto which) {
+          auto rows16 = [&](const uint32_t (&acc)[8], const float2 (&rks)[2], int col, auto which) {
             constexpr int side = decltype(which)::value;
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float2 rk = *reinterpret_cast<const float2 *>(rkp + col + 8 * j);
+              const float2 rk = rks[j];
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 float v0 = __uint_as_float(acc[4 * j + 2 * m]), v1 = __uint_as_float(acc[4 * j + 2 * m + 1]);
@@ -495,44 +501,46 @@ __global__ void __launch_bounds__(kSThreads, 1)
               }
             }
             constexpr int kEach = G == 8 ? 1 : 2;  // keys of every 8 that this thread keeps
-            if (seq == owner) {
+            if constexpr (!SCORES) {
 #pragma unroll
-              for (int e = 0; e < 2 * kEach; ++e) live += top[e] > 0.0f ? 1 : 0;
-            }
-            if (store) {
-              if (pairs) {
+              for (int e = 0; e < 2 * kEach; ++e) live += reads && top[e] > 0.0f ? 1 : 0;
+            } else if (pairs) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  if constexpr (G == 8)
-                    dst[col + 8 * j] = p.alpha * top[j];
-                  else
-                    *reinterpret_cast<float2 *>(dst + col + 8 * j) =
-                        make_float2(p.alpha * top[2 * j], p.alpha * top[2 * j + 1]);
-                }
-              } else {
-                const int room = rest - col - 2 * q4 - odd;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                  for (int e = 0; e < kEach; ++e)
-                    if (8 * j + e < room) dst[col + 8 * j + e] = p.alpha * top[kEach * j + e];
+              for (int j = 0; j < 2; ++j) {
+                if constexpr (G == 8)
+                  st_global_if(reads, dst + col + 8 * j, p.alpha * top[j]);
+                else
+                  st_global_v2_if(reads, dst + col + 8 * j, p.alpha * top[2 * j], p.alpha * top[2 * j + 1]);
               }
+            } else {
+              const int room = rest - col - 2 * q4 - odd;
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < kEach; ++e)
+                  st_global_if(reads && 8 * j + e < room, dst + col + 8 * j + e, p.alpha * top[kEach * j + e]);
             }
           };
           // each load is on its way while the rows before it are worked on
           uint32_t a[8], b[8];
           const int col0 = first_part * kPartCols, col1 = col0 + p.groups * kPartCols;
           tmem_load_16x256b_x2(stage + col0, a);
+          float2 rks[2] = {*reinterpret_cast<const float2 *>(rkp + col0),
+                           *reinterpret_cast<const float2 *>(rkp + col0 + 8)};
 #pragma unroll 1
           for (int col = col0; col < col1; col += 16) {
             tmem_wait_ld(a);
             tmem_load_16x256b_x2(stage + col + (16u << 16), b);
-            rows16(a, col, std::integral_constant<int, 0>{});
+            rows16(a, rks, col, std::integral_constant<int, 0>{});
             tmem_wait_ld(b);
-            if (col + 16 < col1) tmem_load_16x256b_x2(stage + col + 16, a);
-            rows16(b, col, std::integral_constant<int, 1>{});
+            const int next = col + 16 < col1 ? col + 16 : col0;  // past the last: read, not used
+            tmem_load_16x256b_x2(stage + next, a);
+            rows16(b, rks, col, std::integral_constant<int, 1>{});
+            rks[0] = *reinterpret_cast<const float2 *>(rkp + next);
+            rks[1] = *reinterpret_cast<const float2 *>(rkp + next + 8);
             group_scores(col);
           }
+          tmem_wait_ld(a);
           tmem_wait_st();
           tc_fence_before_sync();  // P is read by the tensor cores
           __syncwarp();
@@ -569,11 +577,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
       // sequences whose tiles it holds.
       const int first_seq = w.t0 < tp ? 0 : (w.t0 - tp) / ts;
       const int last_seq = w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
-      // this thread's sequence's count and its four rows' weight sums, over the lanes that share
-      // them
-      live += __shfl_xor_sync(0xffffffffu, live, 1);
-      live += __shfl_xor_sync(0xffffffffu, live, 2);
-      if constexpr (G == 8) live += __shfl_xor_sync(0xffffffffu, live, 4);
+      // its four rows' weight sums and (without scores) its sequence's count, over the lanes that
+      // share them
+      if constexpr (!SCORES) {
+        live += __shfl_xor_sync(0xffffffffu, live, 1);
+        live += __shfl_xor_sync(0xffffffffu, live, 2);
+        if constexpr (G == 8) live += __shfl_xor_sync(0xffffffffu, live, 4);
+      }
       float dsum = 0.0f;
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
@@ -585,7 +595,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
       float *rec = p.rec + sp.slot(w.rb, w.piece, w.g) * kRecWords;
       if (seq >= first_seq && seq <= last_seq) {
         rec[kRecNum + part * kRows + quarter * 32 + (lane >> 2) + 8 * q4] = dsum;
-        if (q4 == 0 && odd == 0) reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + part * 32 + seq] = live;
+        if (!SCORES && q4 == 0 && odd == 0)
+          reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + part * 32 + seq] = live;
       }
       // the numerators: lane l holds row l of the quarter, of sequence
       const int row_seq = quarter * kSeqsQ + (lane & 7) / (G / 4);
@@ -718,7 +729,11 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     const int64_t N = sp.P + sp.n, a = (blockIdx.x % p.hist_splits) * static_cast<int64_t>(p.hist_keys);
     const int m = static_cast<int>(N - a < p.hist_keys ? N - a : p.hist_keys);
     const float *su = p.sel + u * p.score_stride + a;
-    auto count = [&](float x) { atomicAdd(&s_mem[order_key(x) >> 21], 1u); };
+    int live = 0;
+    auto count = [&](float x) {
+      live += x > 0.0f ? 1 : 0;
+      atomicAdd(&s_mem[order_key(x) >> 21], 1u);
+    };
     if (p.hist_vec) {
       const float4 *s4 = reinterpret_cast<const float4 *>(su);
       constexpr int kLoads = 4;  // in flight per thread
@@ -736,6 +751,8 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     } else {
       for (int e = threadIdx.x; e < m; e += kFThreads) count(su[e]);
     }
+    live = __reduce_add_sync(0xffffffffu, live);
+    if (lane == 0 && live != 0) atomicAdd(&p.n_surv[u], live);
     __syncthreads();
     for (int k = threadIdx.x; k < kHistBins; k += kFThreads)
       if (s_mem[k] != 0u) atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
@@ -782,7 +799,7 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     acc.w += x.w;
     if (lane < kParts) {
       den += rec[kRecNum + lane * kRows + r];
-      live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
+      if (p.hist == nullptr) live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
     }
   }
   float *s_acc = reinterpret_cast<float *>(s_mem);            // [8 warps][128]
@@ -817,7 +834,7 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
   if (threadIdx.x < kHeadDim) {
     const float z = p.c / p.alpha / p.alpha + dsum;
     p.out[static_cast<int64_t>(row) * kHeadDim + threadIdx.x] = z != 0.0f ? num / z : 0.0f;
-    if (threadIdx.x == 0 && hq % sp.G == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
+    if (p.hist == nullptr && threadIdx.x == 0 && hq % sp.G == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
   }
 }
 
@@ -873,7 +890,9 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   p.pair_own = p.pair_prefix && sp.P % 2 == 0;
   p.alpha = a.alpha;
   p.eps = a.eps;
-  auto kernel = sp.G == 4 ? shared_decode_kernel<4> : shared_decode_kernel<8>;
+  p.n_surv = a.n_surv;
+  auto kernel = a.sel_scores != nullptr ? (sp.G == 4 ? shared_decode_kernel<4, true> : shared_decode_kernel<8, true>)
+                                        : (sp.G == 4 ? shared_decode_kernel<4, false> : shared_decode_kernel<8, false>);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(sp.ctas())), dim3(kSThreads), static_cast<size_t>(kSSmem),
