@@ -226,10 +226,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
-  pdl_wait_primary();
-  pdl_launch_dependents();
 
-  // Every role walks the CTA's stretches in the same order, and their tiles through the rings
+  // Every role waits for the kernels before this one (pdl_wait_primary) where it first touches
+  // global memory, with its first addresses at hand.  Every role walks the CTA's stretches in the same order, and their tiles through the rings
   // by a running tile count i: stage i % kRing, phase (i / kRing) & 1.  Stretch k's query and
   // output barriers take phase k & 1.
   // where tile t of the walk's stretch lies: the maps, the plane and the row
@@ -251,6 +250,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           const uint32_t ph = ((i / kRing) - 1) & 1;
           int plane, row;
           const CUtensorMap *map = place(t, plane, row) ? &tm_ko : &tm_kp;
+          if (i == 0) pdl_wait_primary();
           if (i >= kRing && !mbar_wait(&sfull[s], ph)) {
             ok = false;
             break;
@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           ok = false;
           break;
         }
+        if (k == 0) pdl_wait_primary();
         mbar_arrive_expect_tx(qfull, kTileB);
         for (int e = 0; e < 4; ++e) {  // a quarter of the rows at a time (block_row)
           const int seq = w.rb * kSeqs + e * (32 / G);
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     if (!ok && lane == 0) give_up(s_abort, p.flags);
     // the counts that the next kernel adds up start at zero
     if constexpr (SCORES) {
+      pdl_wait_primary();
       uint4 *h = reinterpret_cast<uint4 *>(p.hist);
       const int64_t n4 = static_cast<int64_t>(sp.B) * sp.Hkv * (kHistBins / 4);
       for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRows + r; e < n4; e += static_cast<int64_t>(gridDim.x) * kRows)
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int odd = G == 8 ? (lane >> 2) & 1 : 0;
     int i = 0;
     bool ok = true;
+    pdl_wait_primary();
+    pdl_launch_dependents();
     for (int k = 0; ok && w.next(); ++k) {
       ok = !*s_abort && mbar_wait(qfull, k & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -714,9 +718,9 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
   __syncthreads();
 }
 
-// One launch, two kinds of CTA: the first hist_ctas count the selection's bins of a part of a
-// unit's scores; the others finish one query head's output each from its records.
-__global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishParams p) {
+// One launch, two kinds of CTA: the first hist_ctas count the survivors and the selection's bins of
+// a part of a unit's scores; the others finish two query heads' outputs each from their records.
+__global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const FinishParams p) {
   __shared__ __align__(16) uint32_t s_mem[kHistBins];
   const SharedSplit &sp = p.sp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -732,7 +736,9 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     int live = 0;
     auto count = [&](float x) {
       live += x > 0.0f ? 1 : 0;
-      atomicAdd(&s_mem[order_key(x) >> 21], 1u);
+      // order_key(x) >> 21: the top bits of a positive score, the inverted ones of a negative
+      const int t = __float_as_int(x + 0.0f) >> 21;  // (-0 counts as 0)
+      atomicAdd(&s_mem[t >= 0 ? t + kHistBins / 2 : ~t], 1u);
     };
     if (p.hist_vec) {
       const float4 *s4 = reinterpret_cast<const float4 *>(su);
@@ -758,13 +764,12 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
       if (s_mem[k] != 0u) atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
     return;
   }
-  pdl_wait_primary();  // the records are complete
-  pdl_launch_dependents();
-  const int row = static_cast<int>(blockIdx.x) - p.hist_ctas;
+  // two query heads' outputs: rows row, row + 1 of one sequence and KV head
+  const int row = (static_cast<int>(blockIdx.x) - p.hist_ctas) * 2 + (warp & 1);
   const int Hq = sp.G * sp.Hkv;
-  const int b = row / Hq, hq = row % Hq, g = hq / sp.G;
+  const int b = row / Hq, hq = row - b * Hq, g = hq / sp.G;
   const int seqs = kRows / sp.G;
-  const int rb = b / seqs, seq = b % seqs, h = hq % sp.G;
+  const int rb = b / seqs, seq = b - rb * seqs, h = hq - g * sp.G;
   const int r = sp.G == 4 ? block_row<4>(seq, h) : block_row<8>(seq, h);
   // the pieces whose record holds this row: those with prefix tiles of this KV head, then
   // those with own tiles of this sequence
@@ -782,16 +787,18 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     if (qc <= qb) qc = qb + 1;
   }
   const int n1 = qb - qa + 1, nrec = n1 + (qd >= qc ? qd - qc + 1 : 0);
-  auto record = [&](int i) {
-    return p.rec + sp.slot(rb, i < n1 ? qa + i : qc + (i - n1), g) * kRecWords;
-  };
-  // each warp adds every eighth record, lane l dims 4l .. 4l + 3; then the warps in order
+  const float *first = p.rec + sp.slot(rb, qa, g) * kRecWords;
+  const int64_t gap = static_cast<int64_t>(qc - qa - n1) * kRecWords;  // past the prefix's records
+  pdl_wait_primary();  // the records are complete
+  pdl_launch_dependents();
+  // four warps a row, each adds every fourth record, lane l dims 4l .. 4l + 3; then the warps
+  // in order
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float den = 0.0f;
   int live = 0;
 #pragma unroll 4
-  for (int i = warp; i < nrec; i += kFWarps) {
-    const float *rec = record(i);
+  for (int i = warp >> 1; i < nrec; i += kFWarps / 2) {
+    const float *rec = first + static_cast<int64_t>(i) * kRecWords + (i < n1 ? 0 : gap);
     const float4 x = *reinterpret_cast<const float4 *>(rec + r * kHeadDim + 4 * lane);
     acc.x += x.x;
     acc.y += x.y;
@@ -802,7 +809,7 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
       if (p.hist == nullptr) live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
     }
   }
-  float *s_acc = reinterpret_cast<float *>(s_mem);            // [8 warps][128]
+  float *s_acc = reinterpret_cast<float *>(s_mem);                 // [8 warps][128]
   float *s_den = s_acc + kFWarps * kHeadDim;                       // [8][kParts]
   int *s_live = reinterpret_cast<int *>(s_den + kParts * kFWarps);  // [8][kParts]
   *reinterpret_cast<float4 *>(s_acc + warp * kHeadDim + 4 * lane) = acc;
@@ -811,31 +818,37 @@ __global__ void __launch_bounds__(kFThreads) shared_finish_kernel(const FinishPa
     s_live[warp * kParts + lane] = live;
   }
   __syncthreads();
+  // thread: dimension tid % 128 of the first (tid < 128) or the second row
+  const int mine = threadIdx.x / kHeadDim, d = threadIdx.x % kHeadDim;
   float num = 0.0f, dsum = 0.0f;
   int nlive = 0;
-  if (threadIdx.x < kHeadDim) {
 #pragma unroll
-    for (int k = 0; k < kFWarps; ++k) num += s_acc[k * kHeadDim + threadIdx.x];
+  for (int k = 0; k < kFWarps / 2; ++k) {
+    num += s_acc[(2 * k + mine) * kHeadDim + d];
 #pragma unroll
-    for (int k = 0; k < kParts * kFWarps; ++k) {
-      dsum += s_den[k];
-      nlive += s_live[k];
+    for (int e = 0; e < kParts; ++e) {
+      dsum += s_den[(2 * k + mine) * kParts + e];
+      nlive += s_live[(2 * k + mine) * kParts + e];
     }
   }
   num *= kWeightScale;
   dsum *= kWeightScale;
+  const int row0 = (static_cast<int>(blockIdx.x) - p.hist_ctas) * 2;
   const bool bad = !(fabsf(num) <= 3.402823466e38f);
   if (__syncthreads_or(bad)) {
     float *s_sum = reinterpret_cast<float *>(s_mem);  // [129]
-    row_term_by_term(p, b, hq, s_sum + 256, s_sum + 512, s_sum);
-    num = s_sum[threadIdx.x < kHeadDim ? threadIdx.x : 0];
-    dsum = s_sum[kHeadDim];
+    for (int k = 0; k < 2; ++k) {
+      row_term_by_term(p, b, row0 + k - b * Hq, s_sum + 256, s_sum + 512, s_sum);
+      if (mine == k) {
+        num = s_sum[d];
+        dsum = s_sum[kHeadDim];
+      }
+      __syncthreads();
+    }
   }
-  if (threadIdx.x < kHeadDim) {
-    const float z = p.c / p.alpha / p.alpha + dsum;
-    p.out[static_cast<int64_t>(row) * kHeadDim + threadIdx.x] = z != 0.0f ? num / z : 0.0f;
-    if (p.hist == nullptr && threadIdx.x == 0 && hq % sp.G == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
-  }
+  const float z = p.c / p.alpha / p.alpha + dsum;
+  p.out[static_cast<int64_t>(row0 + mine) * kHeadDim + d] = z != 0.0f ? num / z : 0.0f;
+  if (p.hist == nullptr && threadIdx.x == 0 && h == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
 }
 
 }  // namespace
@@ -912,12 +925,12 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.hist = a.sel_hist;
   f.score_stride = a.score_stride;
   const int64_t units = static_cast<int64_t>(sp.B) * sp.Hkv;
-  // scores per histogram CTA: six CTAs to an SM, 2,048 to 16,384 scores each
-  const int64_t N = sp.P + sp.n, share = (units * N / (6 * a.sm_count) + 1023) / 1024 * 1024;
-  f.hist_keys = static_cast<int32_t>(share < 2048 ? 2048 : share > 16384 ? 16384 : share);
+  // scores per histogram CTA: four CTAs to an SM, 2,048 scores each at least
+  const int64_t N = sp.P + sp.n, share = (units * N / (4 * a.sm_count) + 1023) / 1024 * 1024;
+  f.hist_keys = static_cast<int32_t>(share < 2048 ? 2048 : share < N ? share : N);
   f.hist_splits = static_cast<int32_t>((N + f.hist_keys - 1) / f.hist_keys);
   const int64_t hist_ctas = a.sel_hist != nullptr ? units * f.hist_splits : 0;
-  if (hist_ctas + units * sp.G > INT32_MAX) return cudaErrorInvalidValue;
+  if (hist_ctas + units * sp.G / 2 > INT32_MAX) return cudaErrorInvalidValue;
   f.hist_ctas = static_cast<int32_t>(hist_ctas);
   f.hist_vec = a.score_stride % 4 == 0;
   f.out = a.out;
@@ -925,7 +938,7 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.alpha = a.alpha;
   f.c = a.c;
   f.eps = a.eps;
-  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(f.hist_ctas + units * sp.G)), dim3(kFThreads),
+  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(f.hist_ctas + units * sp.G / 2)), dim3(kFThreads),
                     0, stream, 0u, f);
 }
 
