@@ -168,6 +168,15 @@ __device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *m
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d_hint(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                                 int32_t x, int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
 // 16-byte asynchronous copy global -> shared through the load pipeline (not the TMA
 // unit): cheap to issue from every lane, waited for with cp_async_wait_all.
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
@@ -270,6 +279,12 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 
@@ -564,7 +579,7 @@ __device__ __forceinline__ float row_square_sum(const uint8_t *tile, int box_byt
   float a[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) a[i] = 0.0f;
-#pragma unroll
+#pragma unroll 2
   for (int c = 0; c < 8; ++c) {
     const int pc = (c ^ turn) * 16;
     const uint4 x0 = *reinterpret_cast<const uint4 *>(tile + r * 128 + pc);

@@ -84,6 +84,7 @@ struct SharedParams {
   uint32_t *hist;          // [B, Hkv, 2048], zeroed here, and so are the survivor counts (with scores)
   int32_t *n_surv;
   int64_t score_stride;
+  int32_t first_round;     // -1 (the epilogue's empty round)
   int32_t groups;          // epilogue groups, 1 or 2: two take alternate tiles
   int32_t pair_prefix, pair_own;  // score rows of prefix / own tiles start on 8 bytes
   float alpha, eps;
@@ -239,25 +240,29 @@ __global__ void __launch_bounds__(kSThreads, 1)
     plane = own ? (w.rb * kSeqs + x / ts) * sp.Hkv + w.g : w.g;
     return own;
   };
+  // L2: rows that one CTA reads go first; the prefix's stay for the other row blocks, if any
+  const uint64_t once = policy_evict_first(), shared = sp.blocks > 1 ? policy_evict_normal() : once;
   if (warp == 0) {
     // ------------------------------------------------------------------ K producer
     if (lane == 0) {
       int i = 0;
       bool ok = true;
       while (ok && w.next()) {
+#pragma unroll 1
         for (int t = w.t0; t < w.t1; ++t, ++i) {
           const int s = i % kRing;
           const uint32_t ph = ((i / kRing) - 1) & 1;
           int plane, row;
-          const CUtensorMap *map = place(t, plane, row) ? &tm_ko : &tm_kp;
+          const bool own = place(t, plane, row);
+          const CUtensorMap *map = own ? &tm_ko : &tm_kp;
           if (i == 0) pdl_wait_primary();
           if (i >= kRing && !mbar_wait(&sfull[s], ph)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&kfull[s], kTileB);
-          tma_load_3d(sK + s * kTileB, map, &kfull[s], 0, row, plane);
-          tma_load_3d(sK + s * kTileB + kBox, map, &kfull[s], 64, row, plane);
+          tma_load_3d_hint(sK + s * kTileB, map, &kfull[s], 0, row, plane, own ? once : shared);
+          tma_load_3d_hint(sK + s * kTileB + kBox, map, &kfull[s], 64, row, plane, own ? once : shared);
           *s_kissued = i + 1;
         }
       }
@@ -276,23 +281,26 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
         if (k == 0) pdl_wait_primary();
         mbar_arrive_expect_tx(qfull, kTileB);
+#pragma unroll 1
         for (int e = 0; e < 4; ++e) {  // a quarter of the rows at a time (block_row)
           const int seq = w.rb * kSeqs + e * (32 / G);
           tma_load_5d(sQ + e * 4096, &tm_q, qfull, 0, 0, seq, 0, w.g);
           tma_load_5d(sQ + kBox + e * 4096, &tm_q, qfull, 64, 0, seq, 0, w.g);
         }
         *s_qissued = k + 1;
+#pragma unroll 1
         for (int t = w.t0; t < w.t1; ++t, ++i) {
           const int s = i % kRing;
           int plane, row;
-          const CUtensorMap *map = place(t, plane, row) ? &tm_vo : &tm_vp;
+          const bool own = place(t, plane, row);
+          const CUtensorMap *map = own ? &tm_vo : &tm_vp;
           if (i >= kRing && !mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&vfull[s], kTileB);
-          tma_load_3d(sV + s * kTileB, map, &vfull[s], 0, row, plane);
-          tma_load_3d(sV + s * kTileB + kBox, map, &vfull[s], 64, row, plane);
+          tma_load_3d_hint(sV + s * kTileB, map, &vfull[s], 0, row, plane, own ? once : shared);
+          tma_load_3d_hint(sV + s * kTileB + kBox, map, &vfull[s], 64, row, plane, own ? once : shared);
           *s_vissued = i + 1;
         }
       }
@@ -308,6 +316,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     bool ok = true;
     for (int k = 0; ok && w.next(); ++k) {
       ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(qfull, k & 1));
+#pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
         ok = mbar_wait(&kfull[s], (i / kRing) & 1) &&
@@ -338,6 +347,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     bool ok = true;
     for (int k = 0; ok && w.next(); ++k) {
       ok = __all_sync(0xffffffffu, !*s_abort && (k == 0 || mbar_wait(ofree, (k - 1) & 1)));
+#pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
         ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[s], (i / kRing) & 1);
@@ -373,6 +383,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     int i = 0;
     bool ok = true;
     while (ok && w.next()) {
+#pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
         ok = mbar_wait(&kfull[s], (i / kRing) & 1);
@@ -393,8 +404,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
       pdl_wait_primary();
       uint4 *h = reinterpret_cast<uint4 *>(p.hist);
       const int64_t n4 = static_cast<int64_t>(sp.B) * sp.Hkv * (kHistBins / 4);
+#pragma unroll 1
       for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRows + r; e < n4; e += static_cast<int64_t>(gridDim.x) * kRows)
         h[e] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
       for (int64_t e = static_cast<int64_t>(blockIdx.x) * kRows + r; e < static_cast<int64_t>(sp.B) * sp.Hkv;
            e += static_cast<int64_t>(gridDim.x) * kRows)
         p.n_surv[e] = 0;
@@ -416,14 +429,25 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int odd = G == 8 ? (lane >> 2) & 1 : 0;
     int i = 0;
     bool ok = true;
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    for (int k = 0; ok && w.next(); ++k) {
+    // Round -1 walks the code that ends a stretch without a stretch, before there is anything to
+    // do: that code runs once per CTA, and fetching it then, at the end, took about 2 us.
+#pragma unroll 1
+    for (int k = p.first_round; ok; ++k) {
+      const bool real = k >= 0;
+      float rq[4], den[4][2];
+      int live = 0;  // keys of this thread's share with a group maximum above zero
+#pragma unroll
+      for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
+      if (real) {
+      if (k == 0) {
+        pdl_wait_primary();
+        pdl_launch_dependents();
+      }
+      if (!w.next()) break;
       ok = !*s_abort && mbar_wait(qfull, k & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // 1 / rms of the thread's four rows: each lane takes one of its four lanes' rows
-      float rq[4];
       {
         const float ss = row_square_sum(sQ, kBox, quarter * 32 + (lane >> 2) + 8 * q4, (lane & 3) * 2 + ((lane >> 2) & 1));
         const float mine = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
@@ -440,10 +464,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
       float *scores = SCORES && valid ? p.sel + (static_cast<int64_t>(w.rb * kSeqs + seq) * sp.Hkv + w.g) *
                                                     p.score_stride + 2 * q4 + odd
                                       : nullptr;
-      float den[4][2];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
-      int live = 0;  // keys of this thread's share with a group maximum above zero
       // this group's tiles: every groups-th of the running count
       const int skip = (group - i) & (p.groups - 1);
       for (int t = w.t0 + skip, it = i + skip; t < w.t1; t += p.groups, it += p.groups) {
@@ -570,17 +590,18 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ok = mbar_wait(ofull, k & 1) && !*s_abort;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      }
       tc_fence_after_sync();
       uint32_t o[kPartCols];
       tmem_load_x32(tmem + lane_base + kColO + part_col, o);
       tmem_wait_ld(o);
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ofree);  // the next stretch's P V may overwrite O
+      if (real && lane == 0) mbar_arrive(ofree);  // the next stretch's P V may overwrite O
       // The record: every row when the stretch holds prefix tiles, else the rows of the
       // sequences whose tiles it holds.
-      const int first_seq = w.t0 < tp ? 0 : (w.t0 - tp) / ts;
-      const int last_seq = w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
+      const int first_seq = !real ? kSeqs : w.t0 < tp ? 0 : (w.t0 - tp) / ts;
+      const int last_seq = !real ? -1 : w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
       // its four rows' weight sums and (without scores) its sequence's count, over the lanes that
       // share them
       if constexpr (!SCORES) {
@@ -624,6 +645,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int qi = *s_qissued;
     if (qi > 0) mbar_wait(qfull, (qi - 1) & 1);
     const int nk = *s_kissued, nv = *s_vissued;
+#pragma unroll 1
     for (int s = 0; s < kRing; ++s) {
       int uses = nk > s ? (nk - 1 - s) / kRing + 1 : 0;
       if (uses) mbar_wait(&kfull[s], (uses - 1) & 1);
@@ -653,6 +675,7 @@ struct FinishParams {
   int64_t score_stride;
   int32_t hist_ctas, hist_splits;  // CTAs of the histogram part; per (sequence, KV head)
   int32_t hist_keys;               // scores a histogram CTA counts
+  int32_t rows;                    // query heads a finishing CTA takes: 1 or 2
   int32_t hist_vec;                // score rows start on 16 bytes
   float *out;
   int32_t *n_surv;
@@ -671,6 +694,7 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
     s_q[tid] = __uint_as_float(static_cast<uint32_t>(p.q[(static_cast<int64_t>(b) * sp.G * sp.Hkv + hq) * kHeadDim + tid]) << 16);
   __syncthreads();
   float qs = 0.0f;
+#pragma unroll 1
   for (int d = 0; d < kHeadDim; ++d) qs = fmaf(s_q[d], s_q[d], qs);
   const float rq = rsqrtf(qs * (1.0f / kHeadDim) + p.eps);
   const int64_t N = sp.P + sp.n;
@@ -683,6 +707,7 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
       const uint16_t *kr = j < sp.P ? p.kp + (g * p.prefix_stride + j) * kHeadDim
                                     : p.ko + (unit * p.cache_stride + j - sp.P) * kHeadDim;
       float dot = 0.0f, k0 = 0.0f, k1 = 0.0f;
+#pragma unroll 2
       for (int d = 0; d < kHeadDim; d += 2) {
         const uint32_t x = *reinterpret_cast<const uint32_t *>(kr + d);
         dot = fmaf(s_q[d], bf16lo(x), dot);
@@ -697,6 +722,7 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
     if (tid < kHeadDim) {
       float a = 0.0f, z = 0.0f;
       const int m = N - j0 < kFThreads ? static_cast<int>(N - j0) : kFThreads;
+#pragma unroll 1
       for (int i = 0; i < m; ++i) {
         const float wi = s_w[i];
         if (wi == 0.0f) continue;
@@ -720,11 +746,12 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
 
 // One launch, two kinds of CTA: the first hist_ctas count the survivors and the selection's bins of
 // a part of a unit's scores; the others finish two query heads' outputs each from their records.
-__global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const FinishParams p) {
+__global__ void __launch_bounds__(kFThreads, 4) shared_finish_kernel(const FinishParams p) {
   __shared__ __align__(16) uint32_t s_mem[kHistBins];
   const SharedSplit &sp = p.sp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) < p.hist_ctas) {
+#pragma unroll 1
     for (int e = threadIdx.x; e < kHistBins; e += kFThreads) s_mem[e] = 0u;
     __syncthreads();
     pdl_wait_primary();  // the scores are complete
@@ -744,6 +771,7 @@ __global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const Finis
       const float4 *s4 = reinterpret_cast<const float4 *>(su);
       constexpr int kLoads = 4;  // in flight per thread
       const int m4 = m / 4;
+#pragma unroll 1
       for (int e = threadIdx.x; e < m4; e += kLoads * kFThreads) {
         float4 x[kLoads];
 #pragma unroll
@@ -755,17 +783,21 @@ __global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const Finis
       }
       if (static_cast<int>(threadIdx.x) < m % 4) count(su[m4 * 4 + threadIdx.x]);
     } else {
+#pragma unroll 2
       for (int e = threadIdx.x; e < m; e += kFThreads) count(su[e]);
     }
     live = __reduce_add_sync(0xffffffffu, live);
     if (lane == 0 && live != 0) atomicAdd(&p.n_surv[u], live);
     __syncthreads();
+#pragma unroll 2
     for (int k = threadIdx.x; k < kHistBins; k += kFThreads)
       if (s_mem[k] != 0u) atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
     return;
   }
-  // two query heads' outputs: rows row, row + 1 of one sequence and KV head
-  const int row = (static_cast<int>(blockIdx.x) - p.hist_ctas) * 2 + (warp & 1);
+  // one or two query heads' outputs: rows row0 (and row0 + 1, of the same KV head), each by
+  // `slices` of the CTA's warps
+  const int rows = p.rows, slices = kFWarps / rows;
+  const int row0 = (static_cast<int>(blockIdx.x) - p.hist_ctas) * rows, row = row0 + warp % rows;
   const int Hq = sp.G * sp.Hkv;
   const int b = row / Hq, hq = row - b * Hq, g = hq / sp.G;
   const int seqs = kRows / sp.G;
@@ -791,22 +823,36 @@ __global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const Finis
   const int64_t gap = static_cast<int64_t>(qc - qa - n1) * kRecWords;  // past the prefix's records
   pdl_wait_primary();  // the records are complete
   pdl_launch_dependents();
-  // four warps a row, each adds every fourth record, lane l dims 4l .. 4l + 3; then the warps
-  // in order
+  // each warp adds every slices-th record, lane l dims 4l .. 4l + 3; then the warps in order
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float den = 0.0f;
   int live = 0;
-#pragma unroll 4
-  for (int i = warp >> 1; i < nrec; i += kFWarps / 2) {
-    const float *rec = first + static_cast<int64_t>(i) * kRecWords + (i < n1 ? 0 : gap);
-    const float4 x = *reinterpret_cast<const float4 *>(rec + r * kHeadDim + 4 * lane);
-    acc.x += x.x;
-    acc.y += x.y;
-    acc.z += x.z;
-    acc.w += x.w;
-    if (lane < kParts) {
-      den += rec[kRecNum + lane * kRows + r];
-      if (p.hist == nullptr) live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
+  constexpr int kBatch = 8;  // records in flight per warp
+#pragma unroll 1
+  for (int i0 = warp / rows; i0 < nrec; i0 += kBatch * slices) {
+    float4 x[kBatch];
+    float xd[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int i = i0 + e * slices;
+      x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      xd[e] = 0.0f;
+      if (i < nrec) {
+        const float *rec = first + static_cast<int64_t>(i) * kRecWords + (i < n1 ? 0 : gap);
+        x[e] = *reinterpret_cast<const float4 *>(rec + r * kHeadDim + 4 * lane);
+        if (lane < kParts) {
+          xd[e] = rec[kRecNum + lane * kRows + r];
+          if (p.hist == nullptr) live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      acc.x += x[e].x;
+      acc.y += x[e].y;
+      acc.z += x[e].z;
+      acc.w += x[e].w;
+      den += xd[e];
     }
   }
   float *s_acc = reinterpret_cast<float *>(s_mem);                 // [8 warps][128]
@@ -820,24 +866,27 @@ __global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const Finis
   __syncthreads();
   // thread: dimension tid % 128 of the first (tid < 128) or the second row
   const int mine = threadIdx.x / kHeadDim, d = threadIdx.x % kHeadDim;
+  const bool has = mine < rows;
   float num = 0.0f, dsum = 0.0f;
   int nlive = 0;
-#pragma unroll
-  for (int k = 0; k < kFWarps / 2; ++k) {
-    num += s_acc[(2 * k + mine) * kHeadDim + d];
-#pragma unroll
-    for (int e = 0; e < kParts; ++e) {
-      dsum += s_den[(2 * k + mine) * kParts + e];
-      nlive += s_live[(2 * k + mine) * kParts + e];
+  if (has) {
+#pragma unroll 1
+    for (int k = mine; k < kFWarps; k += rows) {
+      num += s_acc[k * kHeadDim + d];
+      const float4 z4 = *reinterpret_cast<const float4 *>(s_den + k * kParts);
+      const int4 l4 = *reinterpret_cast<const int4 *>(s_live + k * kParts);
+      dsum += (z4.x + z4.y) + (z4.z + z4.w);
+      nlive += (l4.x + l4.y) + (l4.z + l4.w);
     }
   }
+  static_assert(kParts == 4, "a warp's sums are one vector");
   num *= kWeightScale;
   dsum *= kWeightScale;
-  const int row0 = (static_cast<int>(blockIdx.x) - p.hist_ctas) * 2;
   const bool bad = !(fabsf(num) <= 3.402823466e38f);
   if (__syncthreads_or(bad)) {
     float *s_sum = reinterpret_cast<float *>(s_mem);  // [129]
-    for (int k = 0; k < 2; ++k) {
+#pragma unroll 1
+    for (int k = 0; k < rows; ++k) {
       row_term_by_term(p, b, row0 + k - b * Hq, s_sum + 256, s_sum + 512, s_sum);
       if (mine == k) {
         num = s_sum[d];
@@ -846,6 +895,7 @@ __global__ void __launch_bounds__(kFThreads, 6) shared_finish_kernel(const Finis
       __syncthreads();
     }
   }
+  if (!has) return;
   const float z = p.c / p.alpha / p.alpha + dsum;
   p.out[static_cast<int64_t>(row0 + mine) * kHeadDim + d] = z != 0.0f ? num / z : 0.0f;
   if (p.hist == nullptr && threadIdx.x == 0 && h == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
@@ -898,6 +948,7 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   p.sel = a.sel_scores;
   p.hist = a.sel_hist;
   p.score_stride = a.score_stride;
+  p.first_round = -1;
   p.groups = EMBLA_GROUPS;
   p.pair_prefix = a.score_stride % 2 == 0;
   p.pair_own = p.pair_prefix && sp.P % 2 == 0;
@@ -930,7 +981,10 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.hist_keys = static_cast<int32_t>(share < 2048 ? 2048 : share < N ? share : N);
   f.hist_splits = static_cast<int32_t>((N + f.hist_keys - 1) / f.hist_keys);
   const int64_t hist_ctas = a.sel_hist != nullptr ? units * f.hist_splits : 0;
-  if (hist_ctas + units * sp.G / 2 > INT32_MAX) return cudaErrorInvalidValue;
+  // two rows per CTA, a row's records over four warps, where that still gives every SM a few CTAs;
+  // eight warps a row for smaller batches (more records in flight)
+  f.rows = units * sp.G >= 4 * static_cast<int64_t>(a.sm_count) ? 2 : 1;
+  if (hist_ctas + units * sp.G / f.rows > INT32_MAX) return cudaErrorInvalidValue;
   f.hist_ctas = static_cast<int32_t>(hist_ctas);
   f.hist_vec = a.score_stride % 4 == 0;
   f.out = a.out;
@@ -938,7 +992,7 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.alpha = a.alpha;
   f.c = a.c;
   f.eps = a.eps;
-  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(f.hist_ctas + units * sp.G / 2)), dim3(kFThreads),
+  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(f.hist_ctas + units * sp.G / f.rows)), dim3(kFThreads),
                     0, stream, 0u, f);
 }
 
