@@ -659,6 +659,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
 constexpr int kFThreads = 256;
 constexpr int kFWarps = kFThreads / 32;
+constexpr int kFCtasPerSm = 4;
+constexpr int kHistStep = 1024;  // a CTA's share of the scores starts at a multiple of this
+constexpr int kItemSteps = 6;    // an item's time in steps
 
 struct FinishParams {
   SharedSplit sp;
@@ -669,10 +672,10 @@ struct FinishParams {
   const float *sel;
   uint32_t *hist;
   int64_t score_stride;
-  int32_t hist_ctas, hist_splits;  // CTAs of the histogram part; per (sequence, KV head)
-  int32_t hist_keys;               // scores a histogram CTA counts
-  int32_t rows;                    // query heads a finishing CTA takes: 1 or 2
+  // padded scores per CTA: hist_few for the first hist_few_first by rank, hist_many for the others
+  int64_t hist_few, hist_many, hist_few_first;
   int32_t hist_vec;                // score rows start on 16 bytes
+  int32_t rows;                    // query heads per item: 1 or 2
   float *out;
   int32_t *n_surv;
   float alpha, c, eps;
@@ -740,22 +743,158 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
   __syncthreads();
 }
 
-// One launch, two kinds of CTA: the first hist_ctas count the survivors and the selection's bins of
-// a part of a unit's scores; the others finish two query heads' outputs each from their records.
-__global__ void __launch_bounds__(kFThreads, 4) shared_finish_kernel(const FinishParams p) {
+// The batch's outputs from the records, then the survivors' counts and the selection's histograms
+// from the scores: one wave of CTAs, each with its share of both.
+__global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(const FinishParams p) {
   __shared__ __align__(16) uint32_t s_mem[kHistBins];
   const SharedSplit &sp = p.sp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (static_cast<int>(blockIdx.x) < p.hist_ctas) {
+  const int Hq = sp.G * sp.Hkv;
+  // An item: one or two query heads' outputs, rows row0 (and row0 + 1, of the same KV head), each
+  // by `slices` of the CTA's warps.  The first round has no records and writes nothing: it
+  // fetches the code while the decode's last CTAs run.
+  const int rows = p.rows, slices = kFWarps / rows, items = sp.B * Hq / rows;
+  // Consecutive CTAs share an SM, so the CTA's rank spreads the items over the SMs.
+  const int rank = static_cast<int>(blockIdx.x % kFCtasPerSm * (gridDim.x / kFCtasPerSm) + blockIdx.x / kFCtasPerSm);
+  int item = rank;
+  bool real = false;
 #pragma unroll 1
-    for (int e = threadIdx.x; e < kHistBins; e += kFThreads) s_mem[e] = 0u;
-    __syncthreads();
-    pdl_wait_primary();  // the scores are complete
-    pdl_launch_dependents();
-    const int64_t u = blockIdx.x / p.hist_splits;
-    const int64_t N = sp.P + sp.n, a = (blockIdx.x % p.hist_splits) * static_cast<int64_t>(p.hist_keys);
-    const int m = static_cast<int>(N - a < p.hist_keys ? N - a : p.hist_keys);
-    const float *su = p.sel + u * p.score_stride + a;
+  while (true) {
+    const int row0 = (item < items ? item : 0) * rows, row = row0 + warp % rows;
+    const int b = row / Hq, hq = row - b * Hq, g = hq / sp.G;
+    const int seqs = kRows / sp.G;
+    const int rb = b / seqs, seq = b - rb * seqs, h = hq - g * sp.G;
+    const int r = sp.G == 4 ? block_row<4>(seq, h) : block_row<8>(seq, h);
+    // the pieces whose record holds this row: those with prefix tiles of this KV head, then
+    // those with own tiles of this sequence
+    const uint32_t gt = static_cast<uint32_t>(sp.group_tiles(rb)), T = gt * sp.Hkv;
+    const uint32_t Q = static_cast<uint32_t>(sp.pieces(rb)), base = g * gt;
+    int qa = 0, qb = -1, qc = 0, qd = -1;
+    if (sp.tp > 0) {
+      qa = static_cast<int>(sp.piece_of_tile(base, T, Q));
+      qb = static_cast<int>(sp.piece_of_tile(base + static_cast<uint32_t>(sp.tp) - 1, T, Q));
+    }
+    if (sp.ts > 0) {
+      const uint32_t own = base + static_cast<uint32_t>(sp.tp + seq * sp.ts);
+      qc = static_cast<int>(sp.piece_of_tile(own, T, Q));
+      qd = static_cast<int>(sp.piece_of_tile(own + static_cast<uint32_t>(sp.ts) - 1, T, Q));
+      if (qc <= qb) qc = qb + 1;
+    }
+    const int n1 = qb - qa + 1, all = n1 + (qd >= qc ? qd - qc + 1 : 0);
+    const float *first = p.rec + sp.slot(rb, qa, g) * kRecWords;
+    const int64_t gap = static_cast<int64_t>(qc - qa - n1) * kRecWords;  // past the prefix's records
+    // (twice for the first item: the round without records, then the item)
+#pragma unroll 1
+    while (true) {
+      const int nrec = real ? all : 0;
+      // each warp adds every slices-th record, lane l dims 4l .. 4l + 3; then the warps in order
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float den = 0.0f;
+      int live = 0;
+      constexpr int kBatch = 8;  // records in flight per warp (past the last: read again, not used)
+      const int part = lane & (kParts - 1);
+#pragma unroll 1
+      for (int i0 = warp / rows; i0 < nrec; i0 += kBatch * slices) {
+        float4 x[kBatch];
+        float xd[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = i0 + e * slices < nrec ? i0 + e * slices : nrec - 1;
+          const float *rec = first + static_cast<int64_t>(i) * kRecWords + (i < n1 ? 0 : gap);
+          x[e] = *reinterpret_cast<const float4 *>(rec + r * kHeadDim + 4 * lane);
+          xd[e] = rec[kRecNum + part * kRows + r];
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          if (i0 + e * slices < nrec) {
+            acc.x += x[e].x;
+            acc.y += x[e].y;
+            acc.z += x[e].z;
+            acc.w += x[e].w;
+            den += xd[e];
+          }
+        }
+      }
+      if (p.hist == nullptr && lane < kParts) {  // the survivors that the decode counted
+        for (int i = warp / rows; i < nrec; i += slices)
+          live += reinterpret_cast<const int32_t *>(first + static_cast<int64_t>(i) * kRecWords +
+                                                    (i < n1 ? 0 : gap))[kRecNum + kRecDen + lane * 32 + seq];
+      }
+      float *s_acc = reinterpret_cast<float *>(s_mem);                 // [8 warps][128]
+      float *s_den = s_acc + kFWarps * kHeadDim;                       // [8][kParts]
+      int *s_live = reinterpret_cast<int *>(s_den + kParts * kFWarps);  // [8][kParts]
+      *reinterpret_cast<float4 *>(s_acc + warp * kHeadDim + 4 * lane) = acc;
+      if (lane < kParts) {
+        s_den[warp * kParts + lane] = den;
+        s_live[warp * kParts + lane] = live;
+      }
+      __syncthreads();
+      // thread: dimension tid % 128 of the first (tid < 128) or the second row
+      const int mine = threadIdx.x / kHeadDim, d = threadIdx.x % kHeadDim;
+      float num = 0.0f, dsum = 0.0f;
+      int nlive = 0;
+      if (mine < rows) {
+#pragma unroll 4
+        for (int k = mine; k < kFWarps; k += rows) {
+          num += s_acc[k * kHeadDim + d];
+          const float4 z4 = *reinterpret_cast<const float4 *>(s_den + k * kParts);
+          const int4 l4 = *reinterpret_cast<const int4 *>(s_live + k * kParts);
+          dsum += (z4.x + z4.y) + (z4.z + z4.w);
+          nlive += (l4.x + l4.y) + (l4.z + l4.w);
+        }
+      }
+      static_assert(kParts == 4, "a warp's sums are one vector");
+      num *= kWeightScale;
+      dsum *= kWeightScale;
+      const bool bad = !(fabsf(num) <= 3.402823466e38f);
+      if (__syncthreads_or(bad)) {
+        float *s_sum = reinterpret_cast<float *>(s_mem);  // [129]
+#pragma unroll 1
+        for (int k = 0; k < rows; ++k) {
+          row_term_by_term(p, b, row0 + k - b * Hq, s_sum + 256, s_sum + 512, s_sum);
+          if (mine == k) {
+            num = s_sum[d];
+            dsum = s_sum[kHeadDim];
+          }
+          __syncthreads();
+        }
+      }
+      const float z = p.c / p.alpha / p.alpha + dsum;
+      if (real && mine < rows) {
+        p.out[static_cast<int64_t>(row0 + mine) * kHeadDim + d] = z != 0.0f ? num / z : 0.0f;
+        if (p.hist == nullptr && threadIdx.x == 0 && h == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
+      }
+      if (real) break;
+      pdl_wait_primary();  // the records and scores are complete
+      pdl_launch_dependents();
+      real = true;
+      if (item >= items) break;
+    }
+    item += static_cast<int>(gridDim.x);
+    if (item >= items) break;
+  }
+  if (p.hist == nullptr) return;
+
+  // The scores of all units one after another, each padded to N4 keys: this CTA's share of them,
+  // counted unit by unit in shared memory.
+  __syncthreads();
+#pragma unroll 1
+  for (int e = threadIdx.x; e < kHistBins; e += kFThreads) s_mem[e] = 0u;
+  const int64_t N = sp.P + sp.n, N4 = (N + kHistStep - 1) / kHistStep * kHistStep;
+  // (CTAs with one more item than others take less of the scores)
+  const int64_t more = p.hist_few_first;
+  int64_t at = rank < more ? rank * p.hist_few : more * p.hist_few + (rank - more) * p.hist_many;
+  const int64_t stop_all = static_cast<int64_t>(sp.B) * sp.Hkv * N4;
+  const int64_t share = rank < more ? p.hist_few : p.hist_many;
+  const int64_t stop = at + share < stop_all ? at + share : stop_all;
+#pragma unroll 1
+  while (at < stop) {
+    const int64_t u = at / N4, j0 = at - u * N4;
+    const int64_t len = N4 - j0 < stop - at ? N4 - j0 : stop - at;
+    const int m = static_cast<int>(len < N - j0 ? len : N - j0);  // keys there are
+    at += len;
+    const float *su = p.sel + u * p.score_stride + j0;
+    __syncthreads();  // the bins are zero
     int live = 0;
     auto count = [&](float x) {
       live += x > 0.0f ? 1 : 0;
@@ -779,7 +918,7 @@ __global__ void __launch_bounds__(kFThreads, 4) shared_finish_kernel(const Finis
       }
       if (static_cast<int>(threadIdx.x) < m % 4) count(su[m4 * 4 + threadIdx.x]);
     } else {
-#pragma unroll 2
+#pragma unroll 4
       for (int e = threadIdx.x; e < m; e += kFThreads) count(su[e]);
     }
     live = __reduce_add_sync(0xffffffffu, live);
@@ -787,114 +926,11 @@ __global__ void __launch_bounds__(kFThreads, 4) shared_finish_kernel(const Finis
     __syncthreads();
 #pragma unroll 2
     for (int k = threadIdx.x; k < kHistBins; k += kFThreads)
-      if (s_mem[k] != 0u) atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
-    return;
-  }
-  // one or two query heads' outputs: rows row0 (and row0 + 1, of the same KV head), each by
-  // `slices` of the CTA's warps
-  const int rows = p.rows, slices = kFWarps / rows;
-  const int row0 = (static_cast<int>(blockIdx.x) - p.hist_ctas) * rows, row = row0 + warp % rows;
-  const int Hq = sp.G * sp.Hkv;
-  const int b = row / Hq, hq = row - b * Hq, g = hq / sp.G;
-  const int seqs = kRows / sp.G;
-  const int rb = b / seqs, seq = b - rb * seqs, h = hq - g * sp.G;
-  const int r = sp.G == 4 ? block_row<4>(seq, h) : block_row<8>(seq, h);
-  // the pieces whose record holds this row: those with prefix tiles of this KV head, then
-  // those with own tiles of this sequence
-  const uint32_t gt = static_cast<uint32_t>(sp.group_tiles(rb)), T = gt * sp.Hkv;
-  const uint32_t Q = static_cast<uint32_t>(sp.pieces(rb)), base = g * gt;
-  int qa = 0, qb = -1, qc = 0, qd = -1;
-  if (sp.tp > 0) {
-    qa = static_cast<int>(sp.piece_of_tile(base, T, Q));
-    qb = static_cast<int>(sp.piece_of_tile(base + static_cast<uint32_t>(sp.tp) - 1, T, Q));
-  }
-  if (sp.ts > 0) {
-    const uint32_t own = base + static_cast<uint32_t>(sp.tp + seq * sp.ts);
-    qc = static_cast<int>(sp.piece_of_tile(own, T, Q));
-    qd = static_cast<int>(sp.piece_of_tile(own + static_cast<uint32_t>(sp.ts) - 1, T, Q));
-    if (qc <= qb) qc = qb + 1;
-  }
-  const int n1 = qb - qa + 1, nrec = n1 + (qd >= qc ? qd - qc + 1 : 0);
-  const float *first = p.rec + sp.slot(rb, qa, g) * kRecWords;
-  const int64_t gap = static_cast<int64_t>(qc - qa - n1) * kRecWords;  // past the prefix's records
-  pdl_wait_primary();  // the records are complete
-  pdl_launch_dependents();
-  // each warp adds every slices-th record, lane l dims 4l .. 4l + 3; then the warps in order
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float den = 0.0f;
-  int live = 0;
-  constexpr int kBatch = 8;  // records in flight per warp
-#pragma unroll 1
-  for (int i0 = warp / rows; i0 < nrec; i0 += kBatch * slices) {
-    float4 x[kBatch];
-    float xd[kBatch];
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      const int i = i0 + e * slices;
-      x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      xd[e] = 0.0f;
-      if (i < nrec) {
-        const float *rec = first + static_cast<int64_t>(i) * kRecWords + (i < n1 ? 0 : gap);
-        x[e] = *reinterpret_cast<const float4 *>(rec + r * kHeadDim + 4 * lane);
-        if (lane < kParts) {
-          xd[e] = rec[kRecNum + lane * kRows + r];
-          if (p.hist == nullptr) live += reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane * 32 + seq];
-        }
+      if (s_mem[k] != 0u) {
+        atomicAdd(&p.hist[u * kHistBins + k], s_mem[k]);
+        s_mem[k] = 0u;
       }
-    }
-#pragma unroll
-    for (int e = 0; e < kBatch; ++e) {
-      acc.x += x[e].x;
-      acc.y += x[e].y;
-      acc.z += x[e].z;
-      acc.w += x[e].w;
-      den += xd[e];
-    }
   }
-  float *s_acc = reinterpret_cast<float *>(s_mem);                 // [8 warps][128]
-  float *s_den = s_acc + kFWarps * kHeadDim;                       // [8][kParts]
-  int *s_live = reinterpret_cast<int *>(s_den + kParts * kFWarps);  // [8][kParts]
-  *reinterpret_cast<float4 *>(s_acc + warp * kHeadDim + 4 * lane) = acc;
-  if (lane < kParts) {
-    s_den[warp * kParts + lane] = den;
-    s_live[warp * kParts + lane] = live;
-  }
-  __syncthreads();
-  // thread: dimension tid % 128 of the first (tid < 128) or the second row
-  const int mine = threadIdx.x / kHeadDim, d = threadIdx.x % kHeadDim;
-  const bool has = mine < rows;
-  float num = 0.0f, dsum = 0.0f;
-  int nlive = 0;
-  if (has) {
-#pragma unroll 1
-    for (int k = mine; k < kFWarps; k += rows) {
-      num += s_acc[k * kHeadDim + d];
-      const float4 z4 = *reinterpret_cast<const float4 *>(s_den + k * kParts);
-      const int4 l4 = *reinterpret_cast<const int4 *>(s_live + k * kParts);
-      dsum += (z4.x + z4.y) + (z4.z + z4.w);
-      nlive += (l4.x + l4.y) + (l4.z + l4.w);
-    }
-  }
-  static_assert(kParts == 4, "a warp's sums are one vector");
-  num *= kWeightScale;
-  dsum *= kWeightScale;
-  const bool bad = !(fabsf(num) <= 3.402823466e38f);
-  if (__syncthreads_or(bad)) {
-    float *s_sum = reinterpret_cast<float *>(s_mem);  // [129]
-#pragma unroll 1
-    for (int k = 0; k < rows; ++k) {
-      row_term_by_term(p, b, row0 + k - b * Hq, s_sum + 256, s_sum + 512, s_sum);
-      if (mine == k) {
-        num = s_sum[d];
-        dsum = s_sum[kHeadDim];
-      }
-      __syncthreads();
-    }
-  }
-  if (!has) return;
-  const float z = p.c / p.alpha / p.alpha + dsum;
-  p.out[static_cast<int64_t>(row0 + mine) * kHeadDim + d] = z != 0.0f ? num / z : 0.0f;
-  if (p.hist == nullptr && threadIdx.x == 0 && h == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
 }
 
 }  // namespace
@@ -971,24 +1007,28 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.hist = a.sel_hist;
   f.score_stride = a.score_stride;
   const int64_t units = static_cast<int64_t>(sp.B) * sp.Hkv;
-  // scores per histogram CTA: four CTAs to an SM, 2,048 scores each at least
-  const int64_t N = sp.P + sp.n, share = (units * N / (4 * a.sm_count) + 1023) / 1024 * 1024;
-  f.hist_keys = static_cast<int32_t>(share < 2048 ? 2048 : share < N ? share : N);
-  f.hist_splits = static_cast<int32_t>((N + f.hist_keys - 1) / f.hist_keys);
-  const int64_t hist_ctas = a.sel_hist != nullptr ? units * f.hist_splits : 0;
-  // two rows per CTA, a row's records over four warps, where that still gives every SM a few CTAs;
-  // eight warps a row for smaller batches (more records in flight)
+  // two rows per item, a row's records over four warps, where that still gives every SM a few
+  // items; eight warps a row for smaller batches (more records in flight)
   f.rows = units * sp.G >= 4 * static_cast<int64_t>(a.sm_count) ? 2 : 1;
-  if (hist_ctas + units * sp.G / f.rows > INT32_MAX) return cudaErrorInvalidValue;
-  f.hist_ctas = static_cast<int32_t>(hist_ctas);
+  // one wave of CTAs at most: a second one would find the first's caches cold again
+  const int64_t N4 = (sp.P + sp.n + kHistStep - 1) / kHistStep * kHistStep;
+  const int64_t items = units * sp.G / f.rows, steps = a.sel_hist != nullptr ? units * (N4 / kHistStep) : 0;
+  const int64_t most = static_cast<int64_t>(kFCtasPerSm) * a.sm_count, want = items > steps ? items : steps;
+  const int64_t ctas = ((want < most ? want : most) + kFCtasPerSm - 1) / kFCtasPerSm * kFCtasPerSm;
+  // an item takes about as long as kItemSteps steps of scores: the CTAs that have one more item
+  // than the others have that much less to count
+  f.hist_few_first = items % ctas;
+  const int64_t even = (steps + f.hist_few_first * kItemSteps + ctas - 1) / ctas;
+  const int64_t few = even > kItemSteps ? even - kItemSteps : 0;
+  f.hist_few = few * kHistStep;
+  f.hist_many = (steps - f.hist_few_first * few + ctas - f.hist_few_first - 1) / (ctas - f.hist_few_first) * kHistStep;
   f.hist_vec = a.score_stride % 4 == 0;
   f.out = a.out;
   f.n_surv = a.n_surv;
   f.alpha = a.alpha;
   f.c = a.c;
   f.eps = a.eps;
-  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(f.hist_ctas + units * sp.G / f.rows)), dim3(kFThreads),
-                    0, stream, 0u, f);
+  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kFThreads), 0, stream, 0u, f);
 }
 
 }  // namespace embla
