@@ -680,7 +680,8 @@ embla_status embla_full_decode_shared(const embla_shape *shape, int64_t prefix_l
     return EMBLA_ERR_INVALID_ARG;
   // TMA plane coordinates and the second kernel's grid are 32-bit
   if (units * G > INT32_MAX / 2) return EMBLA_ERR_UNSUPPORTED;
-  const int sms = sm_count_of(current_device());
+  const int dev = current_device();
+  const int sms = sm_count_of(dev);  // 0 past kMaxDevices
   if (sms <= 0) return EMBLA_ERR_CUDA;
   const SharedSplit sp = shared_split(shape->batch, shape->n_kv_heads, G, prefix_len, n, sms);
   if (!sp.fits()) return EMBLA_ERR_UNSUPPORTED;
@@ -738,6 +739,8 @@ embla_status embla_full_decode_shared(const embla_shape *shape, int64_t prefix_l
   a.alpha = alpha;
   a.c = c;
   a.eps = eps;
+  a.group = G;
+  a.device = dev;
   a.sm_count = sms;
   return cuda_status(launch_shared_decode(a, sp, s));
 }

@@ -233,7 +233,8 @@ struct SharedCall {
   int32_t *n_surv;
   uint32_t *flags;
   float alpha, c, eps;
-  int sm_count;
+  int group;             // query heads per KV head
+  int device, sm_count;  // the current device (below 64)
 };
 cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cudaStream_t stream);
 

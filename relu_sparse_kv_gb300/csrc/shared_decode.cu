@@ -30,6 +30,7 @@
 // that those are heads of one sequence: the group maximum that the selection ranks is taken
 // within a thread (over lanes it cost two and a half instructions per score on the pipe that
 // bound the epilogue).
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -972,6 +973,19 @@ size_t shared_workspace_bytes(const SharedSplit &sp) {
   return static_cast<size_t>(sp.slot(sp.blocks, 0, 0)) * kRecWords * 4 + 16;
 }
 
+// The kernel's shared-memory limit is a setting of the device's context: made by the first call
+// on a device (or by several at once, to the same value).
+template <class Kernel>
+cudaError_t allow_smem_once(const SharedCall &a, Kernel kernel) {
+  static std::atomic<uint64_t> done[4];  // by kernel: head groups x scores; a bit per device
+  const int which = (a.group == 8 ? 2 : 0) + (a.sel_scores != nullptr ? 1 : 0);
+  const uint64_t bit = uint64_t{1} << a.device;
+  if (done[which].load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmem);
+  if (e == cudaSuccess) done[which].fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cudaStream_t stream) {
   SharedParams p;
   p.sp = sp;
@@ -988,7 +1002,7 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   p.n_surv = a.n_surv;
   auto kernel = a.sel_scores != nullptr ? (sp.G == 4 ? shared_decode_kernel<4, true> : shared_decode_kernel<8, true>)
                                         : (sp.G == 4 ? shared_decode_kernel<4, false> : shared_decode_kernel<8, false>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSSmem);
+  cudaError_t e = allow_smem_once(a, kernel);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(static_cast<unsigned>(sp.ctas())), dim3(kSThreads), static_cast<size_t>(kSSmem),
                  stream, 0u, *a.tm_q, *a.tm_kp, *a.tm_vp, *a.tm_ko, *a.tm_vo, p);

@@ -530,8 +530,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(W * 32, W <= kSpWar
     // P enters the product as two bf16 parts (hi + lo, about 16 bits), so the weights the
     // values are summed with are the ones l sums
     const uint32_t ph0 = pack_bf16x2(pz[0], pz[1]), ph1 = pack_bf16x2(pz[2], pz[3]);
-    const uint32_t pl0 = pack_bf16x2(pz[0] - bf16lo(ph0), pz[1] - bf16hi(ph0));
-    const uint32_t pl1 = pack_bf16x2(pz[2] - bf16lo(ph1), pz[3] - bf16hi(ph1));
+    const float pr[4] = {pz[0] - bf16lo(ph0), pz[1] - bf16hi(ph0), pz[2] - bf16lo(ph1), pz[3] - bf16hi(ph1)};
+    const uint32_t pl0 = pack_bf16x2(pr[0], pr[1]), pl1 = pack_bf16x2(pr[2], pr[3]);
+    // behind a shared prefix a third part, all 24 bits (hi + lo alone leave 1.8e-6 of the output)
+    uint32_t pm0 = 0u, pm1 = 0u;
+    if constexpr (SHARED) {
+      pm0 = pack_bf16x2(pr[0] - bf16lo(pl0), pr[1] - bf16hi(pl0));
+      pm1 = pack_bf16x2(pr[2] - bf16lo(pl1), pr[3] - bf16hi(pl1));
+    }
     {
       const int mat = lane >> 3, mr = lane & 7;
       const int row = (mat >> 1) * 8 + mr;  // matrices: rows 0-7 / 8-15 x dims +0 / +8
@@ -547,6 +553,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(W * 32, W <= kSpWar
         // a2 dims g / rows 8-15, a3 dims g+8 / rows 8-15
         mma_16816_bf16(o[i], av[0], av[1], av[2], av[3], ph0, ph1);
         mma_16816_bf16(o[i], av[0], av[1], av[2], av[3], pl0, pl1);
+        if constexpr (SHARED) mma_16816_bf16(o[i], av[0], av[1], av[2], av[3], pm0, pm1);
       }
     }
     __syncwarp();  // the stage is read before the next block's copies land in it

@@ -338,8 +338,9 @@ def test_sparse_shared_matches_the_definition(B, Hkv, G, P, n, stride, counts):
     assert ((out.double() - ref).abs() <= tol).all()
 
 
-def test_sparse_shared_equals_the_call_on_whole_caches():
-    """Bit for bit the result of embla_sparse_decode on the contexts put together."""
+def test_sparse_shared_agrees_with_the_call_on_whole_caches():
+    """embla_sparse_decode on the contexts put together: both are within their bounds of the
+    definition (the shared call carries one more part of the probabilities)."""
     B, Hkv, G, P, n = 4, 4, 4, 1000, 200
     q, kp, vp, ko, vo = make(B, Hkv, G, P, n, 91)
     g = torch.Generator(device="cuda").manual_seed(4)
@@ -352,7 +353,8 @@ def test_sparse_shared_equals_the_call_on_whole_caches():
     V = torch.cat([vp[None].expand(B, -1, -1, -1), vo], 2).contiguous()
     E.embla_sparse_decode(E.Shape(B, Hkv * G, Hkv, D, P + n, P + n), q, K, V, idx, cnt, b)
     torch.cuda.synchronize()
-    assert torch.equal(a, b)
+    _, tol = sparse_reference(q, kp, vp, ko, vo, P, idx, cnt, D ** -0.5)
+    assert ((a - b).double().abs() <= 2 * tol).all()
 
 
 def test_sparse_shared_flags_indices_outside_the_context():
