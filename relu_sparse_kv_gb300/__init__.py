@@ -21,7 +21,6 @@ Tensors (torch, on the current CUDA device, C-contiguous):
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -60,11 +59,6 @@ class Shape:
     def c(self) -> _Shape:
         return _Shape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.ctx_len,
                       self.cache_stride)
-
-    @functools.cached_property
-    def ref(self):
-        """The shape as the C calls take it (they read it only)."""
-        return ctypes.byref(self.c())
 
     @property
     def units(self) -> int:
@@ -343,7 +337,7 @@ def embla_quantize_kv_e4m3(shape: Shape, pos: int, k_rows, v_rows, k_codes, k_sc
     """Quantise T tokens' K and V rows (bf16 [B, Hkv, T, D]) into rows pos .. pos + T - 1 of the
     8-bit caches (codes uint8 [B, Hkv, cache_stride, D], scales float32 [B, Hkv, cache_stride])."""
     T = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
-    _call("embla_quantize_kv_e4m3", shape.ref, pos, T, k_rows.data_ptr(), v_rows.data_ptr(),
+    _call("embla_quantize_kv_e4m3", ctypes.byref(shape.c()), pos, T, k_rows.data_ptr(), v_rows.data_ptr(),
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
           _stream(stream))
 
@@ -353,7 +347,7 @@ def embla_dequantize_kv_e4m3(shape: Shape, pos: int, k_codes, k_scales, v_codes,
     """Read rows pos .. pos + n_rows - 1 of the 8-bit caches back as bf16 into the first n_rows
     rows of k_rows and v_rows (bf16 [B, Hkv, T, D], T >= n_rows; n_rows defaults to T)."""
     T = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
-    _call("embla_dequantize_kv_e4m3", shape.ref, pos, T if n_rows is None else n_rows,
+    _call("embla_dequantize_kv_e4m3", ctypes.byref(shape.c()), pos, T if n_rows is None else n_rows,
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
           k_rows.data_ptr(), v_rows.data_ptr(), T, _stream(stream))
 
@@ -563,7 +557,7 @@ def embla_sparse_decode_per_head(shape: Shape, q, k_cache, v_cache, idx, count, 
 
 
 def embla_full_decode_shared_workspace_size(shape: Shape, prefix_len: int) -> int:
-    return library().embla_full_decode_shared_workspace_size(shape.ref, prefix_len)
+    return library().embla_full_decode_shared_workspace_size(ctypes.byref(shape.c()), prefix_len)
 
 
 def _shared_caches(shape: Shape, prefix_len: int, k_prefix, v_prefix, k_cache, v_cache):
@@ -587,22 +581,27 @@ def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefi
     cache_stride=score_stride)."""
     B, Hkv = shape.batch, shape.n_kv_heads
     heads = (B, shape.n_q_heads, shape.head_dim)
-    _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
-                (n_surv, torch.int32, (B, Hkv), "n_surv"),
-                *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
+    tensors = [(q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
+               (n_surv, torch.int32, (B, Hkv), "n_surv"),
+               *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)]
     score_stride = 0
     if sel_scores is not None:
         if sel_scores.dim() != 3:
             raise ValueError("sel_scores must be [B, Hkv, score_stride]")
         score_stride = sel_scores.shape[2]
-        _check_here((sel_scores, torch.float32, (B, Hkv, score_stride), "sel_scores"))
+        tensors.append((sel_scores, torch.float32, (B, Hkv, score_stride), "sel_scores"))
     if sel_hist is not None:
-        _check_here((sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist"))
+        tensors.append((sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist"))
+    if workspace is not None:
+        tensors.append((workspace, workspace.dtype, workspace.shape, "workspace"))
+    _check_here(*tensors)
     # a workspace of the caller's is checked against the size by the C call
     ws = workspace
     if ws is None:
         ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device)
-    _call("embla_full_decode_shared", shape.ref, prefix_len, k_prefix.shape[1], q.data_ptr(),
+        if stream is not None:
+            ws.record_stream(stream)  # its memory is not handed out again before the call is done
+    _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
           k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), alpha, c,
           eps, out.data_ptr(), n_surv.data_ptr(), _ptr(sel_scores), score_stride, _ptr(sel_hist),
           ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
@@ -621,7 +620,7 @@ def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_pre
     _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
                 (idx, torch.int32, (B, Hkv, idx_stride), "idx"), (count, torch.int32, (B, Hkv), "count"),
                 *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
-    _call("embla_sparse_decode_shared", shape.ref, prefix_len, k_prefix.shape[1], q.data_ptr(),
+    _call("embla_sparse_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
           k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           idx.data_ptr(), idx_stride, count.data_ptr(),
           shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream))

@@ -15,21 +15,34 @@
 //   O += P V     (P = w' as two bf16 matrices hi + lo, about 17 bits of weight, in tensor
 //                memory over S; V as the cached rows lie)
 // A tile of a sequence's own keys runs through the same operands with every other sequence's
-// weights zero.  The value tile is read whole: a prefix key is dead for all of 128 rows far
-// too rarely to skip (0.95^128).
+// weights zero.  Value tiles are read whole: a prefix key is dead for all of 128 rows far too
+// rarely to skip (0.95^128), and fetching an own tile's live rows alone would put another trip to
+// memory between its scores and its products.
 //
-// Bound by HBM up to one row block (64 KB of K and V per tile at the SM's share of the
-// bandwidth takes longer than its products); the grid is one CTA per SM, shared out over the
-// row blocks so that the CTAs of different row blocks walk the same prefix tiles at the same
-// time (read from HBM once).
+// Weights reach the value product as hi + lo, two bf16 roundings: 2.5e-6 of the output against
+// 64 bits.  A third part would cost half as many products again and 64 more tensor-memory columns
+// per tile than there are.  Denominators, scores and the sum over records are fp32.
+//
+// Work split: one CTA per SM, each one piece of a row block's tile list; the CTAs of different row
+// blocks walk the same prefix tiles at the same time, so the prefix comes from HBM once.
 //
 // Warp roles: 0 TMA producer of K (a ring of 3 tiles); 1 issuer of S; 2 issuer of P V; 3 TMA
-// producer of the query rows and of V (a ring of 3: its waits do not hold up K); 4-7 key norms, one thread per key; 8-23 epilogue, each a quarter of the query rows and of the
-// tile's keys.  The epilogue reads S in the fragment layout of the warp MMAs, where a thread
-// holds rows l, l + 8, l + 16 and l + 24 of its quarter, and the query rows lie in the block so
-// that those are heads of one sequence: the group maximum that the selection ranks is taken
-// within a thread (over lanes it cost two and a half instructions per score on the pipe that
-// bound the epilogue).
+// producer of the query rows and of V (a ring of 3: its waits do not hold up K); 4-7 key norms,
+// one thread per key; 8-23 epilogue, two groups of eight warps on alternate tiles, each warp a
+// quarter of the query rows and half of the tile's keys.  The epilogue reads S in the fragment
+// layout of the warp MMAs, where a thread holds rows l, l + 8, l + 16 and l + 24 of its quarter,
+// and the query rows lie in the block so that those are heads of one sequence: the group maximum
+// that the selection ranks is taken within a thread (by shuffles it cost two and a half
+// instructions per score on the pipe that bound the epilogue).
+//
+// What bounds it (clock stamps of one CTA): up to 128 query rows HBM, 64 KB of K and V per tile in
+// about 2,800 cycles against 2,250 for the epilogue and 1,536 for the products; beyond that the
+// epilogue, whose sixteen warps issue about 1,400 instructions per tile and scheduler.  The fixed
+// part of a call is about 11 us: 2 until the first tile lands, 2.5 from a tile's landing to its
+// products, 1.5 for writing the records (10 MB at once), 4 for the finishing kernel.  Measured, a
+// call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 29.6 us (97 MB needed, 3.3
+// TB/s); B 8, GQA 8, 32k 19.2 us; B 64, 64k, 1,024 own 75.6 us (285 MB, 3.8 TB/s; 13 us of it
+// the histogram's reading of 68 MB of scores that no longer fit L2).
 #include <atomic>
 #include <type_traits>
 
@@ -82,15 +95,14 @@ struct SharedParams {
   float *rec;
   uint32_t *flags;
   float *sel;              // [B, Hkv, score_stride] or null
-  uint32_t *hist;          // [B, Hkv, 2048], zeroed here, and so are the survivor counts (with scores)
+  uint32_t *hist;          // [B, Hkv, 2048] and n_surv [B, Hkv]: zeroed here when there are scores
   int32_t *n_surv;
   int64_t score_stride;
-  int32_t first_round;     // -1 (the epilogue's empty round)
   int32_t pair_prefix, pair_own;  // score rows of prefix / own tiles start on 8 bytes
   float alpha, eps;
 };
 
-// Two fp32 lanes at once, each rounded as the scalar operation would be.
+// Two fp32 lanes at once, each rounded as the scalar operation would be: half the instructions.
 __device__ __forceinline__ void mul2(float &a0, float &a1, float b0, float b1) {
   asm("{\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%0, %1};\n\t"
@@ -229,10 +241,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
 
   // Every role waits for the kernels before this one (pdl_wait_primary) where it first touches
-  // global memory, with its first addresses at hand.  Every role walks the CTA's stretches in the same order, and their tiles through the rings
-  // by a running tile count i: stage i % kRing, phase (i / kRing) & 1.  Stretch k's query and
-  // output barriers take phase k & 1.
-  // where tile t of the walk's stretch lies: the maps, the plane and the row
+  // global memory, with its first addresses at hand.  Every role walks the CTA's stretches in the
+  // same order, and their tiles through the rings by a running tile count i: stage i % kRing,
+  // phase (i / kRing) & 1.  Stretch k's query and output barriers take phase k & 1.
+
+  // where tile t of the walk's stretch lies (own keys or the prefix's): the plane and the row
   auto place = [&](int t, int &plane, int &row) {
     const bool own = t >= tp;
     const int x = t - tp;
@@ -427,24 +440,16 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int odd = G == 8 ? (lane >> 2) & 1 : 0;
     int i = 0;
     bool ok = true;
-    // Round -1 walks the code that ends a stretch without a stretch, before there is anything to
-    // do: that code runs once per CTA, and fetching it then, at the end, took about 2 us.
-#pragma unroll 1
-    for (int k = p.first_round; ok; ++k) {
-      const bool real = k >= 0;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    for (int k = 0; ok && w.next(); ++k) {
+      ok = !*s_abort && mbar_wait(qfull, k & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       float rq[4], den[4][2];
       int live = 0;  // keys of this thread's share with a group maximum above zero
 #pragma unroll
       for (int m = 0; m < 4; ++m) den[m][0] = den[m][1] = 0.0f;
-      if (real) {
-      if (k == 0) {
-        pdl_wait_primary();
-        pdl_launch_dependents();
-      }
-      if (!w.next()) break;
-      ok = !*s_abort && mbar_wait(qfull, k & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
       // 1 / rms of the thread's four rows: each lane takes one of its four lanes' rows
       {
         const float ss = row_square_sum(sQ, kBox, quarter * 32 + (lane >> 2) + 8 * q4, (lane & 3) * 2 + ((lane >> 2) & 1));
@@ -587,18 +592,17 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ok = mbar_wait(ofull, k & 1) && !*s_abort;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      }
       tc_fence_after_sync();
       uint32_t o[kPartCols];
       tmem_load_x32(tmem + lane_base + kColO + part_col, o);
       tmem_wait_ld(o);
       tc_fence_before_sync();
       __syncwarp();
-      if (real && lane == 0) mbar_arrive(ofree);  // the next stretch's P V may overwrite O
+      if (lane == 0) mbar_arrive(ofree);  // the next stretch's P V may overwrite O
       // The record: every row when the stretch holds prefix tiles, else the rows of the
       // sequences whose tiles it holds.
-      const int first_seq = !real ? kSeqs : w.t0 < tp ? 0 : (w.t0 - tp) / ts;
-      const int last_seq = !real ? -1 : w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
+      const int first_seq = w.t0 < tp ? 0 : (w.t0 - tp) / ts;
+      const int last_seq = w.t0 < tp ? w.nb - 1 : (w.t1 - 1 - tp) / ts;
       // its four rows' weight sums and (without scores) its sequence's count, over the lanes that
       // share them
       if constexpr (!SCORES) {
@@ -660,9 +664,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
 constexpr int kFThreads = 256;
 constexpr int kFWarps = kFThreads / 32;
-constexpr int kFCtasPerSm = 4;
+constexpr int kFCtasPerSm = 3;   // registers for ten records in flight per warp
 constexpr int kHistStep = 1024;  // a CTA's share of the scores starts at a multiple of this
-constexpr int kItemSteps = 6;    // an item's time in steps
+constexpr int kItemSteps = 12;   // an item's time in steps (B 32: 28.0 us, with 6 29.0)
 
 struct FinishParams {
   SharedSplit sp;
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float den = 0.0f;
       int live = 0;
-      constexpr int kBatch = 8;  // records in flight per warp (past the last: read again, not used)
+      constexpr int kBatch = 10;  // records in flight per warp (past the last: read again, not used)
       const int part = lane & (kParts - 1);
 #pragma unroll 1
       for (int i0 = warp / rows; i0 < nrec; i0 += kBatch * slices) {
@@ -994,7 +998,6 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   p.sel = a.sel_scores;
   p.hist = a.sel_hist;
   p.score_stride = a.score_stride;
-  p.first_round = -1;
   p.pair_prefix = a.score_stride % 2 == 0;
   p.pair_own = p.pair_prefix && sp.P % 2 == 0;
   p.alpha = a.alpha;
