@@ -26,9 +26,8 @@
 // Work split: one CTA per SM, each one piece of a row block's tile list; the CTAs of different row
 // blocks walk the same prefix tiles at the same time, so the prefix comes from HBM once.
 //
-// Warp roles: 0 TMA producer of K (a ring of 3 tiles); 1 issuer of S; 2 issuer of P V; 3 TMA
-// producer of the query rows and of V (a ring of 3: its waits do not hold up K); 4-7 key norms,
-// one thread per key; 8-23 epilogue, two groups of eight warps on alternate tiles, each warp a
+// Warp roles: 0 TMA producer of K (two tiles); 1 issuer of S; 2 issuer of P V; 3 TMA producer of
+// the query rows and of V (two tiles; its waits do not hold up K); 4-7 key norms, one thread per key; 8-23 epilogue, two groups of eight warps on alternate tiles, each warp a
 // quarter of the query rows and half of the tile's keys.  The epilogue reads S in the fragment
 // layout of the warp MMAs, where a thread holds rows l, l + 8, l + 16 and l + 24 of its quarter,
 // and the query rows lie in the block so that those are heads of one sequence: the group maximum
@@ -53,7 +52,8 @@ namespace embla {
 namespace {
 
 constexpr int kRows = 128;               // query rows of a row block
-constexpr int kRing = 3;                 // K, V, key-norm stages and S/P buffers
+constexpr int kRing = 3;                 // key norms and S/P buffers
+constexpr int kStages = 2;               // K stages, V stages (three of each were no faster)
 constexpr int kWarpPV = 2;
 constexpr int kWarpV = 3;
 constexpr int kWarpNorm = 4;             // first of the key-norm warps
@@ -71,10 +71,10 @@ constexpr int kBox = 128 * 128;          // one [128 rows][64 bf16] box, 16 KB
 constexpr int kTileB = 2 * kBox;         // a 128 x 128 bf16 tile
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kTileB;
-constexpr int kOffV = kOffK + kRing * kTileB;
-constexpr int kOffRK = kOffV + kRing * kTileB;
+constexpr int kOffV = kOffK + kStages * kTileB;
+constexpr int kOffRK = kOffV + kStages * kTileB;
 constexpr int kOffBar = kOffRK + kRing * kRows * 4;
-constexpr int kNBars = 1 + 5 * kRing + 3;
+constexpr int kNBars = 1 + 2 * kStages + 3 * kRing + 3;
 constexpr int kOffMisc = kOffBar + kNBars * 8;
 constexpr int kSSmem = kOffMisc + 32 + 1024;  // + room to align the base to 1024
 static_assert(kSSmem <= 227 * 1024, "shared memory per CTA");
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
   float *sRK = reinterpret_cast<float *>(smem + kOffRK);
   uint64_t *qfull = reinterpret_cast<uint64_t *>(smem + kOffBar);
   uint64_t *kfull = qfull + 1;
-  uint64_t *vfull = kfull + kRing;
-  uint64_t *sfull = vfull + kRing;   // S done and the key norms taken: the K stage is free
+  uint64_t *vfull = kfull + kStages;
+  uint64_t *sfull = vfull + kStages;   // S done and the key norms taken: the K stage is free
   uint64_t *pfull = sfull + kRing;
   uint64_t *pvdone = pfull + kRing;  // P V done: the V stage, S/P buffer and norms are free
   uint64_t *ofull = pvdone + kRing;  // a stretch's P V all done
@@ -204,9 +204,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const int tp = static_cast<int>(sp.tp), ts = static_cast<int>(sp.ts);  // prefix, own tiles
 
   if (warp == 0) {
-    if (lane < kRing) {
+    if (lane < kStages) {
       mbar_init(&kfull[lane], 1);
       mbar_init(&vfull[lane], 1);
+    }
+    if (lane < kRing) {
       mbar_init(&sfull[lane], 1 + kNormWarps);  // the S issuer's commit and the norms
       mbar_init(&pfull[lane], kEpiWarps / kGroups);
       mbar_init(&pvdone[lane], 1);
@@ -242,8 +244,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
   // Every role waits for the kernels before this one (pdl_wait_primary) where it first touches
   // global memory, with its first addresses at hand.  Every role walks the CTA's stretches in the
-  // same order, and their tiles through the rings by a running tile count i: stage i % kRing,
-  // phase (i / kRing) & 1.  Stretch k's query and output barriers take phase k & 1.
+  // same order, and their tiles through the rings by a running tile count i: K and V stage
+  // i % kStages, S/P buffer i % kRing, each in its ring's phase.  Stretch k's query and output
+  // barriers take phase k & 1.
 
   // where tile t of the walk's stretch lies (own keys or the prefix's): the plane and the row
   auto place = [&](int t, int &plane, int &row) {
@@ -263,13 +266,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
       while (ok && w.next()) {
 #pragma unroll 1
         for (int t = w.t0; t < w.t1; ++t, ++i) {
-          const int s = i % kRing;
-          const uint32_t ph = ((i / kRing) - 1) & 1;
+          const int s = i % kStages;
           int plane, row;
           const bool own = place(t, plane, row);
           const CUtensorMap *map = own ? &tm_ko : &tm_kp;
           if (i == 0) pdl_wait_primary();
-          if (i >= kRing && !mbar_wait(&sfull[s], ph)) {
+          if (i >= kStages && !mbar_wait(&sfull[(i - kStages) % kRing], ((i - kStages) / kRing) & 1)) {
             ok = false;
             break;
           }
@@ -303,11 +305,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
         *s_qissued = k + 1;
 #pragma unroll 1
         for (int t = w.t0; t < w.t1; ++t, ++i) {
-          const int s = i % kRing;
+          const int s = i % kStages;
           int plane, row;
           const bool own = place(t, plane, row);
           const CUtensorMap *map = own ? &tm_vo : &tm_vp;
-          if (i >= kRing && !mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1)) {
+          if (i >= kStages && !mbar_wait(&pvdone[(i - kStages) % kRing], ((i - kStages) / kRing) & 1)) {
             ok = false;
             break;
           }
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
-        ok = mbar_wait(&kfull[s], (i / kRing) & 1) &&
+        ok = mbar_wait(&kfull[i % kStages], (i / kStages) & 1) &&
              (i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1));
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           for (int kk = 0; kk < 8; ++kk) {
             // dims 16kk..16kk+15: 32 bytes into a 128-byte row; dims 64.. start the second box
             const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
-            tc_mma_bf16(tmem + s * 128, qdesc + off, kdesc + static_cast<uint64_t>((s * kTileB) >> 4) + off,
+            tc_mma_bf16(tmem + s * 128, qdesc + off, kdesc + static_cast<uint64_t>((i % kStages * kTileB) >> 4) + off,
                         kIdescS, kk > 0 ? 1u : 0u);
           }
           tc_commit(&sfull[s]);
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
-        ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[s], (i / kRing) & 1);
+        ok = mbar_wait(&pfull[s], (i / kRing) & 1) && mbar_wait(&vfull[i % kStages], (i / kStages) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
           for (int kk = 0; kk < 8; ++kk) {
             // keys 16kk..16kk+15: in their group of 16 columns hi takes the first 8, lo the rest
             const uint32_t a_hi = tmem + s * 128 + kk * 16;
-            const uint64_t vd = vdesc + static_cast<uint64_t>((s * kTileB + kk * 2048) >> 4);
+            const uint64_t vd = vdesc + static_cast<uint64_t>((i % kStages * kTileB + kk * 2048) >> 4);
             tc_mma_bf16_tmem_a(tmem + kColO, a_hi, vd, kIdescPV, (t > w.t0 || kk > 0) ? 1u : 0u);
             tc_mma_bf16_tmem_a(tmem + kColO, a_hi + 8, vd, kIdescPV, 1u);
           }
@@ -399,10 +401,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
         const int s = i % kRing;
-        ok = mbar_wait(&kfull[s], (i / kRing) & 1);
+        ok = mbar_wait(&kfull[i % kStages], (i / kStages) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const float rk = rsqrtf(row_square_sum(sK + s * kTileB, kBox, r, r & 7) * (1.0f / kHeadDim) + p.eps);
+        const float rk = rsqrtf(row_square_sum(sK + i % kStages * kTileB, kBox, r, r & 7) * (1.0f / kHeadDim) + p.eps);
         ok = i < kRing || mbar_wait(&pvdone[s], ((i / kRing) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -647,10 +649,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
     if (qi > 0) mbar_wait(qfull, (qi - 1) & 1);
     const int nk = *s_kissued, nv = *s_vissued;
 #pragma unroll 1
-    for (int s = 0; s < kRing; ++s) {
-      int uses = nk > s ? (nk - 1 - s) / kRing + 1 : 0;
+    for (int s = 0; s < kStages; ++s) {
+      int uses = nk > s ? (nk - 1 - s) / kStages + 1 : 0;
       if (uses) mbar_wait(&kfull[s], (uses - 1) & 1);
-      uses = nv > s ? (nv - 1 - s) / kRing + 1 : 0;
+      uses = nv > s ? (nv - 1 - s) / kStages + 1 : 0;
       if (uses) mbar_wait(&vfull[s], (uses - 1) & 1);
     }
   }
