@@ -12,10 +12,14 @@ Tolerances, from the arithmetic of the kernels (u = 2^-24, half a step of fp32):
            one per record: with n_add of them the sum is off by at most 4u n_add sum w |v|; the
            denominators the same over n_add / 2.
   out      the sum's error over the normaliser, plus |out| times the normaliser's relative error."""
+import numpy as np
 import pytest
 import torch
 
+import gen
+import oracle
 import relu_sparse_kv_gb300 as E
+from helpers import assert_close, to_dev
 
 pytestmark = pytest.mark.gpu
 D = 128
@@ -135,6 +139,7 @@ CASES = [
     (70, 4, 4, 384, 5, 384, 8, 392),        # three row blocks, the last of six
     (2, 4, 4, 20000, 700, 20000, 1000, 20704),  # pieces of many tiles
     (4, 4, 4, 1024, 3001, 1024, 3001, 4032),    # own contexts longer than the prefix
+    (2500, 1, 8, 129, 2, 130, 3, 132),          # more row blocks than SMs
 ]
 
 
@@ -250,6 +255,56 @@ def test_nan_keys_and_queries_stay_their_own():
     ref, tol, _, _ = reference(q[2:3, :G], kp[:1], vp[:1], k3, torch.cat([vo[2, 0, :5], vo[2, 0, 6:]])[None, None],
                                P, n - 1, 1.0, 1.0, EPS)
     assert ((out[2, :G].double() - ref[0]).abs() <= tol[0]).all()
+
+
+@pytest.mark.parametrize("Hq,P", [(16, 1500), (16, 2048 - 128), (32, 1), (32, 2047)])
+def test_one_sequence_split_anywhere_matches_the_oracle(Hq, P):
+    """A generated context (scores and selection kept away from ties) cut into a prefix and own keys:
+    the oracle's survivor counts and selection exactly, its outputs to the usual tolerance."""
+    n_all, Hkv = 2048, 4
+    fl = gen.make_full_layer(seed=7, layer=0, B=1, Hq=Hq, Hkv=Hkv, D=D, n=n_all, pattern="bernoulli",
+                             frac=0.3, sparse_layers=(1,))
+    q, K, V = to_dev(fl.q), to_dev(fl.K), to_dev(fl.V)
+    kp, vp = K[0, :, :P].contiguous(), V[0, :, :P].contiguous()
+    ko, vo = K[:, :, P:].contiguous(), V[:, :, P:].contiguous()
+    n = n_all - P
+    out, ns, scores, hist = run(q, kp, vp, ko, vo, P, n)
+    ref_out, ref_sig, ref_ns = oracle.full_decode_batch(fl.q, fl.K, fl.V, n_all)
+    assert_close(out.cpu().numpy(), ref_out, what="shared full output")
+    assert np.array_equal(ns.cpu().numpy(), ref_ns)
+    idx = torch.empty(1, Hkv, 1152, dtype=torch.int32, device="cuda")
+    cnt = torch.empty(1, Hkv, dtype=torch.int32, device="cuda")
+    E.embla_select_topk(E.Shape(1, Hq, Hkv, D, n_all, n_all), scores, hist, idx, cnt)
+    sout = torch.empty(1, Hq, D, device="cuda")
+    qs = to_dev(fl.sparse_q[0])
+    E.embla_sparse_decode_shared(E.Shape(1, Hq, Hkv, D, n, n), P, qs, kp, vp, ko, vo, idx, cnt, sout)
+    torch.cuda.synchronize()
+    ref_idx, ref_cnt = oracle.select_topk_batch(ref_sig, n_all)
+    assert np.array_equal(cnt.cpu().numpy(), ref_cnt) and np.array_equal(idx.cpu().numpy(), ref_idx)
+    assert_close(sout.cpu().numpy(), oracle.sparse_decode_batch(fl.sparse_q[0], fl.K, fl.V, ref_idx, ref_cnt),
+                 what="shared sparse output")
+
+
+def test_two_calls_on_two_streams_at_once():
+    """Two batches behind different prefixes, each with its own workspace on its own stream, eight
+    calls of each in flight together: the bits of the calls made alone."""
+    sizes = [(12, 4, 4, 5000, 64), (9, 2, 8, 7000, 33)]
+    xs = [make(B, Hkv, G, P, n, 200 + B) for B, Hkv, G, P, n in sizes]
+    alone = [run(*x, P, n) for x, (_, _, _, P, n) in zip(xs, sizes)]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    got = []
+    for x, (B, Hkv, G, P, n) in zip(xs, sizes):
+        shape = E.Shape(B, Hkv * G, Hkv, D, n, n)
+        ws = torch.empty(E.embla_full_decode_shared_workspace_size(shape, P), dtype=torch.uint8, device="cuda")
+        got.append((shape, ws, [torch.full_like(t, -3) for t in alone[len(got)]]))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for x, (_, _, _, P, _), st, (shape, ws, o) in zip(xs, sizes, streams, got):
+            E.embla_full_decode_shared(shape, P, *x, *o, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    assert E.embla_device_check() == 0
+    for a, (_, _, o) in zip(alone, got):
+        assert all(torch.equal(s, t) for s, t in zip(a, o))
 
 
 def chain(x, P, n, sstride, topk=1024, recent=128):
