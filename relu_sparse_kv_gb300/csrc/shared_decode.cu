@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
 
-  // Every role waits for the kernels before this one (pdl_wait_primary) where it first touches
-  // global memory, with its first addresses at hand.  Every role walks the CTA's stretches in the
+  // Every role waits for the kernels before this one (pdl_wait_primary) by itself, with its first
+  // addresses at hand, and before any wait that has a time limit: a kernel that runs long ahead
+  // of this one is not a timeout here.  Every role walks the CTA's stretches in the
   // same order, and their tiles through the rings by a running tile count i: K and V stage
   // i % kStages, S/P buffer i % kRing, each in its ring's phase.  Stretch k's query and output
   // barriers take phase k & 1.
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
     int i = 0;
     bool ok = true;
+    pdl_wait_primary();
     for (int k = 0; ok && w.next(); ++k) {
       ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(qfull, k & 1));
 #pragma unroll 1
@@ -360,6 +362,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const uint64_t vdesc = smem_desc_sw128_mn(smem_u32(sV), kBox);
     int i = 0, done = 0;
     bool ok = true;
+    pdl_wait_primary();
     for (int k = 0; ok && w.next(); ++k) {
       ok = __all_sync(0xffffffffu, !*s_abort && (k == 0 || mbar_wait(ofree, (k - 1) & 1)));
 #pragma unroll 1
@@ -397,6 +400,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int r = (warp - kWarpNorm) * 32 + lane;  // this thread's key of every tile
     int i = 0;
     bool ok = true;
+    pdl_wait_primary();
     while (ok && w.next()) {
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++i) {
@@ -416,7 +420,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
     if (!ok && lane == 0) give_up(s_abort, p.flags);
     // the counts that the next kernel adds up start at zero
     if constexpr (SCORES) {
-      pdl_wait_primary();
       uint4 *h = reinterpret_cast<uint4 *>(p.hist);
       const int64_t n4 = static_cast<int64_t>(sp.B) * sp.Hkv * (kHistBins / 4);
 #pragma unroll 1

@@ -99,6 +99,27 @@ def test_zero_tiny_huge_infinite_and_nan_rows():
     check(1, 1, 4, 12, 0, k, k.flip(2).contiguous())
 
 
+def test_rows_past_32_bit_offsets():
+    """Codes of the second plane and of late rows lie past 2^31 bytes, the bf16 rows read back past
+    2^32 bytes."""
+    B, Hkv, T, ncap = 1, 2, 33, (1 << 24) + 100
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(B, Hkv, T, D, device="cuda", generator=g).bfloat16()
+    codes = [torch.empty(B, Hkv, ncap, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.empty(B, Hkv, ncap, device="cuda") for _ in range(2)]
+    pos = ncap - T
+    sh = E.Shape(B, 4 * Hkv, Hkv, D, 0, ncap)
+    E.embla_quantize_kv_e4m3(sh, pos, x, x, codes[0], scales[0], codes[1], scales[1])
+    back = [torch.zeros(B, Hkv, ncap, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    E.embla_dequantize_kv_e4m3(sh, pos, codes[0], scales[0], codes[1], scales[1], *back, n_rows=T)
+    torch.cuda.synchronize()
+    v, s = definition(x)
+    for c, sc, b in zip(codes, scales, back):
+        assert torch.equal(c[:, :, pos:].view(E4M3).double(), v) and torch.equal(sc[:, :, pos:], s)
+        assert torch.equal(b[:, :, :T].float(), (v.float() * s[..., None]).bfloat16().float())
+        assert (b[:, :, T:T + 50] == 0).all()
+
+
 @pytest.mark.parametrize("B,Hkv,G,ncap,pos,T,stride", [
     (1, 4, 4, 1, 0, 1, 1), (8, 2, 8, 300, 299, 1, 7), (3, 2, 8, 1037, 500, 37, 37), (1, 1, 4, 129, 1, 128, 200),
     (2, 4, 4, 4096, 0, 4096, 4096),

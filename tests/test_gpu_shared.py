@@ -170,6 +170,49 @@ def test_full_shared_without_selection_outputs_and_with_a_used_workspace():
     assert err.value.status == 3
 
 
+def test_full_shared_with_buffers_on_sixteen_bytes_only():
+    """Every buffer 16 bytes off a 32-byte boundary: the same bits as with wider alignment."""
+    B, Hkv, G, P, n = 5, 4, 4, 700, 45
+    x = make(B, Hkv, G, P, n, 23)
+    a = run(*x, P, n, 752)
+
+    def shifted(t, fill=None):
+        raw = torch.empty(t.numel() * t.element_size() + 32, dtype=torch.uint8, device="cuda")
+        start = (16 - raw.data_ptr()) % 32
+        v = raw[start:start + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        assert v.data_ptr() % 32 == 16
+        return v.copy_(t) if fill is None else v.fill_(fill)
+
+    shape = E.Shape(B, Hkv * G, Hkv, D, n, n)
+    o = [shifted(t, 777) for t in a]
+    ws = shifted(torch.empty(E.embla_full_decode_shared_workspace_size(shape, P), dtype=torch.uint8, device="cuda"))
+    E.embla_full_decode_shared(shape, P, *[shifted(t) for t in x], *o, workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(a, o))
+
+
+def test_planes_past_32_bit_offsets():
+    """Prefix and own planes more than 2^31 elements apart (and rows of the own caches past 2^32
+    bytes): the definition on the rows that are there, for both calls."""
+    B, Hkv, G, P, n, stride = 2, 2, 8, 300, 40, (1 << 24) + 5
+    q, kp, vp, ko, vo = make(B, Hkv, G, P, n, 27)
+    far = []
+    for t, planes in ((kp, (Hkv,)), (vp, (Hkv,)), (ko, (B, Hkv)), (vo, (B, Hkv))):
+        big = torch.empty(*planes, stride, D, dtype=torch.bfloat16, device="cuda")
+        big[..., :t.shape[-2], :] = t
+        big[..., t.shape[-2]:t.shape[-2] + 200, :] = float("nan")
+        far.append(big)
+    assert far[2][1, 1].data_ptr() - far[2].data_ptr() > 1 << 33
+    check((q, *far), P, n, 344)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    idx = torch.randint(0, P + n, (B, Hkv, 64), device="cuda", generator=g, dtype=torch.int32)
+    cnt = torch.full((B, Hkv), 64, dtype=torch.int32, device="cuda")
+    out = torch.empty(B, Hkv * G, D, device="cuda")
+    E.embla_sparse_decode_shared(E.Shape(B, Hkv * G, Hkv, D, n, stride), P, q, *far, idx, cnt, out)
+    ref, tol = sparse_reference(q, kp, vp, ko, vo, P, idx, cnt, D ** -0.5)
+    assert ((out.double() - ref).abs() <= tol).all()
+
+
 def test_full_shared_agrees_with_the_decode_of_whole_contexts():
     """The same contexts as B separate caches through embla_full_decode: scores agree to fp32
     rounding (60u of sum |q^ k^| <= 128 on either side), outputs to both calls' bounds."""
