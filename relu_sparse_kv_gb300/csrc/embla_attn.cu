@@ -924,7 +924,7 @@ embla_status embla_dequantize_kv_e4m3(const embla_shape *shape, int64_t pos, int
   const DequantizeParams p = {
       {{k_codes, k_scales, static_cast<uint16_t *>(k_rows)},
        {v_codes, v_scales, static_cast<uint16_t *>(v_rows)}},
-      units * n_rows, n_rows, shape->cache_stride, pos, rows_stride};
+      units * n_rows, n_rows, shape->cache_stride, pos, rows_stride, 0};
   return cuda_status(launch_dequantize_rows(p, static_cast<cudaStream_t>(stream)));
 }
 

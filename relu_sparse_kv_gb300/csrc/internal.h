@@ -148,8 +148,9 @@ struct DequantizeJob {
 struct DequantizeParams {
   DequantizeJob job[2];
   int64_t rows, tokens, cache_stride, pos, dst_stride;
+  int dst32;  // set by the launcher: both destinations start on 32 bytes
 };
-cudaError_t launch_dequantize_rows(const DequantizeParams &p, cudaStream_t stream);
+cudaError_t launch_dequantize_rows(DequantizeParams p, cudaStream_t stream);
 
 size_t sparse_workspace_bytes(int64_t units, int G, int idx_stride);
 // k_scales / v_scales: per-token scales of 8-bit E4M3 caches, or both null for bf16 caches.

@@ -133,8 +133,13 @@ __global__ void __launch_bounds__(kCodeThreads) dequantize_rows_kernel(const Deq
   const uint2 e0 = scaled_bf16x4(c.x, s), e1 = scaled_bf16x4(c.y, s);
   const uint2 e2 = scaled_bf16x4(c.z, s), e3 = scaled_bf16x4(c.w, s);
   uint4 *dst = reinterpret_cast<uint4 *>(rows + (u * p.dst_stride + t) * kHeadDim) + 2 * part;
-  dst[0] = make_uint4(e0.x, e0.y, e1.x, e1.y);
-  dst[1] = make_uint4(e2.x, e2.y, e3.x, e3.y);
+  const uint4 lo = make_uint4(e0.x, e0.y, e1.x, e1.y), hi = make_uint4(e2.x, e2.y, e3.x, e3.y);
+  if (p.dst32) {  // whole sectors
+    st_global_v8(dst, lo, hi);
+  } else {
+    dst[0] = lo;
+    dst[1] = hi;
+  }
 }
 
 // Blocks for `rows` rows of each of two arrays: one row per eight lanes.
@@ -147,8 +152,9 @@ cudaError_t launch_quantize_rows(const QuantizeParams &p, cudaStream_t stream) {
   return launch_pdl(quantize_rows_kernel, dim3(row_blocks(p.rows), 2), dim3(kCodeThreads), 0, stream, 0u, p);
 }
 
-cudaError_t launch_dequantize_rows(const DequantizeParams &p, cudaStream_t stream) {
+cudaError_t launch_dequantize_rows(DequantizeParams p, cudaStream_t stream) {
   if (p.rows == 0) return cudaSuccess;
+  p.dst32 = ((reinterpret_cast<uintptr_t>(p.job[0].dst) | reinterpret_cast<uintptr_t>(p.job[1].dst)) & 31u) == 0;
   return launch_pdl(dequantize_rows_kernel, dim3(row_blocks(p.rows), 2), dim3(kCodeThreads), 0, stream, 0u, p);
 }
 

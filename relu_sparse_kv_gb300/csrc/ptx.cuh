@@ -501,6 +501,12 @@ __device__ __forceinline__ void st_global_v8(float *dst, float a0, float a1, flo
                : "memory");
 }
 
+__device__ __forceinline__ void st_global_v8(void *dst, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // Two floats (dst 8-byte aligned) or one to global memory where `on` holds: a predicated store, no
 // branch.
 __device__ __forceinline__ void st_global_v2_if(bool on, float *dst, float a0, float a1) {

@@ -140,6 +140,23 @@ def test_read_back(B, Hkv, G, ncap, pos, T, stride):
         assert (r[:, :, T:] == 3.0).all()
 
 
+def test_read_back_into_rows_on_sixteen_bytes_only():
+    B, Hkv, T = 2, 2, 77
+    g = torch.Generator(device="cuda").manual_seed(11)
+    kc = torch.randint(0, 256, (B, Hkv, T, D), device="cuda", generator=g, dtype=torch.int32).to(torch.uint8)
+    ks = torch.rand(B, Hkv, T, device="cuda", generator=g)
+    raw = torch.zeros(2, B * Hkv * T * D + 16, dtype=torch.bfloat16, device="cuda")
+    rows = []
+    for r in raw:
+        start = (16 - r.data_ptr()) % 32 // 2
+        rows.append(r[start:start + B * Hkv * T * D].view(B, Hkv, T, D))
+        assert rows[-1].data_ptr() % 32 == 16
+    E.embla_dequantize_kv_e4m3(E.Shape(B, 16, Hkv, D, 0, T), 0, kc, ks, kc, ks, *rows)
+    torch.cuda.synchronize()
+    want = (kc.view(E4M3).float() * ks[..., None]).bfloat16().float().nan_to_num(nan=1.5)
+    assert all(torch.equal(r.float().nan_to_num(nan=1.5), want) for r in rows)
+
+
 def test_round_trip_error_and_idempotence():
     """scale * decode(code) is within 2^-4 |x| + 2^-10 scale (half a step of E4M3, normal or
     subnormal) of x, plus the bf16 rounding of what is read back (2^-8 of it), and the fp32
