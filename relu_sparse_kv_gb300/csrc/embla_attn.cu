@@ -7,7 +7,9 @@
 
 #include "embla_attn.h"
 #include "internal.h"
+#include "kv_codes.h"
 #include "ptx.cuh"
+#include "shared_prefix.h"
 
 using namespace embla;
 
@@ -770,11 +772,9 @@ embla_status embla_sparse_decode_shared(const embla_shape *shape, int64_t prefix
   const int sms = sm_count_of(current_device());
   if (sms <= 0) return EMBLA_ERR_CUDA;
   const SharedRows prefix = {k_prefix, v_prefix, prefix_len, prefix_stride};
-  return cuda_status(launch_sparse_decode(G, false, shape->n_q_heads, q, k_cache, v_cache, nullptr,
-                                          nullptr, idx, idx_stride, count, units,
-                                          shape->n_kv_heads, prefix_len + shape->ctx_len,
-                                          shape->cache_stride, tau, out, nullptr, flags, sms,
-                                          static_cast<cudaStream_t>(stream), &prefix));
+  return cuda_status(launch_sparse_decode_shared(
+      G, shape->n_q_heads, q, prefix, k_cache, v_cache, idx, idx_stride, count, units, shape->n_kv_heads,
+      prefix_len + shape->ctx_len, shape->cache_stride, tau, out, flags, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t embla_relu2_mlp_workspace_size(int64_t d, int64_t f) {

@@ -37,23 +37,23 @@
 // What bounds it (clock stamps of one CTA): up to 128 query rows HBM, 64 KB of K and V per tile in
 // about 2,800 cycles against 2,250 for the epilogue and 1,536 for the products; beyond that the
 // epilogue, whose sixteen warps issue about 1,400 instructions per tile and scheduler.  The fixed
-// part of a call is about 11 us: 2 until the first tile lands, 2.5 from a tile's landing to its
-// products, 1.5 for writing the records (10 MB at once), 4 for the finishing kernel.  Measured, a
-// call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 29.6 us (97 MB needed, 3.3
-// TB/s); B 8, GQA 8, 32k 19.2 us; B 64, 64k, 1,024 own 75.6 us (285 MB, 3.8 TB/s; 13 us of it
-// the histogram's reading of 68 MB of scores that no longer fit L2).
+// part of a call is about 9 us: 2 until the first tile lands, 2.5 from a tile's landing to its
+// products, 1.5 for writing the records (10 MB at once), 2 to 3 for the finishing kernel.  Measured,
+// a call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 28.0 us (97 MB needed, 3.5
+// TB/s); B 8, GQA 8, 32k 16.0 us; B 64, 64k, 1,024 own 77.4 us (285 MB, 3.7 TB/s; 13 us of it the
+// histogram's reading of 68 MB of scores that no longer fit L2).
 #include <atomic>
 #include <type_traits>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "ptx_blocks.cuh"
+#include "shared_prefix.h"
 
 namespace embla {
 namespace {
 
 constexpr int kRows = 128;               // query rows of a row block
 constexpr int kRing = 3;                 // key norms and S/P buffers
-constexpr int kStages = 2;               // K stages, V stages (three of each were no faster)
+constexpr int kStages = 2;               // K stages, V stages (three of each: within 3 % either way)
 constexpr int kWarpPV = 2;
 constexpr int kWarpV = 3;
 constexpr int kWarpNorm = 4;             // first of the key-norm warps

@@ -23,6 +23,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "shared_prefix.h"
 
 namespace cg = cooperative_groups;
 
@@ -282,7 +283,11 @@ struct DotsF32 {
 //        S holds, per lane, head lane/4 and rows 2(lane%4), +1 of each 8-row tile, which
 //        is exactly the B operand layout the next product needs);
 //   O^T += V^T . P^T  as MMAs with M = dims (8 tiles of 16), N = heads, K = the 16 rows.
-// P enters the second product as two bf16 parts (hi + lo); l sums the fp32 values.
+// P enters the second product as two bf16 parts (hi + lo), behind a shared prefix as three; l sums
+// the fp32 values.  Behind a shared prefix a row comes from the prefix's plane or the unit's own
+// one by its index.  What bounds it there is the gather: B 32, 32k prefix, 1,152 rows for each of
+// 128 units (75 MB of 256-byte rows, 52 MB of them distinct) 15.7 us; 12 warps per CTA instead of
+// 9 took 15.7 us too, and a prefetch of the later rounds' rows into L2 18.8 us.
 
 // 9 warps x 16 rows = 144 rows: a cluster of 8 covers 1152 (two CTAs to an SM); the wide
 // variant, 18 warps and a cluster of 4 (one CTA to an SM), takes over when 8 CTAs per unit
@@ -908,14 +913,13 @@ size_t sparse_workspace_bytes(int64_t units, int G, int idx_stride) {
   return 0;
 }
 
-cudaError_t launch_sparse_decode(int G, bool per_head, int Hq, const void *q, const void *k_cache,
-                                 const void *v_cache,
-                                 const float *k_scales, const float *v_scales, const int32_t *idx, int idx_stride, const int32_t *count,
-                                 int64_t units, int Hkv, int64_t n, int64_t ncap, float tau,
-                                 float *out, void *workspace, uint32_t *flags, int sm_count,
-                                 cudaStream_t stream, const SharedRows *prefix) {
-  (void)Hkv;
-  (void)workspace;
+// launch_sparse_decode, or with a prefix launch_sparse_decode_shared.
+static cudaError_t launch_sparse_any(int G, bool per_head, int Hq, const void *q, const void *k_cache,
+                                     const void *v_cache, const float *k_scales, const float *v_scales,
+                                     const int32_t *idx, int idx_stride, const int32_t *count,
+                                     int64_t units, int Hkv, int64_t n, int64_t ncap, float tau,
+                                     float *out, uint32_t *flags, int sm_count, cudaStream_t stream,
+                                     const SharedRows *prefix) {
   if (units == 0) return cudaSuccess;
   SparseParams p = {};
   p.q = static_cast<const uint16_t *>(q);
@@ -956,7 +960,6 @@ cudaError_t launch_sparse_decode(int G, bool per_head, int Hq, const void *q, co
   const dim3 grid(static_cast<unsigned>(units * cl));
   if (prefix != nullptr) {
     // rows from two places: one unit per (sequence, KV head), bf16 caches
-    if (per_head || k_scales != nullptr) return cudaErrorInvalidValue;
     p.Kp = static_cast<const uint8_t *>(prefix->k);
     p.Vp = static_cast<const uint8_t *>(prefix->v);
     p.plen = prefix->len;
@@ -973,6 +976,26 @@ cudaError_t launch_sparse_decode(int G, bool per_head, int Hq, const void *q, co
   if (G == 4) return launch_sparse_g<4>(grid, p, stream);
   if (G == 8) return launch_sparse_g<8>(grid, p, stream);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_sparse_decode(int G, bool per_head, int Hq, const void *q, const void *k_cache,
+                                 const void *v_cache,
+                                 const float *k_scales, const float *v_scales, const int32_t *idx, int idx_stride, const int32_t *count,
+                                 int64_t units, int Hkv, int64_t n, int64_t ncap, float tau,
+                                 float *out, void *workspace, uint32_t *flags, int sm_count,
+                                 cudaStream_t stream) {
+  (void)workspace;
+  return launch_sparse_any(G, per_head, Hq, q, k_cache, v_cache, k_scales, v_scales, idx, idx_stride, count,
+                           units, Hkv, n, ncap, tau, out, flags, sm_count, stream, nullptr);
+}
+
+cudaError_t launch_sparse_decode_shared(int G, int Hq, const void *q, const SharedRows &prefix,
+                                        const void *k_cache, const void *v_cache, const int32_t *idx,
+                                        int idx_stride, const int32_t *count, int64_t units, int Hkv,
+                                        int64_t n, int64_t ncap, float tau, float *out,
+                                        uint32_t *flags, int sm_count, cudaStream_t stream) {
+  return launch_sparse_any(G, false, Hq, q, k_cache, v_cache, nullptr, nullptr, idx, idx_stride, count, units,
+                           Hkv, n, ncap, tau, out, flags, sm_count, stream, &prefix);
 }
 
 cudaError_t launch_window_decode(int G, const void *q, const void *k_win, const void *v_win,

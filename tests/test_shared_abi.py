@@ -140,7 +140,7 @@ def test_binding_refuses_host_tensors_and_wrong_types():
 HARNESS = r"""
 #include <cstdio>
 #include <vector>
-#include "internal.h"
+#include "shared_prefix.h"
 using namespace embla;
 // Every tile of every row block belongs to exactly one stretch; a stretch's record slot is its
 // own and lies inside the workspace; the records of a row are those of the stretches that hold
