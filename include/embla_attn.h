@@ -260,7 +260,7 @@ embla_status embla_sparse_decode_e4m3(const embla_shape *shape, const void *q,
  *   shape      ctx_len = own keys per sequence (0 is allowed; the current token is the last
  *              one), cache_stride of the own caches
  *   prefix_len >= 0; prefix_stride >= prefix_len: rows between the prefix's planes.
- *              prefix_len + ctx_len <= 2^31 - 257
+ *              prefix_len + ctx_len <= 2^31 - 257.  The full decode takes strides below 2^32
  *   k_prefix, v_prefix  bf16 [Hkv, prefix_stride, D] (not read, and NULL is allowed, when
  *              prefix_len is 0; the same for the own caches when ctx_len is 0)
  *

@@ -682,6 +682,8 @@ embla_status embla_full_decode_shared(const embla_shape *shape, int64_t prefix_l
     return EMBLA_ERR_INVALID_ARG;
   // TMA plane coordinates and the second kernel's grid are 32-bit
   if (units * G > INT32_MAX / 2) return EMBLA_ERR_UNSUPPORTED;
+  // TMA strides stay below 2^40 bytes
+  if (prefix_stride > UINT32_MAX || shape->cache_stride > UINT32_MAX) return EMBLA_ERR_UNSUPPORTED;
   const int dev = current_device();
   const int sms = sm_count_of(dev);  // 0 past kMaxDevices
   if (sms <= 0) return EMBLA_ERR_CUDA;

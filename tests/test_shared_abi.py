@@ -83,6 +83,7 @@ def _full(lib, shape=None, plen=300, pstride=300, q=A[0], kp=A[1], vp=A[2], k=A[
     (dict(shape=_shape(head_dim=64)), UNSUPPORTED), (dict(shape=_shape(n_q_heads=12)), UNSUPPORTED),
     (dict(shape=_shape(ctx_len=129)), INVALID), (dict(shape=_shape(batch=-1)), INVALID),
     (dict(shape=_shape(batch=1 << 27)), UNSUPPORTED),       # 2^31 query heads
+    (dict(pstride=1 << 32), UNSUPPORTED), (dict(shape=_shape(cache_stride=1 << 32)), UNSUPPORTED),  # 1 TB per plane
 ])
 def test_full_shared_refusals(lib, kw, status):
     assert _full(lib, **kw) == status
