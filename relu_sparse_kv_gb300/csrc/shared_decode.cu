@@ -40,8 +40,9 @@
 // part of a call is about 9 us: 2 until the first tile lands, 2.5 from a tile's landing to its
 // products, 1.5 for writing the records (10 MB at once), 2 to 3 for the finishing kernel.  Measured,
 // a call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 28.0 us (97 MB needed, 3.5
-// TB/s); B 8, GQA 8, 32k 16.0 us; B 64, 64k, 1,024 own 77.4 us (285 MB, 3.7 TB/s; 13 us of it the
-// histogram's reading of 68 MB of scores that no longer fit L2).
+// TB/s); B 8, GQA 8, 32k 16.0 us; B 64, 64k, 1,024 own 75.5 us (285 MB, 3.8 TB/s; 11 us of it the
+// histogram's reading of 68 MB of scores, most of which L2 no longer holds, stored evict_last or
+// not).
 #include <atomic>
 #include <type_traits>
 
@@ -910,11 +911,11 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
       live += x > 0.0f ? 1 : 0;
       // order_key(x) >> 21: the top bits of a positive score, the inverted ones of a negative
       const int t = __float_as_int(x + 0.0f) >> 21;  // (-0 counts as 0)
-      atomicAdd(&s_mem[t >= 0 ? t + kHistBins / 2 : ~t], 1u);
+      atomicAdd(&s_mem[t ^ (t >> 31 | kHistBins / 2)], 1u);
     };
     if (p.hist_vec) {
       const float4 *s4 = reinterpret_cast<const float4 *>(su);
-      constexpr int kLoads = 4;  // in flight per thread
+      constexpr int kLoads = 8;  // in flight per thread (B 64, 64k: 75.5 us; 4: 77.4, 12 and a second batch ahead: no faster)
       const int m4 = m / 4;
 #pragma unroll 1
       for (int e = threadIdx.x; e < m4; e += kLoads * kFThreads) {
