@@ -42,7 +42,7 @@
 // a call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 28.0 us (97 MB needed, 3.5
 // TB/s); B 8, GQA 8, 32k 16.0 us; B 64, 64k, 1,024 own 75.5 us (285 MB, 3.8 TB/s; 11 us of it the
 // histogram's reading of 68 MB of scores, most of which L2 no longer holds, stored evict_last or
-// not).
+// not).  Without scores and histogram: 25.3, 15.2 and 60.6 us.
 #include <atomic>
 #include <type_traits>
 
@@ -756,6 +756,7 @@ __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int 
 
 // The batch's outputs from the records, then the survivors' counts and the selection's histograms
 // from the scores: one wave of CTAs, each with its share of both.
+template <bool SCORES>
 __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(const FinishParams p) {
   __shared__ __align__(16) uint32_t s_mem[kHistBins];
   const SharedSplit &sp = p.sp;
@@ -801,7 +802,15 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
       // each warp adds every slices-th record, lane l dims 4l .. 4l + 3; then the warps in order
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       float den = 0.0f;
+      // without scores, the survivors that the decode counted: eight of the warp's records at a time,
+      // four lanes (a count each) to a record, the first eight on their way with the sums
+      auto counted = [&](int i) {
+        const float *rec = first + static_cast<int64_t>(i) * kRecWords + (i < n1 ? 0 : gap);
+        return reinterpret_cast<const int32_t *>(rec)[kRecNum + kRecDen + lane % kParts * 32 + seq];
+      };
+      const int i1 = warp / rows + lane / kParts * slices;
       int live = 0;
+      if (!SCORES && i1 < nrec) live = counted(i1);
       constexpr int kBatch = 10;  // records in flight per warp (past the last: read again, not used)
       const int part = lane & (kParts - 1);
 #pragma unroll 1
@@ -826,19 +835,16 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
           }
         }
       }
-      if (p.hist == nullptr && lane < kParts) {  // the survivors that the decode counted
-        for (int i = warp / rows; i < nrec; i += slices)
-          live += reinterpret_cast<const int32_t *>(first + static_cast<int64_t>(i) * kRecWords +
-                                                    (i < n1 ? 0 : gap))[kRecNum + kRecDen + lane * 32 + seq];
+      if constexpr (!SCORES) {
+        for (int i = i1 + 32 / kParts * slices; i < nrec; i += 32 / kParts * slices) live += counted(i);
+        live = __reduce_add_sync(0xffffffffu, live);
       }
       float *s_acc = reinterpret_cast<float *>(s_mem);                 // [8 warps][128]
       float *s_den = s_acc + kFWarps * kHeadDim;                       // [8][kParts]
-      int *s_live = reinterpret_cast<int *>(s_den + kParts * kFWarps);  // [8][kParts]
+      int *s_live = reinterpret_cast<int *>(s_den + kParts * kFWarps);  // [8]
       *reinterpret_cast<float4 *>(s_acc + warp * kHeadDim + 4 * lane) = acc;
-      if (lane < kParts) {
-        s_den[warp * kParts + lane] = den;
-        s_live[warp * kParts + lane] = live;
-      }
+      if (lane < kParts) s_den[warp * kParts + lane] = den;
+      if (!SCORES && lane == 0) s_live[warp] = live;
       __syncthreads();
       // thread: dimension tid % 128 of the first (tid < 128) or the second row
       const int mine = threadIdx.x / kHeadDim, d = threadIdx.x % kHeadDim;
@@ -849,9 +855,8 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
         for (int k = mine; k < kFWarps; k += rows) {
           num += s_acc[k * kHeadDim + d];
           const float4 z4 = *reinterpret_cast<const float4 *>(s_den + k * kParts);
-          const int4 l4 = *reinterpret_cast<const int4 *>(s_live + k * kParts);
           dsum += (z4.x + z4.y) + (z4.z + z4.w);
-          nlive += (l4.x + l4.y) + (l4.z + l4.w);
+          if constexpr (!SCORES) nlive += s_live[k];
         }
       }
       static_assert(kParts == 4, "a warp's sums are one vector");
@@ -873,7 +878,7 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
       const float z = p.c / p.alpha / p.alpha + dsum;
       if (real && mine < rows) {
         p.out[static_cast<int64_t>(row0 + mine) * kHeadDim + d] = z != 0.0f ? num / z : 0.0f;
-        if (p.hist == nullptr && threadIdx.x == 0 && h == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
+        if (!SCORES && threadIdx.x == 0 && h == 0) p.n_surv[static_cast<int64_t>(b) * sp.Hkv + g] = nlive;
       }
       if (real) break;
       pdl_wait_primary();  // the records and scores are complete
@@ -884,7 +889,7 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
     item += static_cast<int>(gridDim.x);
     if (item >= items) break;
   }
-  if (p.hist == nullptr) return;
+  if constexpr (!SCORES) return;
 
   // The scores of all units one after another, each padded to N4 keys: this CTA's share of them,
   // counted unit by unit in shared memory.
@@ -1051,7 +1056,8 @@ cudaError_t launch_shared_decode(const SharedCall &a, const SharedSplit &sp, cud
   f.alpha = a.alpha;
   f.c = a.c;
   f.eps = a.eps;
-  return launch_pdl(shared_finish_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kFThreads), 0, stream, 0u, f);
+  return launch_pdl(a.sel_scores != nullptr ? shared_finish_kernel<true> : shared_finish_kernel<false>,
+                    dim3(static_cast<unsigned>(ctas)), dim3(kFThreads), 0, stream, 0u, f);
 }
 
 }  // namespace embla
