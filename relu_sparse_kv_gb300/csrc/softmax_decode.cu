@@ -960,8 +960,10 @@ static cudaError_t launch_sparse_any(int G, bool per_head, int Hq, const void *q
   const dim3 grid(static_cast<unsigned>(units * cl));
   if (prefix != nullptr) {
     // rows from two places: one unit per (sequence, KV head), bf16 caches
-    p.Kp = static_cast<const uint8_t *>(prefix->k);
-    p.Vp = static_cast<const uint8_t *>(prefix->v);
+    // (absent rows' copies of no bytes start at the first prefix row: with no prefix, whose
+    // pointers may be null, at the queries)
+    p.Kp = static_cast<const uint8_t *>(prefix->len > 0 ? prefix->k : q);
+    p.Vp = static_cast<const uint8_t *>(prefix->len > 0 ? prefix->v : q);
     p.plen = prefix->len;
     p.pstride = prefix->stride;
     if (G == 4) return launch_sparse_g<4, true>(grid, p, stream);

@@ -415,7 +415,7 @@ def test_full_then_selection_then_sparse(B, Hkv, G, P, n, sstride):
 
 @pytest.mark.parametrize("B,Hkv,G,P,n,stride,counts", [
     (1, 1, 4, 5, 0, 8, [3]), (3, 2, 8, 0, 50, 64, [0, 50, 1, 17, 16, 33]), (2, 4, 4, 77, 9, 1152, [86, 1, 0, 85, 64, 2, 9, 10]),
-    (40, 4, 4, 1200, 30, 1152, None), (80, 4, 4, 300, 3, 300, None),
+    (40, 4, 4, 1200, 30, 1152, None), (80, 4, 4, 300, 3, 300, None), (2, 2, 8, 3000, 100, 7001, [7001, 0, 6000, 1153]),
 ])
 def test_sparse_shared_matches_the_definition(B, Hkv, G, P, n, stride, counts):
     """Any list of keys in any order, the same key twice, empty lists; entries past the count are
@@ -434,6 +434,32 @@ def test_sparse_shared_matches_the_definition(B, Hkv, G, P, n, stride, counts):
     assert E.embla_device_check() == 0
     ref, tol = sparse_reference(q, kp, vp, ko, vo, P, idx, cnt, D ** -0.5)
     assert ((out.double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("P,n", [(0, 40), (40, 0), (0, 0)])
+def test_sides_without_keys_need_no_memory(P, n):
+    """Null planes for the side without keys: lists that end inside a block, empty ones, and (no keys
+    at all) only empty ones; the full layer on the same contexts."""
+    B, Hkv, G = 3, 2, 8
+    q, kp, vp, ko, vo = make(B, Hkv, G, P, n, 101, P, n)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    idx = torch.randint(0, max(1, P + n), (B, Hkv, 50), device="cuda", generator=g, dtype=torch.int32)
+    cnt = torch.tensor([50, 1, 0, 17, 16, 33] if P + n else [0] * 6, dtype=torch.int32, device="cuda").view(B, Hkv)
+    for t, keys in ((kp, P), (vp, P), (ko, n), (vo, n)):
+        assert keys > 0 or t.data_ptr() == 0
+    out = torch.full((B, Hkv * G, D), float("nan"), device="cuda")
+    sh = E.Shape(B, Hkv * G, Hkv, D, n, n)
+    E.embla_sparse_decode_shared(sh, P, q, kp, vp, ko, vo, idx, cnt, out)
+    full, ns = torch.full_like(out, float("nan")), torch.full((B, Hkv), -1, dtype=torch.int32, device="cuda")
+    E.embla_full_decode_shared(sh, P, q, kp, vp, ko, vo, full, ns)
+    torch.cuda.synchronize()
+    assert E.embla_device_check() == 0
+    if P + n == 0:
+        assert (out == 0).all() and (full == 0).all() and (ns == 0).all()
+        return
+    ref, tol = sparse_reference(q, kp, vp, ko, vo, P, idx, cnt, D ** -0.5)
+    assert ((out.double() - ref).abs() <= tol).all()
+    assert torch.isfinite(full).all() and (ns <= P + n).all() and (ns >= 0).all()
 
 
 def test_sparse_shared_agrees_with_the_call_on_whole_caches():
