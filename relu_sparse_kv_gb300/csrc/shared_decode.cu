@@ -34,9 +34,10 @@
 // that the selection ranks is taken within a thread (by shuffles it cost two and a half
 // instructions per score on the pipe that bound the epilogue).
 //
-// What bounds it (clock stamps of one CTA): up to 128 query rows HBM, 64 KB of K and V per tile in
-// about 2,800 cycles against 2,250 for the epilogue and 1,536 for the products; beyond that the
-// epilogue, whose sixteen warps issue about 1,400 instructions per tile and scheduler.  The fixed
+// What bounds it (clock stamps): up to 128 query rows HBM, 64 KB of K and V per tile in about
+// 2,800 cycles against 2,250 for the epilogue and 1,536 for the products; with more row blocks HBM
+// and the epilogue (sixteen warps, about 1,400 instructions per tile and scheduler) together: at
+// B 64 the CTAs leave 52 to 58 us after the first load, 336 MB read and written.  The fixed
 // part of a call is about 9 us: 2 until the first tile lands, 2.5 from a tile's landing to its
 // products, 1.5 for writing the records (10 MB at once), 2 to 3 for the finishing kernel.  Measured,
 // a call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 28.0 us (97 MB needed, 3.5
