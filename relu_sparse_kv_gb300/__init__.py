@@ -142,10 +142,10 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, device: int | None = None) -> int | None:
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
 
 
 def _check(t, dtype, shape, name, allow_none=False):
@@ -164,16 +164,17 @@ def _check(t, dtype, shape, name, allow_none=False):
 
 
 def _check_here(*tensors):
-    """Each of (tensor, dtype, shape, name) as _check has it, and on the current device: the
-    kernels launch there."""
+    """Each of (tensor, dtype, shape, name) as _check has it, and on the current device, where the
+    kernels launch; returns that device's index."""
     dev = -1 if tensors[0][0] is None else tensors[0][0].get_device()
     for t, dtype, shape, name in tensors:
         if not (t is not None and t.dtype is dtype and dev >= 0 and t.get_device() == dev
                 and t.shape == shape and t.is_contiguous()):
             _check(t, dtype, shape, name)
             raise ValueError(f"{name} is on {t.device}, other tensors of the call are not")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"the call's tensors are on cuda:{dev}, which is not the current device")
+    return dev
 
 
 def _call(name, *args):
@@ -319,37 +320,37 @@ def embla_append_kv_e4m3(shape: Shape, pos: int, k_code_rows, k_scale_rows, v_co
           _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _stream(stream))
 
 
-def _check_rows_and_codes(shape: Shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales) -> int:
-    """Rows bf16 [B, Hkv, T, D] and 8-bit caches; returns T."""
+def _check_rows_and_codes(shape: Shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales) -> tuple[int, int]:
+    """Rows bf16 [B, Hkv, T, D] and 8-bit caches; returns T and the device."""
     B, Hkv, D, ncap = shape.batch, shape.n_kv_heads, shape.head_dim, shape.cache_stride
     if k_rows is None or k_rows.dim() != 4:
         raise ValueError("k_rows must be [B, Hkv, T, D]")
     T = k_rows.shape[2]
     rows, codes, scales = (B, Hkv, T, D), (B, Hkv, ncap, D), (B, Hkv, ncap)
-    _check_here((k_rows, torch.bfloat16, rows, "k_rows"), (v_rows, torch.bfloat16, rows, "v_rows"),
-                (k_codes, torch.uint8, codes, "k_codes"), (k_scales, torch.float32, scales, "k_scales"),
-                (v_codes, torch.uint8, codes, "v_codes"), (v_scales, torch.float32, scales, "v_scales"))
-    return T
+    dev = _check_here((k_rows, torch.bfloat16, rows, "k_rows"), (v_rows, torch.bfloat16, rows, "v_rows"),
+                      (k_codes, torch.uint8, codes, "k_codes"), (k_scales, torch.float32, scales, "k_scales"),
+                      (v_codes, torch.uint8, codes, "v_codes"), (v_scales, torch.float32, scales, "v_scales"))
+    return T, dev
 
 
 def embla_quantize_kv_e4m3(shape: Shape, pos: int, k_rows, v_rows, k_codes, k_scales, v_codes,
                            v_scales, stream=None):
     """Quantise T tokens' K and V rows (bf16 [B, Hkv, T, D]) into rows pos .. pos + T - 1 of the
     8-bit caches (codes uint8 [B, Hkv, cache_stride, D], scales float32 [B, Hkv, cache_stride])."""
-    T = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
+    T, dev = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
     _call("embla_quantize_kv_e4m3", ctypes.byref(shape.c()), pos, T, k_rows.data_ptr(), v_rows.data_ptr(),
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-          _stream(stream))
+          _stream(stream, dev))
 
 
 def embla_dequantize_kv_e4m3(shape: Shape, pos: int, k_codes, k_scales, v_codes, v_scales, k_rows,
                              v_rows, n_rows: int | None = None, stream=None):
     """Read rows pos .. pos + n_rows - 1 of the 8-bit caches back as bf16 into the first n_rows
     rows of k_rows and v_rows (bf16 [B, Hkv, T, D], T >= n_rows; n_rows defaults to T)."""
-    T = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
+    T, dev = _check_rows_and_codes(shape, k_rows, v_rows, k_codes, k_scales, v_codes, v_scales)
     _call("embla_dequantize_kv_e4m3", ctypes.byref(shape.c()), pos, T if n_rows is None else n_rows,
           k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-          k_rows.data_ptr(), v_rows.data_ptr(), T, _stream(stream))
+          k_rows.data_ptr(), v_rows.data_ptr(), T, _stream(stream, dev))
 
 
 def embla_full_decode_select_workspace_size(shape: Shape, topk: int = 1024, recent: int = 128) -> int:
@@ -594,17 +595,17 @@ def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefi
         tensors.append((sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist"))
     if workspace is not None:
         tensors.append((workspace, workspace.dtype, workspace.shape, "workspace"))
-    _check_here(*tensors)
+    dev = _check_here(*tensors)
     # a workspace of the caller's is checked against the size by the C call
     ws = workspace
     if ws is None:
         ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device)
         if stream is not None:
-            ws.record_stream(stream)  # its memory is not handed out again before the call is done
+            ws.record_stream(stream, dev)  # its memory is not handed out again before the call is done
     _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
           k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), alpha, c,
           eps, out.data_ptr(), n_surv.data_ptr(), _ptr(sel_scores), score_stride, _ptr(sel_hist),
-          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+          ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, dev))
 
 
 def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefix, k_cache, v_cache,
@@ -617,13 +618,13 @@ def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_pre
     if idx is None or idx.dim() != 3:
         raise ValueError("idx must be [B, Hkv, idx_stride]")
     idx_stride = idx.shape[2]
-    _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
-                (idx, torch.int32, (B, Hkv, idx_stride), "idx"), (count, torch.int32, (B, Hkv), "count"),
-                *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
+    dev = _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
+                      (idx, torch.int32, (B, Hkv, idx_stride), "idx"), (count, torch.int32, (B, Hkv), "count"),
+                      *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
     _call("embla_sparse_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
           k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           idx.data_ptr(), idx_stride, count.data_ptr(),
-          shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream))
+          shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream, dev))
 
 
 def embla_window_decode(shape: Shape, q, k_win, v_win, pos: int, out, window: int = 128,
