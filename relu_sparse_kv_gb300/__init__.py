@@ -601,7 +601,7 @@ def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefi
     if ws is None:
         ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device)
         if stream is not None:
-            ws.record_stream(stream, dev)  # its memory is not handed out again before the call is done
+            ws.record_stream(stream)  # its memory is not handed out again before the call is done
     _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
           k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), alpha, c,
           eps, out.data_ptr(), n_surv.data_ptr(), _ptr(sel_scores), score_stride, _ptr(sel_hist),
