@@ -183,9 +183,15 @@ def _call(name, *args):
         raise EmblaError(name, st)
 
 
-def _workspace(nbytes: int, workspace, device):
+def _workspace(nbytes: int, workspace, device, stream=None):
+    """The caller's workspace, or one made for this call.  That one is allocated on the stream it
+    is used on: the allocator hands memory out again in the order of the stream it came from, so
+    whoever had it before is done with it by then, and so is this call before the next."""
     if workspace is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        if stream is None:
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     if workspace.numel() * workspace.element_size() < nbytes:
         raise EmblaError("workspace", 3)
     return workspace
@@ -223,7 +229,7 @@ def embla_full_decode(shape: Shape, q, k_cache, v_cache, out, n_surv, sel_scores
     _check(n_surv, torch.int32, (B, Hkv), "n_surv")
     _check(sel_scores, torch.float32, (B, Hkv, ncap), "sel_scores", allow_none=True)
     _check(sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist", allow_none=True)
-    ws = _workspace(embla_full_decode_workspace_size(shape), workspace, q.device)
+    ws = _workspace(embla_full_decode_workspace_size(shape), workspace, q.device, stream)
     _call("embla_full_decode", ctypes.byref(shape.c()), _ptr(q), _ptr(k_cache), _ptr(v_cache),
           alpha, c, eps, _ptr(out), _ptr(n_surv), _ptr(sel_scores), _ptr(sel_hist), _ptr(ws),
           ws.numel() * ws.element_size(), _stream(stream))
@@ -246,7 +252,7 @@ def embla_full_decode_e4m3(shape: Shape, q, k_codes, k_scales, v_codes, v_scales
     _check(n_surv, torch.int32, (B, Hkv), "n_surv")
     _check(sel_scores, torch.float32, (B, Hkv, ncap), "sel_scores", allow_none=True)
     _check(sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist", allow_none=True)
-    ws = _workspace(embla_full_decode_workspace_size(shape), workspace, q.device)
+    ws = _workspace(embla_full_decode_workspace_size(shape), workspace, q.device, stream)
     _call("embla_full_decode_e4m3", ctypes.byref(shape.c()), _ptr(q), _ptr(k_codes),
           _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), alpha, c, eps, _ptr(out), _ptr(n_surv),
           _ptr(sel_scores), _ptr(sel_hist), _ptr(ws), ws.numel() * ws.element_size(),
@@ -284,7 +290,7 @@ def embla_select_topk(shape: Shape, sel_scores, sel_hist, idx, count, topk: int 
         raise ValueError("idx must be [B, Hkv, idx_stride]")
     _check(count, torch.int32, (B, Hkv), "count")
     ws = _workspace(embla_select_topk_workspace_size(shape, topk, recent), workspace,
-                    sel_scores.device)
+                    sel_scores.device, stream)
     _call("embla_select_topk", ctypes.byref(shape.c()), _ptr(sel_scores), _ptr(sel_hist), topk,
           recent, _ptr(idx), idx.shape[2], _ptr(count), _ptr(ws), ws.numel() * ws.element_size(),
           _stream(stream))
@@ -381,7 +387,7 @@ def embla_full_decode_select(shape: Shape, q, k_cache, v_cache, out, n_surv, sel
     _check(sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist")
     _check_select_outputs(shape, idx, count)
     ws = _workspace(embla_full_decode_select_workspace_size(shape, topk, recent), workspace,
-                    q.device)
+                    q.device, stream)
     _call("embla_full_decode_select", ctypes.byref(shape.c()), _ptr(q), _ptr(k_cache),
           _ptr(v_cache), alpha, c, eps, _ptr(out), _ptr(n_surv), _ptr(sel_scores),
           _ptr(sel_hist), topk, recent, _ptr(idx), idx.shape[2], _ptr(count), _ptr(ws),
@@ -406,7 +412,7 @@ def embla_full_decode_e4m3_select(shape: Shape, q, k_codes, k_scales, v_codes, v
     _check(sel_hist, torch.int32, (B, Hkv, HIST_BINS), "sel_hist")
     _check_select_outputs(shape, idx, count)
     ws = _workspace(embla_full_decode_select_workspace_size(shape, topk, recent), workspace,
-                    q.device)
+                    q.device, stream)
     _call("embla_full_decode_e4m3_select", ctypes.byref(shape.c()), _ptr(q), _ptr(k_codes),
           _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), alpha, c, eps, _ptr(out), _ptr(n_surv),
           _ptr(sel_scores), _ptr(sel_hist), topk, recent, _ptr(idx), idx.shape[2], _ptr(count),
@@ -426,7 +432,7 @@ def embla_sparse_decode(shape: Shape, q, k_cache, v_cache, idx, count, out, tau:
     _check(count, torch.int32, (B, Hkv), "count")
     _check(out, torch.float32, (B, Hq, D), "out")
     tau = D ** -0.5 if tau is None else tau
-    ws = _workspace(embla_sparse_decode_workspace_size(shape, idx.shape[2]), workspace, q.device)
+    ws = _workspace(embla_sparse_decode_workspace_size(shape, idx.shape[2]), workspace, q.device, stream)
     _call("embla_sparse_decode", ctypes.byref(shape.c()), _ptr(q), _ptr(k_cache), _ptr(v_cache),
           _ptr(idx), idx.shape[2], _ptr(count), tau, _ptr(out), _ptr(ws),
           ws.numel() * ws.element_size(), _stream(stream))
@@ -448,7 +454,7 @@ def embla_sparse_decode_e4m3(shape: Shape, q, k_codes, k_scales, v_codes, v_scal
     _check(count, torch.int32, (B, Hkv), "count")
     _check(out, torch.float32, (B, Hq, D), "out")
     tau = D ** -0.5 if tau is None else tau
-    ws = _workspace(embla_sparse_decode_workspace_size(shape, idx.shape[2]), workspace, q.device)
+    ws = _workspace(embla_sparse_decode_workspace_size(shape, idx.shape[2]), workspace, q.device, stream)
     _call("embla_sparse_decode_e4m3", ctypes.byref(shape.c()), _ptr(q), _ptr(k_codes),
           _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(idx), idx.shape[2], _ptr(count),
           tau, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -471,7 +477,7 @@ def embla_prefill(shape: Shape, q, k_cache, v_cache, out, alpha: float = 1.0, c:
     _check(k_cache, torch.bfloat16, (B, Hkv, ncap, D), "k_cache")
     _check(v_cache, torch.bfloat16, (B, Hkv, ncap, D), "v_cache")
     _check(out, torch.float32, (B, Hq, T, D), "out")
-    ws = _workspace(embla_prefill_workspace_size(shape), workspace, q.device)
+    ws = _workspace(embla_prefill_workspace_size(shape), workspace, q.device, stream)
     _call("embla_prefill", ctypes.byref(shape.c()), T, _ptr(q), _ptr(k_cache), _ptr(v_cache),
           alpha, c, eps, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
 
@@ -494,7 +500,7 @@ def embla_relu2_mlp(x, w_up, w_down, y, n_live, workspace=None, stream=None):
     _check(w_down, torch.bfloat16, (f, d), "w_down")
     _check(y, torch.float32, (d,), "y")
     _check(n_live, torch.int32, (1,), "n_live")
-    ws = _workspace(embla_relu2_mlp_workspace_size(d, f), workspace, x.device)
+    ws = _workspace(embla_relu2_mlp_workspace_size(d, f), workspace, x.device, stream)
     _call("embla_relu2_mlp", d, f, _ptr(x), _ptr(w_up), _ptr(w_down), _ptr(y), _ptr(n_live),
           _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
 
@@ -513,7 +519,7 @@ def embla_full_decode_head_scores(shape: Shape, q, k_cache, v_cache, out, n_surv
     _check(n_surv, torch.int32, (B, Hkv), "n_surv")
     _check(head_scores, torch.float32, (B, Hq, ncap), "head_scores")
     _check(head_hist, torch.int32, (B, Hq, HIST_BINS), "head_hist")
-    ws = _workspace(embla_full_decode_workspace_size(shape), workspace, q.device)
+    ws = _workspace(embla_full_decode_workspace_size(shape), workspace, q.device, stream)
     _call("embla_full_decode_head_scores", ctypes.byref(shape.c()), _ptr(q), _ptr(k_cache),
           _ptr(v_cache), alpha, c, eps, _ptr(out), _ptr(n_surv), _ptr(head_scores),
           _ptr(head_hist), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
@@ -531,7 +537,7 @@ def embla_select_topk_per_head(shape: Shape, head_scores, head_hist, idx, count,
     _check(count, torch.int32, (B, Hq), "count")
     nbytes = library().embla_select_topk_per_head_workspace_size(ctypes.byref(shape.c()), topk,
                                                                  recent)
-    ws = _workspace(nbytes, workspace, head_scores.device)
+    ws = _workspace(nbytes, workspace, head_scores.device, stream)
     _call("embla_select_topk_per_head", ctypes.byref(shape.c()), _ptr(head_scores),
           _ptr(head_hist), topk, recent, _ptr(idx), idx.shape[2], _ptr(count), _ptr(ws),
           ws.numel() * ws.element_size(), _stream(stream))
@@ -551,7 +557,7 @@ def embla_sparse_decode_per_head(shape: Shape, q, k_cache, v_cache, idx, count, 
     _check(count, torch.int32, (B, Hq), "count")
     _check(out, torch.float32, (B, Hq, D), "out")
     tau = D ** -0.5 if tau is None else tau
-    ws = _workspace(embla_sparse_decode_workspace_size(shape, idx.shape[2]), workspace, q.device)
+    ws = _workspace(embla_sparse_decode_workspace_size(shape, idx.shape[2]), workspace, q.device, stream)
     _call("embla_sparse_decode_per_head", ctypes.byref(shape.c()), _ptr(q), _ptr(k_cache),
           _ptr(v_cache), _ptr(idx), idx.shape[2], _ptr(count), tau, _ptr(out), _ptr(ws),
           ws.numel() * ws.element_size(), _stream(stream))
@@ -599,9 +605,7 @@ def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefi
     # a workspace of the caller's is checked against the size by the C call
     ws = workspace
     if ws is None:
-        ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device)
-        if stream is not None:
-            ws.record_stream(stream)  # its memory is not handed out again before the call is done
+        ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device, stream)
     _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
           k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), alpha, c,
           eps, out.data_ptr(), n_surv.data_ptr(), _ptr(sel_scores), score_stride, _ptr(sel_hist),
