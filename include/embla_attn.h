@@ -273,7 +273,8 @@ embla_status embla_sparse_decode_e4m3(const embla_shape *shape, const void *q,
  * The selection is embla_select_topk on a shape whose ctx_len is prefix_len + ctx_len and whose
  * cache_stride is score_stride.  A key of weight zero contributes nothing, whatever its value
  * row holds; a call that meets an infinite or NaN value row gives those sums by a slow path.
- * A NaN score (a key or query row holding NaN, an all-zero row with eps == 0) weighs nothing.
+ * A NaN score (a key or query row holding NaN, an all-zero row with eps == 0) weighs nothing, and
+ * a key whose scores are NaN for every head of the group has sigma_j = -infinity: it ranks last.
  *
  * embla_sparse_decode_shared: embla_sparse_decode on those contexts.
  *   idx, idx_stride, count   as for embla_sparse_decode, indices in [0, prefix_len + ctx_len)

@@ -45,6 +45,7 @@
 // histogram's reading of 68 MB of scores, most of which L2 no longer holds, stored evict_last or
 // not).  Without scores and histogram: 25.3, 15.2 and 60.6 us.
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "ptx_blocks.cuh"
@@ -123,6 +124,13 @@ __device__ __forceinline__ void add2(float &a0, float &a1, float b0, float b1) {
       "mov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
+}
+
+// The largest of three; NaN counts as absent.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // A CTA's part of the work: pieces of row block rb's tile list, and the stretch (the part of
@@ -503,13 +511,19 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float2 rk = rks[j];
+              float s0 = 0.0f, s1 = 0.0f;  // the first of the two rows' scores
 #pragma unroll
               for (int m = 0; m < 2; ++m) {
                 float v0 = __uint_as_float(acc[4 * j + 2 * m]), v1 = __uint_as_float(acc[4 * j + 2 * m + 1]);
                 mul2(v0, v1, rk.x, rk.y);
                 mul2(v0, v1, rq[2 * side + m], rq[2 * side + m]);
-                top[2 * j] = side == 0 && m == 0 ? v0 : fmaxf(top[2 * j], v0);
-                top[2 * j + 1] = side == 0 && m == 0 ? v1 : fmaxf(top[2 * j + 1], v1);
+                if (m == 0) {
+                  s0 = v0, s1 = v1;
+                } else {
+                  // from minus infinity: a key whose score is NaN for every head ranks last
+                  top[2 * j] = max3(side == 0 ? -INFINITY : top[2 * j], s0, v0);
+                  top[2 * j + 1] = max3(side == 0 ? -INFINITY : top[2 * j + 1], s1, v1);
+                }
                 float w0 = __saturatef(v0 * f), w1 = __saturatef(v1 * f);
                 mul2(w0, w1, w0, w1);
                 add2(den[2 * side + m][0], den[2 * side + m][1], w0, w1);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import relu_sparse_kv_gb300 as E
-from test_gpu_shared import D, make, run
+from test_gpu_shared import D, histogram, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,42 @@ def test_workspaces_of_calls_on_different_streams_do_not_meet():
     assert E.embla_device_check() == 0
     for o in outs:
         assert all(torch.equal(a, b) for a, b in zip(alone, o))
+
+
+@pytest.mark.parametrize("G,Hkv,sstride", [(4, 4, 2304), (4, 2, 2301), (8, 2, 2304)])
+def test_keys_without_a_number_rank_last(G, Hkv, sstride):
+    """NaN key rows in the prefix and in own caches, all-zero rows with eps = 0, a NaN query head:
+    scores, counts, histogram and selection are those of embla_full_decode on the whole contexts
+    (scores to the tests' 60u of 128, which is 5e-4; the selection of the call's own scores exactly)."""
+    B, P, n = 3, 2200, 100
+    q, kp, vp, ko, vo = make(B, Hkv, G, P, n, 400 + G)
+    kp[0, 5, 3] = float("nan")
+    kp[1, 40:60] = 0.0
+    kp[:, 700:1200] = float("nan")
+    ko[1, 1, 99] = float("nan")
+    ko[2, 0, :64] = 0.0
+    q[0, 2] = float("nan")             # one head of a group: the others rank the keys
+    q[2, Hkv * G - G:] = 0.0           # a whole group of zero queries: no score at all
+    N = P + n
+    out, ns, scores, hist = run(q, kp, vp, ko, vo, P, n, sstride, eps=0.0)
+    K = torch.cat([kp[None].expand(B, -1, -1, -1), ko], 2).contiguous()
+    V = torch.cat([vp[None].expand(B, -1, -1, -1), vo], 2).contiguous()
+    out2, ns2, sig2 = torch.empty_like(out), torch.empty_like(ns), torch.empty(B, Hkv, N, device="cuda")
+    E.embla_full_decode(E.Shape(B, Hkv * G, Hkv, D, N, N), q, K, V, out2, ns2, sig2, torch.empty_like(hist), eps=0.0)
+    torch.cuda.synchronize()
+    got = scores[..., :N]
+    gone = got == -float("inf")
+    assert torch.equal(gone, sig2 == -float("inf")) and torch.isfinite(got[~gone]).all()
+    assert gone[:, 0, 5].all() and gone[:, 1, 40:60].all() and gone[1, 1, P + 99] and gone[2, 0, P:P + 64].all()
+    assert gone[2, Hkv - 1].all() and not gone[0, 0].all()
+    assert ((got - sig2)[~gone].abs() <= 5e-4).all()
+    assert torch.equal(ns, (got > 0).sum(-1).int()) and torch.equal(hist, histogram(got))
+    idx = torch.full((B, Hkv, 1152), -9, dtype=torch.int32, device="cuda")
+    cnt = torch.empty(B, Hkv, dtype=torch.int32, device="cuda")
+    E.embla_select_topk(E.Shape(B, Hkv * G, Hkv, D, N, sstride), scores, hist, idx, cnt)
+    # equal scores: the smaller index first
+    best = got[..., :N - 128].sort(dim=-1, descending=True, stable=True).indices[..., :1024].sort(-1).values
+    want = torch.cat([best, torch.arange(N - 128, N, device="cuda").expand(B, Hkv, -1)], -1)
+    numbers = ~gone[..., :N - 128].all(-1)  # (a unit without any number has no best keys)
+    assert (cnt == 1152)[numbers].all() and torch.equal(idx.long()[numbers], want[numbers])
+    assert E.embla_device_check() == 0
