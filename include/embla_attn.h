@@ -168,7 +168,8 @@ embla_status embla_full_decode_static_scratch(const embla_shape *shape, const vo
  * keys with the highest sel_scores among j < n - recent (equal scores: the
  * smaller index first) together with the `recent` newest keys n-recent..n-1;
  * every key when n <= topk + recent.
- *   sel_scores, sel_hist  as written by embla_full_decode for the same shape
+ *   sel_scores, sel_hist  as written by embla_full_decode for the same shape (no NaN; a key
+ *              without a score holds -infinity and is selected after every other)
  *   topk, recent          >= 0 (1024 and 128 in Embla 1)
  *   idx        int32 [B, Hkv, idx_stride], idx_stride >= topk + recent:
  *              selected key indices in ascending order; entries at and past

@@ -30,6 +30,8 @@
 //      distributed shared memory, and writes its indices in ascending order.
 #include <cooperative_groups.h>
 
+#include <cmath>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -540,6 +542,12 @@ __device__ __forceinline__ float key_float(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+// The lowest score of bin b.  The bin of minus infinity (key 0x007FFFFF) begins with keys of NaN,
+// which no score compares with: minus infinity is the lowest score there.
+__device__ __forceinline__ float bin_floor(uint32_t b) {
+  return b == (0x007FFFFFu >> 21) ? -INFINITY : key_float(b << 21);
+}
+
 constexpr int kUMaxCluster = 8;
 #ifndef EMBLA_SEL_CHUNK_TARGET
 #define EMBLA_SEL_CHUNK_TARGET 8192
@@ -804,7 +812,7 @@ __global__ void __launch_bounds__(kUThreads, 1) select_single_kernel(const FastP
   // order keys of b* are [b* << 21, (b* + 1) << 21): a score at or above f_take is selected,
   // one at or above f_lo and below f_take is a candidate
   const uint32_t bstar = static_cast<uint32_t>(sh.bin);
-  const float f_lo = key_float(bstar << 21);
+  const float f_lo = bin_floor(bstar);
   const float f_take = bstar + 1 < kHistBins ? key_float((bstar + 1) << 21) : __uint_as_float(0x7FC00000u);
   int need = p.topk - sh.above;
 
@@ -1062,7 +1070,7 @@ __global__ void __launch_bounds__(kUThreads, 1) select_cluster_kernel(const Fast
   // order keys of b* are [b* << 21, (b* + 1) << 21): a score at or above f_take is selected,
   // one at or above f_lo and below f_take is a candidate
   const uint32_t bstar = static_cast<uint32_t>(sh.bin);
-  const float f_lo = key_float(bstar << 21);
+  const float f_lo = bin_floor(bstar);
   const float f_take = bstar + 1 < kHistBins ? key_float((bstar + 1) << 21) : __uint_as_float(0x7FC00000u);
   int need = p.topk - sh.above;
 
