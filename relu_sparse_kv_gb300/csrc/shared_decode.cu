@@ -487,6 +487,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       for (int t = w.t0 + skip, it = i + skip; t < w.t1; t += kGroups, it += kGroups) {
         const int s = it % kRing;
         ok = mbar_wait(&sfull[s], (it / kRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);  // the warp works on the tile together or not at all
         if (!ok) break;
         const bool own = t >= tp;
         const int x = t - tp;
@@ -608,7 +609,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
       }
       i += w.t1 - w.t0;
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ok = mbar_wait(ofull, k & 1) && !*s_abort;
       ok = __all_sync(0xffffffffu, ok);
