@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     // The warp walks together and one lane issues (elect_one).
     const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
     const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
-    int i = 0;
+    int i = 0, done = 0;
     bool ok = true;
     pdl_wait_primary();
     for (int k = 0; ok && w.next(); ++k) {
@@ -363,10 +363,18 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
         __syncwarp();
       }
-      if (ok && elect_one()) tc_commit(qempty);
-      __syncwarp();
+      if (ok) {
+        if (elect_one()) tc_commit(qempty);
+        __syncwarp();
+        done = k + 1;
+      }
     }
     if (!ok && lane == 0) give_up(s_abort, p.flags);
+    // every MMA of this warp has completed, and its last commit arrived, before the tensor memory
+    // is released and the CTA leaves (also when another role has given up)
+    if (i > 0) mbar_wait(&sfull[(i - 1) % kRing], ((i - 1) / kRing) & 1);
+    if (done > 0) mbar_wait(qempty, (done - 1) & 1);
+    __syncwarp();
   } else if (warp == kWarpPV) {
     // ------------------------------------------------------------------ P V issuer
     const uint64_t vdesc = smem_desc_sw128_mn(smem_u32(sV), kBox);
