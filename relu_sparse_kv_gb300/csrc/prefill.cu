@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (idx < 0) break;
       const RowBlock rb = row_block(p, idx);
       const int64_t pos = rb.p0 + r;  // this row's position
-      ok = !*s_abort && mbar_wait(qfull, k & 1);
+      // (every decision to go on is the warp's: what follows is warp-wide)
+      ok = __all_sync(0xffffffffu, !*s_abort && mbar_wait(qfull, k & 1));
       float a2 = 0.0f;  // alpha^2 / (mean(q^2) + eps)
       if (ok) {
         float a[8];
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int kt = 0; ok && kt < rb.nkt; ++kt, ++g) {
         const int sb = g % kRing;
         ok = mbar_wait(&sfull[sb], (g / kRing) & 1) && mbar_wait(&rkfull[sb], (g / kRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t cols = tmem + lane_base + sb * 128 + cg * kEpiCols;
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           mbar_arrive_after(&rkempty[sb], used);
         }
       }
-      if (ok) ok = mbar_wait(ofull, k & 1) && !*s_abort;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(ofull, k & 1) && !*s_abort);
       // The row's output: O from tensor memory; the parts of each row add their weight sums,
       // exchanged through the first O column of each part once every part has read its O.
       uint32_t o[kEpiCols];
