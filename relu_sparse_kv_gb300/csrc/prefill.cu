@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (lane == 0) {
       const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
       const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
-      int g = 0;
+      int g = 0, blocks = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int idx = block_of(p, k, cta, G);
@@ -284,9 +284,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           tc_commit(&sfull[sb]);
         }
-        if (ok) tc_commit(qempty);
+        if (ok) {
+          tc_commit(qempty);
+          blocks = k + 1;
+        }
       }
       if (!ok) set_abort_p(s_abort, p.flags);
+      // every MMA of this thread has completed, and its last commit arrived, before the tensor
+      // memory is released and the CTA leaves (also when another role has given up)
+      if (g > 0) mbar_wait(&sfull[(g - 1) % kRing], ((g - 1) / kRing) & 1);
+      if (blocks > 0) mbar_wait(qempty, (blocks - 1) & 1);
     }
     __syncwarp();
   } else if (warp == kWarpPV) {
