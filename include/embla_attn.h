@@ -276,6 +276,9 @@ embla_status embla_sparse_decode_e4m3(const embla_shape *shape, const void *q,
  * row holds; a call that meets an infinite or NaN value row gives those sums by a slow path.
  * A NaN score (a key or query row holding NaN, an all-zero row with eps == 0) weighs nothing, and
  * a key whose scores are NaN for every head of the group has sigma_j = -infinity: it ranks last.
+ * Scores and value sums run on the tensor cores; the weights enter the value product as two bf16
+ * parts (hi + lo, about 17 bits), and sums longer than 8,192 keys are continued in fp32: the output
+ * is within 4e-5 of sum w |v| / (c + sum w) for a context of any length (a few 1e-6 for short ones).
  *
  * embla_sparse_decode_shared: embla_sparse_decode on those contexts.
  *   idx, idx_stride, count   as for embla_sparse_decode, indices in [0, prefix_len + ctx_len)

@@ -89,6 +89,14 @@ __device__ __forceinline__ void st_global_if(bool on, float *dst, float a) {
       : "memory");
 }
 
+// Four floats added to global memory (dst 16-byte aligned): the additions of one thread to one
+// address happen in its order.
+__device__ __forceinline__ void red_global_add_v4(float *dst, float a0, float a1, float a2, float a3) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "f"(a0), "f"(a1),
+               "f"(a2), "f"(a3)
+               : "memory");
+}
+
 // a - lo(w), b - hi(w) for the two bf16 values packed in w (each one rounding in fp32).
 __device__ __forceinline__ void sub_bf16x2(uint32_t w, float &a, float &b) {
   asm("{\n\t.reg .b16 lo, hi, m;\n\t"

@@ -85,8 +85,8 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) MN-major
 constexpr int kColO = kRing * 128, kTmemCols = 512;
 
-// A record: the numerators of 128 rows, each row's denominator and each sequence's
-// survivor count for each quarter of the tiles' keys.
+// A record, the sums of one KV head's tiles in one piece: the numerators of 128 rows, each row's
+// denominator and each sequence's survivor count for each quarter of the tiles' keys.
 constexpr int kRecNum = kRows * kHeadDim;
 constexpr int kRecDen = kParts * kRows;
 constexpr int kRecCnt = kParts * 32;
@@ -133,15 +133,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// A CTA's part of the work: pieces of row block rb's tile list, and the stretch (the part of
-// it inside one KV head's list) at hand.
+// The tensor cores add to an fp32 accumulator by cutting the sum off, not rounding it: values of one
+// sign lose 4.5e-7 of their sum per tile (measured: 1.3e-5 after 32 tiles, 1.15e-3 after 2,048).  So the
+// sum in tensor memory ends after kMaxTiles tiles and goes to the record, where the next one is
+// added with a rounding of its own: at most 2.9e-5 for a prefix of any length, at 5 us every 64
+// tiles (2,048 tiles per CTA: 2.32 ms, in one sum 2.16; B 64 with a 64k prefix has 40 and ends
+// nowhere: 75.5 us, with 32 tiles at most 79.7).
+constexpr int kMaxTiles = 64;
+
+// A CTA's part of the work: a piece of row block rb's tile list, taken in stretches of at most
+// kMaxTiles tiles of one KV head's list.
 struct Walk {
   int rb, nb;        // the row block, its sequences
   uint32_t gt;       // tiles per KV head
   uint32_t t, end;   // the next tile, the piece's end
   int piece;
   int g, t0, t1;     // stretch: KV head, tiles [t0, t1) of its list
+  int s0;            // the first tile of the head's list in this piece
   __device__ Walk(const SharedSplit &sp, int cta) {
+    g = -1;
     rb = sp.block_of_cta(cta);
     piece = cta - rb * sp.ctas_full;
     nb = sp.sequences(rb);
@@ -152,11 +162,13 @@ struct Walk {
   }
   __device__ bool next() {
     if (t >= end) return false;
-    g = static_cast<int>(t / gt);
-    t0 = static_cast<int>(t - g * gt);
-    const uint32_t left = end - t;
-    t1 = static_cast<int>(gt - t0 < left ? gt : t0 + left);
-    t += t1 - t0;
+    const int head = static_cast<int>(t / gt);
+    t0 = static_cast<int>(t - head * gt);
+    if (head != g) g = head, s0 = t0;
+    uint32_t m = gt - t0 < end - t ? gt - t0 : end - t;
+    if (m > kMaxTiles) m = kMaxTiles;
+    t1 = t0 + static_cast<int>(m);
+    t += m;
     return true;
   }
 };
@@ -648,15 +660,33 @@ __global__ void __launch_bounds__(kSThreads, 1)
         if (m == q4) dsum = d;
       }
       float *rec = p.rec + sp.slot(w.rb, w.piece, w.g) * kRecWords;
-      if (seq >= first_seq && seq <= last_seq) {
-        rec[kRecNum + part * kRows + quarter * 32 + (lane >> 2) + 8 * q4] = dsum;
-        if (!SCORES && q4 == 0 && odd == 0)
-          reinterpret_cast<int32_t *>(rec)[kRecNum + kRecDen + part * 32 + seq] = live;
-      }
+      float *rec_den = rec + kRecNum + part * kRows + quarter * 32 + (lane >> 2) + 8 * q4;
+      int32_t *rec_cnt = reinterpret_cast<int32_t *>(rec) + kRecNum + kRecDen + part * 32 + seq;
+      const bool counts = !SCORES && q4 == 0 && odd == 0;
       // the numerators: lane l holds row l of the quarter, of sequence
       const int row_seq = quarter * kSeqsQ + (lane & 7) / (G / 4);
-      if (row_seq >= first_seq && row_seq <= last_seq) {
-        float *dst = rec + (quarter * 32 + lane) * kHeadDim + part_col;
+      float *dst = rec + (quarter * 32 + lane) * kHeadDim + part_col;
+      const bool den_here = seq >= first_seq && seq <= last_seq, num_here = row_seq >= first_seq && row_seq <= last_seq;
+      // the last sequence that earlier stretches of the head's list wrote rows for (-1: none)
+      int written = -1;
+      if (__builtin_expect(w.t0 != w.s0, 0)) {
+        written = w.s0 < tp ? w.nb - 1 : (w.t0 - 1 - tp) / ts;
+        // added to those by the same threads, in their order
+        if (den_here && seq <= written) {
+          atomicAdd(rec_den, dsum);
+          if (counts) atomicAdd(rec_cnt, live);
+        }
+        if (num_here && row_seq <= written)
+#pragma unroll
+          for (int c = 0; c < kPartCols; c += 4)
+            red_global_add_v4(dst + c, __uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
+                              __uint_as_float(o[c + 3]));
+      }
+      if (den_here && seq > written) {
+        *rec_den = dsum;
+        if (counts) *rec_cnt = live;
+      }
+      if (num_here && row_seq > written) {
 #pragma unroll
         for (int c = 0; c < kPartCols; c += 8)
           st_global_v8(dst + c, __uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),

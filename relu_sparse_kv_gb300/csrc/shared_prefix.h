@@ -10,7 +10,7 @@ namespace embla {
 // of one KV head of 128 / G sequences make a row block; its work per KV head is a list of
 // 128-key tiles, the prefix's tp tiles and then each of its sequences' ts own tiles, and the
 // lists of the KV heads follow one another.  Each row block's list is cut into as many equal
-// pieces as it gets CTAs; the record of the stretch of KV head g inside piece q lives in
+// pieces as it gets CTAs; the record of KV head g's tiles inside piece q lives in
 // slot(rb, q, g).  Tiles times pieces of a row block stay below 2^31 (fits()), so the device
 // splits in 32 bits.
 struct SharedSplit {

@@ -83,3 +83,40 @@ def test_keys_without_a_number_rank_last(G, Hkv, sstride):
     numbers = ~gone[..., :N - 128].all(-1)  # (a unit without any number has no best keys)
     assert (cnt == 1152)[numbers].all() and torch.equal(idx.long()[numbers], want[numbers])
     assert E.embla_device_check() == 0
+
+
+@pytest.mark.parametrize("Hkv,G,P,n,scores", [
+    (1, 8, 262144, 0, True), (1, 4, 262144, 0, False),  # 2,048 prefix tiles per CTA
+    (2, 8, 1000, 1500, True), (2, 4, 130, 900, False),  # own tiles of many sequences, two lists
+])
+def test_sums_of_many_tiles_do_not_drift(Hkv, G, P, n, scores):
+    """A row block per SM, so that a CTA adds up all tiles of its sequences; values of one sign, so
+    that errors add up too.  Bounds of the test file beside this one, with the sums as the kernel
+    takes them: in tensor memory at most 64 tiles of 16 additions (8 steps, hi and lo) of at most
+    4u each, the denominators 8 additions per tile and chain of at most u, and at most 64 fp32
+    additions of such sums, whatever the length of the context."""
+    B, u = 128 // G * E.embla_device_sm_count(), 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(P + n)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+    q, kp, vp = rnd(B, Hkv * G, D), rnd(Hkv, P, D), rnd(Hkv, P, D).abs()
+    ko, vo = rnd(B, Hkv, n, D), rnd(B, Hkv, n, D).abs()
+    out, ns, _, _ = run(q, kp, vp, ko, vo, P, n, sel=scores)
+    norm = lambda x: x / (x.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    for b in (0, 1, 128 // G - 1, B // 2 + 3, B - 1):
+        for h in range(Hkv):
+            rows = slice(h * G, (h + 1) * G)
+            k = norm(torch.cat([kp[h], ko[b, h]]).double())
+            v = torch.cat([vp[h], vo[b, h]]).double()
+            qq = norm(q[b, rows].double())
+            s = (qq @ k.T).clamp(min=0)
+            ds = 60 * u * (qq.abs() @ k.abs().T)
+            w, dw = s.square(), 2 * s * ds + ds.square() + s.square() * (2.0 ** -17 + 2 * u)
+            z = 1 + w.sum(-1, keepdim=True)
+            num, want = w @ v, (w @ v) / z
+            dnum = dw @ v + (4 * u * 16 * 64 + 64 * u) * num
+            dz = dw.sum(-1, keepdim=True) + (8 * 64 + 64) * u * w.sum(-1, keepdim=True) + 4 * u * z
+            tol = (dnum + want * dz) / z + 4 * u * want
+            err = (out[b, rows].double() - want).abs()
+            assert (err <= tol).all(), (b, h, float((err / want).max()), float((err / tol).max()))
+            sure = (qq @ k.T).amax(0)
+            assert int((sure > ds.amax(0)).sum()) <= int(ns[b, h]) <= int((sure > -ds.amax(0)).sum())
