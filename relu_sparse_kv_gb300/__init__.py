@@ -568,29 +568,35 @@ def embla_full_decode_shared_workspace_size(shape: Shape, prefix_len: int) -> in
 
 
 def _shared_caches(shape: Shape, prefix_len: int, k_prefix, v_prefix, k_cache, v_cache):
-    """The checks of k_prefix and v_prefix (bf16 [Hkv, prefix_stride, D] holding prefix_len rows at
-    least) and of the own caches."""
-    if k_prefix is None or k_prefix.dim() != 3 or prefix_len > k_prefix.shape[1]:
-        raise ValueError("k_prefix must be [Hkv, prefix_stride, D], prefix_stride >= prefix_len")
-    pre = (shape.n_kv_heads, k_prefix.shape[1], shape.head_dim)
-    own = (shape.batch, shape.n_kv_heads, shape.cache_stride, shape.head_dim)
-    return ((k_prefix, torch.bfloat16, pre, "k_prefix"), (v_prefix, torch.bfloat16, pre, "v_prefix"),
-            (k_cache, torch.bfloat16, own, "k_cache"), (v_cache, torch.bfloat16, own, "v_cache"))
+    """prefix_stride, and the checks of k_prefix and v_prefix (bf16 [Hkv, prefix_stride, D] holding
+    prefix_len rows at least) and of the own caches.  Both tensors of a side without keys may be None."""
+    stride, checks = 0, []
+    if prefix_len != 0 or k_prefix is not None or v_prefix is not None:
+        if k_prefix is None or k_prefix.dim() != 3 or prefix_len > k_prefix.shape[1]:
+            raise ValueError("k_prefix must be [Hkv, prefix_stride, D], prefix_stride >= prefix_len")
+        stride = k_prefix.shape[1]
+        pre = (shape.n_kv_heads, stride, shape.head_dim)
+        checks += [(k_prefix, torch.bfloat16, pre, "k_prefix"), (v_prefix, torch.bfloat16, pre, "v_prefix")]
+    if shape.ctx_len != 0 or k_cache is not None or v_cache is not None:
+        own = (shape.batch, shape.n_kv_heads, shape.cache_stride, shape.head_dim)
+        checks += [(k_cache, torch.bfloat16, own, "k_cache"), (v_cache, torch.bfloat16, own, "v_cache")]
+    return stride, checks
 
 
 def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefix, k_cache, v_cache,
                              out, n_surv, sel_scores=None, sel_hist=None, alpha: float = 1.0,
                              c: float = 1.0, eps: float = 1e-6, workspace=None, stream=None):
     """embla_full_decode of sequences that share their first prefix_len keys (k_prefix, v_prefix
-    bf16 [Hkv, prefix_stride, D]) and go on with shape.ctx_len keys of their own caches;
+    bf16 [Hkv, prefix_stride, D]) and go on with shape.ctx_len keys of their own caches (a side
+    without keys may be None, None);
     sel_scores fp32 [B, Hkv, score_stride] holds the scores of prefix and own keys, and
     embla_select_topk takes it with Shape(..., ctx_len=prefix_len + shape.ctx_len,
     cache_stride=score_stride)."""
     B, Hkv = shape.batch, shape.n_kv_heads
     heads = (B, shape.n_q_heads, shape.head_dim)
+    prefix_stride, caches = _shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)
     tensors = [(q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
-               (n_surv, torch.int32, (B, Hkv), "n_surv"),
-               *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)]
+               (n_surv, torch.int32, (B, Hkv), "n_surv"), *caches]
     score_stride = 0
     if sel_scores is not None:
         if sel_scores.dim() != 3:
@@ -606,8 +612,8 @@ def embla_full_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_prefi
     ws = workspace
     if ws is None:
         ws = _workspace(embla_full_decode_shared_workspace_size(shape, prefix_len), None, q.device, stream)
-    _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
-          k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), alpha, c,
+    _call("embla_full_decode_shared", ctypes.byref(shape.c()), prefix_len, prefix_stride, q.data_ptr(),
+          _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache), alpha, c,
           eps, out.data_ptr(), n_surv.data_ptr(), _ptr(sel_scores), score_stride, _ptr(sel_hist),
           ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream, dev))
 
@@ -622,11 +628,12 @@ def embla_sparse_decode_shared(shape: Shape, prefix_len: int, q, k_prefix, v_pre
     if idx is None or idx.dim() != 3:
         raise ValueError("idx must be [B, Hkv, idx_stride]")
     idx_stride = idx.shape[2]
+    prefix_stride, caches = _shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache)
     dev = _check_here((q, torch.bfloat16, heads, "q"), (out, torch.float32, heads, "out"),
                       (idx, torch.int32, (B, Hkv, idx_stride), "idx"), (count, torch.int32, (B, Hkv), "count"),
-                      *_shared_caches(shape, prefix_len, k_prefix, v_prefix, k_cache, v_cache))
-    _call("embla_sparse_decode_shared", ctypes.byref(shape.c()), prefix_len, k_prefix.shape[1], q.data_ptr(),
-          k_prefix.data_ptr(), v_prefix.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                      *caches)
+    _call("embla_sparse_decode_shared", ctypes.byref(shape.c()), prefix_len, prefix_stride, q.data_ptr(),
+          _ptr(k_prefix), _ptr(v_prefix), _ptr(k_cache), _ptr(v_cache),
           idx.data_ptr(), idx_stride, count.data_ptr(),
           shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream, dev))
 

@@ -120,3 +120,22 @@ def test_sums_of_many_tiles_do_not_drift(Hkv, G, P, n, scores):
             assert (err <= tol).all(), (b, h, float((err / want).max()), float((err / tol).max()))
             sure = (qq @ k.T).amax(0)
             assert int((sure > ds.amax(0)).sum()) <= int(ns[b, h]) <= int((sure > -ds.amax(0)).sum())
+
+
+def test_sides_without_keys_may_be_none():
+    """None for the prefix, or the own caches, of a call without keys there: the bits of the call with
+    empty tensors."""
+    for P, n in ((0, 300), (300, 0)):
+        q, kp, vp, ko, vo = make(3, 2, 8, P, n, 51)
+        planes = [t if t.numel() else None for t in (kp, vp, ko, vo)]
+        sh, full = E.Shape(3, 16, 2, D, n, n), run(q, kp, vp, ko, vo, P, n)
+        o = buffers_like(full)
+        E.embla_full_decode_shared(sh, P, q, *planes, *o)
+        idx = torch.arange(P + n, device="cuda", dtype=torch.int32).expand(3, 2, -1).contiguous()
+        cnt = torch.full((3, 2), P + n, dtype=torch.int32, device="cuda")
+        a, b = torch.empty_like(full[0]), torch.empty_like(full[0])
+        E.embla_sparse_decode_shared(sh, P, q, kp, vp, ko, vo, idx, cnt, a)
+        E.embla_sparse_decode_shared(sh, P, q, *planes, idx, cnt, b)
+        torch.cuda.synchronize()
+        assert E.embla_device_check() == 0
+        assert all(torch.equal(s, t) for s, t in zip(full, o)) and torch.equal(a, b)
