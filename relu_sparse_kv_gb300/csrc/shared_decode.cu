@@ -830,24 +830,10 @@ __global__ void __launch_bounds__(kFThreads, kFCtasPerSm) shared_finish_kernel(c
     const int seqs = kRows / sp.G;
     const int rb = b / seqs, seq = b - rb * seqs, h = hq - g * sp.G;
     const int r = sp.G == 4 ? block_row<4>(seq, h) : block_row<8>(seq, h);
-    // the pieces whose record holds this row: those with prefix tiles of this KV head, then
-    // those with own tiles of this sequence
-    const uint32_t gt = static_cast<uint32_t>(sp.group_tiles(rb)), T = gt * sp.Hkv;
-    const uint32_t Q = static_cast<uint32_t>(sp.pieces(rb)), base = g * gt;
-    int qa = 0, qb = -1, qc = 0, qd = -1;
-    if (sp.tp > 0) {
-      qa = static_cast<int>(sp.piece_of_tile(base, T, Q));
-      qb = static_cast<int>(sp.piece_of_tile(base + static_cast<uint32_t>(sp.tp) - 1, T, Q));
-    }
-    if (sp.ts > 0) {
-      const uint32_t own = base + static_cast<uint32_t>(sp.tp + seq * sp.ts);
-      qc = static_cast<int>(sp.piece_of_tile(own, T, Q));
-      qd = static_cast<int>(sp.piece_of_tile(own + static_cast<uint32_t>(sp.ts) - 1, T, Q));
-      if (qc <= qb) qc = qb + 1;
-    }
-    const int n1 = qb - qa + 1, all = n1 + (qd >= qc ? qd - qc + 1 : 0);
-    const float *first = p.rec + sp.slot(rb, qa, g) * kRecWords;
-    const int64_t gap = static_cast<int64_t>(qc - qa - n1) * kRecWords;  // past the prefix's records
+    const SharedSplit::RowPieces pc = sp.row_pieces(rb, seq, g);
+    const int n1 = pc.prefix, all = n1 + pc.rest;
+    const float *first = p.rec + sp.slot(rb, pc.first, g) * kRecWords;
+    const int64_t gap = static_cast<int64_t>(pc.own - pc.first - n1) * kRecWords;  // past the prefix's records
     // (twice for the first item: the round without records, then the item)
 #pragma unroll 1
     while (true) {

@@ -39,6 +39,28 @@ struct SharedSplit {
   __host__ __device__ uint32_t piece_of_tile(uint32_t t, uint32_t T, uint32_t Q) const {
     return ((t + 1) * Q - 1) / T;
   }
+  // The pieces whose records hold the rows of a row block's sequence seq for KV head g: those with
+  // prefix tiles of g, [first, first + prefix), then those with own tiles of seq only,
+  // [own, own + rest).
+  struct RowPieces {
+    int first, prefix, own, rest;
+  };
+  __host__ __device__ RowPieces row_pieces(int rb, int seq, int g) const {
+    const uint32_t gt = static_cast<uint32_t>(group_tiles(rb)), T = gt * Hkv;
+    const uint32_t Q = static_cast<uint32_t>(pieces(rb)), base = g * gt;
+    int qa = 0, qb = -1, qc = 0, qd = -1;
+    if (tp > 0) {
+      qa = static_cast<int>(piece_of_tile(base, T, Q));
+      qb = static_cast<int>(piece_of_tile(base + static_cast<uint32_t>(tp) - 1, T, Q));
+    }
+    if (ts > 0) {
+      const uint32_t first_own = base + static_cast<uint32_t>(tp + seq * ts);
+      qc = static_cast<int>(piece_of_tile(first_own, T, Q));
+      qd = static_cast<int>(piece_of_tile(first_own + static_cast<uint32_t>(ts) - 1, T, Q));
+      if (qc <= qb) qc = qb + 1;
+    }
+    return {qa, qb - qa + 1, qc, qd >= qc ? qd - qc + 1 : 0};
+  }
   __host__ __device__ int64_t slot(int rb, int64_t piece, int g) const {
     return static_cast<int64_t>(rb) * (ctas_full + Hkv) + piece + g;
   }
