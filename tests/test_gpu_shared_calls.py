@@ -139,3 +139,30 @@ def test_sides_without_keys_may_be_none():
         torch.cuda.synchronize()
         assert E.embla_device_check() == 0
         assert all(torch.equal(s, t) for s, t in zip(full, o)) and torch.equal(a, b)
+
+
+def test_sparse_weights_enter_the_value_sum_whole():
+    """Two selected rows, scores 0 and s = -x y exactly (one nonzero element each), values powers of two:
+    out = v p / (1 + p), p = 2^z, z = -tau2 x y.  With u = 2^-24: z carries 3u |z| (tau2 and the product),
+    2.1u of p; exp2f 2 ulp, 4u; the value sum three additions (the parts of p) of 2u each at most, the
+    sum of weights u and 6.1u p / (1 + p) of p, the division 2u: 18u of out in all, and 2u for the
+    merges.  p in two bf16 parts alone would be off by up to 2^-18 = 64u."""
+    B, Hkv, G, P, n, tau, u = 64, 4, 4, 3, 1, 0.5, 2.0 ** -24
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q = torch.zeros(B, Hkv * G, D, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = (1 + torch.rand(B, Hkv * G, device="cuda", generator=g)).bfloat16()
+    kp = torch.zeros(Hkv, P, D, device="cuda", dtype=torch.bfloat16)
+    ko = torch.zeros(B, Hkv, n, D, device="cuda", dtype=torch.bfloat16)
+    ko[..., 0] = -(torch.rand(B, Hkv, n, device="cuda", generator=g) * 0.5 + 0.1).bfloat16()
+    two = lambda *s: (2.0 ** torch.randint(-3, 4, s, device="cuda", generator=g)).bfloat16()
+    vp, vo = torch.zeros_like(kp), two(B, Hkv, n, D)
+    idx = torch.tensor([1, P], dtype=torch.int32, device="cuda").expand(B, Hkv, 2).contiguous()
+    cnt = torch.full((B, Hkv), 2, dtype=torch.int32, device="cuda")
+    out = torch.empty(B, Hkv * G, D, device="cuda")
+    E.embla_sparse_decode_shared(E.Shape(B, Hkv * G, Hkv, D, n, n), P, q, kp, vp, ko, vo, idx, cnt, out, tau=tau)
+    torch.cuda.synchronize()
+    s = q.view(B, Hkv, G, D)[..., 0].double() * ko[..., 0].double()
+    p = torch.exp(tau * s)
+    want = (p / (1 + p))[..., None] * vo[:, :, 0, None].double()
+    err = ((out.view(B, Hkv, G, D).double() - want) / want).abs().max()
+    assert err <= 20 * u, float(err / u)
