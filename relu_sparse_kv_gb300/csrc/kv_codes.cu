@@ -10,7 +10,7 @@
 // product y = fl(x_d inv) is within 2^-22 of the quotient.  A tie of the E4M3 grid has at most
 // five significant bits, and a quotient 7 X 2^m / A of integers X, A < 2^8 that is not a tie T
 // differs from it by at least 1 / (31 * 255) > 2^-13 of it (the integers 7 X 2^m and T A
-// differ by one at least).  So y rounded to 17 significant bits is the tie itself when the
+// differ by one at least).  So y rounded to 17 fraction bits (18 significant ones) is the tie itself when the
 // quotient is one, and on the quotient's side of it when not: the conversion of that gives the
 // correctly rounded code.
 //
@@ -32,7 +32,7 @@ constexpr uint32_t kBf16Inf = 0x7F80u;
 // below 2^-109 the reciprocal 448 / a could overflow: such rows divide
 constexpr uint32_t kBf16Tiny = 0x0900u;
 
-// y rounded to 17 significant bits (to nearest; y is finite).
+// y rounded to 17 fraction bits (to nearest; y is finite).
 __device__ __forceinline__ float snap17(float y) {
   return __uint_as_float((__float_as_uint(y) + 0x20u) & ~0x3Fu);
 }

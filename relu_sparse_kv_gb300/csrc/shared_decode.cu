@@ -20,8 +20,9 @@
 // memory between its scores and its products.
 //
 // Weights reach the value product as hi + lo, two bf16 roundings: 2.5e-6 of the output against
-// 64 bits.  A third part would cost half as many products again and 64 more tensor-memory columns
-// per tile than there are.  Denominators, scores and the sum over records are fp32.
+// 64 bits (4.9e-6 at 40 tiles per CTA, see kMaxTiles).  A third part would cost half as many products
+// again and 64 more tensor-memory columns per tile than there are.  Denominators, scores and the
+// sums over records are fp32.
 //
 // Work split: one CTA per SM, each one piece of a row block's tile list; the CTAs of different row
 // blocks walk the same prefix tiles at the same time, so the prefix comes from HBM once.
@@ -40,10 +41,10 @@
 // B 64 the CTAs leave 52 to 58 us after the first load, 336 MB read and written.  The fixed
 // part of a call is about 9 us: 2 until the first tile lands, 2.5 from a tile's landing to its
 // products, 1.5 for writing the records (10 MB at once), 2 to 3 for the finishing kernel.  Measured,
-// a call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 28.0 us (97 MB needed, 3.5
-// TB/s); B 8, GQA 8, 32k 16.0 us; B 64, 64k, 1,024 own 75.5 us (285 MB, 3.8 TB/s; 11 us of it the
+// a call in a graph of calls: B 32, GQA 4, 32k prefix, 300 own keys 29.1 us (97 MB needed, 3.3
+// TB/s); B 8, GQA 8, 32k 16.2 us; B 64, 64k, 1,024 own 75.6 us (285 MB, 3.8 TB/s; 11 us of it the
 // histogram's reading of 68 MB of scores, most of which L2 no longer holds, stored evict_last or
-// not).  Without scores and histogram: 25.3, 15.2 and 60.6 us.
+// not).  Without scores and histogram: 25.0, 15.6 and 61.0 us.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -725,7 +726,7 @@ constexpr int kFThreads = 256;
 constexpr int kFWarps = kFThreads / 32;
 constexpr int kFCtasPerSm = 3;   // registers for ten records in flight per warp
 constexpr int kHistStep = 1024;  // a CTA's share of the scores starts at a multiple of this
-constexpr int kItemSteps = 12;   // an item's time in steps (B 32: 28.0 us, with 6 29.0)
+constexpr int kItemSteps = 12;   // an item's time in steps (with 6, B 32 took 1 us more)
 
 struct FinishParams {
   SharedSplit sp;
@@ -747,8 +748,9 @@ struct FinishParams {
 
 // A row whose sums are not finite, term by term: the products of a whole value tile give NaN
 // where a weight of zero meets a value that is infinite or NaN, and a key of weight zero (or
-// another sequence's key) contributes nothing here.  One pass over all keys per row: slow,
-// and only for inputs that hold such values.
+// another sequence's key) contributes nothing here.  One pass of a CTA over all keys per row, for
+// every row whose block met such a value: slow (one NaN row in the prefix: 0.26 ms at B 4 behind 2k keys,
+// 5 ms at B 32 behind 32k, 33 ms at B 64 behind 64k), and only for inputs that hold such values.
 __device__ __noinline__ void row_term_by_term(const FinishParams &p, int b, int hq, float *s_q, float *s_w,
                                               float *s_sum) {
   const SharedSplit &sp = p.sp;

@@ -285,9 +285,11 @@ struct DotsF32 {
 //   O^T += V^T . P^T  as MMAs with M = dims (8 tiles of 16), N = heads, K = the 16 rows.
 // P enters the second product as two bf16 parts (hi + lo), behind a shared prefix as three; l sums
 // the fp32 values.  Behind a shared prefix a row comes from the prefix's plane or the unit's own
-// one by its index.  What bounds it there is the gather: B 32, 32k prefix, 1,152 rows for each of
-// 128 units (75 MB of 256-byte rows, 52 MB of them distinct) 15.7 us; 12 warps per CTA instead of
-// 9 took 15.7 us too, and a prefetch of the later rounds' rows into L2 18.8 us.
+// one by its index.  There B 32 behind a 32k prefix, 1,152 rows for each of 128 units (75 MB of
+// 256-byte rows, 52 MB of them distinct), takes 16.4 us.  No rate bounds it (2.7 TB/s from DRAM, 4.0
+// into the SMs, a third of the issue slots): a warp's four rounds of 16 rows each wait for their
+// copies, and 256 CTAs leave 48 of the 304 slots empty.  12 warps per CTA instead of 9 took the same
+// time, and a prefetch of the later rounds' rows into L2 3 us more.
 
 // 9 warps x 16 rows = 144 rows: a cluster of 8 covers 1152 (two CTAs to an SM); the wide
 // variant, 18 warps and a cluster of 4 (one CTA to an SM), takes over when 8 CTAs per unit
@@ -537,7 +539,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(W * 32, W <= kSpWar
     const uint32_t ph0 = pack_bf16x2(pz[0], pz[1]), ph1 = pack_bf16x2(pz[2], pz[3]);
     const float pr[4] = {pz[0] - bf16lo(ph0), pz[1] - bf16hi(ph0), pz[2] - bf16lo(ph1), pz[3] - bf16hi(ph1)};
     const uint32_t pl0 = pack_bf16x2(pr[0], pr[1]), pl1 = pack_bf16x2(pr[2], pr[3]);
-    // behind a shared prefix a third part, all 24 bits (hi + lo alone leave 1.8e-6 of the output)
+    // behind a shared prefix a third part, all 24 bits (hi + lo alone leave 1.8e-6 of the output, now 3.8e-7)
     uint32_t pm0 = 0u, pm1 = 0u;
     if constexpr (SHARED) {
       pm0 = pack_bf16x2(pr[0] - bf16lo(pl0), pr[1] - bf16hi(pl0));
