@@ -310,7 +310,8 @@ embla_status embla_sparse_decode_shared(const embla_shape *shape, int64_t prefix
  *
  * embla_full_decode_head_scores: the full-layer decode (out and n_surv exactly as
  *   embla_full_decode) that writes each head's scores instead of the group's:
- *   head_scores fp32 [B, Hq, cache_stride] (s_hj for j < n; rows >= n not written) and
+ *   head_scores fp32 [B, Hq, cache_stride] (s_hj for j < n, -infinity where that is NaN; rows
+ *   >= n not written) and
  *   head_hist uint32 [B, Hq, 2048] (the order-key histogram of each head's scores).
  *   Workspace: embla_full_decode_workspace_size.
  * embla_select_topk_per_head: embla_select_topk over the B*Hq units of those scores:

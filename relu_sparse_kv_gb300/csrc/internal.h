@@ -100,8 +100,9 @@ cudaError_t launch_full_decode(int G, bool kv8, const CUtensorMap &tm_k, const C
                                cudaStream_t stream, const SelectJob *sj = nullptr);
 
 size_t select_workspace_bytes(int64_t units, int64_t ctx_len);
-// hist[u] = 2048-bin counts of the order keys' top 11 bits of scores[u][0..n) (every unit).
-cudaError_t launch_score_hist(const float *scores, int64_t units, int64_t n, int64_t ncap,
+// hist[u] = 2048-bin counts of the order keys' top 11 bits of scores[u][0..n) (every unit); NaN
+// scores become minus infinity.
+cudaError_t launch_score_hist(float *scores, int64_t units, int64_t n, int64_t ncap,
                               uint32_t *hist, cudaStream_t stream);
 cudaError_t launch_select(const float *sel_scores, const uint32_t *sel_hist, int64_t units,
                           int64_t n, int64_t ncap, int topk, int recent, int32_t *idx,

@@ -50,3 +50,36 @@ def test_nan_keys_fill_the_selection_behind_a_prefix():
     want, count = oracle.select_topk_batch(scores.cpu().numpy(), N)
     assert np.array_equal(cnt.cpu().numpy(), count) and np.array_equal(idx.cpu().numpy(), want)
     assert (cnt == 1152).all() and E.embla_device_check() == 0
+
+
+def test_nan_keys_rank_last_for_every_query_head():
+    """Scores per query head with NaN key rows, zero key rows (eps = 0) and a NaN query head: minus
+    infinity there, and the
+    selection as the oracle makes it of those scores."""
+    B, Hq, Hkv, n = 2, 16, 4, 2600
+    g = torch.Generator(device="cuda").manual_seed(33)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()
+    q, K, V = rnd(B, Hq, D), rnd(B, Hkv, n, D), rnd(B, Hkv, n, D)
+    K[:, :, 11, 5] = float("nan")
+    K[:, 1, 100:140] = 0.0
+    K[:, 2, 300:2100] = float("nan")
+    q[0, 1] = float("nan")
+    before = K.clone()
+    shape = E.Shape(B, Hq, Hkv, D, n, n)
+    out, ns = torch.empty(B, Hq, D, device="cuda"), torch.empty(B, Hkv, dtype=torch.int32, device="cuda")
+    hs = torch.empty(B, Hq, n, device="cuda")
+    hh = torch.empty(B, Hq, E.HIST_BINS, dtype=torch.int32, device="cuda")
+    E.embla_full_decode_head_scores(shape, q, K, V, out, ns, hs, hh, eps=0.0)
+    idx = torch.full((B, Hq, 1152), -1, dtype=torch.int32, device="cuda")
+    cnt = torch.empty(B, Hq, dtype=torch.int32, device="cuda")
+    E.embla_select_topk_per_head(shape, hs, hh, idx, cnt)
+    torch.cuda.synchronize()
+    assert E.embla_device_check() == 0 and torch.equal(K.view(torch.int16), before.view(torch.int16))
+    s = hs.cpu().numpy()
+    gone = np.isneginf(s)
+    assert not np.isnan(s).any() and gone[:, :, 11].all() and gone[:, 4:8, 100:140].all()
+    assert gone[:, 8:12, 300:2100].all() and gone[0, 1].all() and gone[1, 1].sum() == 1
+    assert np.array_equal(hh.cpu().numpy(), np.stack([[np.bincount(order_key_np(s[b, h]) >> 21, minlength=E.HIST_BINS)
+                                                       for h in range(Hq)] for b in range(B)]))
+    want, count = oracle.select_topk_batch(s, n)
+    assert np.array_equal(cnt.cpu().numpy(), count) and np.array_equal(idx.cpu().numpy(), want)
