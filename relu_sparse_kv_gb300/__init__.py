@@ -16,7 +16,10 @@ Tensors (torch, on the current CUDA device, C-contiguous):
   sel_scores     fp32  [B, Hkv, cache_stride]
   sel_hist       int32 [B, Hkv, 2048]  (holds uint32 counts)
   idx            int32 [B, Hkv, idx_stride]
-  workspace      uint8 (any shape), at least the *_workspace_size result
+  workspace      uint8 (any shape), at least the *_workspace_size result; None: one made for the
+                 call, on its stream
+  stream         a torch.cuda.Stream (None: the current one), ordered after the inputs' writers
+                 by the caller; tensors freed before the call has finished need record_stream
 """
 from __future__ import annotations
 

@@ -10,9 +10,9 @@
 // product y = fl(x_d inv) is within 2^-22 of the quotient.  A tie of the E4M3 grid has at most
 // five significant bits, and a quotient 7 X 2^m / A of integers X, A < 2^8 that is not a tie T
 // differs from it by at least 1 / (31 * 255) > 2^-13 of it (the integers 7 X 2^m and T A
-// differ by one at least).  So y rounded to 17 fraction bits (18 significant ones) is the tie itself when the
-// quotient is one, and on the quotient's side of it when not: the conversion of that gives the
-// correctly rounded code.
+// differ by one at least).  So y rounded to 17 fraction bits (18 significant ones) is the tie
+// itself when the quotient is one, and on the quotient's side of it when not: the conversion of
+// that gives the correctly rounded code.
 //
 // Eight lanes take a row, 16 values each (32 bytes of bf16, 16 of codes), so a warp moves 1 KB and
 // 512 bytes in one piece; K and V are the grid's y.  Bound by HBM, 388 bytes per row either way:
