@@ -1417,12 +1417,13 @@ __global__ void __launch_bounds__(512) score_hist_kernel(float *scores, int64_t 
   __syncthreads();
   const int64_t u = blockIdx.x;
   float *su = scores + u * ncap;
-  for (int64_t j = threadIdx.x; j < n; j += blockDim.x) {
-    float s = su[j];
-    if (s != s) su[j] = s = -INFINITY;
-    atomicAdd(&s_h[order_key(s) >> 21], 1u);
-  }
+  // NaN counts as minus infinity; it is written so after the count, where that bin holds any (a
+  // store in this loop cost 6 us of 114 at B 8, 32k)
+  for (int64_t j = threadIdx.x; j < n; j += blockDim.x) atomicAdd(&s_h[order_key(fmaxf(su[j], -INFINITY)) >> 21], 1u);
   __syncthreads();
+  if (s_h[0x007FFFFFu >> 21] != 0u)
+    for (int64_t j = threadIdx.x; j < n; j += blockDim.x)
+      if (su[j] != su[j]) su[j] = -INFINITY;
   for (int b = threadIdx.x; b < kHistBins; b += blockDim.x) hist[u * kHistBins + b] = s_h[b];
 }
 
