@@ -402,6 +402,85 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
                                  void *stream);
 
 /*
+ * Batches whose sequences have different lengths.  Their tokens lie packed, one sequence behind the
+ * other: sequence b of shape->batch is tokens cu_tokens[b] .. cu_tokens[b + 1] - 1 of n_tokens
+ * (int32 [batch + 1] in device memory, ascending, from 0 on; a sequence may be empty).  Rows are
+ * token-major, bf16 [n_tokens, heads, 128], with `stride` elements from one token to the next (at
+ * least heads * 128, a multiple of 8), so that q, k and v may be parts of one projection's rows.  Tokens behind
+ * the last sequence have no outputs: their rows are left as they were.  shape->ctx_len and
+ * shape->cache_stride are not used by these calls.  The lengths are read on the device: one captured
+ * graph serves every batch that fits n_tokens and shape->batch.  Entries that do not ascend or lie outside
+ * 0 .. n_tokens read and write nothing outside the arrays, but which rows then get an output is not
+ * defined (the two attention calls report them, bit 0 of embla_device_check).  At most 2^30 tokens.
+ *
+ * embla_rope_qkv — "Three kinds of attention" (Sliding window): queries and keys of the window
+ * layers rotated at their positions, normed per head before if asked for, in one pass, and the rings
+ * that embla_window_decode and embla_window_decode_ragged read brought up to date.  Whole prompts or one
+ * token per sequence (cu_tokens = 0, 1, .. batch).
+ *   pos0       int32 [batch]: the position (>= 0) of each sequence's first token here, or NULL: 0.
+ *              Positions stay below 2^31
+ *   q, k, v    bf16 [n_tokens, Hq | Hkv | Hkv, 128]; v is read for the rings only
+ *   norm       0: rows as they are; else each row of q and k first becomes
+ *              x / sqrt(mean(x^2) + eps) * gain (eps finite and >= 0)
+ *   q_gain, k_gain  fp32 [128] or NULL (1); NULL without norm
+ *   rope_base  > 0: pair (2i, 2i+1) is turned by position * rope_base^(-2i/128)
+ *   q_out      bf16 [n_tokens, Hq, 128] (dense);  k_out  bf16 [n_tokens, Hkv, 128] or NULL: the rows,
+ *              computed in fp32 and rounded once.  q_out may be q and k_out k where those are
+ *              dense; no other overlap of inputs and outputs
+ *   window     ring size, 1..1024;  k_win, v_win  bf16 [batch, Hkv, window, 128] or both NULL (no
+ *              rings, window not used): the newest min(length, window) tokens of each sequence go to slot
+ *              position % window, other slots are not touched
+ *
+ * embla_window_prefill — "Three kinds of attention" (Sliding window), for prompts: causal softmax
+ * attention over the newest `window` keys.  The queries of sequence b are the last of its keys
+ * cu_keys[b] .. cu_keys[b + 1] - 1 (of n_keys): with Lq queries and Lk keys, query t sees the keys
+ * max(0, p - window + 1) .. p, p = Lk - Lq + t, and gets 0 where there are none.
+ *   cu_keys    int32 [batch + 1] or NULL: cu_tokens (then n_keys must be n_tokens)
+ *   q          bf16 [n_tokens, Hq, 128];  k, v  bf16 [n_keys, Hkv, 128], rotated already
+ *   window     >= 1 (128 in Embla 1); a window of the longest sequence or more sees everything
+ *   tau        softmax scale, finite
+ *   out        bf16 [n_tokens, Hq, 128] (dense)
+ * Scores, maxima, sums and value sums are fp32; the weights enter the value product as bf16 (relative
+ * to a reference within 2^8 of the row's largest), one rounding as large as the output's.  A key that a
+ * query does not see contributes nothing, whatever its rows hold; infinite or NaN values among the rows
+ * read beside a query's own have its output computed by a slow path.
+ *
+ * embla_prefill_packed — embla_prefill for packed prompts ("Sevren Sparse Attention learns to be sparse"):
+ * the same queries and keys as embla_window_prefill's, no window, ReLU^2 weights of RMS-normalised
+ * rows: out = sum w v / (c + sum w) over the keys 0 .. p, 0 where that is 0.
+ *   alpha, c, eps   as for embla_full_decode
+ *   workspace  the keys' norms: embla_prefill_packed_workspace_size(shape, n_keys) bytes, 16-byte aligned
+ *   every other argument as for embla_window_prefill
+ * Precision as for embla_window_prefill.  A NaN score weighs nothing; a key of weight zero contributes
+ * nothing, whatever its value row holds (by the slow path where that is infinite or NaN).
+ *
+ * embla_window_decode_ragged — embla_window_decode for sequences at positions of their own.
+ *   q          bf16 [batch, Hq, 128], rotated already (embla_rope_qkv)
+ *   pos        int32 [batch]: the current token's position; below 0: no keys, the output is 0
+ *   k_win, v_win, window, tau, out   as for embla_window_decode (out fp32 [batch, Hq, 128])
+ */
+embla_status embla_rope_qkv(const embla_shape *shape, int64_t n_tokens, const int32_t *cu_tokens,
+                            const int32_t *pos0, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *v, int64_t v_stride, float rope_base,
+                            int norm, float eps, const float *q_gain, const float *k_gain,
+                            void *q_out, void *k_out, int32_t window, void *k_win, void *v_win,
+                            void *stream);
+embla_status embla_window_prefill(const embla_shape *shape, int64_t n_tokens, const int32_t *cu_tokens,
+                                  int64_t n_keys, const int32_t *cu_keys, const void *q,
+                                  int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, int64_t window, float tau, void *out,
+                                  void *stream);
+size_t embla_prefill_packed_workspace_size(const embla_shape *shape, int64_t n_keys);
+embla_status embla_prefill_packed(const embla_shape *shape, int64_t n_tokens, const int32_t *cu_tokens,
+                                  int64_t n_keys, const int32_t *cu_keys, const void *q,
+                                  int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, float alpha, float c, float eps, void *out,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+embla_status embla_window_decode_ragged(const embla_shape *shape, const void *q, const void *k_win,
+                                        const void *v_win, int32_t window, const int32_t *pos,
+                                        float tau, float *out, void *stream);
+
+/*
  * Cache append — the decode step's token written into the caches the calls above
  * read ("Three kinds of attention": a full layer keeps every token's K and V).
  * Row `pos` of every (b, g) plane is copied from a packed array of one row per plane:
@@ -480,8 +559,8 @@ embla_status embla_skip_stats(const embla_shape *shape, const float *sel_scores,
  * trapping.  This call synchronises `stream`, copies the word to *flags and,
  * if `clear` is non-zero, resets it.  Returns EMBLA_ERR_DEVICE_CHECK when any
  * flag was set, EMBLA_OK otherwise.
- *   bit 0  index out of range (sparse decode)
- *   bit 1  a wait for data in flight timed out (full decode, selection)
+ *   bit 0  index out of range (sparse decode; a packed sequence's entries)
+ *   bit 1  a wait for data in flight timed out (full decode, selection, prefill)
  */
 embla_status embla_device_check(uint32_t *flags, int clear, void *stream);
 

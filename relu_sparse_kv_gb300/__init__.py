@@ -16,6 +16,9 @@ Tensors (torch, on the current CUDA device, C-contiguous):
   sel_scores     fp32  [B, Hkv, cache_stride]
   sel_hist       int32 [B, Hkv, 2048]  (holds uint32 counts)
   idx            int32 [B, Hkv, idx_stride]
+  packed rows    bf16 [T, heads, D] of sequences of different lengths, one behind the other; the
+                 tokens may lie apart (parts of one projection's rows), heads and dims not
+  cu_tokens      int32 [B + 1]: sequence b is tokens cu_tokens[b] .. cu_tokens[b + 1] - 1
   workspace      uint8 (any shape), at least the *_workspace_size result; None: one made for the
                  call, on its stream
   stream         a torch.cuda.Stream (None: the current one), ordered after the inputs' writers
@@ -128,6 +131,14 @@ def library() -> ctypes.CDLL:
             "embla_window_decode_workspace_size": (sz, [P, i32]),
             "embla_window_decode": (ctypes.c_int, [P, vp, vp, vp, i32, i64, f32, f32, vp, vp, sz,
                                                    vp]),
+            "embla_rope_qkv": (ctypes.c_int, [P, i64, vp, vp, vp, i64, vp, i64, vp, i64, f32, ctypes.c_int,
+                                              f32, vp, vp, vp, vp, i32, vp, vp, vp]),
+            "embla_window_prefill": (ctypes.c_int, [P, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, i64,
+                                                    f32, vp, vp]),
+            "embla_prefill_packed_workspace_size": (sz, [P, i64]),
+            "embla_prefill_packed": (ctypes.c_int, [P, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, f32,
+                                                    f32, f32, vp, vp, sz, vp]),
+            "embla_window_decode_ragged": (ctypes.c_int, [P, vp, vp, vp, i32, vp, f32, vp, vp]),
             "embla_skip_stats": (ctypes.c_int, [P, vp, i32, vp, vp, vp]),
             "embla_device_check": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int,
                                                   vp]),
@@ -651,6 +662,120 @@ def embla_window_decode(shape: Shape, q, k_win, v_win, pos: int, out, window: in
     tau = D ** -0.5 if tau is None else tau
     _call("embla_window_decode", ctypes.byref(shape.c()), _ptr(q), _ptr(k_win), _ptr(v_win),
           window, pos, rope_base, tau, _ptr(out), None, 0, _stream(stream))
+
+
+def _packed_rows(t, heads: int, D: int, name: str) -> tuple[int, int, int]:
+    """Tokens, elements from one token to the next and device of packed rows bf16 [T, heads, D]."""
+    if t is None or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [T, {heads}, {D}]")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    T, step = t.shape[0], t.stride(0)
+    if T == 0:
+        return 0, heads * D, t.get_device()
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D) or (T > 1 and step < heads * D):
+        raise ValueError(f"{name}: heads and dims must be dense, tokens apart")
+    return T, step if T > 1 else heads * D, t.get_device()
+
+
+def _packed_qkv(shape: Shape, cu_tokens, cu_keys, q, k, v, out):
+    """Checks of the two attention calls on packed prompts; tokens, keys and strides, and the device."""
+    D, cu = shape.head_dim, (shape.batch + 1,)
+    T, q_step, dev = _packed_rows(q, shape.n_q_heads, D, "q")
+    N, k_step, dev_k = _packed_rows(k, shape.n_kv_heads, D, "k")
+    Nv, v_step, dev_v = _packed_rows(v, shape.n_kv_heads, D, "v")
+    if N != Nv or (cu_keys is None and N != T):
+        raise ValueError("k and v must be [T, Hkv, D], or [n_keys, Hkv, D] beside cu_keys")
+    checks = [(out, torch.bfloat16, (T, shape.n_q_heads, D), "out"), (cu_tokens, torch.int32, cu, "cu_tokens")]
+    if cu_keys is not None:
+        checks.append((cu_keys, torch.int32, cu, "cu_keys"))
+    if _check_here(*checks) != dev or dev_k != dev or dev_v != dev:
+        raise ValueError("the call's tensors are on different devices")
+    return (T, cu_tokens.data_ptr(), N, _ptr(cu_keys), q.data_ptr(), q_step, k.data_ptr(), k_step,
+            v.data_ptr(), v_step), dev
+
+
+def embla_rope_qkv(shape: Shape, cu_tokens, pos0, q, k, v, q_out, k_out, rope_base: float = 10000.0,
+                   norm_eps: float | None = None, q_gain=None, k_gain=None, k_win=None, v_win=None,
+                   stream=None):
+    """Packed queries and keys rotated at their positions pos0[b] + 0, 1, .. (int32 [B]; None: 0), normed
+    per head before where norm_eps is given (gains float32 [D]), into q_out [T, Hq, D] and k_out
+    [T, Hkv, D] (None: not written); the newest rows of k and v into the rings k_win, v_win
+    [B, Hkv, window, D] where given."""
+    B, Hq, Hkv, D = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
+    T, q_step, dev = _packed_rows(q, Hq, D, "q")
+    Tk, k_step, dev_k = _packed_rows(k, Hkv, D, "k")
+    if Tk != T:
+        raise ValueError("q and k must have the same tokens")
+    checks = [(q_out, torch.bfloat16, (T, Hq, D), "q_out"), (cu_tokens, torch.int32, (B + 1,), "cu_tokens")]
+    if pos0 is not None:
+        checks.append((pos0, torch.int32, (B,), "pos0"))
+    if k_out is not None:
+        checks.append((k_out, torch.bfloat16, (T, Hkv, D), "k_out"))
+    for gain, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if gain is not None:
+            checks.append((gain, torch.float32, (D,), name))
+    window, v_step, dev_v = 0, Hkv * D, dev
+    if k_win is not None or v_win is not None:
+        if k_win is None or k_win.dim() != 4:
+            raise ValueError("k_win must be [B, Hkv, window, D]")
+        window = k_win.shape[2]
+        if window < 1:
+            raise ValueError("a ring has one slot at least")
+        ring = (B, Hkv, window, D)
+        checks += [(k_win, torch.bfloat16, ring, "k_win"), (v_win, torch.bfloat16, ring, "v_win")]
+        Tv, v_step, dev_v = _packed_rows(v, Hkv, D, "v")
+        if Tv != T:
+            raise ValueError("q and v must have the same tokens")
+    if _check_here(*checks) != dev or dev_k != dev or dev_v != dev:
+        raise ValueError("the call's tensors are on different devices")
+    _call("embla_rope_qkv", ctypes.byref(shape.c()), T, cu_tokens.data_ptr(), _ptr(pos0), q.data_ptr(), q_step,
+          k.data_ptr(), k_step, _ptr(v) if window else None, v_step, rope_base, 0 if norm_eps is None else 1,
+          0.0 if norm_eps is None else norm_eps, _ptr(q_gain), _ptr(k_gain), q_out.data_ptr(), _ptr(k_out),
+          window, _ptr(k_win), _ptr(v_win), _stream(stream, dev))
+
+
+def embla_window_prefill(shape: Shape, cu_tokens, q, k, v, out, window: int = 128, tau: float | None = None,
+                         cu_keys=None, stream=None):
+    """Causal softmax attention of packed prompts over the newest `window` keys: q, out bf16 [T, Hq, D],
+    k and v bf16 [T, Hkv, D], or [n_keys, Hkv, D] with cu_keys (int32 [B + 1]) where sequences have
+    more keys than queries (the queries are the last ones)."""
+    args, dev = _packed_qkv(shape, cu_tokens, cu_keys, q, k, v, out)
+    _call("embla_window_prefill", ctypes.byref(shape.c()), *args, window,
+          shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream, dev))
+
+
+def embla_prefill_packed_workspace_size(shape: Shape, n_keys: int) -> int:
+    return library().embla_prefill_packed_workspace_size(ctypes.byref(shape.c()), n_keys)
+
+
+def embla_prefill_packed(shape: Shape, cu_tokens, q, k, v, out, alpha: float = 1.0, c: float = 1.0,
+                         eps: float = 1e-6, cu_keys=None, workspace=None, stream=None):
+    """embla_prefill for packed prompts: causal ReLU^2 attention, rows as for embla_window_prefill."""
+    args, dev = _packed_qkv(shape, cu_tokens, cu_keys, q, k, v, out)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(embla_prefill_packed_workspace_size(shape, k.shape[0]), None, q.device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, on cuda:{dev}")
+    _call("embla_prefill_packed", ctypes.byref(shape.c()), *args, alpha, c, eps, out.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size(), _stream(stream, dev))
+
+
+def embla_window_decode_ragged(shape: Shape, q, k_win, v_win, pos, out, tau: float | None = None, stream=None):
+    """embla_window_decode with each sequence at its own position pos[b] (int32 [B], below 0: no keys):
+    q bf16 [B, Hq, D] rotated already, rings bf16 [B, Hkv, window, D], out fp32 [B, Hq, D]."""
+    B, Hkv, D = shape.batch, shape.n_kv_heads, shape.head_dim
+    if k_win is None or k_win.dim() != 4:
+        raise ValueError("k_win must be [B, Hkv, window, D]")
+    heads, ring = (B, shape.n_q_heads, D), (B, Hkv, k_win.shape[2], D)
+    dev = _check_here((q, torch.bfloat16, heads, "q"), (k_win, torch.bfloat16, ring, "k_win"),
+                      (v_win, torch.bfloat16, ring, "v_win"), (pos, torch.int32, (B,), "pos"),
+                      (out, torch.float32, heads, "out"))
+    _call("embla_window_decode_ragged", ctypes.byref(shape.c()), q.data_ptr(), k_win.data_ptr(), v_win.data_ptr(),
+          ring[2], pos.data_ptr(), D ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream, dev))
 
 
 def embla_skip_stats(shape: Shape, sel_scores, keys_needed, chunks_needed, chunk: int = 8,

@@ -2,6 +2,7 @@
 // encoding and the launches of the kernels in this directory.  Declarations and the
 // meaning of every argument are in include/embla_attn.h.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -9,6 +10,7 @@
 #include "internal.h"
 #include "kv_codes.h"
 #include "ptx.cuh"
+#include "ragged.h"
 #include "shared_prefix.h"
 
 using namespace embla;
@@ -173,6 +175,34 @@ bool encode_query_block(CUtensorMap *map, const void *q, int batch, int Hq, int 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Packed token rows [tokens][heads][128] bf16, `stride` elements between tokens, 128B swizzle.
+// Queries: 4-D, boxes of {64 columns, G heads of one group, 128 / G tokens}, 128 rows token by token.
+bool encode_packed_queries(CUtensorMap *map, const void *q, uint64_t tokens, uint64_t stride, int Hkv, int G) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = kHeadDim * 2, g = static_cast<cuuint64_t>(G);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), g, static_cast<cuuint64_t>(Hkv), tokens};
+  const cuuint64_t strides[3] = {row, row * g, stride * 2};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(G), 1u, static_cast<cuuint32_t>(128 / G)};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Keys or values: 3-D, boxes of {64 columns, 1 head, box_rows tokens}; rows past the last are zeros.
+bool encode_packed_keys(CUtensorMap *map, const void *base, uint64_t rows, uint64_t stride, int Hkv,
+                        uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(Hkv), rows};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim * 2), stride * 2};
+  const cuuint32_t box[3] = {64u, 1u, box_rows};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool finite(float x) { return x == x && x - x == 0.0f; }
@@ -204,6 +234,13 @@ bool rows_in_cache(const embla_shape *s, int64_t pos, int64_t count) {
   return s->cache_stride >= 0 && pos >= 0 && count >= 0 && pos <= s->cache_stride &&
          count <= s->cache_stride - pos;
 }
+
+// Packed rows of `heads` heads may lie `stride` elements apart: whole rows, 16-byte steps.
+bool token_stride_ok(int64_t stride, int32_t heads) {
+  return stride >= static_cast<int64_t>(heads) * kHeadDim && stride % 8 == 0;
+}
+constexpr int64_t kMaxPackedTokens = static_cast<int64_t>(1) << 30;
+constexpr int64_t kMaxPackedStride = static_cast<int64_t>(1) << 38;  // TMA strides stay below 2^40 bytes
 
 embla_status cuda_status(cudaError_t e) { return e == cudaSuccess ? EMBLA_OK : EMBLA_ERR_CUDA; }
 
@@ -826,6 +863,180 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
     return EMBLA_ERR_INVALID_ARG;
   return cuda_status(launch_window_decode(G, q, k_win, v_win, units, window, pos, rope_base, tau,
                                           out, static_cast<cudaStream_t>(stream)));
+}
+
+embla_status embla_rope_qkv(const embla_shape *shape, int64_t n_tokens, const int32_t *cu_tokens,
+                            const int32_t *pos0, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *v, int64_t v_stride, float rope_base,
+                            int norm, float eps, const float *q_gain, const float *k_gain,
+                            void *q_out, void *k_out, int32_t window, void *k_win, void *v_win,
+                            void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, false);
+  if (st != EMBLA_OK) return st;
+  if (n_tokens < 0 || !(finite(rope_base) && rope_base > 0.0f)) return EMBLA_ERR_INVALID_ARG;
+  if (norm ? !(finite(eps) && eps >= 0.0f) : (q_gain || k_gain)) return EMBLA_ERR_INVALID_ARG;
+  const bool ring = k_win || v_win;
+  if (ring && (!k_win || !v_win || window < 1 || window > 1024)) return EMBLA_ERR_INVALID_ARG;
+  if (n_tokens == 0 || shape->batch == 0) return EMBLA_OK;
+  if (!cu_tokens || !q || !k || !q_out || (ring && !v)) return EMBLA_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, shape->n_q_heads) || !token_stride_ok(k_stride, shape->n_kv_heads) ||
+      (ring && !token_stride_ok(v_stride, shape->n_kv_heads)))
+    return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(cu_tokens) || !aligned16(pos0) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(k_win) || !aligned16(v_win))
+    return EMBLA_ERR_INVALID_ARG;
+  if (n_tokens > kMaxPackedTokens || n_tokens * shape->n_kv_heads > INT32_MAX) return EMBLA_ERR_UNSUPPORTED;
+  if (q_stride > kMaxPackedStride || k_stride > kMaxPackedStride || (ring && v_stride > kMaxPackedStride))
+    return EMBLA_ERR_UNSUPPORTED;
+  RopeParams p = {};
+  p.seqs = {cu_tokens, n_tokens, shape->batch};
+  p.pos0 = pos0;
+  p.q = {static_cast<const uint16_t *>(q), q_stride};
+  p.k = {static_cast<const uint16_t *>(k), k_stride};
+  p.v = {static_cast<const uint16_t *>(v), v_stride};
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.k_out = static_cast<uint16_t *>(k_out);
+  p.k_win = static_cast<uint16_t *>(k_win);
+  p.v_win = static_cast<uint16_t *>(v_win);
+  p.q_gain = q_gain;
+  p.k_gain = k_gain;
+  p.eps = eps;
+  p.norm = norm ? 1 : 0;
+  p.window = window;
+  p.Hkv = shape->n_kv_heads;
+  for (int i = 0; i < kHeadDim / 2; ++i) {
+    // the fraction of a circle that pair i turns by per position (whole circles do not count)
+    const double f = std::pow(static_cast<double>(rope_base), -2.0 * i / kHeadDim) / 6.283185307179586476925286766559;
+    p.turn[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
+  }
+  return cuda_status(launch_rope_qkv(G, p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// Causal attention over packed prompts; the caller fills in what belongs to the kind of weights.
+embla_status packed_prefill_impl(int mode, const embla_shape *shape, int G, int64_t n_tokens,
+                                 const int32_t *cu_tokens, int64_t n_keys, const int32_t *cu_keys,
+                                 const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                 const void *v, int64_t v_stride, int64_t window, PackedPrefillParams p,
+                                 void *out, void *workspace, size_t workspace_bytes, void *stream) {
+  if (n_tokens < 0 || n_keys < 0 || (!cu_keys && n_keys != n_tokens)) return EMBLA_ERR_INVALID_ARG;
+  if (n_tokens == 0 || shape->batch == 0) return EMBLA_OK;
+  const bool norms = mode == kPackedRelu2 && n_keys > 0;
+  if (!cu_tokens || !q || !out || (n_keys > 0 && (!k || !v)) || (norms && !workspace)) return EMBLA_ERR_INVALID_ARG;
+  if (!token_stride_ok(q_stride, shape->n_q_heads) ||
+      (n_keys > 0 && (!token_stride_ok(k_stride, shape->n_kv_heads) || !token_stride_ok(v_stride, shape->n_kv_heads))))
+    return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(cu_tokens) || !aligned16(cu_keys) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(out) || !aligned16(workspace))
+    return EMBLA_ERR_INVALID_ARG;
+  if (n_tokens > kMaxPackedTokens || n_keys > kMaxPackedTokens || n_keys * shape->n_kv_heads > INT32_MAX)
+    return EMBLA_ERR_UNSUPPORTED;
+  if (q_stride > kMaxPackedStride || (n_keys > 0 && (k_stride > kMaxPackedStride || v_stride > kMaxPackedStride)))
+    return EMBLA_ERR_UNSUPPORTED;
+  p.blocks = packed_blocks(n_tokens, shape->batch, G, shape->n_kv_heads);
+  if (p.blocks > INT32_MAX) return EMBLA_ERR_UNSUPPORTED;
+  if (norms && workspace_bytes < packed_workspace_bytes(n_keys, shape->n_kv_heads)) return EMBLA_ERR_WORKSPACE;
+  const int sms = sm_count_of(current_device());
+  p.flags = flags_ptr();
+  if (sms <= 0 || !p.flags) return EMBLA_ERR_CUDA;
+  if (window > kMaxPackedTokens) window = kMaxPackedTokens;  // more than any sequence has
+  const uint32_t rows = static_cast<uint32_t>(packed_tile_keys(mode, G, window));
+  CUtensorMap tm_q, tm_k, tm_v;
+  // (without keys no tile is loaded, and the maps of K and V stand in for nothing)
+  if (n_keys == 0) {
+    k = v = q;
+    k_stride = v_stride = q_stride;
+  }
+  const uint64_t map_rows = static_cast<uint64_t>(n_keys > 0 ? n_keys : 1);
+  if (!encode_packed_queries(&tm_q, q, static_cast<uint64_t>(n_tokens), static_cast<uint64_t>(q_stride),
+                             shape->n_kv_heads, G) ||
+      !encode_packed_keys(&tm_k, k, map_rows, static_cast<uint64_t>(k_stride), shape->n_kv_heads, rows) ||
+      !encode_packed_keys(&tm_v, v, map_rows, static_cast<uint64_t>(v_stride), shape->n_kv_heads, rows))
+    return EMBLA_ERR_CUDA;
+  p.cu_q = cu_tokens;
+  p.cu_k = cu_keys ? cu_keys : cu_tokens;
+  p.q = {static_cast<const uint16_t *>(q), q_stride};
+  p.k = {static_cast<const uint16_t *>(k), k_stride};
+  p.v = {static_cast<const uint16_t *>(v), v_stride};
+  p.rk = static_cast<const float *>(workspace);
+  p.out = static_cast<uint16_t *>(out);
+  p.tokens = n_tokens;
+  p.keys = n_keys;
+  p.rk_stride = packed_rk_stride(n_keys);
+  p.batch = shape->batch;
+  p.Hkv = shape->n_kv_heads;
+  p.window = static_cast<int32_t>(window);
+  p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
+  return cuda_status(launch_packed_prefill(mode, G, tm_q, tm_k, tm_v, p, static_cast<float *>(workspace), sms,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+embla_status embla_window_prefill(const embla_shape *shape, int64_t n_tokens, const int32_t *cu_tokens,
+                                  int64_t n_keys, const int32_t *cu_keys, const void *q,
+                                  int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, int64_t window, float tau, void *out,
+                                  void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, false);
+  if (st != EMBLA_OK) return st;
+  if (window < 1 || !finite(tau)) return EMBLA_ERR_INVALID_ARG;
+  PackedPrefillParams p = {};
+  // scores are kept in base 2; a scale of zero stays above it, so that unseen keys at minus infinity do
+  p.tau2 = tau == 0.0f ? 0x1p-100f : tau * 1.4426950408889634f;
+  return packed_prefill_impl(kPackedSoftmax, shape, G, n_tokens, cu_tokens, n_keys, cu_keys, q, q_stride, k, k_stride,
+                             v, v_stride, window, p, out, nullptr, 0, stream);
+}
+
+size_t embla_prefill_packed_workspace_size(const embla_shape *shape, int64_t n_keys) {
+  int G = 0;
+  if (check_shape(shape, &G, false) != EMBLA_OK || n_keys < 1 || n_keys > kMaxPackedTokens) return 0;
+  return packed_workspace_bytes(n_keys, shape->n_kv_heads);
+}
+
+embla_status embla_prefill_packed(const embla_shape *shape, int64_t n_tokens, const int32_t *cu_tokens,
+                                  int64_t n_keys, const int32_t *cu_keys, const void *q,
+                                  int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                  int64_t v_stride, float alpha, float c, float eps, void *out,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, false);
+  if (st != EMBLA_OK) return st;
+  if (!(finite(alpha) && alpha > 0.0f) || !(finite(c) && c >= 0.0f) || !(finite(eps) && eps >= 0.0f))
+    return EMBLA_ERR_INVALID_ARG;
+  PackedPrefillParams p = {};
+  p.alpha = alpha;
+  p.c = c;
+  p.eps = eps;
+  return packed_prefill_impl(kPackedRelu2, shape, G, n_tokens, cu_tokens, n_keys, cu_keys, q, q_stride, k, k_stride, v,
+                             v_stride, kMaxPackedTokens, p, out, workspace, workspace_bytes, stream);
+}
+
+embla_status embla_window_decode_ragged(const embla_shape *shape, const void *q, const void *k_win,
+                                        const void *v_win, int32_t window, const int32_t *pos,
+                                        float tau, float *out, void *stream) {
+  int G = 0;
+  embla_status st = check_shape(shape, &G, false);
+  if (st != EMBLA_OK) return st;
+  if (window < 1 || window > 1024 || !finite(tau)) return EMBLA_ERR_INVALID_ARG;
+  const int64_t units = static_cast<int64_t>(shape->batch) * shape->n_kv_heads;
+  if (units == 0) return EMBLA_OK;
+  if (!q || !k_win || !v_win || !pos || !out) return EMBLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_win) || !aligned16(v_win) || !aligned16(pos) || !aligned16(out))
+    return EMBLA_ERR_INVALID_ARG;
+  if (units > INT32_MAX / 8) return EMBLA_ERR_UNSUPPORTED;
+  const RaggedWindowParams p = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(k_win),
+                                static_cast<const uint8_t *>(v_win), pos, out, shape->n_kv_heads, window,
+                                tau * 1.4426950408889634f};
+  return cuda_status(launch_window_decode_ragged(G, units, p, static_cast<cudaStream_t>(stream)));
 }
 
 embla_status embla_skip_stats(const embla_shape *shape, const float *sel_scores, int32_t chunk,

@@ -1,0 +1,135 @@
+// Queries and keys of packed tokens normed per head and rotated at their positions in one pass,
+// the newest rows of every sequence written into its window rings ("The Architecture of Embla 1",
+// "Three kinds of attention": the window layers are the positional ones, and a ring holds keys
+// that were rotated when they were written).
+//
+//   y = x                                    or  x / sqrt(mean(x^2) + eps) * gain   (fp32)
+//   (y_2i, y_2i+1) turned by p base^(-2i/D)                                         (fp32)
+//   rounded once to bf16.
+//
+// The angle.  A pair turns by f_i = base^(-2i/D) / (2 pi) of a circle per position, and only the
+// fraction of p f_i counts.  The host gives F_i = f_i 2^64 rounded to an integer: p F_i modulo 2^64 is that
+// fraction with no error but F_i's own (p 2^-54 of a circle from the double it came from, 2^-33 at
+// a position of 2^20), by one integer product and no 64-bit floats.  Its top 32 bits, as a signed part
+// of half a circle, go to sincospif.
+//
+// Sixteen lanes take the G query heads and the key head of one KV group of one token, 16 bytes of
+// each row per lane, so a lane works out its four angles once for G + 1 rows and has all of their
+// loads in flight together.  Nothing is read twice and nothing waits on another lane but the norm's
+// sum: bound by HBM.
+#include "ptx_blocks.cuh"
+#include "ragged.h"
+
+namespace embla {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeLanes = 16;  // lanes per (token, KV group)
+constexpr int kRopePerBlock = kRopeThreads / kRopeLanes;
+
+// How many sequences end at or before token t (cu[b + 1] <= t), found by the sixteen lanes of a
+// half warp 16 ways at a time: the sequence that t lies in, or `batch` past the last one.
+__device__ __forceinline__ int sequence_of(const PackedTokens &s, int64_t t, int sl, uint32_t half) {
+  int lo = 0, hi = s.batch;  // the answer lies in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 15) / 16;
+    const int at = lo + (sl + 1) * step;  // sequences lo .. at - 1 end by t if number at - 1 does
+    const bool past = at <= hi && s.cu[at] <= t;
+    const int n = __popc(__ballot_sync(half, past) & half);
+    const int from = lo + n * step;
+    hi = min(hi, from + step - 1);
+    lo = from;
+  }
+  return lo;
+}
+
+template <int G, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  pdl_wait_primary();  // the rows are written; whoever read the old outputs and rings is done
+  pdl_launch_dependents();
+  const int sl = threadIdx.x % kRopeLanes;
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopePerBlock + threadIdx.x / kRopeLanes;
+  const int64_t t = w / p.Hkv;
+  const int g = static_cast<int>(w - t * p.Hkv);
+  if (t >= p.seqs.tokens) return;  // (half warps leave whole)
+  const int d = sl * 8;            // this lane's dims d .. d + 7: pairs 4 sl .. 4 sl + 3
+  uint4 x[G + 1], v = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int h = 0; h < G; ++h)
+    x[h] = __ldcs(reinterpret_cast<const uint4 *>(p.q.base + t * p.q.stride + (g * G + h) * kHeadDim + d));
+  x[G] = __ldcs(reinterpret_cast<const uint4 *>(p.k.base + t * p.k.stride + g * kHeadDim + d));
+  const int b = sequence_of(p.seqs, t, sl, half);
+  if (b >= p.seqs.batch) return;  // behind the last sequence
+  const int64_t first = p.seqs.cu[b], end = p.seqs.cu[b + 1];
+  if (t < first) return;
+  const uint32_t pos = (p.pos0 ? static_cast<uint32_t>(p.pos0[b]) : 0u) + static_cast<uint32_t>(t - first);
+  const bool ring = p.k_win != nullptr && t >= end - p.window;  // among the newest
+  if (ring) v = __ldcs(reinterpret_cast<const uint4 *>(p.v.base + t * p.v.stride + g * kHeadDim + d));
+  float c[4], s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t half_turns = static_cast<int32_t>((pos * p.turn[4 * sl + i]) >> 32);
+    sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s[i], &c[i]);
+  }
+  float gq[8], gk[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    gq[i] = NORM && p.q_gain ? p.q_gain[d + i] : 1.0f;
+    gk[i] = NORM && p.k_gain ? p.k_gain[d + i] : 1.0f;
+  }
+#pragma unroll
+  for (int h = 0; h <= G; ++h) {
+    const uint32_t r[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+    float rs = 1.0f;
+    if constexpr (NORM) {
+      float a = 0.0f, e = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sq_acc_bf16x2(r[i], a, e);
+      a += e;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(half, a, o);
+      rs = 1.0f / sqrtf(a * (1.0f / kHeadDim) + p.eps);
+    }
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float e = bf16lo(r[i]), f = bf16hi(r[i]);
+      if constexpr (NORM) {
+        e *= rs * (h < G ? gq[2 * i] : gk[2 * i]);
+        f *= rs * (h < G ? gq[2 * i + 1] : gk[2 * i + 1]);
+      }
+      y[i] = pack_bf16x2(e * c[i] - f * s[i], e * s[i] + f * c[i]);
+    }
+    x[h] = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  if (p.q_out) {
+    uint16_t *to = p.q_out + (t * p.Hkv + g) * G * kHeadDim + d;
+#pragma unroll
+    for (int h = 0; h < G; ++h) *reinterpret_cast<uint4 *>(to + h * kHeadDim) = x[h];
+  }
+  if (p.k_out) *reinterpret_cast<uint4 *>(p.k_out + (t * p.Hkv + g) * kHeadDim + d) = x[G];
+  if (ring) {
+    const int64_t row = (static_cast<int64_t>(b) * p.Hkv + g) * p.window + pos % static_cast<uint32_t>(p.window);
+    *reinterpret_cast<uint4 *>(p.k_win + row * kHeadDim + d) = x[G];
+    *reinterpret_cast<uint4 *>(p.v_win + row * kHeadDim + d) = v;
+  }
+}
+
+template <int G>
+cudaError_t launch_rope_g(const RopeParams &p, cudaStream_t stream) {
+  const int64_t blocks = (p.seqs.tokens * p.Hkv + kRopePerBlock - 1) / kRopePerBlock;
+  return launch_pdl(p.norm ? rope_kernel<G, true> : rope_kernel<G, false>, dim3(static_cast<unsigned>(blocks)),
+                    dim3(kRopeThreads), 0, stream, 0u, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_qkv(int G, const RopeParams &p, cudaStream_t stream) {
+  if (p.seqs.tokens == 0) return cudaSuccess;
+  if (G == 4) return launch_rope_g<4>(p, stream);
+  if (G == 8) return launch_rope_g<8>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace embla
