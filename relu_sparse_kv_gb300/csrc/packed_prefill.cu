@@ -37,21 +37,23 @@
 // A block's sequence.  The host knows no lengths, so block numbers are spread with room to spare: sequence
 // b owns the numbers from floor(cu_q[b] / R) + b (R tokens to a block), which is enough for its blocks,
 // and a number past them is skipped.  The owner is found by a 32-way search.
+#include <type_traits>
+
 #include "ptx_blocks.cuh"
 #include "ragged.h"
 
 namespace embla {
 namespace {
 
-constexpr int kEpiWarps = 8;
-constexpr int kWarpPV = 2 + kEpiWarps;
-constexpr int kThreads = (3 + kEpiWarps) * 32;
-constexpr int kRing = 3;           // K and V stages, S/P buffers
+#ifndef EMBLA_SHORT_SPAN
+#define EMBLA_SHORT_SPAN 240
+#endif
+constexpr int kTeamWarps = 8;      // warps that turn a block's scores into weights
+constexpr int kRing = 3;           // V stages and S/P buffers
 constexpr int kBoxQ = 128 * 128;   // [128 rows][64 bf16]
 constexpr float kSlack = 8.0f;     // P stays below 2^kSlack
 constexpr uint64_t kLimitNs = 10000000000ull;  // 10 s: a row computed key by key holds the others up
-constexpr int kColO = kRing * 128, kTmemCols = 512;
-static_assert(kColO + 128 <= kTmemCols, "tensor memory");
+constexpr int kTmemCols = 512;
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) MN-major
 
 // What a block is, relative to its first key row k0: row i / G's newest key is p0 + i, its oldest
@@ -64,21 +66,27 @@ struct Block {
   int32_t k0;     // first key row of tile 0
   int32_t p0;     // the first token's newest key, less k0
   int32_t seq0;   // the sequence's first key, less k0
-  int32_t pad;
+  int32_t tile0;  // tiles of the blocks before
 };
 
-template <int N>
+// TEAMS sets of kTeamWarps warps take blocks in turn; each has query rows, an O and row sums of its own.
+template <int N, int TEAMS>
 struct Layout {
+  static constexpr int kThreads = (4 + TEAMS * kTeamWarps) * 32;
+  static constexpr int kWarpPV = 2 + TEAMS * kTeamWarps, kWarpV = kWarpPV + 1;
+  static constexpr int kRingK = N < 128 ? 4 : 3;  // K stages
+  static constexpr int kColO = kRing * N;  // TEAMS times 128 columns
+  static_assert(kColO + TEAMS * 128 <= kTmemCols, "tensor memory");
   static constexpr int kBoxKV = N * 128;  // [N rows][64 bf16]
   static constexpr int kStage = 2 * kBoxKV;
-  static constexpr int kOffK = 2 * kBoxQ;
-  static constexpr int kOffV = kOffK + kRing * kStage;
-  static constexpr int kOffSum = kOffV + kRing * kStage;  // [2][128] row sums
-  static constexpr int kOffBlock = kOffSum + 2 * 128 * 4;
-  static constexpr int kOffBar = kOffBlock + 2 * static_cast<int>(sizeof(Block));
-  static constexpr int kNBars = 5 * kRing + 4;
+  static constexpr int kOffK = TEAMS * 2 * kBoxQ;
+  static constexpr int kOffV = kOffK + kRingK * kStage;
+  static constexpr int kOffSum = kOffV + kRing * kStage;  // [TEAMS][2][128] row sums
+  static constexpr int kOffBlock = kOffSum + TEAMS * 2 * 128 * 4;
+  static constexpr int kOffBar = kOffBlock + TEAMS * static_cast<int>(sizeof(Block));
+  static constexpr int kNBars = 2 * kRingK + 4 * kRing + 4 * TEAMS;
   static constexpr int kOffMisc = kOffBar + kNBars * 8;
-  static constexpr int kBytes = kOffMisc + 16 + 1024;  // + room to align the base to 1024
+  static constexpr int kBytes = kOffMisc + 32 + 1024;  // + room to align the base to 1024
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -89,55 +97,70 @@ __device__ __forceinline__ void set_abort(volatile int *abort_flag, uint32_t *fl
   atomicOr(flags, kFlagWaitTimeout);
 }
 
-// The k-th block number of CTA c among P: a round of P at a time, alternate rounds in reverse
-// order, so the CTAs' sums of key tiles stay close.  -1 past the end.
-__device__ __forceinline__ int64_t block_of(const PackedPrefillParams &p, int k, int c, int P) {
-  const int64_t idx = static_cast<int64_t>(k) * P + ((k & 1) ? P - 1 - c : c);
-  return idx < p.blocks ? idx : -1;
-}
-
 // Entries that do not ascend or lie outside the rows.
 __device__ __forceinline__ bool bad_sequence(const PackedPrefillParams &p, int64_t q_lo, int64_t q_hi, int64_t k_lo,
                                              int64_t k_hi) {
   return q_lo < 0 || q_hi < q_lo || q_hi > p.tokens || k_lo < 0 || k_hi < k_lo || k_hi > p.keys;
 }
 
-// Block number idx (the whole warp calls); tiles < 0 where there is none.
+// The blocks of a CTA, one after the other (the whole warp calls).
 template <int MODE, int N, int G>
-__device__ __forceinline__ Block find_block(const PackedPrefillParams &p, int64_t idx, int lane) {
-  constexpr int R = 128 / G;
-  Block r = {};
-  r.tiles = -1;
-  r.g = static_cast<int32_t>(idx % p.Hkv);
-  const int64_t v = p.blocks / p.Hkv - 1 - idx / p.Hkv;  // the last ones, with the most keys, first
-  // sequences whose successor's numbers begin at or before v
-  int lo = 0, hi = p.batch;
-  while (hi > lo) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + (lane + 1) * step;
-    const bool past = at <= hi && p.cu_q[at] / R + at <= v;
-    const int n = __popc(__ballot_sync(0xffffffffu, past));
-    const int from = lo + n * step;
-    hi = min(hi, from + step - 1);
-    lo = from;
+struct BlockFinder {
+  static constexpr int R = 128 / G;
+  int cta, ctas, round = 0;
+  // the sequence found last: its block numbers, queries and keys
+  int64_t first = 0, end = 0, q_lo = 0, q_hi = 0, k_lo = 0, k_hi = 0;
+  __device__ BlockFinder(int c, int n) : cta(c), ctas(n) {}
+
+  // The sequence that owns block number v becomes the one found last; false where there is none.
+  __device__ __forceinline__ bool find(const PackedPrefillParams &p, int64_t v, int lane) {
+    if (v >= first && v < end) return true;
+    int lo = 0, hi = p.batch;  // sequences whose successor's numbers begin at or before v
+    while (hi > lo) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = lo + (lane + 1) * step;
+      const bool past = at <= hi && p.cu_q[at] / R + at <= v;
+      const int n = __popc(__ballot_sync(0xffffffffu, past));
+      const int from = lo + n * step;
+      hi = min(hi, from + step - 1);
+      lo = from;
+    }
+    if (lo >= p.batch) return false;
+    q_lo = p.cu_q[lo], q_hi = p.cu_q[lo + 1], k_lo = p.cu_k[lo], k_hi = p.cu_k[lo + 1];
+    first = end = q_lo / R + lo;
+    if (bad_sequence(p, q_lo, q_hi, k_lo, k_hi)) return false;
+    end = first + (q_hi - q_lo + R - 1) / R;
+    return v >= first && v < end;
   }
-  if (lo >= p.batch) return r;
-  const int64_t q_lo = p.cu_q[lo], q_hi = p.cu_q[lo + 1], k_lo = p.cu_k[lo], k_hi = p.cu_k[lo + 1];
-  if (bad_sequence(p, q_lo, q_hi, k_lo, k_hi)) return r;
-  const int64_t t0 = (v - (q_lo / R + lo)) * R, lq = q_hi - q_lo, lk = k_hi - k_lo;
-  if (t0 < 0 || t0 >= lq) return r;
-  r.q0 = static_cast<int32_t>(q_lo + t0);
-  r.nq = static_cast<int32_t>(lq - t0 < R ? lq - t0 : R);
-  const int64_t first = lk - lq + t0, last = first + r.nq - 1;  // newest keys of the first and last token
-  const int64_t oldest = first - p.window + 1 > 0 ? first - p.window + 1 : 0;
-  int64_t k0 = k_lo + oldest;
-  if (MODE == kPackedRelu2) k0 &= ~static_cast<int64_t>(3);  // (the key norms are read in pairs)
-  r.tiles = last < 0 ? 0 : static_cast<int32_t>((k_lo + last - k0) / N) + 1;
-  r.k0 = static_cast<int32_t>(k0);
-  r.p0 = static_cast<int32_t>(k_lo + first - k0);
-  r.seq0 = static_cast<int32_t>(k_lo - k0);
-  return r;
-}
+
+  // The next block; tiles < 0 after the last.  A round of numbers is dealt at a time, alternate rounds in
+  // reverse order, so the CTAs' sums of key tiles stay close.
+  __device__ __forceinline__ Block next(const PackedPrefillParams &p, int lane) {
+    Block r = {};
+    r.tiles = -1;
+    for (;; ++round) {
+      const int64_t idx = static_cast<int64_t>(round) * ctas + ((round & 1) ? ctas - 1 - cta : cta);
+      if (static_cast<int64_t>(round) * ctas >= p.blocks) return r;
+      if (idx >= p.blocks) continue;
+      const int64_t v = p.blocks / p.Hkv - 1 - idx / p.Hkv;  // the last ones, with the most keys, first
+      if (!find(p, v, lane)) continue;
+      const int64_t t0 = (v - first) * R, lq = q_hi - q_lo, lk = k_hi - k_lo;
+      r.g = static_cast<int32_t>(idx % p.Hkv);
+      r.q0 = static_cast<int32_t>(q_lo + t0);
+      r.nq = static_cast<int32_t>(lq - t0 < R ? lq - t0 : R);
+      const int64_t newest = lk - lq + t0, last = newest + r.nq - 1;  // of the first and last token
+      const int64_t oldest = newest - p.window + 1 > 0 ? newest - p.window + 1 : 0;
+      int64_t k0 = k_lo + oldest;
+      if (MODE == kPackedRelu2) k0 &= ~static_cast<int64_t>(3);  // (the key norms are read in pairs)
+      r.tiles = last < 0 ? 0 : static_cast<int32_t>((k_lo + last - k0) / N) + 1;
+      r.k0 = static_cast<int32_t>(k0);
+      r.p0 = static_cast<int32_t>(k_lo + newest - k0);
+      r.seq0 = static_cast<int32_t>(k_lo - k0);
+      ++round;
+      return r;
+    }
+  }
+};
 
 // Row r of a block (token r / G, head r % G) computed key by key: columns 64 half .. + 63 of its
 // output, by one warp.  In two passes, so that no partial sum is larger than the result needs:
@@ -220,12 +243,34 @@ __device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block 
                                 2 * lane) = pack_bf16x2(a0, a1);
 }
 
-template <int MODE, int N, int G>
-__global__ void __launch_bounds__(kThreads, 1)
+// Scores of 16 rows x N keys to registers: element 4j + 2i + e is row l / 4 + 8i, key 8j + 2(l % 4) + e; and
+// their weights back over them, packed in pairs: word 2j + i.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&acc)[N / 2]) {
+  static_assert(N == 128 || N == 80, "key tile");
+  if constexpr (N == 128) {
+    tmem_load_16x256b_x16(taddr, acc);
+  } else {
+    tmem_load_16x256b_x8(taddr, *reinterpret_cast<uint32_t(*)[32]>(&acc[0]));
+    tmem_load_16x256b_x2(taddr + 64, *reinterpret_cast<uint32_t(*)[8]>(&acc[32]));
+  }
+  tmem_wait_ld(acc);
+}
+template <int N>
+__device__ __forceinline__ void store_weights(uint32_t taddr, const uint32_t (&w)[N / 4]) {
+  if constexpr (N == 128) {
+    tmem_store_16x128b_x16(taddr, w);
+  } else {
+    tmem_store_16x128b_x8(taddr, *reinterpret_cast<const uint32_t(*)[16]>(&w[0]));
+    tmem_store_16x128b_x2(taddr + 32, *reinterpret_cast<const uint32_t(*)[4]>(&w[16]));
+  }
+}
+
+template <int MODE, int N, int G, int TEAMS>
+__global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     packed_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedPrefillParams p) {
-  using L = Layout<N>;
-  static_assert(N % 16 == 0 && N <= 128, "key tile");
+  using L = Layout<N, TEAMS>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -233,41 +278,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   float *sSum = reinterpret_cast<float *>(smem + L::kOffSum);
   Block *sBlock = reinterpret_cast<Block *>(smem + L::kOffBlock);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
-  // A K stage is free once its tile's S is done (sfull), a V stage once its P V is done
-  // (pvdone).  Block k's barriers take phase k & 1, tile g's phase (g / kRing) & 1.
-  uint64_t *kfull = bars, *vfull = kfull + kRing;
-  uint64_t *sfull = vfull + kRing;   // S of a tile in tensor memory; its K stage free
+  // Tile g has V stage and S/P buffer g % kRing in phase (g / kRing) & 1 and K stage g % kRingK in
+  // phase (g / kRingK) & 1.  Block k has the query rows, the description and the O of team k % TEAMS
+  // in phase (k / TEAMS) & 1.
+  constexpr int kRingK = L::kRingK;
+  uint64_t *kfull = bars, *kempty = kfull + kRingK, *vfull = kempty + kRingK;
+  uint64_t *sfull = vfull + kRing;   // S of a tile in tensor memory
   uint64_t *pfull = sfull + kRing;   // its P written over it
   uint64_t *pvdone = pfull + kRing;  // its P V done: the S/P buffer and the V stage are free
   uint64_t *qfull = pvdone + kRing;  // a block's description and query rows are there
-  uint64_t *qempty = qfull + 1;      // the description read by everyone, the query rows used
-  uint64_t *ofull = qempty + 1;      // a block's P V all done
-  uint64_t *ofree = ofull + 1;       // its O read out of tensor memory
+  uint64_t *qempty = qfull + TEAMS;  // the description read by everyone, the query rows used
+  uint64_t *ofull = qempty + TEAMS;  // a block's P V all done
+  uint64_t *ofree = ofull + TEAMS;   // its O read out of tensor memory
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   uint32_t *s_tmem = misc;
   volatile int *s_abort = reinterpret_cast<volatile int *>(misc + 1);
-  volatile int *s_issued = reinterpret_cast<volatile int *>(misc + 2);   // loads issued: 2 per tile
-  volatile int *s_qissued = reinterpret_cast<volatile int *>(misc + 3);  // query loads issued
+  volatile int *s_issued = reinterpret_cast<volatile int *>(misc + 2);   // K tiles, V tiles and query blocks
+                                                                         // whose loads were issued
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = static_cast<int>(blockIdx.x), P = static_cast<int>(gridDim.x);
 
   if (warp == 0) {
     if (lane < kRing) {
-      mbar_init(&kfull[lane], 1);
       mbar_init(&vfull[lane], 1);
       mbar_init(&sfull[lane], 1);
-      mbar_init(&pfull[lane], kEpiWarps);
+      mbar_init(&pfull[lane], kTeamWarps);
       mbar_init(&pvdone[lane], 1);
     }
+    if (lane < kRingK) {
+      mbar_init(&kfull[lane], 1);
+      mbar_init(&kempty[lane], 1);
+    }
+    if (lane < TEAMS) {
+      mbar_init(&qfull[lane], 1);
+      mbar_init(&qempty[lane], 3 + kTeamWarps);  // the S issuer's commit, the P V issuer, the V loads, the team
+      mbar_init(&ofull[lane], 1);
+      mbar_init(&ofree[lane], kTeamWarps);
+    }
     if (lane == 0) {
-      mbar_init(qfull, 1);
-      mbar_init(qempty, 2 + kEpiWarps);  // the S issuer's commit, the P V issuer, the weights' warps
-      mbar_init(ofull, 1);
-      mbar_init(ofree, kEpiWarps);
       *s_abort = 0;
-      *s_issued = 0;
-      *s_qissued = 0;
+      s_issued[0] = s_issued[1] = s_issued[2] = 0;
     }
     fence_barrier_init();
   }
@@ -283,61 +334,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ blocks and loads
+    // ------------------------------------------------------------------ blocks, Q and K loads
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
     }
-    int g = 0, k = 0;
-    bool ok = true, more = true;
-    for (int n = 0; ok && more; ++n) {
-      const int64_t idx = block_of(p, n, cta, P);
-      more = idx >= 0;
-      Block b = {};
-      b.tiles = -1;
-      if (more) {
-        b = find_block<MODE, N, G>(p, idx, lane);
-        if (b.tiles < 0) continue;
-      }
+    BlockFinder<MODE, N, G> finder(cta, P);
+    Block b = finder.next(p, lane);
+    int g = 0;
+    bool ok = true;
+    for (int k = 0, ends = 0; ok && ends < TEAMS; ++k) {  // (each team is told of the end)
+      const int s = k % TEAMS;
+      b.tile0 = g;
       if (lane == 0) {
-        // the query buffer and the description are free once the block before is done with them
-        ok = k == 0 || wait_bar(qempty, (k - 1) & 1);
+        // the query rows and the description are free once the team's block before is done with them
+        ok = k < TEAMS || wait_bar(&qempty[s], ((k / TEAMS) - 1) & 1);
         if (ok) {
-          sBlock[k & 1] = b;
+          sBlock[s] = b;
           if (b.tiles > 0) {
-            mbar_arrive_expect_tx(qfull, 2 * kBoxQ);
-            tma_load_4d(sQ, &tm_q, qfull, 0, 0, b.g, b.q0);
-            tma_load_4d(sQ + kBoxQ, &tm_q, qfull, 64, 0, b.g, b.q0);
+            uint8_t *to = sQ + s * 2 * kBoxQ;
+            mbar_arrive_expect_tx(&qfull[s], 2 * kBoxQ);
+            tma_load_4d(to, &tm_q, &qfull[s], 0, 0, b.g, b.q0);
+            tma_load_4d(to + kBoxQ, &tm_q, &qfull[s], 64, 0, b.g, b.q0);
           } else {
-            mbar_arrive(qfull);
+            mbar_arrive(&qfull[s]);
           }
-          *s_qissued = k + 1;
+          s_issued[2] = k + 1;
           for (int t = 0; t < b.tiles; ++t, ++g) {
-            const int s = g % kRing;
-            const uint32_t ph = ((g / kRing) - 1) & 1;
-            if (g >= kRing && !wait_bar(&sfull[s], ph)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&kfull[s], L::kStage);
-            tma_load_3d(sK + s * L::kStage, &tm_k, &kfull[s], 0, b.g, b.k0 + t * N);
-            tma_load_3d(sK + s * L::kStage + L::kBoxKV, &tm_k, &kfull[s], 64, b.g, b.k0 + t * N);
-            if (g >= kRing && !wait_bar(&pvdone[s], ph)) {
-              *s_issued = 2 * g + 1;
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&vfull[s], L::kStage);
-            tma_load_3d(sV + s * L::kStage, &tm_v, &vfull[s], 0, b.g, b.k0 + t * N);
-            tma_load_3d(sV + s * L::kStage + L::kBoxKV, &tm_v, &vfull[s], 64, b.g, b.k0 + t * N);
-            *s_issued = 2 * g + 2;
+            const int r = g % kRingK;
+            ok = g < kRingK || wait_bar(&kempty[r], ((g / kRingK) - 1) & 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&kfull[r], L::kStage);
+            tma_load_3d(sK + r * L::kStage, &tm_k, &kfull[r], 0, b.g, b.k0 + t * N);
+            tma_load_3d(sK + r * L::kStage + L::kBoxKV, &tm_k, &kfull[r], 64, b.g, b.k0 + t * N);
+            s_issued[0] = g + 1;
           }
         }
         if (!ok) set_abort(s_abort, p.flags);
       }
-      ++k;
       ok = __shfl_sync(0xffffffffu, ok, 0);
+      g = __shfl_sync(0xffffffffu, g, 0);
+      if (b.tiles < 0)
+        ++ends;
+      else
+        b = finder.next(p, lane);
     }
     // entries that no block could use are reported
     for (int64_t b = static_cast<int64_t>(cta) * 32 + lane; b < p.batch; b += static_cast<int64_t>(P) * 32)
@@ -350,49 +390,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       int g = 0, blocks = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        ok = !*s_abort && wait_bar(qfull, k & 1);
+        const int s = k % TEAMS;
+        ok = !*s_abort && wait_bar(&qfull[s], (k / TEAMS) & 1);
         if (!ok) break;
-        const int tiles = sBlock[k & 1].tiles;
+        const int tiles = sBlock[s].tiles;
         if (tiles < 0) break;
         for (int t = 0; ok && t < tiles; ++t, ++g) {
-          const int sb = g % kRing;
-          ok = wait_bar(&kfull[sb], (g / kRing) & 1) &&
+          const int sb = g % kRing, kb = g % kRingK;
+          ok = wait_bar(&kfull[kb], (g / kRingK) & 1) &&
                (g < kRing || wait_bar(&pvdone[sb], ((g / kRing) - 1) & 1));
           if (!ok) break;
           tc_fence_after_sync();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // dims 16kk .. 16kk + 15: 32 bytes into a 128-byte row; dims 64.. start the second box
-            const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * kBoxQ + (kk & 3) * 32) >> 4);
-            const uint64_t ko = static_cast<uint64_t>((sb * L::kStage + (kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4);
-            tc_mma_bf16(tmem + sb * 128, qdesc + qo, kdesc + ko, kIdescS, kk > 0 ? 1u : 0u);
+            const uint64_t qo = static_cast<uint64_t>(((2 * s + (kk >> 2)) * kBoxQ + (kk & 3) * 32) >> 4);
+            const uint64_t ko = static_cast<uint64_t>((kb * L::kStage + (kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4);
+            tc_mma_bf16(tmem + sb * N, qdesc + qo, kdesc + ko, kIdescS, kk > 0 ? 1u : 0u);
           }
           tc_commit(&sfull[sb]);
+          tc_commit(&kempty[kb]);
         }
         if (ok) {
-          tc_commit(qempty);
+          tc_commit(&qempty[s]);
           blocks = k + 1;
         }
       }
       if (!ok) set_abort(s_abort, p.flags);
-      // every MMA of this thread has completed, and its last commit arrived, before the tensor
+      // every MMA of this thread has completed, and its last commits arrived, before the tensor
       // memory is released and the CTA leaves (also when another role has given up)
       if (g > 0) wait_bar(&sfull[(g - 1) % kRing], ((g - 1) / kRing) & 1);
-      if (blocks > 0) wait_bar(qempty, (blocks - 1) & 1);
+      if (g > 0) wait_bar(&kempty[(g - 1) % kRingK], ((g - 1) / kRingK) & 1);
+      for (int k = blocks - 1; k >= 0 && k >= blocks - TEAMS; --k) wait_bar(&qempty[k % TEAMS], (k / TEAMS) & 1);
     }
     __syncwarp();
-  } else if (warp == kWarpPV) {
+  } else if (warp == L::kWarpPV) {
     // ------------------------------------------------------------------ P V issuer
     if (lane == 0) {
       int g = 0, blocks = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        ok = !*s_abort && wait_bar(qfull, k & 1);
+        const int s = k % TEAMS;
+        ok = !*s_abort && wait_bar(&qfull[s], (k / TEAMS) & 1);
         if (!ok) break;
-        const int tiles = sBlock[k & 1].tiles;
-        mbar_arrive(qempty);
+        const int tiles = sBlock[s].tiles;
+        mbar_arrive(&qempty[s]);
         if (tiles < 0) break;
-        ok = k == 0 || wait_bar(ofree, (k - 1) & 1);  // the block before's O has been read
+        // the O of the team's block before has been read
+        ok = k < TEAMS || wait_bar(&ofree[s], ((k / TEAMS) - 1) & 1);
+        const uint32_t o = tmem + L::kColO + s * 128;
         for (int t = 0; ok && t < tiles; ++t, ++g) {
           const int pb = g % kRing;
           ok = wait_bar(&pfull[pb], (g / kRing) & 1) && wait_bar(&vfull[pb], (g / kRing) & 1);
@@ -402,111 +448,139 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < N / 16; ++kk) {
             // keys 16kk .. 16kk + 15: eight columns of P, V rows 16kk .. (2 KB apart)
             const uint64_t vd = smem_desc_sw128_mn(smem_u32(sV + pb * L::kStage + kk * 2048), L::kBoxKV);
-            tc_mma_bf16_tmem_a(tmem + kColO, tmem + pb * 128 + 8 * kk, vd, kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_bf16_tmem_a(o, tmem + pb * N + 8 * kk, vd, kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
           }
           tc_commit(&pvdone[pb]);
         }
         if (ok) {
-          tc_commit(ofull);
+          tc_commit(&ofull[s]);
           blocks = k + 1;
         }
       }
       if (!ok) set_abort(s_abort, p.flags);
       // every MMA of this thread has completed before the tensor memory is released
       if (g > 0) wait_bar(&pvdone[(g - 1) % kRing], ((g - 1) / kRing) & 1);
-      if (blocks > 0) wait_bar(ofull, (blocks - 1) & 1);
+      for (int k = blocks - 1; k >= 0 && k >= blocks - TEAMS; --k) wait_bar(&ofull[k % TEAMS], (k / TEAMS) & 1);
+    }
+    __syncwarp();
+  } else if (warp == L::kWarpV) {
+    // ------------------------------------------------------------------ V loads
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_v);
+      int g = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int s = k % TEAMS;
+        ok = !*s_abort && wait_bar(&qfull[s], (k / TEAMS) & 1);
+        if (!ok) break;
+        const int tiles = sBlock[s].tiles, head = sBlock[s].g, k0 = sBlock[s].k0;
+        mbar_arrive(&qempty[s]);
+        if (tiles < 0) break;
+        for (int t = 0; t < tiles; ++t, ++g) {
+          const int r = g % kRing;
+          ok = g < kRing || wait_bar(&pvdone[r], ((g / kRing) - 1) & 1);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&vfull[r], L::kStage);
+          tma_load_3d(sV + r * L::kStage, &tm_v, &vfull[r], 0, head, k0 + t * N);
+          tma_load_3d(sV + r * L::kStage + L::kBoxKV, &tm_v, &vfull[r], 64, head, k0 + t * N);
+          s_issued[1] = g + 1;
+        }
+      }
+      if (!ok) set_abort(s_abort, p.flags);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ weights and outputs
-    const int quarter = warp & 3;      // the tensor-memory lanes this warp may reach
-    const int half = (warp - 2) >> 2;  // rows 16 half .. of them; at the end columns 64 half .. of O
-    const int row0 = quarter * 32 + half * 16 + (lane >> 2);  // this lane's rows: row0 and row0 + 8
-    const int q2 = 2 * (lane & 3);                            // its columns: 8j + q2 and the next
+    const int team = (warp - 2) / kTeamWarps;
+    const int quarter = warp & 3;           // the tensor-memory lanes this warp may reach
+    const int half = ((warp - 2) >> 2) & 1; // rows 16 half .. of them; at the end columns 64 half .. of O
+    const int rowa = quarter * 32 + half * 16;  // the warp's first row
+    const int row0 = rowa + (lane >> 2);        // this lane's rows: row0 and row0 + 8
+    const int q2 = 2 * (lane & 3);              // its columns: 8j + q2 and the next
     const uint32_t lanes32 = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t lanes16 = lanes32 + (static_cast<uint32_t>(half * 16) << 16);
+    const uint32_t colo = tmem + L::kColO + team * 128;
     const bool flip = MODE == kPackedSoftmax && p.tau2 < 0.0f;
     const float tau2 = fabsf(p.tau2);
-    int g = 0;
     bool ok = true;
-    for (int k = 0;; ++k) {
-      // (every decision to go on is the group's: what follows is warp-wide and has barriers)
-      ok = __all_sync(0xffffffffu, ok && !*s_abort && wait_bar(qfull, k & 1));
-      ok = named_bar_and(1, kEpiWarps * 32, ok);
+    for (int n = 0;; ++n) {  // the team's n-th block
+      // (every decision to go on is the team's: what follows is warp-wide and has barriers)
+      ok = __all_sync(0xffffffffu, ok && !*s_abort && wait_bar(&qfull[team], n & 1));
+      ok = named_bar_and(1 + team, kTeamWarps * 32, ok);
       if (!ok) break;
-      const Block b = sBlock[k & 1];
+      const Block b = sBlock[team];
       if (b.tiles < 0) break;
       float a2 = 0.0f;  // ReLU^2, row quarter * 32 + lane: alpha^2 / (mean(q^2) + eps)
       if (MODE == kPackedRelu2 && b.tiles > 0) {
         const int r = quarter * 32 + lane;
-        a2 = (p.alpha * p.alpha) / (row_square_sum(sQ, kBoxQ, r, r & 7) * (1.0f / kHeadDim) + p.eps);
+        const uint8_t *rows = sQ + team * 2 * kBoxQ;
+        a2 = (p.alpha * p.alpha) / (row_square_sum(rows, kBoxQ, r, r & 7) * (1.0f / kHeadDim) + p.eps);
         // the query rows are read: every lane's sum depends on them
         const float used = __shfl_sync(0xffffffffu, a2, 0) + __shfl_sync(0xffffffffu, a2, 31);
         __syncwarp();
-        if (lane == 0) mbar_arrive_after(qempty, used);
+        if (lane == 0) mbar_arrive_after(&qempty[team], used);
       } else {
         __syncwarp();
-        if (lane == 0) mbar_arrive(qempty);
+        if (lane == 0) mbar_arrive(&qempty[team]);
       }
-      // the keys that a row sees lie between these two, relative to k0
-      int newest[2], oldest[2];
+      // a row sees the keys oldest .. oldest + span, relative to k0 (none: from far behind the last)
+      int oldest[2];
+      uint32_t span[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        newest[i] = b.p0 + (row0 + 8 * i) / G;
-        oldest[i] = max(b.seq0, newest[i] - p.window + 1);
+        const int newest = b.p0 + (row0 + 8 * i) / G;
+        oldest[i] = max(b.seq0, newest - p.window + 1);
+        span[i] = static_cast<uint32_t>(newest - oldest[i]);
+        if (newest < oldest[i]) {
+          oldest[i] = 1 << 30;
+          span[i] = 0;
+        }
       }
-      // tiles between these two are seen whole by every row of the block
-      const int whole0 = max(b.seq0, b.p0 + b.nq - p.window), whole1 = b.p0;
-      float m[2] = {-INFINITY, -INFINITY};  // reference of each row (base 2)
+      // every row of the warp sees the keys between these two
+      const int whole0 = max(b.seq0, b.p0 + (rowa + 15) / G - p.window + 1), whole1 = b.p0 + rowa / G;
+      float m[2] = {-INFINITY, -INFINITY};    // reference of each row (base 2)
       float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // sums of its weights in this lane, two chains per row
-      for (int t = 0; t < b.tiles; ++t, ++g) {
+      // ReLU^2: the norms of this lane's keys, each read again for the next tile once it is used
+      float2 rk[MODE == kPackedRelu2 ? N / 8 : 1];
+      const float *rkp = nullptr;
+      if constexpr (MODE == kPackedRelu2) {
+        rkp = p.rk + b.g * p.rk_stride + b.k0 + q2;
+        if (b.tiles > 0) {
+#pragma unroll
+          for (int j = 0; j < N / 8; ++j) rk[j] = *reinterpret_cast<const float2 *>(rkp + 8 * j);
+        }
+      }
+      for (int t = 0; t < b.tiles; ++t) {
+        const int g = b.tile0 + t;
         const int sb = g % kRing;
         const int j0 = t * N;
-        float2 rk[MODE == kPackedRelu2 ? N / 8 : 1];
-        if constexpr (MODE == kPackedRelu2) {
-          const float *from = p.rk + b.g * p.rk_stride + b.k0 + j0 + q2;
-#pragma unroll
-          for (int j = 0; j < N / 8; ++j) rk[j] = *reinterpret_cast<const float2 *>(from + 8 * j);
-        }
         ok = __all_sync(0xffffffffu, wait_bar(&sfull[sb], (g / kRing) & 1));
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t cols = tmem + lanes16 + sb * 128;
-        uint32_t acc[N / 2];  // element 4j + 2i + e: row row0 + 8i, key j0 + 8j + q2 + e
-        if constexpr (N == 128) {
-          tmem_load_16x256b_x16(cols, acc);
-          tmem_wait_ld(acc);
-        } else {
-          static_assert(N == 128 || N == 80, "tile loads");
-          uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&acc[0]);
-          uint32_t(&hi)[8] = *reinterpret_cast<uint32_t(*)[8]>(&acc[32]);
-          tmem_load_16x256b_x8(cols, lo);
-          tmem_load_16x256b_x2(cols + 64, hi);
-          tmem_wait_ld(acc);
-        }
-        const bool masked = j0 < whole0 || j0 + N - 1 > whole1;
+        const uint32_t cols = tmem + lanes16 + sb * N;
+        uint32_t acc[N / 2];
+        load_scores<N>(cols, acc);
         uint32_t hi[N / 4];
         if constexpr (MODE == kPackedSoftmax) {
           if (flip) {
 #pragma unroll
             for (int e = 0; e < N / 2; ++e) acc[e] ^= 0x80000000u;
           }
-          if (masked) {
+          // keys that some row of the warp does not see, sixteen at a time
+          if (j0 < whole0 || j0 + N - 1 > whole1) {
+            const int lo[2] = {oldest[0] - j0 - q2, oldest[1] - j0 - q2};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t span = static_cast<uint32_t>(newest[i] - oldest[i]);
-              const int off = j0 + q2 - oldest[i];
-              const bool none = newest[i] < oldest[i];
+            for (int c = 0; c < N; c += 16) {
+              if (j0 + c < whole0 || j0 + c + 15 > whole1) {
 #pragma unroll
-              for (int j = 0; j < N / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (none || static_cast<uint32_t>(off + 8 * j + e) > span) acc[4 * j + 2 * i + e] = 0xFF800000u;
+                for (int e = 0; e < 8; ++e)
+                  if (static_cast<uint32_t>(c + 8 * (e >> 2) + (e & 1) - lo[(e >> 1) & 1]) > span[(e >> 1) & 1])
+                    acc[c / 2 + e] = 0xFF800000u;
+              }
             }
           }
-          float neg[2];
+          float neg[2], sc[2];
           bool grown = false;
-          float sc[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -535,13 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) l[i] *= sc[i >> 1];
 #pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-              uint32_t o[32];
-              tmem_load_16x256b_x8(tmem + lanes16 + kColO + c, o);
+            for (int c = 0; c < 128; c += 16) {
+              uint32_t o[8];
+              tmem_load_16x256b_x2(colo + lanes16 + c, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sc[(e >> 1) & 1]);
-              tmem_store_16x256b_x8(tmem + lanes16 + kColO + c, o);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sc[(e >> 1) & 1]);
+              tmem_store_16x256b_x2(colo + lanes16 + c, o);
             }
           }
 #pragma unroll
@@ -553,45 +627,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tau2, neg[i], neg[i]);
               e0 = exp2_approx(e0);
               e1 = exp2_approx(e1);
-              fma_f32x2(l[2 * i], l[2 * i + 1], e0, e1, 1.0f, 1.0f, l[2 * i], l[2 * i + 1]);
+              add_f32x2(l[2 * i], l[2 * i + 1], e0, e1);
               hi[2 * j + i] = pack_bf16x2(e0, e1);
             }
         } else {
+          const bool next = t + 1 < b.tiles;
+          rkp += N;
+          auto weights = [&](auto with_mask) {
+            const int lo[2] = {oldest[0] - j0 - q2, oldest[1] - j0 - q2};
 #pragma unroll
-          for (int j = 0; j < N / 8; ++j)
+            for (int j = 0; j < N / 8; ++j) {
+              float e[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // (a NaN score weighs nothing: the maximum of NaN and 0 is 0)
-              float e0, e1;
-              fma_f32x2(e0, e1, __uint_as_float(acc[4 * j + 2 * i]), __uint_as_float(acc[4 * j + 2 * i + 1]), rk[j].x,
-                        rk[j].y, 0.0f, 0.0f);
-              e0 = fmaxf(e0, 0.0f);
-              e1 = fmaxf(e1, 0.0f);
-              if (masked) {
-                const int c = j0 + 8 * j + q2;
-                if (c < oldest[i] || c > newest[i]) e0 = 0.0f;
-                if (c + 1 < oldest[i] || c + 1 > newest[i]) e1 = 0.0f;
+              for (int i = 0; i < 2; ++i)
+                mul_f32x2(e[2 * i], e[2 * i + 1], __uint_as_float(acc[4 * j + 2 * i]),
+                          __uint_as_float(acc[4 * j + 2 * i + 1]), rk[j].x, rk[j].y);
+              if (next) rk[j] = *reinterpret_cast<const float2 *>(rkp + 8 * j);
+              if constexpr (decltype(with_mask)::value) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (static_cast<uint32_t>(8 * j + (i & 1) - lo[i >> 1]) > span[i >> 1]) e[i] = 0.0f;
               }
-              fma_f32x2(e0, e1, e0, e1, e0, e1, 0.0f, 0.0f);
-              const uint32_t h = pack_bf16x2(e0, e1);
-              hi[2 * j + i] = h;
-              // the denominator sums the weights the numerator multiplies
-              fma_f32x2(l[2 * i], l[2 * i + 1], bf16lo(h), bf16hi(h), 1.0f, 1.0f, l[2 * i], l[2 * i + 1]);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                // max(x, 0)^2 = max(x |x|, 0); the denominator sums the weights the numerator multiplies.
+                // (A NaN score makes the row NaN here, and slow_row gives the key no weight.)
+                const uint32_t h = pack_relu_bf16x2(e[2 * i] * fabsf(e[2 * i]), e[2 * i + 1] * fabsf(e[2 * i + 1]));
+                hi[2 * j + i] = h;
+                add_bf16x2(h, l[2 * i], l[2 * i + 1]);
+              }
             }
+          };
+          // one code path per case, so that the common one has no mask
+          if (j0 < whole0 || j0 + N - 1 > whole1)
+            weights(std::true_type{});
+          else
+            weights(std::false_type{});
         }
-        if constexpr (N == 128) {
-          tmem_store_16x128b_x16(cols, hi);
-        } else {
-          tmem_store_16x128b_x8(cols, *reinterpret_cast<const uint32_t(*)[16]>(&hi[0]));
-          tmem_store_16x128b_x2(cols + 32, *reinterpret_cast<const uint32_t(*)[4]>(&hi[16]));
-        }
+        store_weights<N>(cols, hi);
         tmem_wait_st();
         tc_fence_before_sync();  // P is read by the tensor cores
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[sb]);
       }
       // the row sums, for the lanes that finish the rows
-      float *sum = sSum + (k & 1) * 128;
+      float *sum = sSum + (2 * team + (n & 1)) * 128;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = l[2 * i] + l[2 * i + 1];
@@ -599,20 +679,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         if (q2 == 0) sum[row0 + 8 * i] = x;
       }
-      ok = __all_sync(0xffffffffu, ok && !*s_abort && wait_bar(ofull, k & 1));
-      ok = named_bar_and(1, kEpiWarps * 32, ok);
+      ok = __all_sync(0xffffffffu, ok && !*s_abort && wait_bar(&ofull[team], n & 1));
+      ok = named_bar_and(1 + team, kTeamWarps * 32, ok);
       if (!ok) break;
       tc_fence_after_sync();
       // row quarter * 32 + lane, columns 64 half .. + 63
       const int r = quarter * 32 + lane;
-      uint32_t o[64];
-#pragma unroll
-      for (int c = 0; c < 64; c += 32)
-        tmem_load_x32(tmem + lanes32 + kColO + half * 64 + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
-      tmem_wait_ld(o);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ofree);  // the next block's P V may overwrite O
       const float s = sum[r];
       float f;  // 0 where no key weighs anything
       if (MODE == kPackedRelu2) {
@@ -623,29 +695,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool live = r / G < b.nq;
       const bool empty = f == 0.0f;
-      float chk = 0.0f;  // NaN if an output is infinite or NaN
-      uint32_t y[32];
+      float chk0 = 0.0f, chk1 = 0.0f;  // NaN if an output is infinite or NaN
+      uint16_t *dst = p.out + (static_cast<int64_t>(b.q0 + r / G) * p.Hkv * G + b.g * G + r % G) * kHeadDim + half * 64;
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float y0 = __uint_as_float(o[2 * c]) * f, y1 = __uint_as_float(o[2 * c + 1]) * f;
-        chk = fmaf(y0, 0.0f, fmaf(y1, 0.0f, chk));
-        y[c] = empty ? 0u : pack_bf16x2(y0, y1);
-      }
-      if (live) {
-        uint16_t *dst = p.out + (static_cast<int64_t>(b.q0 + r / G) * p.Hkv * G + b.g * G + r % G) * kHeadDim + half * 64;
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t o[32], y[16];
+        tmem_load_x32(colo + lanes32 + half * 64 + c, o);
+        tmem_wait_ld(o);
+        if (c == 32) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ofree[team]);  // the team's next P V may overwrite O
+        }
 #pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-          const uint4 w0 = make_uint4(y[c], y[c + 1], y[c + 2], y[c + 3]);
-          const uint4 w1 = make_uint4(y[c + 4], y[c + 5], y[c + 6], y[c + 7]);
-          if (p.out32) {  // whole sectors
-            st_global_v8(dst + 2 * c, w0, w1);
-          } else {
-            *reinterpret_cast<uint4 *>(dst + 2 * c) = w0;
-            *reinterpret_cast<uint4 *>(dst + 2 * c + 8) = w1;
+        for (int e = 0; e < 16; ++e) {
+          float y0, y1;
+          mul_f32x2(y0, y1, __uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]), f, f);
+          fma_f32x2(chk0, chk1, y0, y1, 0.0f, 0.0f, chk0, chk1);
+          y[e] = pack_bf16x2(y0, y1);
+        }
+        if (empty) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = 0u;
+        }
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            const uint4 w0 = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            const uint4 w1 = make_uint4(y[e + 4], y[e + 5], y[e + 6], y[e + 7]);
+            if (p.out32) {  // whole sectors
+              st_global_v8(dst + c + 2 * e, w0, w1);
+            } else {
+              *reinterpret_cast<uint4 *>(dst + c + 2 * e) = w0;
+              *reinterpret_cast<uint4 *>(dst + c + 2 * e + 8) = w1;
+            }
           }
         }
+        __syncwarp();
       }
-      uint32_t bad = __ballot_sync(0xffffffffu, live && !empty && chk != 0.0f);
+      uint32_t bad = __ballot_sync(0xffffffffu, live && !empty && chk0 + chk1 != 0.0f);
       while (bad) {
         const int at = __ffs(bad) - 1;
         bad &= bad - 1;
@@ -661,16 +749,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No copy may still be landing in shared memory when the CTA leaves.  Without an abort
     // every copy issued was waited for by the role that used it; after one, wait (bounded)
     // for the last armed phase of every barrier that a copy completes.
-    const int qi = *s_qissued;
-    if (qi > 0) wait_bar(qfull, (qi - 1) & 1);
-    const int issued = *s_issued;  // 2 per key tile: K, V
-    const int nk = (issued + 1) / 2, nv = issued / 2;
-    for (int s = 0; s < kRing; ++s) {
-      int uses = nk > s ? (nk - 1 - s) / kRing + 1 : 0;
-      if (uses) wait_bar(&kfull[s], (uses - 1) & 1);
-      uses = nv > s ? (nv - 1 - s) / kRing + 1 : 0;
-      if (uses) wait_bar(&vfull[s], (uses - 1) & 1);
-    }
+    const int nk = s_issued[0], nv = s_issued[1], nq = s_issued[2];
+    for (int g = nk - 1; g >= 0 && g >= nk - kRingK; --g) wait_bar(&kfull[g % kRingK], (g / kRingK) & 1);
+    for (int g = nv - 1; g >= 0 && g >= nv - kRing; --g) wait_bar(&vfull[g % kRing], (g / kRing) & 1);
+    for (int k = nq - 1; k >= 0 && k >= nq - TEAMS; --k) wait_bar(&qfull[k % TEAMS], (k / TEAMS) & 1);
   }
   if (warp == 1) {
     tc_fence_after_sync();
@@ -702,27 +784,28 @@ __global__ void __launch_bounds__(256) packed_knorm_kernel(const PackedPrefillPa
   const uint32_t mine = 0xFFu << (threadIdx.x & 24);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(mine, a, o);
-  if (part == 0) rk[g * p.rk_stride + j] = 1.0f / sqrtf(a * (1.0f / kHeadDim) + p.eps);
+  // (a row of zeros with eps = 0 has no direction: it weighs nothing)
+  const float z = a * (1.0f / kHeadDim) + p.eps;
+  if (part == 0) rk[g * p.rk_stride + j] = z == 0.0f ? 0.0f : 1.0f / sqrtf(z);
 }
 
-template <int MODE, int N, int G>
+template <int MODE, int N, int G, int TEAMS>
 cudaError_t launch_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                           const PackedPrefillParams &p, int ctas, cudaStream_t stream) {
-  auto kernel = packed_prefill_kernel<MODE, N, G>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<N>::kBytes);
+  using L = Layout<N, TEAMS>;
+  auto kernel = packed_prefill_kernel<MODE, N, G, TEAMS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), static_cast<size_t>(Layout<N>::kBytes),
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(L::kThreads), static_cast<size_t>(L::kBytes),
                     stream, 0u, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
 
-// Keys per tile: a block of 128 / G tokens sees window + 128 / G - 1 keys at most.
+// A block of 128 / G tokens sees window + 128 / G - 1 keys at most.  Where three tiles of 80 hold them, a
+// block is a few microseconds' work, and two teams of warps on blocks in turn hide each other's waits.
 int packed_tile_keys(int mode, int G, int64_t window) {
-  (void)mode;
-  (void)G;
-  (void)window;
-  return 128;
+  return mode == kPackedSoftmax && window + 128 / G - 1 <= EMBLA_SHORT_SPAN ? 80 : 128;
 }
 
 int64_t packed_rk_stride(int64_t keys) { return (keys + 3) & ~static_cast<int64_t>(3); }
@@ -746,13 +829,17 @@ cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, cons
     if (e != cudaSuccess) return e;
   }
   const int ctas = static_cast<int>(p.blocks < sm_count ? p.blocks : sm_count);
-  if (mode == kPackedRelu2) {
-    if (G == 4) return launch_packed<kPackedRelu2, 128, 4>(tm_q, tm_k, tm_v, p, ctas, stream);
-    if (G == 8) return launch_packed<kPackedRelu2, 128, 8>(tm_q, tm_k, tm_v, p, ctas, stream);
-    return cudaErrorInvalidValue;
+  const bool shorter = packed_tile_keys(mode, G, p.window) == 80;
+  if (G == 4) {
+    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 4, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
+    if (shorter) return launch_packed<kPackedSoftmax, 80, 4, 2>(tm_q, tm_k, tm_v, p, ctas, stream);
+    return launch_packed<kPackedSoftmax, 128, 4, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
   }
-  if (G == 4) return launch_packed<kPackedSoftmax, 128, 4>(tm_q, tm_k, tm_v, p, ctas, stream);
-  if (G == 8) return launch_packed<kPackedSoftmax, 128, 8>(tm_q, tm_k, tm_v, p, ctas, stream);
+  if (G == 8) {
+    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 8, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
+    if (shorter) return launch_packed<kPackedSoftmax, 80, 8, 2>(tm_q, tm_k, tm_v, p, ctas, stream);
+    return launch_packed<kPackedSoftmax, 128, 8, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
+  }
   return cudaErrorInvalidValue;
 }
 

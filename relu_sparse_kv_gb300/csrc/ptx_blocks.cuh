@@ -73,7 +73,7 @@ __device__ __forceinline__ void tmem_store_16x128b_x2(uint32_t taddr, const uint
                : "memory");
 }
 
-// The same fragment layouts, wider: 64 or 128 columns of 16 lanes to registers and 64 back
+// The same fragment layouts, wider: 64 or 128 columns of 16 lanes to registers, 16 back
 // (16x256b), 32 or 64 columns from registers (16x128b).
 __device__ __forceinline__ void tmem_load_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -108,18 +108,10 @@ __device__ __forceinline__ void tmem_load_16x256b_x16(uint32_t taddr, uint32_t (
         "=r"(r[63])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_store_16x256b_x8(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {"
-      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
-      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32"
-      "};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void tmem_store_16x256b_x2(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_store_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -157,6 +149,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+// Two floats, negative ones as 0, as bf16x2 (round to nearest even; NaN stays), first in the low half.
+__device__ __forceinline__ uint32_t pack_relu_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.relu.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// a += lo(w), b += hi(w) for the two bf16 values packed in w.
+__device__ __forceinline__ void add_bf16x2(uint32_t w, float &a, float &b) {
+  asm("{\n\t.reg .b16 lo, hi, one;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "mov.b16 one, 0x3F80;\n\t"
+      "fma.rn.f32.bf16 %0, lo, one, %0;\n\t"
+      "fma.rn.f32.bf16 %1, hi, one, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(w));
+}
 // Two lanes at once (Blackwell's paired fp32 pipe), each rounded as the scalar operation would be:
 // a * b + c.
 __device__ __forceinline__ void fma_f32x2(float &y0, float &y1, float a0, float a1, float b0, float b1, float c0,
@@ -169,6 +177,26 @@ __device__ __forceinline__ void fma_f32x2(float &y0, float &y1, float a0, float 
       "mov.b64 {%0, %1}, x;\n\t}"
       : "=f"(y0), "=f"(y1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+// a * b.
+__device__ __forceinline__ void mul_f32x2(float &y0, float &y1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// a += b.
+__device__ __forceinline__ void add_f32x2(float &a0, float &a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
 }
 
 // 32 bytes to global memory in one store (dst 32-byte aligned).
