@@ -53,6 +53,7 @@ constexpr int kRing = 3;           // V stages and S/P buffers
 constexpr int kBoxQ = 128 * 128;   // [128 rows][64 bf16]
 constexpr float kSlack = 8.0f;     // P stays below 2^kSlack
 constexpr uint64_t kLimitNs = 10000000000ull;  // 10 s: a row computed key by key holds the others up
+constexpr int kBlocksAhead = 4;    // descriptions of blocks in flight
 constexpr int kTmemCols = 512;
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) MN-major
 
@@ -69,7 +70,7 @@ struct Block {
   int32_t tile0;  // tiles of the blocks before
 };
 
-// TEAMS sets of kTeamWarps warps take blocks in turn; each has query rows, an O and row sums of its own.
+// TEAMS sets of kTeamWarps warps take blocks in turn; each has query rows and an O of its own.
 template <int N, int TEAMS>
 struct Layout {
   static constexpr int kThreads = (4 + TEAMS * kTeamWarps) * 32;
@@ -81,16 +82,15 @@ struct Layout {
   static constexpr int kStage = 2 * kBoxKV;
   static constexpr int kOffK = TEAMS * 2 * kBoxQ;
   static constexpr int kOffV = kOffK + kRingK * kStage;
-  static constexpr int kOffSum = kOffV + kRing * kStage;  // [TEAMS][2][128] row sums
-  static constexpr int kOffBlock = kOffSum + TEAMS * 2 * 128 * 4;
-  static constexpr int kOffBar = kOffBlock + TEAMS * static_cast<int>(sizeof(Block));
-  static constexpr int kNBars = 2 * kRingK + 4 * kRing + 4 * TEAMS;
+  static constexpr int kOffBlock = kOffV + kRing * kStage;
+  static constexpr int kOffBar = kOffBlock + kBlocksAhead * static_cast<int>(sizeof(Block));
+  static constexpr int kNBars = 2 * kRingK + (3 + TEAMS) * kRing + 2 * kBlocksAhead + 4 * TEAMS;
   static constexpr int kOffMisc = kOffBar + kNBars * 8;
   static constexpr int kBytes = kOffMisc + 32 + 1024;  // + room to align the base to 1024
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, kLimitNs); }
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) { return mbar_wait_long(bar, parity, kLimitNs); }
 
 __device__ __forceinline__ void set_abort(volatile int *abort_flag, uint32_t *flags) {
   *abort_flag = 1;
@@ -98,31 +98,32 @@ __device__ __forceinline__ void set_abort(volatile int *abort_flag, uint32_t *fl
 }
 
 // Entries that do not ascend or lie outside the rows.
-__device__ __forceinline__ bool bad_sequence(const PackedPrefillParams &p, int64_t q_lo, int64_t q_hi, int64_t k_lo,
-                                             int64_t k_hi) {
+__device__ __forceinline__ bool bad_sequence(const PackedPrefillParams &p, int q_lo, int q_hi, int k_lo, int k_hi) {
   return q_lo < 0 || q_hi < q_lo || q_hi > p.tokens || k_lo < 0 || k_hi < k_lo || k_hi > p.keys;
 }
 
-// The blocks of a CTA, one after the other (the whole warp calls).
+// The blocks of a CTA, one after the other (the whole warp calls).  Tokens, keys and block numbers lie
+// below 2^31.
 template <int MODE, int N, int G>
 struct BlockFinder {
   static constexpr int R = 128 / G;
-  int cta, ctas, round = 0;
+  uint32_t at, step, numbers;  // this CTA's place in the next round of numbers, and numbers per KV head
   // the sequence found last: its block numbers, queries and keys
-  int64_t first = 0, end = 0, q_lo = 0, q_hi = 0, k_lo = 0, k_hi = 0;
-  __device__ BlockFinder(int c, int n) : cta(c), ctas(n) {}
+  int first = 0, end = 0, q_lo = 0, q_hi = 0, k_lo = 0, k_hi = 0;
+  __device__ BlockFinder(const PackedPrefillParams &p, uint32_t cta, uint32_t ctas)
+      : at(cta), step(ctas), numbers(static_cast<uint32_t>(p.blocks) / static_cast<uint32_t>(p.Hkv)) {}
 
   // The sequence that owns block number v becomes the one found last; false where there is none.
-  __device__ __forceinline__ bool find(const PackedPrefillParams &p, int64_t v, int lane) {
+  __device__ __forceinline__ bool find(const PackedPrefillParams &p, int v, int lane) {
     if (v >= first && v < end) return true;
     int lo = 0, hi = p.batch;  // sequences whose successor's numbers begin at or before v
     while (hi > lo) {
-      const int step = (hi - lo + 31) / 32;
-      const int at = lo + (lane + 1) * step;
-      const bool past = at <= hi && p.cu_q[at] / R + at <= v;
+      const int w = (hi - lo + 31) / 32;
+      const int i = lo + (lane + 1) * w;
+      const bool past = i <= hi && p.cu_q[i] / R + i <= v;
       const int n = __popc(__ballot_sync(0xffffffffu, past));
-      const int from = lo + n * step;
-      hi = min(hi, from + step - 1);
+      const int from = lo + n * w;
+      hi = min(hi, from + w - 1);
       lo = from;
     }
     if (lo >= p.batch) return false;
@@ -138,35 +139,36 @@ struct BlockFinder {
   __device__ __forceinline__ Block next(const PackedPrefillParams &p, int lane) {
     Block r = {};
     r.tiles = -1;
-    for (;; ++round) {
-      const int64_t idx = static_cast<int64_t>(round) * ctas + ((round & 1) ? ctas - 1 - cta : cta);
-      if (static_cast<int64_t>(round) * ctas >= p.blocks) return r;
-      if (idx >= p.blocks) continue;
-      const int64_t v = p.blocks / p.Hkv - 1 - idx / p.Hkv;  // the last ones, with the most keys, first
+    for (;;) {
+      // (a round reversed: its places from the round's last one down; past the numbers' end none)
+      const uint32_t idx = at;
+      const uint32_t base = idx - idx % step;
+      if (base >= static_cast<uint32_t>(p.blocks)) return r;
+      at = base + step + (step - 1 - (idx - base));
+      if (idx >= static_cast<uint32_t>(p.blocks)) continue;
+      const uint32_t up = idx / static_cast<uint32_t>(p.Hkv);
+      const int v = static_cast<int>(numbers - 1 - up);  // the last ones, with the most keys, first
       if (!find(p, v, lane)) continue;
-      const int64_t t0 = (v - first) * R, lq = q_hi - q_lo, lk = k_hi - k_lo;
-      r.g = static_cast<int32_t>(idx % p.Hkv);
-      r.q0 = static_cast<int32_t>(q_lo + t0);
-      r.nq = static_cast<int32_t>(lq - t0 < R ? lq - t0 : R);
-      const int64_t newest = lk - lq + t0, last = newest + r.nq - 1;  // of the first and last token
-      const int64_t oldest = newest - p.window + 1 > 0 ? newest - p.window + 1 : 0;
-      int64_t k0 = k_lo + oldest;
-      if (MODE == kPackedRelu2) k0 &= ~static_cast<int64_t>(3);  // (the key norms are read in pairs)
-      r.tiles = last < 0 ? 0 : static_cast<int32_t>((k_lo + last - k0) / N) + 1;
-      r.k0 = static_cast<int32_t>(k0);
-      r.p0 = static_cast<int32_t>(k_lo + newest - k0);
-      r.seq0 = static_cast<int32_t>(k_lo - k0);
-      ++round;
+      const int t0 = (v - first) * R, lq = q_hi - q_lo, lk = k_hi - k_lo;
+      r.g = static_cast<int>(idx - up * static_cast<uint32_t>(p.Hkv));
+      r.q0 = q_lo + t0;
+      r.nq = min(lq - t0, R);
+      const int newest = lk - lq + t0, last = newest + r.nq - 1;  // of the first and last token
+      const int oldest = max(newest - p.window + 1, 0);
+      r.k0 = k_lo + oldest;
+      if (MODE == kPackedRelu2) r.k0 &= ~3;  // (the key norms are read in pairs)
+      r.tiles = last < 0 ? 0 : (k_lo + last - r.k0) / N + 1;
+      r.p0 = k_lo + newest - r.k0;
+      r.seq0 = k_lo - r.k0;
       return r;
     }
   }
 };
 
-// Row r of a block (token r / G, head r % G) computed key by key: columns 64 half .. + 63 of its
-// output, by one warp.  In two passes, so that no partial sum is larger than the result needs:
+// Row r of a block (token r / G, head r % G) computed key by key by one warp.  In two passes, so that no partial sum is larger than the result needs:
 // maximum and sum (ReLU^2: the sum), then the values by their normalised weights.
 template <int MODE, int G>
-__device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block &b, int r, int half, int lane) {
+__device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block &b, int r, int lane) {
   const int i = r / G, h = b.g * G + r % G;
   const uint16_t *q = p.q.base + static_cast<int64_t>(b.q0 + i) * p.q.stride + h * kHeadDim;
   const uint2 qw = *reinterpret_cast<const uint2 *>(q + 4 * lane);
@@ -225,7 +227,7 @@ __device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block 
   }
   const float z = MODE == kPackedRelu2 ? p.c + l : l;
   const float f = z == 0.0f ? 0.0f : 1.0f / z;
-  float a0 = 0.0f, a1 = 0.0f;
+  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // columns 4 lane .. + 3
   for (int64_t j0 = oldest; j0 <= newest; j0 += 32) {
     const float s = score(j0 + lane);
     const float w = MODE == kPackedRelu2 ? s * f : (s == -INFINITY ? 0.0f : exp2f(s - m) * f);
@@ -233,14 +235,16 @@ __device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block 
     for (int c = 0; c < n; ++c) {
       const float wc = __shfl_sync(0xffffffffu, w, c);
       if (MODE == kPackedRelu2 && wc == 0.0f) continue;  // weighs nothing, whatever its value holds
-      const uint32_t x = *reinterpret_cast<const uint32_t *>(p.v.base + (b.k0 + j0 + c) * p.v.stride + b.g * kHeadDim +
-                                                             64 * half + 2 * lane);
-      a0 = fmaf(wc, bf16lo(x), a0);
-      a1 = fmaf(wc, bf16hi(x), a1);
+      const uint2 x = *reinterpret_cast<const uint2 *>(p.v.base + (b.k0 + j0 + c) * p.v.stride + b.g * kHeadDim +
+                                                       4 * lane);
+      a[0] = fmaf(wc, bf16lo(x.x), a[0]);
+      a[1] = fmaf(wc, bf16hi(x.x), a[1]);
+      a[2] = fmaf(wc, bf16lo(x.y), a[2]);
+      a[3] = fmaf(wc, bf16hi(x.y), a[3]);
     }
   }
-  *reinterpret_cast<uint32_t *>(p.out + (static_cast<int64_t>(b.q0 + i) * p.Hkv * G + h) * kHeadDim + 64 * half +
-                                2 * lane) = pack_bf16x2(a0, a1);
+  *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(b.q0 + i) * p.Hkv * G + h) * kHeadDim + 4 * lane) =
+      make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
 }
 
 // Scores of 16 rows x N keys to registers: element 4j + 2i + e is row l / 4 + 8i, key 8j + 2(l % 4) + e; and
@@ -266,6 +270,30 @@ __device__ __forceinline__ void store_weights(uint32_t taddr, const uint32_t (&w
   }
 }
 
+// Eight words of each lane of a quad, word j the lane's part (l % 4) of group j, become the lane's two whole
+// groups 2 (l % 4) and 2 (l % 4) + 1, four words each.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[8], int lane) {
+  // exchange halves with the lane two away, then quarters with the next lane
+  const bool b1 = lane & 2, b0 = lane & 1;
+  uint32_t h[2][4];  // [part of the sender: own half's lane pair bit][group of the lane's half]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t keep = b1 ? w[4 + j] : w[j], send = b1 ? w[j] : w[4 + j];
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, send, 2);
+    h[0][j] = b1 ? got : keep;  // parts of the lanes 0, 1
+    h[1][j] = b1 ? keep : got;  // parts of the lanes 2, 3
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const uint32_t keep = b0 ? h[part][2 + j] : h[part][j], send = b0 ? h[part][j] : h[part][2 + j];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, send, 1);
+      w[4 * j + 2 * part] = b0 ? got : keep;
+      w[4 * j + 2 * part + 1] = b0 ? keep : got;
+    }
+}
+
 template <int MODE, int N, int G, int TEAMS>
 __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     packed_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -275,19 +303,20 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *sQ = smem, *sK = smem + L::kOffK, *sV = smem + L::kOffV;
-  float *sSum = reinterpret_cast<float *>(smem + L::kOffSum);
   Block *sBlock = reinterpret_cast<Block *>(smem + L::kOffBlock);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
   // Tile g has V stage and S/P buffer g % kRing in phase (g / kRing) & 1 and K stage g % kRingK in
-  // phase (g / kRingK) & 1.  Block k has the query rows, the description and the O of team k % TEAMS
-  // in phase (k / TEAMS) & 1.
+  // phase (g / kRingK) & 1.  Block k has the description k % kBlocksAhead, and the query rows and the O
+  // of team k % TEAMS.
   constexpr int kRingK = L::kRingK;
   uint64_t *kfull = bars, *kempty = kfull + kRingK, *vfull = kempty + kRingK;
-  uint64_t *sfull = vfull + kRing;   // S of a tile in tensor memory
-  uint64_t *pfull = sfull + kRing;   // its P written over it
+  // S of a tile in tensor memory: a team's tiles by its own count, so that it sees every phase
+  uint64_t *sfull = vfull + kRing;
+  uint64_t *pfull = sfull + TEAMS * kRing;  // its P written over it
   uint64_t *pvdone = pfull + kRing;  // its P V done: the S/P buffer and the V stage are free
-  uint64_t *qfull = pvdone + kRing;  // a block's description and query rows are there
-  uint64_t *qempty = qfull + TEAMS;  // the description read by everyone, the query rows used
+  uint64_t *bfull = pvdone + kRing;  // a block's description is there
+  uint64_t *bempty = bfull + kBlocksAhead;  // and has been read by everyone
+  uint64_t *qfull = bempty + kBlocksAhead, *qempty = qfull + TEAMS;  // its query rows are there, and used
   uint64_t *ofull = qempty + TEAMS;  // a block's P V all done
   uint64_t *ofree = ofull + TEAMS;   // its O read out of tensor memory
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
@@ -302,7 +331,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
   if (warp == 0) {
     if (lane < kRing) {
       mbar_init(&vfull[lane], 1);
-      mbar_init(&sfull[lane], 1);
+      for (int i = 0; i < TEAMS; ++i) mbar_init(&sfull[i * kRing + lane], 1);
       mbar_init(&pfull[lane], kTeamWarps);
       mbar_init(&pvdone[lane], 1);
     }
@@ -312,9 +341,13 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     }
     if (lane < TEAMS) {
       mbar_init(&qfull[lane], 1);
-      mbar_init(&qempty[lane], 3 + kTeamWarps);  // the S issuer's commit, the P V issuer, the V loads, the team
+      mbar_init(&qempty[lane], 1 + (MODE == kPackedRelu2 ? kTeamWarps : 0));  // S done, and the rows' norms
       mbar_init(&ofull[lane], 1);
       mbar_init(&ofree[lane], kTeamWarps);
+    }
+    if (lane < kBlocksAhead) {
+      mbar_init(&bfull[lane], 1);
+      mbar_init(&bempty[lane], 3 + kTeamWarps);  // the two issuers, the V loads, the team
     }
     if (lane == 0) {
       *s_abort = 0;
@@ -339,18 +372,22 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
     }
-    BlockFinder<MODE, N, G> finder(cta, P);
+    BlockFinder<MODE, N, G> finder(p, cta, P);
     Block b = finder.next(p, lane);
     int g = 0;
     bool ok = true;
     for (int k = 0, ends = 0; ok && ends < TEAMS; ++k) {  // (each team is told of the end)
-      const int s = k % TEAMS;
+      const int s = k % TEAMS, d = k % kBlocksAhead;
       b.tile0 = g;
       if (lane == 0) {
-        // the query rows and the description are free once the team's block before is done with them
-        ok = k < TEAMS || wait_bar(&qempty[s], ((k / TEAMS) - 1) & 1);
+        ok = k < kBlocksAhead || wait_bar(&bempty[d], ((k / kBlocksAhead) - 1) & 1);
         if (ok) {
-          sBlock[s] = b;
+          sBlock[d] = b;
+          mbar_arrive(&bfull[d]);
+        }
+        // (blocks without tiles take their turn with the query rows, but load none)
+        if (ok && b.tiles >= 0) ok = k < TEAMS || wait_bar(&qempty[s], ((k / TEAMS) - 1) & 1);
+        if (ok && b.tiles >= 0) {
           if (b.tiles > 0) {
             uint8_t *to = sQ + s * 2 * kBoxQ;
             mbar_arrive_expect_tx(&qfull[s], 2 * kBoxQ);
@@ -387,15 +424,18 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     if (lane == 0) {
       const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
       const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
-      int g = 0, blocks = 0;
+      int g = 0, blocks = 0, mine[TEAMS] = {};  // tiles, blocks, tiles of each team
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int s = k % TEAMS;
-        ok = !*s_abort && wait_bar(&qfull[s], (k / TEAMS) & 1);
+        const int s = k % TEAMS, d = k % kBlocksAhead;
+        ok = !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1);
         if (!ok) break;
-        const int tiles = sBlock[s].tiles;
+        const int tiles = sBlock[d].tiles;
+        mbar_arrive(&bempty[d]);
         if (tiles < 0) break;
-        for (int t = 0; ok && t < tiles; ++t, ++g) {
+        ok = wait_bar(&qfull[s], (k / TEAMS) & 1);
+        int u = TEAMS > 1 && s ? mine[TEAMS - 1] : mine[0];
+        for (int t = 0; ok && t < tiles; ++t, ++g, ++u) {
           const int sb = g % kRing, kb = g % kRingK;
           ok = wait_bar(&kfull[kb], (g / kRingK) & 1) &&
                (g < kRing || wait_bar(&pvdone[sb], ((g / kRing) - 1) & 1));
@@ -408,9 +448,10 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
             const uint64_t ko = static_cast<uint64_t>((kb * L::kStage + (kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4);
             tc_mma_bf16(tmem + sb * N, qdesc + qo, kdesc + ko, kIdescS, kk > 0 ? 1u : 0u);
           }
-          tc_commit(&sfull[sb]);
+          tc_commit(&sfull[s * kRing + u % kRing]);
           tc_commit(&kempty[kb]);
         }
+        (TEAMS > 1 && s ? mine[TEAMS - 1] : mine[0]) = u;
         if (ok) {
           tc_commit(&qempty[s]);
           blocks = k + 1;
@@ -419,7 +460,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       if (!ok) set_abort(s_abort, p.flags);
       // every MMA of this thread has completed, and its last commits arrived, before the tensor
       // memory is released and the CTA leaves (also when another role has given up)
-      if (g > 0) wait_bar(&sfull[(g - 1) % kRing], ((g - 1) / kRing) & 1);
+      for (int i = 0; i < TEAMS; ++i)
+        if (mine[i] > 0) wait_bar(&sfull[i * kRing + (mine[i] - 1) % kRing], ((mine[i] - 1) / kRing) & 1);
       if (g > 0) wait_bar(&kempty[(g - 1) % kRingK], ((g - 1) / kRingK) & 1);
       for (int k = blocks - 1; k >= 0 && k >= blocks - TEAMS; --k) wait_bar(&qempty[k % TEAMS], (k / TEAMS) & 1);
     }
@@ -430,11 +472,11 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       int g = 0, blocks = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int s = k % TEAMS;
-        ok = !*s_abort && wait_bar(&qfull[s], (k / TEAMS) & 1);
+        const int s = k % TEAMS, d = k % kBlocksAhead;
+        ok = !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1);
         if (!ok) break;
-        const int tiles = sBlock[s].tiles;
-        mbar_arrive(&qempty[s]);
+        const int tiles = sBlock[d].tiles;
+        mbar_arrive(&bempty[d]);
         if (tiles < 0) break;
         // the O of the team's block before has been read
         ok = k < TEAMS || wait_bar(&ofree[s], ((k / TEAMS) - 1) & 1);
@@ -470,11 +512,11 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       int g = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int s = k % TEAMS;
-        ok = !*s_abort && wait_bar(&qfull[s], (k / TEAMS) & 1);
+        const int d = k % kBlocksAhead;
+        ok = !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1);
         if (!ok) break;
-        const int tiles = sBlock[s].tiles, head = sBlock[s].g, k0 = sBlock[s].k0;
-        mbar_arrive(&qempty[s]);
+        const int tiles = sBlock[d].tiles, head = sBlock[d].g, k0 = sBlock[d].k0;
+        mbar_arrive(&bempty[d]);
         if (tiles < 0) break;
         for (int t = 0; t < tiles; ++t, ++g) {
           const int r = g % kRing;
@@ -493,35 +535,40 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     // ------------------------------------------------------------------ weights and outputs
     const int team = (warp - 2) / kTeamWarps;
     const int quarter = warp & 3;           // the tensor-memory lanes this warp may reach
-    const int half = ((warp - 2) >> 2) & 1; // rows 16 half .. of them; at the end columns 64 half .. of O
+    const int half = ((warp - 2) >> 2) & 1;     // rows 16 half .. of them
     const int rowa = quarter * 32 + half * 16;  // the warp's first row
     const int row0 = rowa + (lane >> 2);        // this lane's rows: row0 and row0 + 8
     const int q2 = 2 * (lane & 3);              // its columns: 8j + q2 and the next
-    const uint32_t lanes32 = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t lanes16 = lanes32 + (static_cast<uint32_t>(half * 16) << 16);
-    const uint32_t colo = tmem + L::kColO + team * 128;
+    const uint32_t lanes16 = static_cast<uint32_t>(rowa) << 16;
+    const uint32_t colo = tmem + L::kColO + team * 128 + lanes16;
     const bool flip = MODE == kPackedSoftmax && p.tau2 < 0.0f;
     const float tau2 = fabsf(p.tau2);
     bool ok = true;
-    for (int n = 0;; ++n) {  // the team's n-th block
-      // (every decision to go on is the team's: what follows is warp-wide and has barriers)
-      ok = __all_sync(0xffffffffu, ok && !*s_abort && wait_bar(&qfull[team], n & 1));
-      ok = named_bar_and(1 + team, kTeamWarps * 32, ok);
+    int u = 0;  // the team's tiles
+    for (int k = team, n = 0; ok; k += TEAMS, ++n) {  // the team's n-th block
+      // (every decision to go on is the warp's: what follows is warp-wide)
+      const int d = k % kBlocksAhead;
+      ok = __all_sync(0xffffffffu, !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1));
       if (!ok) break;
-      const Block b = sBlock[team];
+      const Block b = sBlock[d];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bempty[d]);
       if (b.tiles < 0) break;
-      float a2 = 0.0f;  // ReLU^2, row quarter * 32 + lane: alpha^2 / (mean(q^2) + eps)
-      if (MODE == kPackedRelu2 && b.tiles > 0) {
-        const int r = quarter * 32 + lane;
-        const uint8_t *rows = sQ + team * 2 * kBoxQ;
-        a2 = (p.alpha * p.alpha) / (row_square_sum(rows, kBoxQ, r, r & 7) * (1.0f / kHeadDim) + p.eps);
-        // the query rows are read: every lane's sum depends on them
-        const float used = __shfl_sync(0xffffffffu, a2, 0) + __shfl_sync(0xffffffffu, a2, 31);
+      float a2[2] = {0.0f, 0.0f};  // ReLU^2: alpha^2 / (mean(q^2) + eps) of this lane's rows
+      if (MODE == kPackedRelu2) {
+        ok = __all_sync(0xffffffffu, wait_bar(&qfull[team], n & 1));
+        if (!ok) break;
+        // two lanes to a row, a box each
+        const int r = rowa + (lane >> 1);
+        float ss = box_square_sum(sQ + (2 * team + (lane & 1)) * kBoxQ, r, (r & 7) ^ (4 * (lane & 1)));
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        const float a = (p.alpha * p.alpha) / (ss * (1.0f / kHeadDim) + p.eps);
+        a2[0] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2));
+        a2[1] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2) + 16);
+        // the query rows are read: these depend on every lane's sum
+        const float used = __shfl_sync(0xffffffffu, a2[0], 0) + a2[1];
         __syncwarp();
         if (lane == 0) mbar_arrive_after(&qempty[team], used);
-      } else {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qempty[team]);
       }
       // a row sees the keys oldest .. oldest + span, relative to k0 (none: from far behind the last)
       int oldest[2];
@@ -550,11 +597,11 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           for (int j = 0; j < N / 8; ++j) rk[j] = *reinterpret_cast<const float2 *>(rkp + 8 * j);
         }
       }
-      for (int t = 0; t < b.tiles; ++t) {
+      for (int t = 0; t < b.tiles; ++t, ++u) {
         const int g = b.tile0 + t;
         const int sb = g % kRing;
         const int j0 = t * N;
-        ok = __all_sync(0xffffffffu, wait_bar(&sfull[sb], (g / kRing) & 1));
+        ok = __all_sync(0xffffffffu, wait_bar(&sfull[team * kRing + u % kRing], (u / kRing) & 1));
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t cols = tmem + lanes16 + sb * N;
@@ -611,11 +658,11 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 128; c += 16) {
               uint32_t o[8];
-              tmem_load_16x256b_x2(colo + lanes16 + c, o);
+              tmem_load_16x256b_x2(colo + c, o);
               tmem_wait_ld(o);
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sc[(e >> 1) & 1]);
-              tmem_store_16x256b_x2(colo + lanes16 + c, o);
+              tmem_store_16x256b_x2(colo + c, o);
             }
           }
 #pragma unroll
@@ -670,75 +717,79 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[sb]);
       }
-      // the row sums, for the lanes that finish the rows
-      float *sum = sSum + (2 * team + (n & 1)) * 128;
+      if (!ok) break;
+      float f[2];  // what O is multiplied with; 0 where no key weighs anything
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = l[2 * i] + l[2 * i + 1];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        if (q2 == 0) sum[row0 + 8 * i] = x;
+        const float z = MODE == kPackedRelu2 ? p.c + a2[i] * x : x;
+        f[i] = x != 0.0f && z != 0.0f ? (MODE == kPackedRelu2 ? a2[i] / z : 1.0f / z) : 0.0f;
       }
-      ok = __all_sync(0xffffffffu, ok && !*s_abort && wait_bar(&ofull[team], n & 1));
-      ok = named_bar_and(1 + team, kTeamWarps * 32, ok);
+      ok = __all_sync(0xffffffffu, !*s_abort && wait_bar(&ofull[team], n & 1));
       if (!ok) break;
       tc_fence_after_sync();
-      // row quarter * 32 + lane, columns 64 half .. + 63
-      const int r = quarter * 32 + lane;
-      const float s = sum[r];
-      float f;  // 0 where no key weighs anything
-      if (MODE == kPackedRelu2) {
-        const float z = p.c + a2 * s;
-        f = s != 0.0f && z != 0.0f ? a2 / z : 0.0f;
-      } else {
-        f = s != 0.0f ? 1.0f / s : 0.0f;
-      }
-      const bool live = r / G < b.nq;
-      const bool empty = f == 0.0f;
-      float chk0 = 0.0f, chk1 = 0.0f;  // NaN if an output is infinite or NaN
-      uint16_t *dst = p.out + (static_cast<int64_t>(b.q0 + r / G) * p.Hkv * G + b.g * G + r % G) * kHeadDim + half * 64;
+      float chk[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // NaN if an output of the row is infinite or NaN
+      uint16_t *dst[2];
+      bool live[2];
 #pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t o[32], y[16];
-        tmem_load_x32(colo + lanes32 + half * 64 + c, o);
+      for (int i = 0; i < 2; ++i) {
+        const int r = row0 + 8 * i;
+        live[i] = r / G < b.nq;
+        dst[i] = p.out + (static_cast<int64_t>(b.q0 + r / G) * p.Hkv * G + b.g * G + r % G) * kHeadDim + 8 * q2;
+      }
+#pragma unroll
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t o[32], y[2][8];
+        tmem_load_16x256b_x8(colo + c, o);
         tmem_wait_ld(o);
-        if (c == 32) {
+        if (c == 64) {
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ofree[team]);  // the team's next P V may overwrite O
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float y0, y1;
-          mul_f32x2(y0, y1, __uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]), f, f);
-          fma_f32x2(chk0, chk1, y0, y1, 0.0f, 0.0f, chk0, chk1);
-          y[e] = pack_bf16x2(y0, y1);
-        }
-        if (empty) {
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = 0u;
-        }
-        if (live) {
+          for (int i = 0; i < 2; ++i) {
+            float y0, y1;
+            mul_f32x2(y0, y1, __uint_as_float(o[4 * j + 2 * i]), __uint_as_float(o[4 * j + 2 * i + 1]), f[i], f[i]);
+            fma_f32x2(chk[2 * i], chk[2 * i + 1], y0, y1, 0.0f, 0.0f, chk[2 * i], chk[2 * i + 1]);
+            y[i][j] = pack_bf16x2(y0, y1);
+          }
 #pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            const uint4 w0 = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-            const uint4 w1 = make_uint4(y[e + 4], y[e + 5], y[e + 6], y[e + 7]);
+        for (int i = 0; i < 2; ++i) {
+          // the quad's lanes hold columns 2l, 2l + 1 of eight groups of eight; lane l takes the groups
+          // 2l and 2l + 1, 32 bytes, so that the quad stores 128 bytes at once
+          quad_transpose(y[i], lane);
+          if (f[i] == 0.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[i][j] = 0u;
+          }
+          if (live[i]) {
+            const uint4 w0 = make_uint4(y[i][0], y[i][1], y[i][2], y[i][3]);
+            const uint4 w1 = make_uint4(y[i][4], y[i][5], y[i][6], y[i][7]);
             if (p.out32) {  // whole sectors
-              st_global_v8(dst + c + 2 * e, w0, w1);
+              st_global_v8(dst[i] + c, w0, w1);
             } else {
-              *reinterpret_cast<uint4 *>(dst + c + 2 * e) = w0;
-              *reinterpret_cast<uint4 *>(dst + c + 2 * e + 8) = w1;
+              *reinterpret_cast<uint4 *>(dst[i] + c) = w0;
+              *reinterpret_cast<uint4 *>(dst[i] + c + 8) = w1;
             }
           }
         }
         __syncwarp();
       }
-      uint32_t bad = __ballot_sync(0xffffffffu, live && !empty && chk0 + chk1 != 0.0f);
-      while (bad) {
-        const int at = __ffs(bad) - 1;
-        bad &= bad - 1;
-        __syncwarp();
-        slow_row<MODE, G>(p, b, quarter * 32 + at, half, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t bad = __ballot_sync(0xffffffffu, live[i] && f[i] != 0.0f && chk[2 * i] + chk[2 * i + 1] != 0.0f);
+        bad = (bad | bad >> 1 | bad >> 2 | bad >> 3) & 0x11111111u;  // of the quad's four lanes
+        while (bad) {
+          const int at = __ffs(bad) - 1;
+          bad &= bad - 1;
+          __syncwarp();
+          slow_row<MODE, G>(p, b, rowa + (at >> 2) + 8 * i, lane);
+        }
       }
     }
     if (!ok) set_abort(s_abort, p.flags);

@@ -20,6 +20,28 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
+// mbar_wait whose polls let the hardware hold the thread for up to 20 us, so that a warp that waits long
+// leaves the issue slots to the others.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0)
+      t0 = t;
+    else if (t - t0 > limit_ns)
+      return false;
+  }
+}
+
 // 4-D tiled TMA load.
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t c0,
                                             int32_t c1, int32_t c2, int32_t c3) {
@@ -266,6 +288,20 @@ __device__ __forceinline__ float row_square_sum(const uint8_t *tile, int box_byt
     sq_acc_bf16x2(x1.w, a[6], a[7]);
   }
   return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+}
+
+// Sum of squares of the 64 columns of row r in one box of 128-byte rows, pieces taken in turn.
+__device__ __forceinline__ float box_square_sum(const uint8_t *box, int r, int turn) {
+  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int c = 0; c < 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(box + r * 128 + (c ^ turn) * 16);
+    sq_acc_bf16x2(x.x, a[0], a[1]);
+    sq_acc_bf16x2(x.y, a[2], a[3]);
+    sq_acc_bf16x2(x.z, a[0], a[1]);
+    sq_acc_bf16x2(x.w, a[2], a[3]);
+  }
+  return (a[0] + a[1]) + (a[2] + a[3]);
 }
 
 }  // namespace embla
