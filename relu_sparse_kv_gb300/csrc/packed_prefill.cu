@@ -46,7 +46,7 @@ namespace embla {
 namespace {
 
 #ifndef EMBLA_SHORT_SPAN
-#define EMBLA_SHORT_SPAN 240
+#define EMBLA_SHORT_SPAN 1100
 #endif
 constexpr int kTeamWarps = 8;      // warps that turn a block's scores into weights
 constexpr int kRing = 3;           // V stages and S/P buffers
@@ -134,17 +134,23 @@ struct BlockFinder {
     return v >= first && v < end;
   }
 
-  // The next block; tiles < 0 after the last.  A round of numbers is dealt at a time, alternate rounds in
-  // reverse order, so the CTAs' sums of key tiles stay close.
+  // The next block; tiles < 0 after the last.  With a ticket counter each CTA draws its next number when it
+  // is ready for it; without, a round of numbers is dealt at a time, alternate rounds in reverse order, so
+  // the CTAs' sums of key tiles stay close.
   __device__ __forceinline__ Block next(const PackedPrefillParams &p, int lane) {
     Block r = {};
     r.tiles = -1;
     for (;;) {
-      // (a round reversed: its places from the round's last one down; past the numbers' end none)
       const uint32_t idx = at;
       const uint32_t base = idx - idx % step;
       if (base >= static_cast<uint32_t>(p.blocks)) return r;
-      at = base + step + (step - 1 - (idx - base));
+      if (p.ticket != nullptr) {
+        uint32_t drawn = 0;
+        if (lane == 0) drawn = atomicAdd(p.ticket, 1u);
+        at = step + __shfl_sync(0xffffffffu, drawn, 0);
+      } else {
+        at = base + step + (step - 1 - (idx - base));
+      }
       if (idx >= static_cast<uint32_t>(p.blocks)) continue;
       const uint32_t up = idx / static_cast<uint32_t>(p.Hkv);
       const int v = static_cast<int>(numbers - 1 - up);  // the last ones, with the most keys, first
@@ -811,10 +817,12 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
   }
 }
 
-// rk[g][j] = 1 / sqrt(mean(k_j^2) + eps): eight lanes per (key, KV head) row, 32 bytes each.
+// rk[g][j] = 1 / sqrt(mean(k_j^2) + eps): eight lanes per (key, KV head) row, 32 bytes each.  Also sets
+// the attention kernel's ticket counter.
 __global__ void __launch_bounds__(256) packed_knorm_kernel(const PackedPrefillParams p, float *rk) {
   pdl_wait_primary();
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0u;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x / 8;
   const int part = threadIdx.x % 8;
   const int64_t j = row / p.Hkv;
@@ -861,19 +869,22 @@ int packed_tile_keys(int mode, int G, int64_t window) {
 
 int64_t packed_rk_stride(int64_t keys) { return (keys + 3) & ~static_cast<int64_t>(3); }
 
-// The last tile's norms may be read up to a tile past the last row's.
-size_t packed_workspace_bytes(int64_t keys, int Hkv) {
+// The last tile's norms may be read up to a tile past the last row's; then the ticket counter.
+static size_t packed_norm_bytes(int64_t keys, int Hkv) {
   return (static_cast<size_t>(Hkv) * static_cast<size_t>(packed_rk_stride(keys)) * 4 + 128 * 4 + 255) &
          ~static_cast<size_t>(255);
 }
+size_t packed_workspace_bytes(int64_t keys, int Hkv) { return packed_norm_bytes(keys, Hkv) + 256; }
 
 int64_t packed_blocks(int64_t tokens, int batch, int G, int Hkv) { return (tokens / (128 / G) + batch) * Hkv; }
 
 cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                                  const CUtensorMap &tm_v, const PackedPrefillParams &p, float *rk, int sm_count,
+                                  const CUtensorMap &tm_v, PackedPrefillParams p, float *rk, int sm_count,
                                   cudaStream_t stream) {
   if (p.blocks == 0) return cudaSuccess;
+  p.ticket = nullptr;
   if (mode == kPackedRelu2 && p.keys > 0) {
+    p.ticket = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(rk) + packed_norm_bytes(p.keys, p.Hkv));
     const int64_t rows = p.keys * p.Hkv;
     cudaError_t e = launch_pdl(packed_knorm_kernel, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(256), 0, stream,
                                0u, p, rk);

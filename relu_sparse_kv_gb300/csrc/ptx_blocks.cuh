@@ -42,6 +42,13 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, u
   }
 }
 
+// End a group of this thread's cp.async copies; wait until all but the newest `left` groups have landed.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int left>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
+}
+
 // 4-D tiled TMA load.
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t c0,
                                             int32_t c1, int32_t c2, int32_t c3) {

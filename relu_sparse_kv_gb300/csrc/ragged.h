@@ -27,10 +27,11 @@ struct RopeParams {
   uint16_t *k_win, *v_win;  // both null: no rings
   const float *q_gain, *k_gain;
   float eps;
-  int norm, window, Hkv;
+  int norm, window, Hq, Hkv;
+  int block_tokens, out32;      // set by the launcher: tokens per block; outputs start on 32 bytes
   uint64_t turn[kHeadDim / 2];  // pair i turns by turn[i] * 2^-64 of a circle per position
 };
-cudaError_t launch_rope_qkv(int G, const RopeParams &p, cudaStream_t stream);
+cudaError_t launch_rope_qkv(RopeParams p, int sm_count, cudaStream_t stream);
 
 // Rows 0 .. min(pos[b] + 1, window) - 1 of every ring of sequence b.
 struct RaggedWindowParams {
@@ -49,6 +50,7 @@ struct PackedPrefillParams {
   const int32_t *cu_q, *cu_k;  // queries and keys of each sequence
   TokenRows q, k, v;
   const float *rk;             // ReLU^2: 1 / norm of every key row, [Hkv, rk_stride]
+  uint32_t *ticket;            // ReLU^2: block numbers drawn past each CTA's first (set by the launcher)
   uint16_t *out;               // [tokens, Hq, 128] bf16
   uint32_t *flags;
   int64_t tokens, keys, rk_stride;
@@ -64,7 +66,7 @@ int64_t packed_blocks(int64_t tokens, int batch, int G, int Hkv);
 int64_t packed_rk_stride(int64_t keys);
 size_t packed_workspace_bytes(int64_t keys, int Hkv);
 cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                                  const CUtensorMap &tm_v, const PackedPrefillParams &p, float *rk, int sm_count,
+                                  const CUtensorMap &tm_v, PackedPrefillParams p, float *rk, int sm_count,
                                   cudaStream_t stream);
 
 }  // namespace embla

@@ -5,16 +5,18 @@
 //
 // A cluster of CTAs takes a (sequence, KV head) unit, 128 ring rows to a CTA.  In a CTA
 //   - each of eight warps copies 16 K rows and the same V rows into shared memory, all of them in
-//     flight at once, and computes S = Q K^T of its rows as m16n8k16 MMAs (M: the G query heads);
+//     flight at once, and as soon as its K rows are there computes S = Q K^T of them as m16n8k16 MMAs
+//     (M: the G query heads);
 //   - the rows' maximum per head is exchanged, and P = exp2(z - max) written as three bf16 parts
 //     (hi + mid + lo, all 24 bits: the output is fp32);
 //   - each warp computes 16 of the 128 output dims over all 128 rows, O^T = V^T P^T, so no warp's
 //     sums have to be added to another's.
 // One pass, no running rescale.  CTAs of a unit exchange maximum, sum and O through distributed
-// shared memory at the end.
+// shared memory at the end.  Three CTAs fit an SM, so that one's arithmetic has the others' copies
+// beside it.
 #include <cooperative_groups.h>
 
-#include "ptx.cuh"
+#include "ptx_blocks.cuh"
 #include "ragged.h"
 
 namespace cg = cooperative_groups;
@@ -36,7 +38,6 @@ struct RwShared {
   float wm[kRwWarps][8];      // each warp's maximum per head
   float wl[kRwWarps][8];      // and sum
   float m[8], l[8];           // the CTA's
-  float o[8][kHeadDim];       // the CTA's sums, for the cluster
 };
 
 // byte offset of 16-byte piece c of staged row r: eight rows of an ldmatrix read eight bank groups
@@ -45,12 +46,13 @@ __device__ __forceinline__ uint32_t rw_piece(int r, int c) {
 }
 
 template <int G, int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
     window_ragged_kernel(const RaggedWindowParams p) {
   pdl_wait_primary();  // the query, the rings and the positions are complete
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];  // K rows, V rows, RwShared
   RwShared<G> &sh = *reinterpret_cast<RwShared<G> *>(smem + 2 * kRwStage);
+  float(*so)[kHeadDim] = reinterpret_cast<float(*)[kHeadDim]>(smem);  // the CTA's sums for the cluster, over K
   const int rank = CL > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int64_t u = blockIdx.x / CL;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,8 +74,16 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
       // (absent rows read nothing; their address stays inside the ring)
       const int64_t off = (r < rows ? r * kRwRowBytes : -static_cast<int64_t>(r0) * kRwRowBytes) + piece * 16;
       cp_async16_zfill(smem + rw_piece(r, piece), Ku + off, n);
+    }
+    cp_async_commit();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = warp * 16 + 2 * k + (lane >> 4);
+      const uint32_t n = r < rows ? 16u : 0u;
+      const int64_t off = (r < rows ? r * kRwRowBytes : -static_cast<int64_t>(r0) * kRwRowBytes) + piece * 16;
       cp_async16_zfill(smem + kRwStage + rw_piece(r, piece), Vu + off, n);
     }
+    cp_async_commit();
   }
   // query as the A operand of S: row g (head g), dims 16ks + 2t, +1 and +8, +9
   uint32_t qa0[8], qa2[8];
@@ -85,7 +95,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
       qa2[ks] = g < G ? qrow[8 * ks + 4 + t] : 0u;
     }
   }
-  cp_async_wait_all();
+  cp_async_wait<1>();  // the K rows
   __syncwarp();
 
   // S of rows 0-7 (s0) and 8-15 (s1) of this warp's 16
@@ -139,6 +149,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
       b -= bf16hi(h);
     }
   }
+  cp_async_wait<0>();  // the V rows
   __syncthreads();
 
   // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T
@@ -187,7 +198,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
     }
     if (2 * t < G) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sh.o[2 * t + (i & 1)][16 * warp + g + 8 * (i >> 1)] = o[i];
+      for (int i = 0; i < 4; ++i) so[2 * t + (i & 1)][16 * warp + g + 8 * (i >> 1)] = o[i];
     }
     cluster.sync();
     // each CTA finishes its share of the outputs from all the CTAs' states
@@ -209,7 +220,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
         const float f = cm[c] == -INFINITY ? 0.0f : exp2f(cm[c] - M);
         if (f != 0.0f) {
           L = fmaf(other->l[h], f, L);
-          A = fmaf(other->o[h][d], f, A);
+          A = fmaf(cluster.map_shared_rank(&so[0][0], c)[h * kHeadDim + d], f, A);
         }
       }
       p.out[u * G * kHeadDim + i] = L > 0.0f || L != L ? A / L : 0.0f;
@@ -222,7 +233,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 2)
 template <int G, int CL>
 cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, cudaStream_t stream) {
   constexpr int bytes = 2 * kRwStage + static_cast<int>(sizeof(RwShared<G>));
-  static_assert(2 * bytes <= 227 * 1024, "two CTAs per SM");
+  static_assert(3 * (bytes + 1024) <= 228 * 1024, "three CTAs per SM");
   cudaError_t e = cudaFuncSetAttribute(window_ragged_kernel<G, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(window_ragged_kernel<G, CL>, dim3(static_cast<unsigned>(units * CL)), dim3(kRwThreads), bytes,
