@@ -887,10 +887,7 @@ embla_status embla_rope_qkv(const embla_shape *shape, int64_t n_tokens, const in
       !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) || !aligned16(k_out) ||
       !aligned16(k_win) || !aligned16(v_win))
     return EMBLA_ERR_INVALID_ARG;
-  // (ring rows are counted in 32 bits)
-  if (n_tokens > kMaxPackedTokens ||
-      (ring && static_cast<int64_t>(shape->batch) * shape->n_kv_heads * window > INT32_MAX))
-    return EMBLA_ERR_UNSUPPORTED;
+  if (n_tokens > kMaxPackedTokens || n_tokens * shape->n_kv_heads > INT32_MAX) return EMBLA_ERR_UNSUPPORTED;
   if (q_stride > kMaxPackedStride || k_stride > kMaxPackedStride || (ring && v_stride > kMaxPackedStride))
     return EMBLA_ERR_UNSUPPORTED;
   RopeParams p = {};
@@ -908,16 +905,13 @@ embla_status embla_rope_qkv(const embla_shape *shape, int64_t n_tokens, const in
   p.eps = eps;
   p.norm = norm ? 1 : 0;
   p.window = window;
-  p.Hq = shape->n_q_heads;
   p.Hkv = shape->n_kv_heads;
   for (int i = 0; i < kHeadDim / 2; ++i) {
     // the fraction of a circle that pair i turns by per position (whole circles do not count)
     const double f = std::pow(static_cast<double>(rope_base), -2.0 * i / kHeadDim) / 6.283185307179586476925286766559;
     p.turn[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 64));
   }
-  const int sms = sm_count_of(current_device());
-  if (sms <= 0) return EMBLA_ERR_CUDA;
-  return cuda_status(launch_rope_qkv(p, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_rope_qkv(G, p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -27,11 +27,10 @@ struct RopeParams {
   uint16_t *k_win, *v_win;  // both null: no rings
   const float *q_gain, *k_gain;
   float eps;
-  int norm, window, Hq, Hkv;
-  int block_tokens, out32;      // set by the launcher: tokens per block; outputs start on 32 bytes
+  int norm, window, Hkv;
   uint64_t turn[kHeadDim / 2];  // pair i turns by turn[i] * 2^-64 of a circle per position
 };
-cudaError_t launch_rope_qkv(RopeParams p, int sm_count, cudaStream_t stream);
+cudaError_t launch_rope_qkv(int G, const RopeParams &p, cudaStream_t stream);
 
 // Rows 0 .. min(pos[b] + 1, window) - 1 of every ring of sequence b.
 struct RaggedWindowParams {

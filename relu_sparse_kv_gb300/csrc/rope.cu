@@ -9,14 +9,17 @@
 //
 // The angle.  A pair turns by f_i = base^(-2i/D) / (2 pi) of a circle per position, and only the
 // fraction of p f_i counts.  The host gives F_i = f_i 2^64 rounded to an integer: p F_i modulo 2^64 is that
-// fraction with no error but F_i's own (p 2^-54 of a circle from the double it came from, 2^-33 at
+// fraction with no error but F_i's own (p 2^-54 of a circle from the double it came from, 2^-34 at
 // a position of 2^20), by one integer product and no 64-bit floats.  Its top 32 bits, as a signed part
 // of half a circle, go to sincospif.
 //
-// A block takes a few tokens with all their heads.  Half a warp per token finds its sequence (16 ways at
-// a time) and the block works out the tokens' 64 sines and cosines once, into shared memory; then
-// eight lanes take a row, 32 bytes each, so that a warp moves 1 KB in one piece.  The first rows are
-// requested before the angles are worked out.  Bound by HBM.
+// Sixteen lanes take the G query heads and the key head of one KV group of one token, 16 bytes of
+// each row per lane, so a lane works out its four angles once for G + 1 rows and has all of their
+// loads in flight together; nothing waits on another lane but the norms' sums.  Bound by HBM: 4 x 32,768
+// tokens of 16 + 4 heads, normed, in 214 us (6.3 TB/s, 0.92 of a copy's rate); a step of 8 tokens 2.5 us, the
+// launch.  Blocks of tokens that shared their angles through shared memory took 242 us (a barrier and
+// fewer loads in flight), 48 and 80 registers (5 and 3 blocks to an SM) 211 and 257 us but 2.9 and 2.5
+// for the step.
 #include "ptx_blocks.cuh"
 #include "ragged.h"
 
@@ -24,8 +27,8 @@ namespace embla {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = kRopeThreads / 8;  // rows that a block works on at a time
-constexpr int kRopeMaxTokens = 16;           // per block: half a warp each
+constexpr int kRopeLanes = 16;  // lanes per (token, KV group)
+constexpr int kRopePerBlock = kRopeThreads / kRopeLanes;
 
 // How many sequences end at or before token t (cu[b + 1] <= t), found by the sixteen lanes of a
 // half warp 16 ways at a time: the sequence that t lies in, or `batch` past the last one.
@@ -43,182 +46,110 @@ __device__ __forceinline__ int sequence_of(const PackedTokens &s, int64_t t, int
   return lo;
 }
 
-struct RopeToken {
-  uint32_t pos;
-  int32_t slot;  // ring row b * Hkv * window + position % window; -1: not among the newest; -2: no sequence
-};
-
-// 16 values of a row to fp32 (normed and scaled), turned, and back to bf16.  Lane l of eight holds dims
-// 16 l .. 16 l + 15, pairs 8 l .. 8 l + 7: cs[k], k < 2: cosines of pairs 8 l + 4 k .. + 3, k - 2: sines.
-template <bool NORM>
-__device__ __forceinline__ void turn_row(uint4 &x0, uint4 &x1, const float4 (&cs)[4], const float4 *gain, float eps,
-                                         uint32_t mine) {
-  const uint32_t r[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  float rs = 1.0f;
-  if constexpr (NORM) {
-    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sq_acc_bf16x2(r[i], a[2 * (i & 1)], a[2 * (i & 1) + 1]);
-    float ss = (a[0] + a[1]) + (a[2] + a[3]);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(mine, ss, o);
-    rs = 1.0f / sqrtf(ss * (1.0f / kHeadDim) + eps);
-  }
-  const float c[8] = {cs[0].x, cs[0].y, cs[0].z, cs[0].w, cs[1].x, cs[1].y, cs[1].z, cs[1].w};
-  const float s[8] = {cs[2].x, cs[2].y, cs[2].z, cs[2].w, cs[3].x, cs[3].y, cs[3].z, cs[3].w};
-  uint32_t y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float e = bf16lo(r[i]), f = bf16hi(r[i]);
-    if constexpr (NORM) {
-      // gains lie as the cosines do: pieces of four dims, lane by lane
-      const float4 g = gain[(i >> 1) * 8];
-      mul_f32x2(e, f, e, f, i & 1 ? g.z : g.x, i & 1 ? g.w : g.y);
-      mul_f32x2(e, f, e, f, rs, rs);
-    }
-    // (e, f) c + (-f, e) s
-    float u, v;
-    mul_f32x2(u, v, -f, e, s[i], s[i]);
-    fma_f32x2(u, v, e, f, c[i], c[i], u, v);
-    y[i] = pack_bf16x2(u, v);
-  }
-  x0 = make_uint4(y[0], y[1], y[2], y[3]);
-  x1 = make_uint4(y[4], y[5], y[6], y[7]);
-}
-
-template <bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ RopeToken tok[kRopeMaxTokens];
-  __shared__ float4 angles[kRopeMaxTokens][4][8];  // [token][cos, cos, sin, sin][lane]
-  __shared__ float4 gains[2][4][8];                // of queries and keys, pieces of four dims by lane
+template <int G, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads, G == 4 ? 4 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
   pdl_wait_primary();  // the rows are written; whoever read the old outputs and rings is done
   pdl_launch_dependents();
-  const int part = threadIdx.x % 8;
-  const uint32_t mine = 0xFFu << (threadIdx.x & 24);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.block_tokens;
-  const int ntok = static_cast<int>(p.seqs.tokens - t0 < p.block_tokens ? p.seqs.tokens - t0 : p.block_tokens);
-  const int per = p.Hq + p.Hkv + (p.k_win ? p.Hkv : 0);  // rows of a token: queries, keys, values for the ring
-  const int rows = ntok * per;
-
-  // row r of the block: its token, head and kind, and its 32 bytes of this lane
-  auto locate = [&](int r, int &t, int &h) {
-    t = r / per;
-    h = r - t * per;
-  };
-  auto request = [&](int r, uint4 &a, uint4 &b) {
-    int t, h;
-    locate(r, t, h);
-    const uint16_t *src = h < p.Hq            ? p.q.base + (t0 + t) * p.q.stride + h * kHeadDim
-                          : h < p.Hq + p.Hkv ? p.k.base + (t0 + t) * p.k.stride + (h - p.Hq) * kHeadDim
-                                             : p.v.base + (t0 + t) * p.v.stride + (h - p.Hq - p.Hkv) * kHeadDim;
-    const uint4 *at = reinterpret_cast<const uint4 *>(src) + 2 * part;
-    a = __ldcs(at);
-    b = __ldcs(at + 1);
-  };
-  // the first two rows of these lanes (values are asked for when it is known that they are needed)
-  uint4 x[2][2];
-  const int r0 = threadIdx.x / 8;
+  const int sl = threadIdx.x % kRopeLanes;
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRopePerBlock + threadIdx.x / kRopeLanes;
+  const int64_t t = w / p.Hkv;
+  const int g = static_cast<int>(w - t * p.Hkv);
+  if (t >= p.seqs.tokens) return;  // (half warps leave whole)
+  const int d = sl * 8;            // this lane's dims d .. d + 7: pairs 4 sl .. 4 sl + 3
+  uint4 x[G + 1], v = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = r0 + i * kRopeRows;
-    x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows && r % per < p.Hq + p.Hkv) request(r, x[i][0], x[i][1]);
+  for (int h = 0; h < G; ++h)
+    x[h] = __ldcs(reinterpret_cast<const uint4 *>(p.q.base + t * p.q.stride + (g * G + h) * kHeadDim + d));
+  x[G] = __ldcs(reinterpret_cast<const uint4 *>(p.k.base + t * p.k.stride + g * kHeadDim + d));
+  const int b = sequence_of(p.seqs, t, sl, half);
+  if (b >= p.seqs.batch) return;  // behind the last sequence
+  const int64_t first = p.seqs.cu[b], end = p.seqs.cu[b + 1];
+  if (t < first) return;
+  const uint32_t pos = (p.pos0 ? static_cast<uint32_t>(p.pos0[b]) : 0u) + static_cast<uint32_t>(t - first);
+  const bool ring = p.k_win != nullptr && t >= end - p.window;  // among the newest
+  if (ring) v = __ldcs(reinterpret_cast<const uint4 *>(p.v.base + t * p.v.stride + g * kHeadDim + d));
+  float c[4], s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t half_turns = static_cast<int32_t>((pos * p.turn[4 * sl + i]) >> 32);
+    sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s[i], &c[i]);
   }
-
-  {
-    const int i = threadIdx.x / 16, sl = threadIdx.x % 16;
-    const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
-    if (i < ntok) {
-      const int64_t t = t0 + i;
-      const int b = sequence_of(p.seqs, t, sl, half);
-      RopeToken k = {0u, -2};
-      if (b < p.seqs.batch && t >= p.seqs.cu[b]) {
-        k.pos = (p.pos0 ? static_cast<uint32_t>(p.pos0[b]) : 0u) + static_cast<uint32_t>(t - p.seqs.cu[b]);
-        k.slot = -1;
-        if (p.k_win && t >= static_cast<int64_t>(p.seqs.cu[b + 1]) - p.window)
-          k.slot = b * p.Hkv * p.window + static_cast<int32_t>(k.pos % static_cast<uint32_t>(p.window));
-      }
-      if (sl == 0) tok[i] = k;
-      // this token's 64 angles, four to a lane
+  float rs[G + 1];
+  if constexpr (NORM) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int pair = 4 * sl + e;  // lane pair / 8, value pair % 8
-        const int32_t half_turns = static_cast<int32_t>((k.pos * p.turn[pair]) >> 32);
-        float c, s;
-        sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s, &c);
-        reinterpret_cast<float *>(&angles[i][(pair & 4) >> 2][pair >> 3])[pair & 3] = c;
-        reinterpret_cast<float *>(&angles[i][2 + ((pair & 4) >> 2)][pair >> 3])[pair & 3] = s;
+    for (int h = 0; h <= G; ++h) {
+      float a = 0.0f, e = 0.0f;
+      sq_acc_bf16x2(x[h].x, a, e);
+      sq_acc_bf16x2(x[h].y, a, e);
+      sq_acc_bf16x2(x[h].z, a, e);
+      sq_acc_bf16x2(x[h].w, a, e);
+      rs[h] = a + e;
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int h = 0; h <= G; ++h) rs[h] += __shfl_xor_sync(half, rs[h], o);
+#pragma unroll
+    for (int h = 0; h <= G; ++h) rs[h] = rsqrtf(rs[h] * (1.0f / kHeadDim) + p.eps);
+  }
+  float gain[8];
+#pragma unroll
+  for (int h = 0; h <= G; ++h) {
+    if constexpr (NORM) {
+      if (h == 0 || h == G) {  // the queries' gains, then the key's
+        const float *from = h == 0 ? p.q_gain : p.k_gain;
+        const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+        const float4 g0 = from ? *reinterpret_cast<const float4 *>(from + d) : one;
+        const float4 g1 = from ? *reinterpret_cast<const float4 *>(from + d + 4) : one;
+        gain[0] = g0.x, gain[1] = g0.y, gain[2] = g0.z, gain[3] = g0.w;
+        gain[4] = g1.x, gain[5] = g1.y, gain[6] = g1.z, gain[7] = g1.w;
       }
     }
-    if (NORM && threadIdx.x < 64) {
-      const int which = threadIdx.x >> 5, d = threadIdx.x & 31;  // dims 4 d .. 4 d + 3
-      const float *g = which ? p.k_gain : p.q_gain;
-      gains[which][d & 3][d >> 2] =
-          g ? *reinterpret_cast<const float4 *>(g + 4 * d) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    const uint32_t r[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float e = bf16lo(r[i]), f = bf16hi(r[i]);
+      if constexpr (NORM) {
+        mul_f32x2(e, f, e, f, gain[2 * i], gain[2 * i + 1]);
+        mul_f32x2(e, f, e, f, rs[h], rs[h]);
+      }
+      // (e, f) c + (-f, e) s
+      float u, v2;
+      mul_f32x2(u, v2, -f, e, s[i], s[i]);
+      fma_f32x2(u, v2, e, f, c[i], c[i], u, v2);
+      y[i] = pack_bf16x2(u, v2);
     }
+    x[h] = make_uint4(y[0], y[1], y[2], y[3]);
   }
-  __syncthreads();
+  if (p.q_out) {
+    uint16_t *to = p.q_out + (t * p.Hkv + g) * G * kHeadDim + d;
+#pragma unroll
+    for (int h = 0; h < G; ++h) *reinterpret_cast<uint4 *>(to + h * kHeadDim) = x[h];
+  }
+  if (p.k_out) *reinterpret_cast<uint4 *>(p.k_out + (t * p.Hkv + g) * kHeadDim + d) = x[G];
+  if (ring) {
+    const int64_t row = (static_cast<int64_t>(b) * p.Hkv + g) * p.window + pos % static_cast<uint32_t>(p.window);
+    *reinterpret_cast<uint4 *>(p.k_win + row * kHeadDim + d) = x[G];
+    *reinterpret_cast<uint4 *>(p.v_win + row * kHeadDim + d) = v;
+  }
+}
 
-  for (int r = r0; r < rows; r += 2 * kRopeRows) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int ri = r + i * kRopeRows;
-      if (ri >= rows) break;
-      int t, h;
-      locate(ri, t, h);
-      const RopeToken k = tok[t];
-      uint4 a = x[i][0], b = x[i][1];
-      // the row after next of these lanes
-      const int rn = ri + 2 * kRopeRows;
-      if (rn < rows && rn % per < p.Hq + p.Hkv) request(rn, x[i][0], x[i][1]);
-      if (k.slot == -2) continue;  // behind the last sequence
-      const bool value = h >= p.Hq + p.Hkv;
-      uint16_t *to = nullptr;
-      if (value) {
-        if (k.slot < 0) continue;
-        request(ri, a, b);
-      } else {
-        float4 cs[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) cs[e] = angles[t][e][part];
-        turn_row<NORM>(a, b, cs, &gains[h < p.Hq ? 0 : 1][0][part], p.eps, mine);
-        if (h < p.Hq)
-          to = p.q_out + ((t0 + t) * p.Hq + h) * kHeadDim;
-        else if (p.k_out)
-          to = p.k_out + ((t0 + t) * p.Hkv + h - p.Hq) * kHeadDim;
-      }
-      if (to) {
-        uint4 *at = reinterpret_cast<uint4 *>(to) + 2 * part;
-        if (p.out32) {  // whole sectors
-          st_global_v8(at, a, b);
-        } else {
-          at[0] = a;
-          at[1] = b;
-        }
-      }
-      if (h >= p.Hq && k.slot >= 0) {
-        uint16_t *ring = value ? p.v_win : p.k_win;
-        const int64_t head = value ? h - p.Hq - p.Hkv : h - p.Hq;
-        uint4 *at = reinterpret_cast<uint4 *>(ring + (k.slot + head * p.window) * kHeadDim) + 2 * part;
-        at[0] = a;
-        at[1] = b;
-      }
-    }
-  }
+template <int G>
+cudaError_t launch_rope_g(const RopeParams &p, cudaStream_t stream) {
+  const int64_t blocks = (p.seqs.tokens * p.Hkv + kRopePerBlock - 1) / kRopePerBlock;
+  return launch_pdl(p.norm ? rope_kernel<G, true> : rope_kernel<G, false>, dim3(static_cast<unsigned>(blocks)),
+                    dim3(kRopeThreads), 0, stream, 0u, p);
 }
 
 }  // namespace
 
-cudaError_t launch_rope_qkv(RopeParams p, int sm_count, cudaStream_t stream) {
+cudaError_t launch_rope_qkv(int G, const RopeParams &p, cudaStream_t stream) {
   if (p.seqs.tokens == 0) return cudaSuccess;
-  // As many tokens per block as leave two blocks to an SM, a power of two: the search and the angles are
-  // then shared by more rows.
-  p.block_tokens = 1;
-  while (p.block_tokens < kRopeMaxTokens && p.seqs.tokens >= 4ll * sm_count * p.block_tokens) p.block_tokens *= 2;
-  p.out32 = ((reinterpret_cast<uintptr_t>(p.q_out) | reinterpret_cast<uintptr_t>(p.k_out)) & 31u) == 0;
-  const int64_t blocks = (p.seqs.tokens + p.block_tokens - 1) / p.block_tokens;
-  return launch_pdl(p.norm ? rope_kernel<true> : rope_kernel<false>, dim3(static_cast<unsigned>(blocks)),
-                    dim3(kRopeThreads), 0, stream, 0u, p);
+  if (G == 4) return launch_rope_g<4>(p, stream);
+  if (G == 8) return launch_rope_g<8>(p, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace embla
