@@ -41,7 +41,8 @@ struct RaggedWindowParams {
   int32_t Hkv, window;
   float tau2;  // tau * log2(e)
 };
-cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p, cudaStream_t stream);
+cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p, int sm_count,
+                                        cudaStream_t stream);
 
 // Causal attention over packed prompts (kinds of weights).
 constexpr int kPackedSoftmax = 0, kPackedRelu2 = 1;

@@ -3,17 +3,19 @@
 // weighted sum of their values.  Query and keys were rotated when they were written, and a softmax does
 // not ask for the order of its keys: the valid ones are the ring's rows 0 .. min(pos + 1, window) - 1.
 //
-// A cluster of CTAs takes a (sequence, KV head) unit, 128 ring rows to a CTA.  In a CTA
-//   - each of eight warps copies 16 K rows and the same V rows into shared memory, all of them in
-//     flight at once, and as soon as its K rows are there computes S = Q K^T of them as m16n8k16 MMAs
-//     (M: the G query heads);
-//   - the rows' maximum per head is exchanged, and P = exp2(z - max) written as three bf16 parts
-//     (hi + mid + lo, all 24 bits: the output is fp32);
-//   - each warp computes 16 of the 128 output dims over all 128 rows, O^T = V^T P^T, so no warp's
+// A cluster of CTAs takes a (sequence, KV head) unit, an equal share of its valid rows to a CTA.  Where all
+// units' shares of up to 128 rows fit the SMs at once, a CTA takes its share in one step; else it goes
+// through a longer one in steps of 64 rows, the next 64 on their way meanwhile.  In a step
+//   - eight warps take 8 or 16 rows each, copied by themselves, and compute S = Q K^T as m16n8k16 MMAs (M:
+//     the G query heads);
+//   - the rows' maximum per head is exchanged, and P = exp2(z - m) for the running maximum m written as
+//     three bf16 parts (hi + mid + lo, all 24 bits: the output is fp32);
+//   - each warp adds P V to its 16 of the 128 output dims over all the rows, O^T += V^T P^T, so no warp's
 //     sums have to be added to another's.
-// One pass, no running rescale.  CTAs of a unit exchange maximum, sum and O through distributed
-// shared memory at the end.  Three CTAs fit an SM, so that one's arithmetic has the others' copies
-// beside it.
+// The CTAs of a unit each finish a share of its outputs: every one writes its part of them, its maxima
+// and its sums into the others' shared memory, over K rows that are no longer needed (writes do not
+// wait; reading each other's took a third of the kernel's time).  Three CTAs fit an SM, so that
+// one's arithmetic has the others' copies beside it.
 #include <cooperative_groups.h>
 
 #include "ptx_blocks.cuh"
@@ -26,18 +28,25 @@ namespace {
 
 constexpr int kRwWarps = 8;
 constexpr int kRwThreads = kRwWarps * 32;
-constexpr int kRwRows = 128;  // ring rows per CTA
 constexpr int kRwRowBytes = kHeadDim * 2;
-constexpr int kRwStage = kRwRows * kRwRowBytes;  // 32 KB of K, as much of V
-// the parts of P in one row per head, padded so that heads start in different banks
-constexpr int kRwPRow = kRwRows + 8;
+constexpr int kRwBuffer = 128 * kRwRowBytes;  // 32 KB of K rows, as much of V
 
-template <int G>
+// ROWS: ring rows per step, 128 (one step) or 64 (the buffers hold two steps).
+template <int ROWS>
 struct RwShared {
-  uint16_t p[3][8][kRwPRow];  // parts of P, [part][head][row] (heads past G stay zero)
-  float wm[kRwWarps][8];      // each warp's maximum per head
-  float wl[kRwWarps][8];      // and sum
-  float m[8], l[8];           // the CTA's
+  // parts of P, [part][head][row], padded so that heads start in different banks (those past G are zeros)
+  uint16_t p[3][8][ROWS + 8];
+  float wm[2][kRwWarps][8];  // each warp's maximum per head, of one step and the next
+  float wl[kRwWarps][8];     // each warp's sum
+  float l[8];                // the CTA's
+};
+
+// What a CTA of a cluster is sent, over its K rows once it is done with them: every CTA's maxima and
+// sums, and their sums of the outputs that this one finishes.
+template <int G, int CL>
+struct RwReceived {
+  float m[CL][8], l[CL][8];
+  float o[CL][G * kHeadDim / CL];
 };
 
 // byte offset of 16-byte piece c of staged row r: eight rows of an ldmatrix read eight bank groups
@@ -45,45 +54,49 @@ __device__ __forceinline__ uint32_t rw_piece(int r, int c) {
   return static_cast<uint32_t>(r * kRwRowBytes + ((c ^ (r & 7)) << 4));
 }
 
-template <int G, int CL>
+template <int G, int CL, int ROWS>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
     window_ragged_kernel(const RaggedWindowParams p) {
+  constexpr bool kOnce = ROWS == 128;
+  constexpr int kTiles = ROWS / 64;             // n8 tiles of a warp's rows
+  constexpr int kStage = ROWS * kRwRowBytes;
   pdl_wait_primary();  // the query, the rings and the positions are complete
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];  // K rows, V rows, RwShared
-  RwShared<G> &sh = *reinterpret_cast<RwShared<G> *>(smem + 2 * kRwStage);
-  float(*so)[kHeadDim] = reinterpret_cast<float(*)[kHeadDim]>(smem);  // the CTA's sums for the cluster, over K
+  RwShared<ROWS> &sh = *reinterpret_cast<RwShared<ROWS> *>(smem + 2 * kRwBuffer);
   const int rank = CL > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int64_t u = blockIdx.x / CL;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int last = p.pos[u / p.Hkv];
   const int nv = last < 0 ? 0 : (last >= p.window ? p.window : last + 1);  // valid rows of the ring
-  const int r0 = rank * kRwRows;
-  const int rows = max(0, min(kRwRows, nv - r0));  // of this CTA
+  const int share = (nv + CL - 1) / CL;
+  const int r0 = min(nv, rank * share), rows = min(nv, r0 + share) - r0;  // of this CTA
+  const int steps = kOnce ? min(rows, 1) : (rows + ROWS - 1) / ROWS;
 
-  // copies: one instruction moves two whole rows; rows past the valid ones are zeros
-  {
-    const uint8_t *Ku = p.K + (u * p.window + r0) * kRwRowBytes;
-    const uint8_t *Vu = p.V + (u * p.window + r0) * kRwRowBytes;
-    const int piece = lane & 15;
+  // Copies of step c's rows of this warp: an instruction moves two whole rows; rows past the share are
+  // zeros (they read nothing, from an address inside the ring).  A group ends with each call.
+  auto copy = [&](const uint8_t *ring, int c, uint8_t *to) {
+    if (c < steps) {
+      const uint8_t *from = ring + u * p.window * kRwRowBytes;
+      const int piece = lane & 15;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = warp * 16 + 2 * k + (lane >> 4);
-      const uint32_t n = r < rows ? 16u : 0u;
-      // (absent rows read nothing; their address stays inside the ring)
-      const int64_t off = (r < rows ? r * kRwRowBytes : -static_cast<int64_t>(r0) * kRwRowBytes) + piece * 16;
-      cp_async16_zfill(smem + rw_piece(r, piece), Ku + off, n);
+      for (int k = 0; k < 4 * kTiles; ++k) {
+        const int r = warp * 8 * kTiles + 2 * k + (lane >> 4);
+        const bool live = c * ROWS + r < rows;
+        cp_async16_zfill(to + rw_piece(r, piece),
+                         from + (live ? static_cast<int64_t>(r0 + c * ROWS + r) * kRwRowBytes : 0) + piece * 16,
+                         live ? 16u : 0u);
+      }
     }
     cp_async_commit();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = warp * 16 + 2 * k + (lane >> 4);
-      const uint32_t n = r < rows ? 16u : 0u;
-      const int64_t off = (r < rows ? r * kRwRowBytes : -static_cast<int64_t>(r0) * kRwRowBytes) + piece * 16;
-      cp_async16_zfill(smem + kRwStage + rw_piece(r, piece), Vu + off, n);
-    }
-    cp_async_commit();
+  };
+  uint8_t *const bufK = smem, *const bufV = smem + kRwBuffer;
+  copy(p.K, 0, bufK);
+  copy(p.V, 0, bufV);
+  if constexpr (!kOnce) {
+    copy(p.K, 1, bufK + kStage);
+    copy(p.V, 1, bufV + kStage);
   }
   // query as the A operand of S: row g (head g), dims 16ks + 2t, +1 and +8, +9
   uint32_t qa0[8], qa2[8];
@@ -95,72 +108,87 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
       qa2[ks] = g < G ? qrow[8 * ks + 4 + t] : 0u;
     }
   }
-  cp_async_wait<1>();  // the K rows
-  __syncwarp();
-
-  // S of rows 0-7 (s0) and 8-15 (s1) of this warp's 16
   const int mat = lane >> 3, mr = lane & 7;
-  const int wrow = warp * 16;
-  float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  {
-    const uint32_t sK = smem_u32(smem);
-    const int row = wrow + (mat >> 1) * 8 + mr;
+  float m = -INFINITY, l = 0.0f;           // head g: running maximum (base 2), sum over this warp's rows
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dims 16 warp + g (o[0], o[1]) and + 8, heads 2t and 2t + 1
+  if (CL > 1 && steps == 0) cluster_arrive();
+  for (int c = 0; c < steps; ++c) {
+    const int at = kOnce ? 0 : (c & 1) * kStage;
+    if (kOnce)
+      cp_async_wait<1>();  // this warp's K rows (behind them V)
+    else if (c == 0)
+      cp_async_wait<3>();  // (V, K and V)
+    else
+      cp_async_wait<2>();  // (V and K)
+    __syncwarp();
+    // S of the warp's rows, eight to a tile
+    float z[2 * kTiles];  // head g, rows 2t and 2t + 1 of each tile
+    float mx = -INFINITY;
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      uint32_t bk[4];
-      ldmatrix_x4(bk, sK + rw_piece(row, 2 * ks + (mat & 1)));
-      mma_16816_bf16(s0, qa0[ks], 0u, qa2[ks], 0u, bk[0], bk[1]);
-      mma_16816_bf16(s1, qa0[ks], 0u, qa2[ks], 0u, bk[2], bk[3]);
+    for (int j = 0; j < kTiles; ++j) {
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int row = (warp * kTiles + j) * 8;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t bk[4];
+        ldmatrix_x4(bk, smem_u32(bufK + at) + rw_piece(row + mr, 4 * kk + mat));
+        mma_16816_bf16(s, qa0[2 * kk], 0u, qa2[2 * kk], 0u, bk[0], bk[1]);
+        mma_16816_bf16(s, qa0[2 * kk + 1], 0u, qa2[2 * kk + 1], 0u, bk[2], bk[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        z[2 * j + i] = c * ROWS + row + 2 * t + i < rows ? p.tau2 * s[i] : -INFINITY;
+      mx = fmaxf(mx, fmaxf(z[2 * j], z[2 * j + 1]));
     }
-  }
-  // head g, rows 2t, 2t + 1 (z[0], z[1]) and 8 + 2t, 9 + 2t (z[2], z[3]) of the warp's
-  float z[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = wrow + 8 * (i >> 1) + 2 * t + (i & 1);
-    z[i] = r < rows ? p.tau2 * (i < 2 ? s0[i] : s1[i - 2]) : -INFINITY;
-  }
-  float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  if (t == 0) sh.wm[warp][g] = mx;
-  __syncthreads();
-  float m = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kRwWarps; ++w) m = fmaxf(m, sh.wm[w][g]);
-  float pz[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) pz[i] = z[i] == -INFINITY ? 0.0f : exp2f(z[i] - m);
-  float l = (pz[0] + pz[1]) + (pz[2] + pz[3]);
-  l += __shfl_xor_sync(0xffffffffu, l, 1);
-  l += __shfl_xor_sync(0xffffffffu, l, 2);
-  if (t == 0) sh.wl[warp][g] = l;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    uint32_t *to = reinterpret_cast<uint32_t *>(&sh.p[0][g][wrow + 4 * i + 2 * t]);
-    constexpr int kPart = 8 * kRwPRow / 2;  // words from one part to the next
-    float a = pz[i], b = pz[i + 1];
-    const bool head = g < G;  // the operand's heads past G are zeros
-#pragma unroll
-    for (int part = 0; part < 3; ++part) {
-      const uint32_t h = head ? pack_bf16x2(a, b) : 0u;
-      to[part * kPart] = h;
-      a -= bf16lo(h);
-      b -= bf16hi(h);
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    if (t == 0) sh.wm[c & 1][warp][g] = mx;
+    __syncthreads();  // the maxima are there; the K rows of this step and the V rows and P of the last are read
+    if (CL > 1 && c == steps - 1) cluster_arrive();  // the others may write over this CTA's K rows
+    if constexpr (!kOnce) {
+      if (c > 0) copy(p.V, c + 1, bufV + (kStage - at));
+      copy(p.K, c + 2, bufK + at);
     }
-  }
-  cp_async_wait<0>();  // the V rows
-  __syncthreads();
-
-  // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T
-  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dims g (o[0], o[1]) and g + 8, heads 2t and 2t + 1
-  {
-    const uint32_t sV = smem_u32(smem + kRwStage);
-    const int steps = (rows + 15) / 16;
-    for (int k = 0; k < steps; ++k) {
+    float mn = m;
+#pragma unroll
+    for (int w = 0; w < kRwWarps; ++w) mn = fmaxf(mn, sh.wm[c & 1][w][g]);
+    const float sc = m == mn ? 1.0f : exp2f(m - mn);
+    m = mn;
+    float ps = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      float a = z[2 * j] == -INFINITY ? 0.0f : exp2f(z[2 * j] - m);
+      float b = z[2 * j + 1] == -INFINITY ? 0.0f : exp2f(z[2 * j + 1] - m);
+      ps += a + b;
+      uint32_t *to = reinterpret_cast<uint32_t *>(&sh.p[0][g][(warp * kTiles + j) * 8 + 2 * t]);
+      constexpr int kPart = 8 * (ROWS + 8) / 2;  // words from one part to the next
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        const uint32_t h = g < G ? pack_bf16x2(a, b) : 0u;  // (the operand's heads past G are zeros)
+        to[part * kPart] = h;
+        a -= bf16lo(h);
+        b -= bf16hi(h);
+      }
+    }
+    ps += __shfl_xor_sync(0xffffffffu, ps, 1);
+    ps += __shfl_xor_sync(0xffffffffu, ps, 2);
+    l = fmaf(l, sc, ps);
+    if constexpr (!kOnce) {
+      // O follows the maximum; heads 2t and 2t + 1 have their factors in lanes 8t and 8t + 4
+      const float sca = __shfl_sync(0xffffffffu, sc, 8 * t), scb = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
+      o[0] *= sca;
+      o[1] *= scb;
+      o[2] *= sca;
+      o[3] *= scb;
+    }
+    cp_async_wait<kOnce ? 0 : 3>();  // this warp's V rows (behind them K, V and K)
+    __syncthreads();                 // everyone's, and P
+    // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T
+#pragma unroll
+    for (int k = 0; k < ROWS / 16; ++k) {
+      if (c * ROWS + 16 * k >= rows) break;
       uint32_t av[4];
-      const int row = 16 * k + (mat >> 1) * 8 + mr;
-      ldmatrix_x4_trans(av, sV + rw_piece(row, 2 * warp + (mat & 1)));
+      ldmatrix_x4_trans(av, smem_u32(bufV + at) + rw_piece(16 * k + (mat >> 1) * 8 + mr, 2 * warp + (mat & 1)));
 #pragma unroll
       for (int part = 2; part >= 0; --part) {  // the small parts first
         const uint32_t *b = reinterpret_cast<const uint32_t *>(&sh.p[part][g][16 * k + 2 * t]);
@@ -168,13 +196,16 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
       }
     }
   }
-  float ls = 0.0f;  // the CTA's sum for head `lane`
-  if (warp == 0 && lane < 8) {
-#pragma unroll
-    for (int w = 0; w < kRwWarps; ++w) ls += sh.wl[w][lane];
-  }
+  cp_async_wait<0>();  // (empty groups)
+  if (t == 0) sh.wl[warp][g] = l;
+  __syncthreads();
   if constexpr (CL == 1) {
-    if (warp == 0 && lane < 8) sh.l[lane] = ls;
+    if (warp == 0 && lane < 8) {
+      float ls = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRwWarps; ++w) ls += sh.wl[w][lane];
+      sh.l[lane] = ls;
+    }
     __syncthreads();
     if (2 * t < G) {
       float *out = p.out + u * G * kHeadDim + 16 * warp + g;
@@ -186,76 +217,88 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
       }
     }
   } else {
+    constexpr int per = G * kHeadDim / CL;  // outputs that a CTA finishes: parts of one head, or whole heads
     cg::cluster_group cluster = cg::this_cluster();
-    if (warp == 0 && lane < 8) {
-      sh.l[lane] = ls;
-    }
-    if (warp == 1 && lane < 8) {
-      float c = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kRwWarps; ++w) c = fmaxf(c, sh.wm[w][lane]);
-      sh.m[lane] = c;
-    }
+    using Received = RwReceived<G, CL>;
+    Received *mine = reinterpret_cast<Received *>(smem);
+    static_assert(sizeof(Received) <= kRwBuffer, "over the K rows");
+    cluster_wait();  // every CTA of the cluster has read its K rows
     if (2 * t < G) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) so[2 * t + (i & 1)][16 * warp + g + 8 * (i >> 1)] = o[i];
-    }
-    cluster.sync();
-    // each CTA finishes its share of the outputs from all the CTAs' states
-    constexpr int per = G * kHeadDim / CL;
-    for (int li = threadIdx.x; li < per; li += kRwThreads) {
-      const int i = rank * per + li;
-      const int h = i / kHeadDim, d = i % kHeadDim;
-      float cm[CL], M = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < CL; ++c) {
-        cm[c] = cluster.map_shared_rank(&sh, c)->m[h];
-        M = fmaxf(M, cm[c]);
+      for (int i = 0; i < 4; ++i) {
+        const int at = (2 * t + (i & 1)) * kHeadDim + 16 * warp + g + 8 * (i >> 1);
+        cluster.map_shared_rank(mine, at / per)->o[rank][at % per] = o[i];
       }
+    }
+    // maximum and sum of head g (the same in every warp), from warp w to CTA w
+    if (warp < CL && t == 0) {
+      float ls = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRwWarps; ++w) ls += sh.wl[w][g];
+      Received *to = cluster.map_shared_rank(mine, warp);
+      to->m[rank][g] = m;
+      to->l[rank][g] = ls;
+    }
+    cluster_arrive();
+    cluster_wait();  // everything is here, and nobody reads or writes another's shared memory any more
+    for (int li = threadIdx.x; li < per; li += kRwThreads) {
+      const int h = (rank * per + li) / kHeadDim;
+      float M = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) M = fmaxf(M, mine->m[c][h]);
       float L = 0.0f, A = 0.0f;
 #pragma unroll
       for (int c = 0; c < CL; ++c) {
-        const RwShared<G> *other = cluster.map_shared_rank(&sh, c);
         // (a CTA without keys has nothing to add)
-        const float f = cm[c] == -INFINITY ? 0.0f : exp2f(cm[c] - M);
+        const float f = mine->m[c][h] == -INFINITY ? 0.0f : exp2f(mine->m[c][h] - M);
         if (f != 0.0f) {
-          L = fmaf(other->l[h], f, L);
-          A = fmaf(cluster.map_shared_rank(&so[0][0], c)[h * kHeadDim + d], f, A);
+          L = fmaf(mine->l[c][h], f, L);
+          A = fmaf(mine->o[c][li], f, A);
         }
       }
-      p.out[u * G * kHeadDim + i] = L > 0.0f || L != L ? A / L : 0.0f;
+      p.out[u * G * kHeadDim + rank * per + li] = L > 0.0f || L != L ? A / L : 0.0f;
     }
-    cluster_arrive();  // done reading the other CTAs' shared memory
-    cluster_wait();    // and they are done reading this one's
   }
 }
 
-template <int G, int CL>
+template <int G, int CL, int ROWS>
 cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, cudaStream_t stream) {
-  constexpr int bytes = 2 * kRwStage + static_cast<int>(sizeof(RwShared<G>));
+  constexpr int bytes = 2 * kRwBuffer + static_cast<int>(sizeof(RwShared<ROWS>));
   static_assert(3 * (bytes + 1024) <= 228 * 1024, "three CTAs per SM");
-  cudaError_t e = cudaFuncSetAttribute(window_ragged_kernel<G, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto kernel = window_ragged_kernel<G, CL, ROWS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(window_ragged_kernel<G, CL>, dim3(static_cast<unsigned>(units * CL)), dim3(kRwThreads), bytes,
-                    stream, 0u, p);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(units * CL)), dim3(kRwThreads), bytes, stream, 0u, p);
 }
 
-// As many CTAs to a unit as its ring has blocks of 128 rows, rounded up to a power of two.
+// One step of up to 128 rows per CTA where all CTAs are resident at once, or a ring has no more; else
+// longer shares in steps of 64, as many CTAs to a unit as are resident at once.  (8 sequences of 4 KV heads
+// with rings of 1,024 keys: 6.3 us in one step, 7.7 in two of 64; 96 of 2: 27.9 and 23.3; rings of 128: 5.4
+// and 6.4.)
 template <int G>
-cudaError_t launch_rw_g(int64_t units, const RaggedWindowParams &p, cudaStream_t stream) {
-  if (p.window <= kRwRows) return launch_rw<G, 1>(units, p, stream);
-  if (p.window <= 2 * kRwRows) return launch_rw<G, 2>(units, p, stream);
-  if (p.window <= 4 * kRwRows) return launch_rw<G, 4>(units, p, stream);
-  return launch_rw<G, 8>(units, p, stream);
+cudaError_t launch_rw_g(int64_t units, const RaggedWindowParams &p, int sm_count, cudaStream_t stream) {
+  const int64_t resident = 3ll * sm_count;
+  int cl = 1;
+  while (cl * 128 < p.window) cl *= 2;
+  if (cl == 1) return launch_rw<G, 1, 128>(units, p, stream);
+  if (units * cl <= resident) {
+    if (cl == 2) return launch_rw<G, 2, 128>(units, p, stream);
+    if (cl == 4) return launch_rw<G, 4, 128>(units, p, stream);
+    return launch_rw<G, 8, 128>(units, p, stream);
+  }
+  while (cl > 1 && units * cl > resident) cl /= 2;
+  if (cl == 1) return launch_rw<G, 1, 64>(units, p, stream);
+  if (cl == 2) return launch_rw<G, 2, 64>(units, p, stream);
+  return launch_rw<G, 4, 64>(units, p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p, cudaStream_t stream) {
+cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p, int sm_count,
+                                        cudaStream_t stream) {
   if (units == 0) return cudaSuccess;
-  if (p.window < 1 || p.window > 8 * kRwRows) return cudaErrorInvalidValue;
-  if (G == 4) return launch_rw_g<4>(units, p, stream);
-  if (G == 8) return launch_rw_g<8>(units, p, stream);
+  if (G == 4) return launch_rw_g<4>(units, p, sm_count, stream);
+  if (G == 8) return launch_rw_g<8>(units, p, sm_count, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -422,6 +422,25 @@ def test_window_decode_ragged(window, Hkv, G):
     R.assert_within(out, *R.window_decode(q, k, v, pos, D ** -0.5), "ragged window decode")
 
 
+@pytest.mark.parametrize("B,Hkv,G,window", [(70, 4, 4, 1024), (120, 2, 8, 513), (130, 4, 4, 129), (230, 2, 8, 300)])
+def test_window_decode_ragged_of_many_sequences(B, Hkv, G, window):
+    """More sequences than fit the SMs one step each: longer shares, the running maximum rising and falling."""
+    gen = _gen(B)
+    pos = [(37 * b * b) % (2 * window) - 1 for b in range(B)]
+    q = _bf(gen, B, G * Hkv, D, scale=2.0)
+    k, v = _bf(gen, B, Hkv, window, D), _bf(gen, B, Hkv, window, D)
+    u = torch.nn.functional.normalize(torch.randn(D, generator=gen, device=DEV), dim=0)
+    ramp = torch.linspace(-3, 3, window, device=DEV)[:, None] * u
+    q[::2] = (q[::2].float() + 10 * u).bfloat16()
+    k[::4] = (k[::4].float() + ramp).bfloat16()
+    k[2::4] = (k[2::4].float() - ramp).bfloat16()
+    out = torch.full((B, G * Hkv, D), math.nan, device=DEV)
+    E.embla_window_decode_ragged(E.Shape(B, G * Hkv, Hkv, D, 0, 0), q, k, v,
+                                 torch.tensor(pos, dtype=torch.int32, device=DEV), out)
+    _checked()
+    R.assert_within(out, *R.window_decode(q, k, v, pos, D ** -0.5), "ragged window decode")
+
+
 def test_window_decode_ragged_matches_window_decode():
     """All sequences at one position: the batch call with its own rotation of the query, and this one on
     the rotated query, agree within the rounding of that query to bf16 (2^-8 of each element, in the
