@@ -666,35 +666,44 @@ def embla_window_decode(shape: Shape, q, k_win, v_win, pos: int, out, window: in
 
 def _packed_rows(t, heads: int, D: int, name: str) -> tuple[int, int, int]:
     """Tokens, elements from one token to the next and device of packed rows bf16 [T, heads, D]."""
-    if t is None or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+    if t is None or t.dim() != 3:
+        raise ValueError(f"{name} must be [T, {heads}, {D}]")
+    T, h, d = t.shape
+    if h != heads or d != D:
         raise ValueError(f"{name} must be [T, {heads}, {D}]")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    T, step = t.shape[0], t.stride(0)
-    if T == 0:
-        return 0, heads * D, t.get_device()
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D) or (T > 1 and step < heads * D):
+    if t.is_contiguous():
+        return T, heads * D, dev
+    step, head, dim = t.stride()
+    if T > 1 and step < heads * D or heads > 1 and head != D or dim != 1:
         raise ValueError(f"{name}: heads and dims must be dense, tokens apart")
-    return T, step if T > 1 else heads * D, t.get_device()
+    return T, step if T > 1 else heads * D, dev
 
 
-def _packed_qkv(shape: Shape, cu_tokens, cu_keys, q, k, v, out):
-    """Checks of the two attention calls on packed prompts; tokens, keys and strides, and the device."""
-    D, cu = shape.head_dim, (shape.batch + 1,)
-    T, q_step, dev = _packed_rows(q, shape.n_q_heads, D, "q")
-    N, k_step, dev_k = _packed_rows(k, shape.n_kv_heads, D, "k")
-    Nv, v_step, dev_v = _packed_rows(v, shape.n_kv_heads, D, "v")
-    if N != Nv or (cu_keys is None and N != T):
-        raise ValueError("k and v must be [T, Hkv, D], or [n_keys, Hkv, D] beside cu_keys")
-    checks = [(out, torch.bfloat16, (T, shape.n_q_heads, D), "out"), (cu_tokens, torch.int32, cu, "cu_tokens")]
-    if cu_keys is not None:
-        checks.append((cu_keys, torch.int32, cu, "cu_keys"))
-    if _check_here(*checks) != dev or dev_k != dev or dev_v != dev:
-        raise ValueError("the call's tensors are on different devices")
-    return (T, cu_tokens.data_ptr(), N, _ptr(cu_keys), q.data_ptr(), q_step, k.data_ptr(), k_step,
-            v.data_ptr(), v_step), dev
+def _beside(t, dtype, shape: tuple, dev: int, name: str) -> int:
+    """The address of a dense tensor on the call's device."""
+    if not (t is not None and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
+        _check(t, dtype, shape, name)
+        raise ValueError(f"{name} is on {t.device}, other tensors of the call are not")
+    return t.data_ptr()
+
+
+def _same_device(dev: int, *others: int):
+    """All of a call's tensors on one device, the current one, where the kernels launch."""
+    for o in others:
+        if o != dev:
+            raise ValueError("the call's tensors are on different devices")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the call's tensors are on cuda:{dev}, which is not the current device")
+
+
+def _status(name: str, st: int):
+    if st != 0:
+        raise EmblaError(name, st)
 
 
 def embla_rope_qkv(shape: Shape, cu_tokens, pos0, q, k, v, q_out, k_out, rope_base: float = 10000.0,
@@ -709,32 +718,45 @@ def embla_rope_qkv(shape: Shape, cu_tokens, pos0, q, k, v, q_out, k_out, rope_ba
     Tk, k_step, dev_k = _packed_rows(k, Hkv, D, "k")
     if Tk != T:
         raise ValueError("q and k must have the same tokens")
-    checks = [(q_out, torch.bfloat16, (T, Hq, D), "q_out"), (cu_tokens, torch.int32, (B + 1,), "cu_tokens")]
-    if pos0 is not None:
-        checks.append((pos0, torch.int32, (B,), "pos0"))
-    if k_out is not None:
-        checks.append((k_out, torch.bfloat16, (T, Hkv, D), "k_out"))
-    for gain, name in ((q_gain, "q_gain"), (k_gain, "k_gain")):
-        if gain is not None:
-            checks.append((gain, torch.float32, (D,), name))
-    window, v_step, dev_v = 0, Hkv * D, dev
+    _same_device(dev, dev_k)
+    cu = _beside(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens")
+    to_q = _beside(q_out, torch.bfloat16, (T, Hq, D), dev, "q_out")
+    to_k = None if k_out is None else _beside(k_out, torch.bfloat16, (T, Hkv, D), dev, "k_out")
+    first = None if pos0 is None else _beside(pos0, torch.int32, (B,), dev, "pos0")
+    qg = None if q_gain is None else _beside(q_gain, torch.float32, (D,), dev, "q_gain")
+    kg = None if k_gain is None else _beside(k_gain, torch.float32, (D,), dev, "k_gain")
+    window, at_v, v_step, ring_k, ring_v = 0, None, Hkv * D, None, None
     if k_win is not None or v_win is not None:
-        if k_win is None or k_win.dim() != 4:
-            raise ValueError("k_win must be [B, Hkv, window, D]")
+        if k_win is None or k_win.dim() != 4 or k_win.shape[2] < 1:
+            raise ValueError("k_win must be [B, Hkv, window, D], window >= 1")
         window = k_win.shape[2]
-        if window < 1:
-            raise ValueError("a ring has one slot at least")
         ring = (B, Hkv, window, D)
-        checks += [(k_win, torch.bfloat16, ring, "k_win"), (v_win, torch.bfloat16, ring, "v_win")]
+        ring_k = _beside(k_win, torch.bfloat16, ring, dev, "k_win")
+        ring_v = _beside(v_win, torch.bfloat16, ring, dev, "v_win")
         Tv, v_step, dev_v = _packed_rows(v, Hkv, D, "v")
         if Tv != T:
             raise ValueError("q and v must have the same tokens")
-    if _check_here(*checks) != dev or dev_k != dev or dev_v != dev:
-        raise ValueError("the call's tensors are on different devices")
-    _call("embla_rope_qkv", ctypes.byref(shape.c()), T, cu_tokens.data_ptr(), _ptr(pos0), q.data_ptr(), q_step,
-          k.data_ptr(), k_step, _ptr(v) if window else None, v_step, rope_base, 0 if norm_eps is None else 1,
-          0.0 if norm_eps is None else norm_eps, _ptr(q_gain), _ptr(k_gain), q_out.data_ptr(), _ptr(k_out),
-          window, _ptr(k_win), _ptr(v_win), _stream(stream, dev))
+        _same_device(dev, dev_v)
+        at_v = v.data_ptr()
+    _status("embla_rope_qkv", library().embla_rope_qkv(
+        ctypes.byref(shape.c()), T, cu, first, q.data_ptr(), q_step, k.data_ptr(), k_step, at_v, v_step, rope_base,
+        norm_eps is not None, norm_eps or 0.0, qg, kg, to_q, to_k, window, ring_k, ring_v, _stream(stream, dev)))
+
+
+def _packed_qkv(shape: Shape, cu_tokens, cu_keys, q, k, v, out):
+    """Checks of the two attention calls on packed prompts; what they pass for tokens, keys and strides, the
+    output's address and the device."""
+    B, Hq, Hkv, D = shape.batch, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
+    T, q_step, dev = _packed_rows(q, Hq, D, "q")
+    N, k_step, dev_k = _packed_rows(k, Hkv, D, "k")
+    Nv, v_step, dev_v = _packed_rows(v, Hkv, D, "v")
+    if N != Nv or (cu_keys is None and N != T):
+        raise ValueError("k and v must be [T, Hkv, D], or [n_keys, Hkv, D] beside cu_keys")
+    _same_device(dev, dev_k, dev_v)
+    cu = _beside(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens")
+    cuk = None if cu_keys is None else _beside(cu_keys, torch.int32, (B + 1,), dev, "cu_keys")
+    to = _beside(out, torch.bfloat16, (T, Hq, D), dev, "out")
+    return (T, cu, N, cuk, q.data_ptr(), q_step, k.data_ptr(), k_step, v.data_ptr(), v_step), to, dev
 
 
 def embla_window_prefill(shape: Shape, cu_tokens, q, k, v, out, window: int = 128, tau: float | None = None,
@@ -742,9 +764,10 @@ def embla_window_prefill(shape: Shape, cu_tokens, q, k, v, out, window: int = 12
     """Causal softmax attention of packed prompts over the newest `window` keys: q, out bf16 [T, Hq, D],
     k and v bf16 [T, Hkv, D], or [n_keys, Hkv, D] with cu_keys (int32 [B + 1]) where sequences have
     more keys than queries (the queries are the last ones)."""
-    args, dev = _packed_qkv(shape, cu_tokens, cu_keys, q, k, v, out)
-    _call("embla_window_prefill", ctypes.byref(shape.c()), *args, window,
-          shape.head_dim ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream, dev))
+    args, to, dev = _packed_qkv(shape, cu_tokens, cu_keys, q, k, v, out)
+    _status("embla_window_prefill", library().embla_window_prefill(
+        ctypes.byref(shape.c()), *args, window, shape.head_dim ** -0.5 if tau is None else tau, to,
+        _stream(stream, dev)))
 
 
 def embla_prefill_packed_workspace_size(shape: Shape, n_keys: int) -> int:
@@ -754,14 +777,15 @@ def embla_prefill_packed_workspace_size(shape: Shape, n_keys: int) -> int:
 def embla_prefill_packed(shape: Shape, cu_tokens, q, k, v, out, alpha: float = 1.0, c: float = 1.0,
                          eps: float = 1e-6, cu_keys=None, workspace=None, stream=None):
     """embla_prefill for packed prompts: causal ReLU^2 attention, rows as for embla_window_prefill."""
-    args, dev = _packed_qkv(shape, cu_tokens, cu_keys, q, k, v, out)
+    args, to, dev = _packed_qkv(shape, cu_tokens, cu_keys, q, k, v, out)
     ws = workspace
     if ws is None:
         ws = _workspace(embla_prefill_packed_workspace_size(shape, k.shape[0]), None, q.device, stream)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"workspace must be contiguous, on cuda:{dev}")
-    _call("embla_prefill_packed", ctypes.byref(shape.c()), *args, alpha, c, eps, out.data_ptr(), ws.data_ptr(),
-          ws.numel() * ws.element_size(), _stream(stream, dev))
+    _status("embla_prefill_packed", library().embla_prefill_packed(
+        ctypes.byref(shape.c()), *args, alpha, c, eps, to, ws.data_ptr(), ws.numel() * ws.element_size(),
+        _stream(stream, dev)))
 
 
 def embla_window_decode_ragged(shape: Shape, q, k_win, v_win, pos, out, tau: float | None = None, stream=None):
@@ -770,12 +794,17 @@ def embla_window_decode_ragged(shape: Shape, q, k_win, v_win, pos, out, tau: flo
     B, Hkv, D = shape.batch, shape.n_kv_heads, shape.head_dim
     if k_win is None or k_win.dim() != 4:
         raise ValueError("k_win must be [B, Hkv, window, D]")
-    heads, ring = (B, shape.n_q_heads, D), (B, Hkv, k_win.shape[2], D)
-    dev = _check_here((q, torch.bfloat16, heads, "q"), (k_win, torch.bfloat16, ring, "k_win"),
-                      (v_win, torch.bfloat16, ring, "v_win"), (pos, torch.int32, (B,), "pos"),
-                      (out, torch.float32, heads, "out"))
-    _call("embla_window_decode_ragged", ctypes.byref(shape.c()), q.data_ptr(), k_win.data_ptr(), v_win.data_ptr(),
-          ring[2], pos.data_ptr(), D ** -0.5 if tau is None else tau, out.data_ptr(), _stream(stream, dev))
+    dev, window = k_win.get_device(), k_win.shape[2]
+    if dev < 0:
+        raise ValueError("k_win must be a CUDA tensor")
+    heads, ring = (B, shape.n_q_heads, D), (B, Hkv, window, D)
+    args = (_beside(q, torch.bfloat16, heads, dev, "q"), _beside(k_win, torch.bfloat16, ring, dev, "k_win"),
+            _beside(v_win, torch.bfloat16, ring, dev, "v_win"), window,
+            _beside(pos, torch.int32, (B,), dev, "pos"), D ** -0.5 if tau is None else tau,
+            _beside(out, torch.float32, heads, dev, "out"))
+    _same_device(dev)
+    _status("embla_window_decode_ragged", library().embla_window_decode_ragged(
+        ctypes.byref(shape.c()), *args, _stream(stream, dev)))
 
 
 def embla_skip_stats(shape: Shape, sel_scores, keys_needed, chunks_needed, chunk: int = 8,

@@ -942,9 +942,10 @@ embla_status packed_prefill_impl(int mode, const embla_shape *shape, int G, int6
   p.blocks = packed_blocks(n_tokens, shape->batch, G, shape->n_kv_heads);
   if (p.blocks > INT32_MAX) return EMBLA_ERR_UNSUPPORTED;
   if (norms && workspace_bytes < packed_workspace_bytes(n_keys, shape->n_kv_heads)) return EMBLA_ERR_WORKSPACE;
-  const int sms = sm_count_of(current_device());
+  LaunchDevice dev = {current_device(), 0};
+  dev.sms = sm_count_of(dev.index);  // 0 past kMaxDevices
   p.flags = flags_ptr();
-  if (sms <= 0 || !p.flags) return EMBLA_ERR_CUDA;
+  if (dev.sms <= 0 || !p.flags) return EMBLA_ERR_CUDA;
   if (window > kMaxPackedTokens) window = kMaxPackedTokens;  // more than any sequence has
   const uint32_t rows = static_cast<uint32_t>(packed_tile_keys(mode, G, window));
   CUtensorMap tm_q, tm_k, tm_v;
@@ -973,7 +974,7 @@ embla_status packed_prefill_impl(int mode, const embla_shape *shape, int G, int6
   p.Hkv = shape->n_kv_heads;
   p.window = static_cast<int32_t>(window);
   p.out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
-  return cuda_status(launch_packed_prefill(mode, G, tm_q, tm_k, tm_v, p, static_cast<float *>(workspace), sms,
+  return cuda_status(launch_packed_prefill(mode, G, tm_q, tm_k, tm_v, p, static_cast<float *>(workspace), dev,
                                            static_cast<cudaStream_t>(stream)));
 }
 
@@ -1037,9 +1038,10 @@ embla_status embla_window_decode_ragged(const embla_shape *shape, const void *q,
   const RaggedWindowParams p = {static_cast<const uint16_t *>(q), static_cast<const uint8_t *>(k_win),
                                 static_cast<const uint8_t *>(v_win), pos, out, shape->n_kv_heads, window,
                                 tau * 1.4426950408889634f};
-  const int sms = sm_count_of(current_device());
-  if (sms <= 0) return EMBLA_ERR_CUDA;
-  return cuda_status(launch_window_decode_ragged(G, units, p, sms, static_cast<cudaStream_t>(stream)));
+  LaunchDevice dev = {current_device(), 0};
+  dev.sms = sm_count_of(dev.index);  // 0 past kMaxDevices
+  if (dev.sms <= 0) return EMBLA_ERR_CUDA;
+  return cuda_status(launch_window_decode_ragged(G, units, p, dev, static_cast<cudaStream_t>(stream)));
 }
 
 embla_status embla_skip_stats(const embla_shape *shape, const float *sel_scores, int32_t chunk,

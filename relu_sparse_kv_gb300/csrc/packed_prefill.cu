@@ -850,11 +850,12 @@ __global__ void __launch_bounds__(256) packed_knorm_kernel(const PackedPrefillPa
 
 template <int MODE, int N, int G, int TEAMS>
 cudaError_t launch_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                          const PackedPrefillParams &p, int ctas, cudaStream_t stream) {
+                          const PackedPrefillParams &p, const LaunchDevice &dev, cudaStream_t stream) {
   using L = Layout<N, TEAMS>;
-  auto kernel = packed_prefill_kernel<MODE, N, G, TEAMS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  constexpr auto kernel = packed_prefill_kernel<MODE, N, G, TEAMS>;
+  const cudaError_t e = allow_smem_once<kernel>(dev, L::kBytes);
   if (e != cudaSuccess) return e;
+  const int64_t ctas = p.blocks < dev.sms ? p.blocks : dev.sms;  // one per SM
   return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(L::kThreads), static_cast<size_t>(L::kBytes),
                     stream, 0u, tm_q, tm_k, tm_v, p);
 }
@@ -879,8 +880,8 @@ size_t packed_workspace_bytes(int64_t keys, int Hkv) { return packed_norm_bytes(
 int64_t packed_blocks(int64_t tokens, int batch, int G, int Hkv) { return (tokens / (128 / G) + batch) * Hkv; }
 
 cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                                  const CUtensorMap &tm_v, PackedPrefillParams p, float *rk, int sm_count,
-                                  cudaStream_t stream) {
+                                  const CUtensorMap &tm_v, PackedPrefillParams p, float *rk,
+                                  const LaunchDevice &dev, cudaStream_t stream) {
   if (p.blocks == 0) return cudaSuccess;
   p.ticket = nullptr;
   if (mode == kPackedRelu2 && p.keys > 0) {
@@ -890,17 +891,16 @@ cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, cons
                                0u, p, rk);
     if (e != cudaSuccess) return e;
   }
-  const int ctas = static_cast<int>(p.blocks < sm_count ? p.blocks : sm_count);
   const bool shorter = packed_tile_keys(mode, G, p.window) == 80;
   if (G == 4) {
-    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 4, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
-    if (shorter) return launch_packed<kPackedSoftmax, 80, 4, 2>(tm_q, tm_k, tm_v, p, ctas, stream);
-    return launch_packed<kPackedSoftmax, 128, 4, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
+    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 4, 1>(tm_q, tm_k, tm_v, p, dev, stream);
+    if (shorter) return launch_packed<kPackedSoftmax, 80, 4, 2>(tm_q, tm_k, tm_v, p, dev, stream);
+    return launch_packed<kPackedSoftmax, 128, 4, 1>(tm_q, tm_k, tm_v, p, dev, stream);
   }
   if (G == 8) {
-    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 8, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
-    if (shorter) return launch_packed<kPackedSoftmax, 80, 8, 2>(tm_q, tm_k, tm_v, p, ctas, stream);
-    return launch_packed<kPackedSoftmax, 128, 8, 1>(tm_q, tm_k, tm_v, p, ctas, stream);
+    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 8, 1>(tm_q, tm_k, tm_v, p, dev, stream);
+    if (shorter) return launch_packed<kPackedSoftmax, 80, 8, 2>(tm_q, tm_k, tm_v, p, dev, stream);
+    return launch_packed<kPackedSoftmax, 128, 8, 1>(tm_q, tm_k, tm_v, p, dev, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -2,9 +2,27 @@
 // window_ragged.cu, packed_prefill.cu), not part of the ABI.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace embla {
+
+// The device that a call launches on (its index below 64), and its number of SMs.
+struct LaunchDevice {
+  int index, sms;
+};
+
+// Raises a kernel's limit of dynamic shared memory, once per device.
+template <auto Kernel>
+cudaError_t allow_smem_once(const LaunchDevice &dev, int bytes) {
+  static std::atomic<uint64_t> done;  // a bit per device
+  const uint64_t bit = uint64_t{1} << dev.index;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
 
 // Packed tokens: sequence b of `batch` is tokens cu[b] .. cu[b + 1] - 1 of `tokens`.
 struct PackedTokens {
@@ -41,8 +59,8 @@ struct RaggedWindowParams {
   int32_t Hkv, window;
   float tau2;  // tau * log2(e)
 };
-cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p, int sm_count,
-                                        cudaStream_t stream);
+cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p,
+                                        const LaunchDevice &dev, cudaStream_t stream);
 
 // Causal attention over packed prompts (kinds of weights).
 constexpr int kPackedSoftmax = 0, kPackedRelu2 = 1;
@@ -66,7 +84,7 @@ int64_t packed_blocks(int64_t tokens, int batch, int G, int Hkv);
 int64_t packed_rk_stride(int64_t keys);
 size_t packed_workspace_bytes(int64_t keys, int Hkv);
 cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                                  const CUtensorMap &tm_v, PackedPrefillParams p, float *rk, int sm_count,
-                                  cudaStream_t stream);
+                                  const CUtensorMap &tm_v, PackedPrefillParams p, float *rk,
+                                  const LaunchDevice &dev, cudaStream_t stream);
 
 }  // namespace embla

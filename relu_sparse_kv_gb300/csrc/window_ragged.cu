@@ -262,11 +262,11 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
 }
 
 template <int G, int CL, int ROWS>
-cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, cudaStream_t stream) {
+cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
   constexpr int bytes = 2 * kRwBuffer + static_cast<int>(sizeof(RwShared<ROWS>));
   static_assert(3 * (bytes + 1024) <= 228 * 1024, "three CTAs per SM");
-  auto kernel = window_ragged_kernel<G, CL, ROWS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr auto kernel = window_ragged_kernel<G, CL, ROWS>;
+  const cudaError_t e = allow_smem_once<kernel>(dev, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(units * CL)), dim3(kRwThreads), bytes, stream, 0u, p);
 }
@@ -276,29 +276,29 @@ cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, cudaStream_t s
 // with rings of 1,024 keys: 6.3 us in one step, 7.7 in two of 64; 96 of 2: 27.9 and 23.3; rings of 128: 5.4
 // and 6.4.)
 template <int G>
-cudaError_t launch_rw_g(int64_t units, const RaggedWindowParams &p, int sm_count, cudaStream_t stream) {
-  const int64_t resident = 3ll * sm_count;
+cudaError_t launch_rw_g(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
+  const int64_t resident = 3ll * dev.sms;
   int cl = 1;
   while (cl * 128 < p.window) cl *= 2;
-  if (cl == 1) return launch_rw<G, 1, 128>(units, p, stream);
+  if (cl == 1) return launch_rw<G, 1, 128>(units, p, dev, stream);
   if (units * cl <= resident) {
-    if (cl == 2) return launch_rw<G, 2, 128>(units, p, stream);
-    if (cl == 4) return launch_rw<G, 4, 128>(units, p, stream);
-    return launch_rw<G, 8, 128>(units, p, stream);
+    if (cl == 2) return launch_rw<G, 2, 128>(units, p, dev, stream);
+    if (cl == 4) return launch_rw<G, 4, 128>(units, p, dev, stream);
+    return launch_rw<G, 8, 128>(units, p, dev, stream);
   }
   while (cl > 1 && units * cl > resident) cl /= 2;
-  if (cl == 1) return launch_rw<G, 1, 64>(units, p, stream);
-  if (cl == 2) return launch_rw<G, 2, 64>(units, p, stream);
-  return launch_rw<G, 4, 64>(units, p, stream);
+  if (cl == 1) return launch_rw<G, 1, 64>(units, p, dev, stream);
+  if (cl == 2) return launch_rw<G, 2, 64>(units, p, dev, stream);
+  return launch_rw<G, 4, 64>(units, p, dev, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p, int sm_count,
-                                        cudaStream_t stream) {
+cudaError_t launch_window_decode_ragged(int G, int64_t units, const RaggedWindowParams &p,
+                                        const LaunchDevice &dev, cudaStream_t stream) {
   if (units == 0) return cudaSuccess;
-  if (G == 4) return launch_rw_g<4>(units, p, sm_count, stream);
-  if (G == 8) return launch_rw_g<8>(units, p, sm_count, stream);
+  if (G == 4) return launch_rw_g<4>(units, p, dev, stream);
+  if (G == 8) return launch_rw_g<8>(units, p, dev, stream);
   return cudaErrorInvalidValue;
 }
 
