@@ -13,19 +13,20 @@
 // of a matrix product that read the same keys; its key tiles of N rows start at the first key that
 // some row of it sees.  Persistent CTAs, one per SM, take blocks in turn.  Warp roles:
 //   warp 0     finds each block's sequence (below), hands the block's description to the others and
-//              loads by TMA: the 128 query rows once, per tile the K and V rows, in rings of 3.
+//              loads by TMA the 128 query rows (two blocks' worth fit) and the tiles' K rows.
 //   warp 1     tcgen05 issuer of S = Q K^T (M 128 rows x N keys) into one of three tensor-memory
 //              buffers; S of tile t takes the buffer of tile t - 3 once its P V is done.
-//   last warp  tcgen05 issuer of O += P V, P from tensor memory (over its S), V as it lies.
-//   warps 2..9 the weights: a warp takes 16 rows, a row lies in the four lanes of a quad (the
-//              fragment layout of 16x256b loads), so a row's maximum is two shuffles and no
-//              other warp's business, and P, packed in pairs, goes back in 16x128b stores to the
-//              columns of its own rows.
+//   warps 2..  one team or two of eight warps: the weights.  A warp takes 16 rows, a row lies in the four
+//              lanes of a quad (the fragment layout of 16x256b loads), so a row's maximum is two
+//              shuffles and no other warp's business, and P, packed in pairs, goes back in 16x128b stores
+//              to the columns of its own rows.  At the end of a block they divide O and store it.
+//   then       the tcgen05 issuer of O += P V, P from tensor memory (over its S), V as it lies;
+//   and last   the loads of the tiles' V rows.
 //
 // Softmax.  With z = tau log2(e) s, P = exp2(z - m) for a running reference m per row and l = sum P.
 // m follows the maximum only when that has grown by more than 2^8 (kSlack): O, in tensor memory, is then
 // multiplied by exp2(m_old - m) once its last product is done; O / l does not depend on m.  m, l and
-// O are fp32; P enters the product as bf16 (2^-9 of each weight, as much as the output's own
+// O are fp32; P enters the product as bf16 (2^-8 of each weight at most, as much as the output's own
 // rounding to bf16).
 // ReLU^2.  w' = max(dot rk_j, 0)^2, a2 = alpha^2 / (mean(q^2) + eps): out = a2 O' / (c + a2 sum w').
 //
@@ -37,6 +38,19 @@
 // A block's sequence.  The host knows no lengths, so block numbers are spread with room to spare: sequence
 // b owns the numbers from floor(cu_q[b] / R) + b (R tokens to a block), which is enough for its blocks,
 // and a number past them is skipped.  The owner is found by a 32-way search.
+//
+// What bounds it, and what was measured (16 query heads):
+//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 622 us, 1,765
+//     TFLOP/s of visible products (0.93 of the burst rate); softmax over all keys 1,490 (8,192 tokens), there
+//     the exponentials and the maximum add what the tensor cores cannot hide.
+//   - a window of 128 keys: memory.  8 x 16,384 tokens 246 us, 5.45 TB/s (0.80 of a copy's rate); a block is
+//     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
+//     one team of eight warps on tiles of 128 took 480 us, two on tiles of 80 with a barrier per block 315.
+//     With four warps of their own for the outputs beside one team 320 us (they take longer for a
+//     block than its weights do; the long prompt gained, 604 us).
+//   - short prompts: what a block costs beside its tiles, about 4,000 cycles.  Describing blocks earlier, a
+//     second O, teams on alternate tiles of two blocks, and outputs read while the next block's
+//     first weights are worked out each measured the same or slower.
 #include <type_traits>
 
 #include "ptx_blocks.cuh"
@@ -45,9 +59,6 @@
 namespace embla {
 namespace {
 
-#ifndef EMBLA_SHORT_SPAN
-#define EMBLA_SHORT_SPAN 1100
-#endif
 constexpr int kTeamWarps = 8;      // warps that turn a block's scores into weights
 constexpr int kRing = 3;           // V stages and S/P buffers
 constexpr int kBoxQ = 128 * 128;   // [128 rows][64 bf16]
@@ -70,21 +81,22 @@ struct Block {
   int32_t tile0;  // tiles of the blocks before
 };
 
-// TEAMS sets of kTeamWarps warps take blocks in turn; each has query rows and an O of its own.
+// TEAMS sets of kTeamWarps warps take blocks in turn; each has an O of its own.
 template <int N, int TEAMS>
 struct Layout {
   static constexpr int kThreads = (4 + TEAMS * kTeamWarps) * 32;
   static constexpr int kWarpPV = 2 + TEAMS * kTeamWarps, kWarpV = kWarpPV + 1;
-  static constexpr int kRingK = N < 128 ? 4 : 3;  // K stages
+  static constexpr int kRingK = N < 128 ? 4 : 2;  // K stages
+  static constexpr int kQ = 2;                    // blocks whose query rows are there
   static constexpr int kColO = kRing * N;  // TEAMS times 128 columns
   static_assert(kColO + TEAMS * 128 <= kTmemCols, "tensor memory");
   static constexpr int kBoxKV = N * 128;  // [N rows][64 bf16]
   static constexpr int kStage = 2 * kBoxKV;
-  static constexpr int kOffK = TEAMS * 2 * kBoxQ;
+  static constexpr int kOffK = kQ * 2 * kBoxQ;
   static constexpr int kOffV = kOffK + kRingK * kStage;
   static constexpr int kOffBlock = kOffV + kRing * kStage;
   static constexpr int kOffBar = kOffBlock + kBlocksAhead * static_cast<int>(sizeof(Block));
-  static constexpr int kNBars = 2 * kRingK + (3 + TEAMS) * kRing + 2 * kBlocksAhead + 4 * TEAMS;
+  static constexpr int kNBars = 2 * kRingK + (3 + TEAMS) * kRing + 2 * kBlocksAhead + 2 * kQ + 2 * TEAMS;
   static constexpr int kOffMisc = kOffBar + kNBars * 8;
   static constexpr int kBytes = kOffMisc + 32 + 1024;  // + room to align the base to 1024
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -108,6 +120,7 @@ template <int MODE, int N, int G>
 struct BlockFinder {
   static constexpr int R = 128 / G;
   uint32_t at, step, numbers;  // this CTA's place in the next round of numbers, and numbers per KV head
+  bool draw = false;
   // the sequence found last: its block numbers, queries and keys
   int first = 0, end = 0, q_lo = 0, q_hi = 0, k_lo = 0, k_hi = 0;
   __device__ BlockFinder(const PackedPrefillParams &p, uint32_t cta, uint32_t ctas)
@@ -134,23 +147,23 @@ struct BlockFinder {
     return v >= first && v < end;
   }
 
-  // The next block; tiles < 0 after the last.  With a ticket counter each CTA draws its next number when it
-  // is ready for it; without, a round of numbers is dealt at a time, alternate rounds in reverse order, so
-  // the CTAs' sums of key tiles stay close.
+  // The next block; tiles < 0 after the last.  A round of numbers is dealt at a time, alternate rounds in
+  // reverse order, so the CTAs' sums of key tiles stay close.  With a ticket counter that holds for two
+  // rounds, and then each CTA draws its next number when it has asked for the last rows of a block.
   __device__ __forceinline__ Block next(const PackedPrefillParams &p, int lane) {
     Block r = {};
     r.tiles = -1;
     for (;;) {
+      if (draw) {
+        uint32_t ticket = 0;
+        if (lane == 0) ticket = atomicAdd(p.ticket, 1u);
+        at = 2 * step + __shfl_sync(0xffffffffu, ticket, 0);
+      }
       const uint32_t idx = at;
       const uint32_t base = idx - idx % step;
       if (base >= static_cast<uint32_t>(p.blocks)) return r;
-      if (p.ticket != nullptr) {
-        uint32_t drawn = 0;
-        if (lane == 0) drawn = atomicAdd(p.ticket, 1u);
-        at = step + __shfl_sync(0xffffffffu, drawn, 0);
-      } else {
-        at = base + step + (step - 1 - (idx - base));
-      }
+      at = base + step + (step - 1 - (idx - base));
+      draw = p.ticket != nullptr && at >= 2 * step;
       if (idx >= static_cast<uint32_t>(p.blocks)) continue;
       const uint32_t up = idx / static_cast<uint32_t>(p.Hkv);
       const int v = static_cast<int>(numbers - 1 - up);  // the last ones, with the most keys, first
@@ -312,8 +325,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
   Block *sBlock = reinterpret_cast<Block *>(smem + L::kOffBlock);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
   // Tile g has V stage and S/P buffer g % kRing in phase (g / kRing) & 1 and K stage g % kRingK in
-  // phase (g / kRingK) & 1.  Block k has the description k % kBlocksAhead, and the query rows and the O
-  // of team k % TEAMS.
+  // phase (g / kRingK) & 1.  Block k has the description k % kBlocksAhead, the query rows k % kQ
+  // and the O of team k % TEAMS.
   constexpr int kRingK = L::kRingK;
   uint64_t *kfull = bars, *kempty = kfull + kRingK, *vfull = kempty + kRingK;
   // S of a tile in tensor memory: a team's tiles by its own count, so that it sees every phase
@@ -322,8 +335,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
   uint64_t *pvdone = pfull + kRing;  // its P V done: the S/P buffer and the V stage are free
   uint64_t *bfull = pvdone + kRing;  // a block's description is there
   uint64_t *bempty = bfull + kBlocksAhead;  // and has been read by everyone
-  uint64_t *qfull = bempty + kBlocksAhead, *qempty = qfull + TEAMS;  // its query rows are there, and used
-  uint64_t *ofull = qempty + TEAMS;  // a block's P V all done
+  uint64_t *qfull = bempty + kBlocksAhead, *qempty = qfull + L::kQ;  // its query rows are there, and used
+  uint64_t *ofull = qempty + L::kQ;  // a block's P V all done
   uint64_t *ofree = ofull + TEAMS;   // its O read out of tensor memory
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   uint32_t *s_tmem = misc;
@@ -345,9 +358,11 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       mbar_init(&kfull[lane], 1);
       mbar_init(&kempty[lane], 1);
     }
-    if (lane < TEAMS) {
+    if (lane < L::kQ) {
       mbar_init(&qfull[lane], 1);
       mbar_init(&qempty[lane], 1 + (MODE == kPackedRelu2 ? kTeamWarps : 0));  // S done, and the rows' norms
+    }
+    if (lane < TEAMS) {
       mbar_init(&ofull[lane], 1);
       mbar_init(&ofree[lane], kTeamWarps);
     }
@@ -383,7 +398,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     int g = 0;
     bool ok = true;
     for (int k = 0, ends = 0; ok && ends < TEAMS; ++k) {  // (each team is told of the end)
-      const int s = k % TEAMS, d = k % kBlocksAhead;
+      const int s = k % L::kQ, d = k % kBlocksAhead;
       b.tile0 = g;
       if (lane == 0) {
         ok = k < kBlocksAhead || wait_bar(&bempty[d], ((k / kBlocksAhead) - 1) & 1);
@@ -392,7 +407,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           mbar_arrive(&bfull[d]);
         }
         // (blocks without tiles take their turn with the query rows, but load none)
-        if (ok && b.tiles >= 0) ok = k < TEAMS || wait_bar(&qempty[s], ((k / TEAMS) - 1) & 1);
+        if (ok && b.tiles >= 0) ok = k < L::kQ || wait_bar(&qempty[s], ((k / L::kQ) - 1) & 1);
         if (ok && b.tiles >= 0) {
           if (b.tiles > 0) {
             uint8_t *to = sQ + s * 2 * kBoxQ;
@@ -439,7 +454,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
         const int tiles = sBlock[d].tiles;
         mbar_arrive(&bempty[d]);
         if (tiles < 0) break;
-        ok = wait_bar(&qfull[s], (k / TEAMS) & 1);
+        const int q = k % L::kQ;
+        ok = wait_bar(&qfull[q], (k / L::kQ) & 1);
         int u = TEAMS > 1 && s ? mine[TEAMS - 1] : mine[0];
         for (int t = 0; ok && t < tiles; ++t, ++g, ++u) {
           const int sb = g % kRing, kb = g % kRingK;
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             // dims 16kk .. 16kk + 15: 32 bytes into a 128-byte row; dims 64.. start the second box
-            const uint64_t qo = static_cast<uint64_t>(((2 * s + (kk >> 2)) * kBoxQ + (kk & 3) * 32) >> 4);
+            const uint64_t qo = static_cast<uint64_t>(((2 * q + (kk >> 2)) * kBoxQ + (kk & 3) * 32) >> 4);
             const uint64_t ko = static_cast<uint64_t>((kb * L::kStage + (kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4);
             tc_mma_bf16(tmem + sb * N, qdesc + qo, kdesc + ko, kIdescS, kk > 0 ? 1u : 0u);
           }
@@ -459,7 +475,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
         }
         (TEAMS > 1 && s ? mine[TEAMS - 1] : mine[0]) = u;
         if (ok) {
-          tc_commit(&qempty[s]);
+          tc_commit(&qempty[q]);
           blocks = k + 1;
         }
       }
@@ -469,7 +485,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       for (int i = 0; i < TEAMS; ++i)
         if (mine[i] > 0) wait_bar(&sfull[i * kRing + (mine[i] - 1) % kRing], ((mine[i] - 1) / kRing) & 1);
       if (g > 0) wait_bar(&kempty[(g - 1) % kRingK], ((g - 1) / kRingK) & 1);
-      for (int k = blocks - 1; k >= 0 && k >= blocks - TEAMS; --k) wait_bar(&qempty[k % TEAMS], (k / TEAMS) & 1);
+      for (int k = blocks - 1; k >= 0 && k >= blocks - L::kQ; --k) wait_bar(&qempty[k % L::kQ], (k / L::kQ) & 1);
     }
     __syncwarp();
   } else if (warp == L::kWarpPV) {
@@ -560,22 +576,6 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bempty[d]);
       if (b.tiles < 0) break;
-      float a2[2] = {0.0f, 0.0f};  // ReLU^2: alpha^2 / (mean(q^2) + eps) of this lane's rows
-      if (MODE == kPackedRelu2) {
-        ok = __all_sync(0xffffffffu, wait_bar(&qfull[team], n & 1));
-        if (!ok) break;
-        // two lanes to a row, a box each
-        const int r = rowa + (lane >> 1);
-        float ss = box_square_sum(sQ + (2 * team + (lane & 1)) * kBoxQ, r, (r & 7) ^ (4 * (lane & 1)));
-        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-        const float a = (p.alpha * p.alpha) / (ss * (1.0f / kHeadDim) + p.eps);
-        a2[0] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2));
-        a2[1] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2) + 16);
-        // the query rows are read: these depend on every lane's sum
-        const float used = __shfl_sync(0xffffffffu, a2[0], 0) + a2[1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive_after(&qempty[team], used);
-      }
       // a row sees the keys oldest .. oldest + span, relative to k0 (none: from far behind the last)
       int oldest[2];
       uint32_t span[2];
@@ -724,6 +724,24 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
         if (lane == 0) mbar_arrive(&pfull[sb]);
       }
       if (!ok) break;
+      // (late, so that it has the last products' time)
+      float a2[2] = {0.0f, 0.0f};  // ReLU^2: alpha^2 / (mean(q^2) + eps) of this lane's rows
+      if constexpr (MODE == kPackedRelu2) {
+        const int q = k % L::kQ;
+        ok = __all_sync(0xffffffffu, wait_bar(&qfull[q], (k / L::kQ) & 1));
+        if (!ok) break;
+        // two lanes to a row, a box each
+        const int r = rowa + (lane >> 1);
+        float ss = box_square_sum(sQ + (2 * q + (lane & 1)) * kBoxQ, r, (r & 7) ^ (4 * (lane & 1)));
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        const float a = (p.alpha * p.alpha) / (ss * (1.0f / kHeadDim) + p.eps);
+        a2[0] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2));
+        a2[1] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2) + 16);
+        // the query rows are read: these depend on every lane's sum
+        const float used = __shfl_sync(0xffffffffu, a2[0], 0) + a2[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_after(&qempty[q], used);
+      }
       float f[2];  // what O is multiplied with; 0 where no key weighs anything
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -809,7 +827,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     const int nk = s_issued[0], nv = s_issued[1], nq = s_issued[2];
     for (int g = nk - 1; g >= 0 && g >= nk - kRingK; --g) wait_bar(&kfull[g % kRingK], (g / kRingK) & 1);
     for (int g = nv - 1; g >= 0 && g >= nv - kRing; --g) wait_bar(&vfull[g % kRing], (g / kRing) & 1);
-    for (int k = nq - 1; k >= 0 && k >= nq - TEAMS; --k) wait_bar(&qfull[k % TEAMS], (k / TEAMS) & 1);
+    for (int k = nq - 1; k >= 0 && k >= nq - L::kQ; --k) wait_bar(&qfull[k % L::kQ], (k / L::kQ) & 1);
   }
   if (warp == 1) {
     tc_fence_after_sync();
@@ -862,10 +880,13 @@ cudaError_t launch_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_k, cons
 
 }  // namespace
 
-// A block of 128 / G tokens sees window + 128 / G - 1 keys at most.  Where three tiles of 80 hold them, a
-// block is a few microseconds' work, and two teams of warps on blocks in turn hide each other's waits.
+// A block of 128 / G tokens sees window + 128 / G - 1 keys at most.  Up to about a thousand, two teams on
+// tiles of 80 are faster than one on tiles of 128, which waits at each block's ends (2 x 16,384 tokens, 4 KV
+// heads, us: window 128 80 against 108, 256 91 and 130, 512 135 and 173, 1,024 248 and 247; 2 KV heads, 1,024
+// 226 and 242); for 2,048 keys 414 against 389.
+constexpr int64_t kShortSpan = 1100;
 int packed_tile_keys(int mode, int G, int64_t window) {
-  return mode == kPackedSoftmax && window + 128 / G - 1 <= EMBLA_SHORT_SPAN ? 80 : 128;
+  return mode == kPackedSoftmax && window + 128 / G - 1 <= kShortSpan ? 80 : 128;
 }
 
 int64_t packed_rk_stride(int64_t keys) { return (keys + 3) & ~static_cast<int64_t>(3); }
