@@ -173,17 +173,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
     ps += __shfl_xor_sync(0xffffffffu, ps, 1);
     ps += __shfl_xor_sync(0xffffffffu, ps, 2);
     l = fmaf(l, sc, ps);
-    if constexpr (!kOnce) {
-      // O follows the maximum; heads 2t and 2t + 1 have their factors in lanes 8t and 8t + 4
-      const float sca = __shfl_sync(0xffffffffu, sc, 8 * t), scb = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
-      o[0] *= sca;
-      o[1] *= scb;
-      o[2] *= sca;
-      o[3] *= scb;
-    }
+    // O follows the maximum; heads 2t and 2t + 1 have their factors in lanes 8t and 8t + 4
+    const float sca = __shfl_sync(0xffffffffu, sc, 8 * t), scb = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
     cp_async_wait<kOnce ? 0 : 3>();  // this warp's V rows (behind them K, V and K)
     __syncthreads();                 // everyone's, and P
-    // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T
+    // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T.  The tensor cores cut off
+    // what does not fit their sum, so a step has one of its own.
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < ROWS / 16; ++k) {
       if (c * ROWS + 16 * k >= rows) break;
@@ -192,9 +188,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
 #pragma unroll
       for (int part = 2; part >= 0; --part) {  // the small parts first
         const uint32_t *b = reinterpret_cast<const uint32_t *>(&sh.p[part][g][16 * k + 2 * t]);
-        mma_16816_bf16(o, av[0], av[1], av[2], av[3], b[0], b[4]);
+        mma_16816_bf16(d, av[0], av[1], av[2], av[3], b[0], b[4]);
       }
     }
+    o[0] = fmaf(o[0], sca, d[0]);
+    o[1] = fmaf(o[1], scb, d[1]);
+    o[2] = fmaf(o[2], sca, d[2]);
+    o[3] = fmaf(o[3], scb, d[3]);
   }
   cp_async_wait<0>();  // (empty groups)
   if (t == 0) sh.wl[warp][g] = l;
