@@ -3,19 +3,17 @@
 // weighted sum of their values.  Query and keys were rotated when they were written, and a softmax does
 // not ask for the order of its keys: the valid ones are the ring's rows 0 .. min(pos + 1, window) - 1.
 //
-// A cluster of CTAs takes a (sequence, KV head) unit, an equal share of its valid rows to a CTA.  Where all
-// units' shares of up to 128 rows fit the SMs at once, a CTA takes its share in one step; else it goes
-// through a longer one in steps of 64 rows, the next 64 on their way meanwhile.  In a step
-//   - eight warps take 8 or 16 rows each, copied by themselves, and compute S = Q K^T as m16n8k16 MMAs (M:
-//     the G query heads);
-//   - the rows' maximum per head is exchanged, and P = exp2(z - m) for the running maximum m written as
-//     three bf16 parts (hi + mid + lo, all 24 bits: the output is fp32);
-//   - each warp adds P V to its 16 of the 128 output dims over all the rows, O^T += V^T P^T, so no warp's
-//     sums have to be added to another's.
-// The CTAs of a unit each finish a share of its outputs: every one writes its part of them, its maxima
-// and its sums into the others' shared memory, over K rows that are no longer needed (writes do not
-// wait; reading each other's took a third of the kernel's time).  Three CTAs fit an SM, so that
-// one's arithmetic has the others' copies beside it.
+// Two kernels: where the units' rows fit the SMs at once, 128 to a CTA, each CTA takes its share in one
+// step (window_step_kernel); else warps go through longer shares by themselves (window_stream_kernel).
+// Either way a cluster of CTAs may share a unit: each finishes a share of its outputs, and every one
+// writes its part of them, its maxima and its sums into the others' shared memory (writes do not wait;
+// reading each other's took a third of the kernel's time).  P is fp32 in three bf16 parts (hi + mid +
+// lo, all 24 bits), because the output is fp32.
+//
+// 96 sequences of 2 KV heads over rings of 1,024 keys (85 MB): 19.4 us, 4.4 TB/s; of 4 heads (200 MB) 33.2 us,
+// 6.0 TB/s, 0.89 of a copy's rate: the first microseconds, until rows arrive, and the merge do not shrink
+// with the rings.  96 of 4 over rings of 128 (26 MB) 5.4 us; 8 of 4, 3.0 us, the launch and two trips to
+// memory (position, then rows).
 #include <cooperative_groups.h>
 
 #include "ptx_blocks.cuh"
@@ -28,17 +26,16 @@ namespace {
 
 constexpr int kRwWarps = 8;
 constexpr int kRwThreads = kRwWarps * 32;
+constexpr int kRwRows = 128;  // ring rows per CTA, 16 to a warp
 constexpr int kRwRowBytes = kHeadDim * 2;
-constexpr int kRwBuffer = 128 * kRwRowBytes;  // 32 KB of K rows, as much of V
+constexpr int kRwBuffer = kRwRows * kRwRowBytes;  // 32 KB of K rows, as much of V
 
-// ROWS: ring rows per step, 128 (one step) or 64 (the buffers hold two steps).
-template <int ROWS>
 struct RwShared {
   // parts of P, [part][head][row], padded so that heads start in different banks (those past G are zeros)
-  uint16_t p[3][8][ROWS + 8];
-  float wm[2][kRwWarps][8];  // each warp's maximum per head, of one step and the next
-  float wl[kRwWarps][8];     // each warp's sum
-  float l[8];                // the CTA's
+  uint16_t p[3][8][kRwRows + 8];
+  float wm[kRwWarps][8];  // each warp's maximum per head
+  float wl[kRwWarps][8];  // and sum
+  float l[8];             // the CTA's
 };
 
 // What a CTA of a cluster is sent, over its K rows once it is done with them: every CTA's maxima and
@@ -49,21 +46,49 @@ struct RwReceived {
   float o[CL][G * kHeadDim / CL];
 };
 
+// This CTA's share of a unit's outputs from what every CTA of the cluster sent.
+template <int G, int CL>
+__device__ __forceinline__ void finish_outputs(const RwReceived<G, CL> &in, int rank, int64_t u, float *out,
+                                               int threads) {
+  constexpr int per = G * kHeadDim / CL;
+  for (int li = threadIdx.x; li < per; li += threads) {
+    const int h = (rank * per + li) / kHeadDim;
+    float M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) M = fmaxf(M, in.m[c][h]);
+    float L = 0.0f, A = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) {
+      // (a CTA without keys has nothing to add)
+      const float f = in.m[c][h] == -INFINITY ? 0.0f : exp2f(in.m[c][h] - M);
+      if (f != 0.0f) {
+        L = fmaf(in.l[c][h], f, L);
+        A = fmaf(in.o[c][li], f, A);
+      }
+    }
+    out[u * G * kHeadDim + rank * per + li] = L > 0.0f || L != L ? A / L : 0.0f;
+  }
+}
+
 // byte offset of 16-byte piece c of staged row r: eight rows of an ldmatrix read eight bank groups
 __device__ __forceinline__ uint32_t rw_piece(int r, int c) {
   return static_cast<uint32_t>(r * kRwRowBytes + ((c ^ (r & 7)) << 4));
 }
 
-template <int G, int CL, int ROWS>
+// ----------------------------------------------------------------------------- one step
+//
+// Eight warps copy 16 rows each, all of them in flight at once, and compute S = Q K^T of them as m16n8k16
+// MMAs (M: the G query heads) as soon as the K rows are there; the maxima are exchanged and P goes to shared
+// memory; each warp then computes 16 of the 128 output dims over all the rows, O^T = V^T P^T, so no
+// warp's sums have to be added to another's.  Three CTAs fit an SM, so that one's arithmetic has the
+// others' copies beside it.
+template <int G, int CL>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
-    window_ragged_kernel(const RaggedWindowParams p) {
-  constexpr bool kOnce = ROWS == 128;
-  constexpr int kTiles = ROWS / 64;             // n8 tiles of a warp's rows
-  constexpr int kStage = ROWS * kRwRowBytes;
+    window_step_kernel(const RaggedWindowParams p) {
   pdl_wait_primary();  // the query, the rings and the positions are complete
   pdl_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];  // K rows, V rows, RwShared
-  RwShared<ROWS> &sh = *reinterpret_cast<RwShared<ROWS> *>(smem + 2 * kRwBuffer);
+  RwShared &sh = *reinterpret_cast<RwShared *>(smem + 2 * kRwBuffer);
   const int rank = CL > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int64_t u = blockIdx.x / CL;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,32 +97,24 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
   const int nv = last < 0 ? 0 : (last >= p.window ? p.window : last + 1);  // valid rows of the ring
   const int share = (nv + CL - 1) / CL;
   const int r0 = min(nv, rank * share), rows = min(nv, r0 + share) - r0;  // of this CTA
-  const int steps = kOnce ? min(rows, 1) : (rows + ROWS - 1) / ROWS;
 
-  // Copies of step c's rows of this warp: an instruction moves two whole rows; rows past the share are
-  // zeros (they read nothing, from an address inside the ring).  A group ends with each call.
-  auto copy = [&](const uint8_t *ring, int c, uint8_t *to) {
-    if (c < steps) {
-      const uint8_t *from = ring + u * p.window * kRwRowBytes;
-      const int piece = lane & 15;
+  // This warp's rows: an instruction moves two whole ones; rows past the share are zeros (they read
+  // nothing, from an address inside the ring).
+  const int wrow = warp * 16;
+  auto copy = [&](const uint8_t *ring, uint8_t *to) {
+    const uint8_t *from = ring + u * p.window * kRwRowBytes;
+    const int piece = lane & 15;
 #pragma unroll
-      for (int k = 0; k < 4 * kTiles; ++k) {
-        const int r = warp * 8 * kTiles + 2 * k + (lane >> 4);
-        const bool live = c * ROWS + r < rows;
-        cp_async16_zfill(to + rw_piece(r, piece),
-                         from + (live ? static_cast<int64_t>(r0 + c * ROWS + r) * kRwRowBytes : 0) + piece * 16,
-                         live ? 16u : 0u);
-      }
+    for (int k = 0; k < 8; ++k) {
+      const int r = wrow + 2 * k + (lane >> 4);
+      const bool live = r < rows;
+      cp_async16_zfill(to + rw_piece(r, piece),
+                       from + (live ? static_cast<int64_t>(r0 + r) * kRwRowBytes : 0) + piece * 16, live ? 16u : 0u);
     }
     cp_async_commit();
   };
-  uint8_t *const bufK = smem, *const bufV = smem + kRwBuffer;
-  copy(p.K, 0, bufK);
-  copy(p.V, 0, bufV);
-  if constexpr (!kOnce) {
-    copy(p.K, 1, bufK + kStage);
-    copy(p.V, 1, bufV + kStage);
-  }
+  copy(p.K, smem);
+  copy(p.V, smem + kRwBuffer);
   // query as the A operand of S: row g (head g), dims 16ks + 2t, +1 and +8, +9
   uint32_t qa0[8], qa2[8];
   {
@@ -108,97 +125,70 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
       qa2[ks] = g < G ? qrow[8 * ks + 4 + t] : 0u;
     }
   }
+  cp_async_wait<1>();  // the K rows
+  __syncwarp();
+
+  // S of the warp's rows, eight to a tile: head g, rows 2t and 2t + 1 of each
   const int mat = lane >> 3, mr = lane & 7;
-  float m = -INFINITY, l = 0.0f;           // head g: running maximum (base 2), sum over this warp's rows
-  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dims 16 warp + g (o[0], o[1]) and + 8, heads 2t and 2t + 1
-  if (CL > 1 && steps == 0) cluster_arrive();
-  for (int c = 0; c < steps; ++c) {
-    const int at = kOnce ? 0 : (c & 1) * kStage;
-    if (kOnce)
-      cp_async_wait<1>();  // this warp's K rows (behind them V)
-    else if (c == 0)
-      cp_async_wait<3>();  // (V, K and V)
-    else
-      cp_async_wait<2>();  // (V and K)
-    __syncwarp();
-    // S of the warp's rows, eight to a tile
-    float z[2 * kTiles];  // head g, rows 2t and 2t + 1 of each tile
-    float mx = -INFINITY;
+  float z[4], mx = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const int row = (warp * kTiles + j) * 8;
+  for (int j = 0; j < 2; ++j) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int row = wrow + 8 * j;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t bk[4];
-        ldmatrix_x4(bk, smem_u32(bufK + at) + rw_piece(row + mr, 4 * kk + mat));
-        mma_16816_bf16(s, qa0[2 * kk], 0u, qa2[2 * kk], 0u, bk[0], bk[1]);
-        mma_16816_bf16(s, qa0[2 * kk + 1], 0u, qa2[2 * kk + 1], 0u, bk[2], bk[3]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        z[2 * j + i] = c * ROWS + row + 2 * t + i < rows ? p.tau2 * s[i] : -INFINITY;
-      mx = fmaxf(mx, fmaxf(z[2 * j], z[2 * j + 1]));
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t bk[4];
+      ldmatrix_x4(bk, smem_u32(smem) + rw_piece(row + mr, 4 * kk + mat));
+      mma_16816_bf16(s, qa0[2 * kk], 0u, qa2[2 * kk], 0u, bk[0], bk[1]);
+      mma_16816_bf16(s, qa0[2 * kk + 1], 0u, qa2[2 * kk + 1], 0u, bk[2], bk[3]);
     }
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    if (t == 0) sh.wm[c & 1][warp][g] = mx;
-    __syncthreads();  // the maxima are there; the K rows of this step and the V rows and P of the last are read
-    if (CL > 1 && c == steps - 1) cluster_arrive();  // the others may write over this CTA's K rows
-    if constexpr (!kOnce) {
-      if (c > 0) copy(p.V, c + 1, bufV + (kStage - at));
-      copy(p.K, c + 2, bufK + at);
-    }
-    float mn = m;
 #pragma unroll
-    for (int w = 0; w < kRwWarps; ++w) mn = fmaxf(mn, sh.wm[c & 1][w][g]);
-    const float sc = m == mn ? 1.0f : exp2f(m - mn);
-    m = mn;
-    float ps = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      float a = z[2 * j] == -INFINITY ? 0.0f : exp2f(z[2 * j] - m);
-      float b = z[2 * j + 1] == -INFINITY ? 0.0f : exp2f(z[2 * j + 1] - m);
-      ps += a + b;
-      uint32_t *to = reinterpret_cast<uint32_t *>(&sh.p[0][g][(warp * kTiles + j) * 8 + 2 * t]);
-      constexpr int kPart = 8 * (ROWS + 8) / 2;  // words from one part to the next
-#pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        const uint32_t h = g < G ? pack_bf16x2(a, b) : 0u;  // (the operand's heads past G are zeros)
-        to[part * kPart] = h;
-        a -= bf16lo(h);
-        b -= bf16hi(h);
-      }
-    }
-    ps += __shfl_xor_sync(0xffffffffu, ps, 1);
-    ps += __shfl_xor_sync(0xffffffffu, ps, 2);
-    l = fmaf(l, sc, ps);
-    // O follows the maximum; heads 2t and 2t + 1 have their factors in lanes 8t and 8t + 4
-    const float sca = __shfl_sync(0xffffffffu, sc, 8 * t), scb = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
-    cp_async_wait<kOnce ? 0 : 3>();  // this warp's V rows (behind them K, V and K)
-    __syncthreads();                 // everyone's, and P
-    // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T.  The tensor cores cut off
-    // what does not fit their sum, so a step has one of its own.
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < ROWS / 16; ++k) {
-      if (c * ROWS + 16 * k >= rows) break;
-      uint32_t av[4];
-      ldmatrix_x4_trans(av, smem_u32(bufV + at) + rw_piece(16 * k + (mat >> 1) * 8 + mr, 2 * warp + (mat & 1)));
-#pragma unroll
-      for (int part = 2; part >= 0; --part) {  // the small parts first
-        const uint32_t *b = reinterpret_cast<const uint32_t *>(&sh.p[part][g][16 * k + 2 * t]);
-        mma_16816_bf16(d, av[0], av[1], av[2], av[3], b[0], b[4]);
-      }
-    }
-    o[0] = fmaf(o[0], sca, d[0]);
-    o[1] = fmaf(o[1], scb, d[1]);
-    o[2] = fmaf(o[2], sca, d[2]);
-    o[3] = fmaf(o[3], scb, d[3]);
+    for (int i = 0; i < 2; ++i) z[2 * j + i] = row + 2 * t + i < rows ? p.tau2 * s[i] : -INFINITY;
+    mx = fmaxf(mx, fmaxf(z[2 * j], z[2 * j + 1]));
   }
-  cp_async_wait<0>();  // (empty groups)
-  if (t == 0) sh.wl[warp][g] = l;
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  if (t == 0) sh.wm[warp][g] = mx;
   __syncthreads();
+  if constexpr (CL > 1) cluster_arrive();  // this CTA's K rows are read: the others may write over them
+  float m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kRwWarps; ++w) m = fmaxf(m, sh.wm[w][g]);
+  float l = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float a = z[2 * j] == -INFINITY ? 0.0f : exp2f(z[2 * j] - m);
+    float b = z[2 * j + 1] == -INFINITY ? 0.0f : exp2f(z[2 * j + 1] - m);
+    l += a + b;
+    uint32_t *to = reinterpret_cast<uint32_t *>(&sh.p[0][g][wrow + 8 * j + 2 * t]);
+    constexpr int kPart = 8 * (kRwRows + 8) / 2;  // words from one part to the next
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      const uint32_t h = g < G ? pack_bf16x2(a, b) : 0u;  // (the operand's heads past G are zeros)
+      to[part * kPart] = h;
+      a -= bf16lo(h);
+      b -= bf16hi(h);
+    }
+  }
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (t == 0) sh.wl[warp][g] = l;
+  cp_async_wait<0>();  // the V rows
+  __syncthreads();     // everyone's, P and the sums
+
+  // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dims g (o[0], o[1]) and g + 8, heads 2t and 2t + 1
+#pragma unroll
+  for (int k = 0; k < kRwRows / 16; ++k) {
+    if (16 * k >= rows) break;
+    uint32_t av[4];
+    ldmatrix_x4_trans(av, smem_u32(smem + kRwBuffer) + rw_piece(16 * k + (mat >> 1) * 8 + mr, 2 * warp + (mat & 1)));
+#pragma unroll
+    for (int part = 2; part >= 0; --part) {  // the small parts first
+      const uint32_t *b = reinterpret_cast<const uint32_t *>(&sh.p[part][g][16 * k + 2 * t]);
+      mma_16816_bf16(o, av[0], av[1], av[2], av[3], b[0], b[4]);
+    }
+  }
   if constexpr (CL == 1) {
     if (warp == 0 && lane < 8) {
       float ls = 0.0f;
@@ -241,55 +231,231 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
     }
     cluster_arrive();
     cluster_wait();  // everything is here, and nobody reads or writes another's shared memory any more
-    for (int li = threadIdx.x; li < per; li += kRwThreads) {
-      const int h = (rank * per + li) / kHeadDim;
-      float M = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < CL; ++c) M = fmaxf(M, mine->m[c][h]);
-      float L = 0.0f, A = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CL; ++c) {
-        // (a CTA without keys has nothing to add)
-        const float f = mine->m[c][h] == -INFINITY ? 0.0f : exp2f(mine->m[c][h] - M);
-        if (f != 0.0f) {
-          L = fmaf(mine->l[c][h], f, L);
-          A = fmaf(mine->o[c][li], f, A);
-        }
-      }
-      p.out[u * G * kHeadDim + rank * per + li] = L > 0.0f || L != L ? A / L : 0.0f;
-    }
+    finish_outputs<G, CL>(*mine, rank, u, p.out, kRwThreads);
   }
 }
 
-template <int G, int CL, int ROWS>
+// ----------------------------------------------------------------------------- many units
+//
+// Where the units' steps do not fit the SMs at once, warps go through the rows by themselves: each takes
+// every so many blocks of 16 rows of its unit, one block on its way while it works on another, with a
+// running maximum, sum and O (all 128 dims of every head) in registers.  S's accumulators are the operand
+// of the next product as they lie, so P stays in registers too.  Warps and CTAs merge at the end.
+constexpr int kWsWarps = 4;
+constexpr int kWsThreads = kWsWarps * 32;
+constexpr int kWsRows = 16;
+constexpr int kWsBlock = 2 * kWsRows * kRwRowBytes;  // K and V rows of a block: 8 KB
+constexpr int kWsStages = 2;
+
+template <int G>
+struct WsMerge {  // over the rows
+  float m[kWsWarps][8], l[kWsWarps][8];
+  float o[kWsWarps][G][kHeadDim];
+};
+
+template <int G, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kWsThreads, 3)
+    window_stream_kernel(const RaggedWindowParams p) {
+  if constexpr (CL > 1) cluster_arrive();  // (waited for before anything is sent: every CTA has started)
+  pdl_wait_primary();  // the query, the rings and the positions are complete
+  pdl_launch_dependents();
+  extern __shared__ __align__(128) uint8_t smem[];  // rows, then WsMerge; behind them what is received
+  const int rank = CL > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+  const int64_t u = blockIdx.x / CL;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int last = p.pos[u / p.Hkv];
+  const int nv = last < 0 ? 0 : (last >= p.window ? p.window : last + 1);  // valid rows of the ring
+  const int blocks = (nv + kWsRows - 1) / kWsRows;
+  uint8_t *rows = smem + warp * kWsStages * kWsBlock;
+  // Block n's rows into a stage: an instruction moves two whole rows; rows past the valid ones are zeros
+  // (they read nothing, from an address inside the ring).  A group ends with each call.
+  auto copy = [&](int n, int stage) {
+    if (n < blocks) {
+      uint8_t *to = rows + stage * kWsBlock;
+      const int piece = lane & 15;
+      const int64_t unit = u * p.window * kRwRowBytes + piece * 16;
+#pragma unroll
+      for (int k = 0; k < kWsRows / 2; ++k) {
+        const int r = 2 * k + (lane >> 4);
+        const bool live = n * kWsRows + r < nv;
+        const int64_t off = unit + (live ? static_cast<int64_t>(n * kWsRows + r) * kRwRowBytes : 0);
+        cp_async16_zfill(to + rw_piece(r, piece), p.K + off, live ? 16u : 0u);
+        cp_async16_zfill(to + kWsRows * kRwRowBytes + rw_piece(r, piece), p.V + off, live ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+  };
+  constexpr int kStep = CL * kWsWarps;
+  const int first = rank * kWsWarps + warp;
+  copy(first, 0);
+  copy(first + kStep, 1);
+  // query as the A operand of S: row g (head g), dims 16ks + 2t, +1 and +8, +9
+  uint32_t qa0[8], qa2[8];
+  {
+    const uint32_t *qrow = reinterpret_cast<const uint32_t *>(p.q + (u * G + (g < G ? g : 0)) * kHeadDim);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      qa0[ks] = g < G ? qrow[8 * ks + t] : 0u;
+      qa2[ks] = g < G ? qrow[8 * ks + 4 + t] : 0u;
+    }
+  }
+  float m = -INFINITY, l = 0.0f;  // head g: running maximum (base 2) and sum
+  float o[8][4];                  // O^T tile i: dims 16i + g (+8), heads 2t and 2t + 1
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+  const int mat = lane >> 3, row = (mat >> 1) * 8 + (lane & 7);
+  int stage = 0;
+  for (int n = first; n < blocks; n += kStep, stage ^= 1) {
+    cp_async_wait<1>();
+    __syncwarp();
+    const uint32_t sK = smem_u32(rows + stage * kWsBlock), sV = sK + kWsRows * kRwRowBytes;
+    float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+      uint32_t bk[4];
+      ldmatrix_x4(bk, sK + rw_piece(row, 2 * ks + (mat & 1)));
+      mma_16816_bf16(s0, qa0[ks], 0u, qa2[ks], 0u, bk[0], bk[1]);
+      mma_16816_bf16(s1, qa0[ks], 0u, qa2[ks], 0u, bk[2], bk[3]);
+    }
+    // head g, rows 2t, 2t + 1 (s0) and 8 + 2t, 9 + 2t (s1)
+    float z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      z[i] = n * kWsRows + 8 * (i >> 1) + 2 * t + (i & 1) < nv ? p.tau2 * (i < 2 ? s0[i] : s1[i - 2]) : -INFINITY;
+    float mn = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+    mn = fmaxf(m, fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2)));
+    const float sc = m == mn ? 1.0f : exp2f(m - mn);
+    m = mn;
+    float ps = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[i] = z[i] == -INFINITY ? 0.0f : exp2f(z[i] - m);
+      ps += z[i];
+    }
+    ps += __shfl_xor_sync(0xffffffffu, ps, 1);
+    ps += __shfl_xor_sync(0xffffffffu, ps, 2);
+    l = fmaf(l, sc, ps);
+    uint32_t part[3][2];  // P in three bf16 parts
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        part[k][i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
+        z[2 * i] -= bf16lo(part[k][i]);
+        z[2 * i + 1] -= bf16hi(part[k][i]);
+      }
+    const float sca = __shfl_sync(0xffffffffu, sc, 8 * t), scb = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t av[4];
+      ldmatrix_x4_trans(av, sV + rw_piece(row, 2 * i + (mat & 1)));
+      // (the tensor cores cut off what does not fit their sum, so a block has one of its own)
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 2; k >= 0; --k) mma_16816_bf16(d, av[0], av[1], av[2], av[3], part[k][0], part[k][1]);
+      o[i][0] = fmaf(o[i][0], sca, d[0]);
+      o[i][1] = fmaf(o[i][1], scb, d[1]);
+      o[i][2] = fmaf(o[i][2], sca, d[2]);
+      o[i][3] = fmaf(o[i][3], scb, d[3]);
+    }
+    __syncwarp();  // the stage is read before the next copies land in it
+    copy(n + 2 * kStep, stage);
+  }
+  cp_async_wait<0>();
+  __syncthreads();  // every warp is done with its rows
+  WsMerge<G> &mg = *reinterpret_cast<WsMerge<G> *>(smem);
+  static_assert(sizeof(WsMerge<G>) <= kWsWarps * kWsStages * kWsBlock, "over the rows");
+  if (t == 0) {
+    mg.m[warp][g] = m;
+    mg.l[warp][g] = l;
+  }
+  if (2 * t < G) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mg.o[warp][2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)] = o[i][e];
+  }
+  __syncthreads();
+  using Received = RwReceived<G, CL>;
+  Received *mine = reinterpret_cast<Received *>(smem + kWsWarps * kWsStages * kWsBlock);
+  constexpr int per = G * kHeadDim / CL;  // outputs that a CTA finishes: parts of one head, or whole heads
+  if constexpr (CL > 1) cluster_wait();
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    // thread: dim threadIdx.x of head h
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWsWarps; ++w) M = fmaxf(M, mg.m[w][h]);
+    float L = 0.0f, A = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWsWarps; ++w) {
+      // (a warp without rows has nothing to add)
+      const float f = mg.m[w][h] == -INFINITY ? 0.0f : exp2f(mg.m[w][h] - M);
+      if (f != 0.0f) {
+        L = fmaf(mg.l[w][h], f, L);
+        A = fmaf(mg.o[w][h][threadIdx.x], f, A);
+      }
+    }
+    if constexpr (CL == 1) {
+      p.out[(u * G + h) * kHeadDim + threadIdx.x] = L > 0.0f || L != L ? A / L : 0.0f;
+    } else {
+      const int at = h * kHeadDim + threadIdx.x;
+      Received *to = cg::this_cluster().map_shared_rank(mine, at / per);
+      to->o[rank][at % per] = A;
+      if (at % per == 0 || (at & (kHeadDim - 1)) == 0) {
+        // the first of this CTA's, or of a head: maximum and sum beside it
+        to->m[rank][h] = M;
+        to->l[rank][h] = L;
+      }
+    }
+  }
+  if constexpr (CL > 1) {
+    cluster_arrive();
+    cluster_wait();  // everything is here, and nobody writes another's shared memory any more
+    finish_outputs<G, CL>(*mine, rank, u, p.out, kWsThreads);
+  }
+}
+
+template <int G, int CL>
 cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
-  constexpr int bytes = 2 * kRwBuffer + static_cast<int>(sizeof(RwShared<ROWS>));
+  constexpr int bytes = 2 * kRwBuffer + static_cast<int>(sizeof(RwShared));
   static_assert(3 * (bytes + 1024) <= 228 * 1024, "three CTAs per SM");
-  constexpr auto kernel = window_ragged_kernel<G, CL, ROWS>;
+  constexpr auto kernel = window_step_kernel<G, CL>;
   const cudaError_t e = allow_smem_once<kernel>(dev, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(units * CL)), dim3(kRwThreads), bytes, stream, 0u, p);
 }
 
-// One step of up to 128 rows per CTA where all CTAs are resident at once, or a ring has no more; else
-// longer shares in steps of 64, as many CTAs to a unit as are resident at once.  (8 sequences of 4 KV heads
-// with rings of 1,024 keys: 6.3 us in one step, 7.7 in two of 64; 96 of 2: 27.9 and 23.3; rings of 128: 5.4
-// and 6.4.)
+template <int G, int CL>
+cudaError_t launch_ws(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
+  constexpr int bytes = kWsWarps * kWsStages * kWsBlock + static_cast<int>(sizeof(RwReceived<G, CL>));
+  static_assert(3 * (bytes + 1024) <= 228 * 1024, "three CTAs per SM");
+  constexpr auto kernel = window_stream_kernel<G, CL>;
+  const cudaError_t e = allow_smem_once<kernel>(dev, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(units * CL)), dim3(kWsThreads), bytes, stream, 0u, p);
+}
+
+// One step of up to 128 rows per CTA where all CTAs are resident at once, or a ring has no more; else as
+// many CTAs of four warps to a unit as are resident at once.  (64 sequences of 4 KV heads with rings of 512
+// keys: 19.0 us in steps, 14.6 streamed; 96 of 2 with 1,024: 27.9 and 19.4; 8 of 4 with 1,024, which fit: 6.3.)
 template <int G>
 cudaError_t launch_rw_g(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
   const int64_t resident = 3ll * dev.sms;
   int cl = 1;
   while (cl * 128 < p.window) cl *= 2;
-  if (cl == 1) return launch_rw<G, 1, 128>(units, p, dev, stream);
+  if (cl == 1) return launch_rw<G, 1>(units, p, dev, stream);
   if (units * cl <= resident) {
-    if (cl == 2) return launch_rw<G, 2, 128>(units, p, dev, stream);
-    if (cl == 4) return launch_rw<G, 4, 128>(units, p, dev, stream);
-    return launch_rw<G, 8, 128>(units, p, dev, stream);
+    if (cl == 2) return launch_rw<G, 2>(units, p, dev, stream);
+    if (cl == 4) return launch_rw<G, 4>(units, p, dev, stream);
+    return launch_rw<G, 8>(units, p, dev, stream);
   }
   while (cl > 1 && units * cl > resident) cl /= 2;
-  if (cl == 1) return launch_rw<G, 1, 64>(units, p, dev, stream);
-  if (cl == 2) return launch_rw<G, 2, 64>(units, p, dev, stream);
-  return launch_rw<G, 4, 64>(units, p, dev, stream);
+  if (cl == 1) return launch_ws<G, 1>(units, p, dev, stream);
+  if (cl == 2) return launch_ws<G, 2>(units, p, dev, stream);
+  return launch_ws<G, 4>(units, p, dev, stream);
 }
 
 }  // namespace
