@@ -421,7 +421,8 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  *              Positions stay below 2^31
  *   q, k, v    bf16 [n_tokens, Hq | Hkv | Hkv, 128]; v is read for the rings only
  *   norm       0: rows as they are; else each row of q and k first becomes
- *              x / sqrt(mean(x^2) + eps) * gain (eps finite and >= 0)
+ *              x / sqrt(mean(x^2) + eps) * gain (eps finite and >= 0; a row of zeros with eps == 0
+ *              becomes NaN)
  *   q_gain, k_gain  fp32 [128] or NULL (1); NULL without norm
  *   rope_base  > 0: pair (2i, 2i+1) is turned by position * rope_base^(-2i/128)
  *   q_out      bf16 [n_tokens, Hq, 128] (dense);  k_out  bf16 [n_tokens, Hkv, 128] or NULL: the rows,
@@ -439,11 +440,12 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  *   q          bf16 [n_tokens, Hq, 128];  k, v  bf16 [n_keys, Hkv, 128], rotated already
  *   window     >= 1 (128 in Embla 1); a window of the longest sequence or more sees everything
  *   tau        softmax scale, finite
- *   out        bf16 [n_tokens, Hq, 128] (dense)
+ *   out        bf16 [n_tokens, Hq, 128] (dense); it overlaps no input
  * Scores, maxima, sums and value sums are fp32; the weights enter the value product as bf16 (relative
- * to a reference within 2^8 of the row's largest), one rounding as large as the output's.  A key that a
- * query does not see contributes nothing, whatever its rows hold; infinite or NaN values among the rows
- * read beside a query's own have its output computed by a slow path.
+ * to a reference within 2^8 of the row's largest), one rounding as large as the output's (2^-8; value sums
+ * of one sign lose up to 6e-7 more per 80 or 128 keys, 6e-4 at 131,072).  A key that a query does not see
+ * contributes nothing, whatever its rows hold; a query beside whose keys a tile holds infinite or NaN
+ * values has its output computed by a slow path, a few hundred times its usual time.
  *
  * embla_prefill_packed — embla_prefill for packed prompts ("Sevren Sparse Attention learns to be sparse"):
  * the same queries and keys as embla_window_prefill's, no window, ReLU^2 weights of RMS-normalised

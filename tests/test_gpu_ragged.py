@@ -487,6 +487,122 @@ def test_window_decode_ragged_graph_and_nan_rows():
     assert broken[2, :8, 9].all() and broken[3, 8:].all() and int(broken.sum()) == 8 + 8 * D
 
 
+# ----------------------------------------------------------------------------- calls
+
+def test_offsets_past_32_bits():
+    """Tokens 16 MB apart: rows lie past 2^32 bytes (and 2^32 elements) from the first."""
+    lens, Hkv = [150, 0, 170], 2
+    T, Hq, step = sum(lens), 16, 1 << 24
+    x = torch.empty(T * step, dtype=torch.bfloat16, device=DEV)
+    assert x.numel() > 1 << 32
+    x = x.view(T, step)[:, :(Hq + 2 * Hkv) * D].unflatten(1, (Hq + 2 * Hkv, D))
+    near = _bf(_gen(30), T, Hq + 2 * Hkv, D)
+    x.copy_(near)
+    shape, cu = E.Shape(3, Hq, Hkv, D, 0, 0), _cu(lens)
+    parts = lambda y: (y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:])
+    near[3, -1, 5] = x[3, -1, 5] = math.nan  # (a value row that makes its readers take the slow path)
+    outs = []
+    for y in (x, near):
+        q, k, v = parts(y)
+        out = [torch.empty(T, Hq, D, dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+        k_out = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=DEV)
+        rings = [torch.zeros(3, Hkv, 64, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        E.embla_window_prefill(shape, cu, q, k, v, out[0], window=70)
+        E.embla_prefill_packed(shape, cu, q, k, v, out[1])
+        E.embla_rope_qkv(shape, cu, None, q, k, v, out[2], k_out, k_win=rings[0], v_win=rings[1])
+        _checked()
+        outs.append([*out, k_out, *rings])
+    for a, b in zip(*outs):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_rope_and_decode_on_a_stream_and_in_a_graph():
+    """Positions and lengths are read as the graph runs; calls on another stream see what that stream wrote."""
+    gen = _gen(31)
+    B, Hkv, W = 3, 4, 16
+    shape = E.Shape(B, 16, Hkv, D, 0, 0)
+    q, k, v = _fused(gen, 12, 16, Hkv)
+    cu, pos0 = _cu([4, 4, 4]), torch.tensor([0, 10, 30], dtype=torch.int32, device=DEV)
+    last, qb = pos0 + 3, _bf(gen, B, 16, D)
+    q_out, k_out = torch.zeros(12, 16, D, dtype=torch.bfloat16, device=DEV), torch.zeros(12, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    rings = [torch.zeros(B, Hkv, W, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    out = torch.zeros(B, 16, D, device=DEV)
+
+    def step(stream=None):
+        E.embla_rope_qkv(shape, cu, pos0, q, k, v, q_out, k_out, k_win=rings[0], v_win=rings[1], stream=stream)
+        E.embla_window_decode_ragged(shape, qb, *rings, last, out, stream=stream)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens, first in (([4, 4, 4], [0, 10, 30]), ([1, 0, 11], [5, 3, 100]), ([12, 0, 0], [40, 0, 0])):
+        cu.copy_(_cu(lens))
+        pos0.copy_(torch.tensor(first, dtype=torch.int32))
+        last.copy_(torch.tensor([f + n - 1 for f, n in zip(first, lens)], dtype=torch.int32))
+        graph.replay()
+        _checked()
+        at = R.starts(lens)
+        pos = torch.cat([torch.arange(f, f + n, device=DEV) for f, n in zip(first, lens)])
+        R.assert_within(q_out, *R.rope(q, pos, 10000.0), "replayed queries")
+        for b, n in enumerate(lens):
+            for t in range(max(0, n - W), n):
+                assert torch.equal(rings[0][b, :, (first[b] + t) % W], k_out[at[b] + t])
+                assert torch.equal(rings[1][b, :, (first[b] + t) % W], v[at[b] + t])
+        R.assert_within(out, *R.window_decode(qb, *rings, last.tolist(), D ** -0.5), "replayed decode")
+    before = out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q_out.zero_()
+        out.zero_()
+        for r in rings:
+            r[:, :, 5:9] = 0.0
+    step(stream=side)
+    torch.cuda.synchronize()
+    R.assert_within(q_out, *R.rope(q, pos, 10000.0), "on a stream")
+    assert torch.isfinite(out).all() and out.shape == before.shape
+
+
+def test_rope_refuses_what_it_cannot_read():
+    gen = _gen(32)
+    shape, cu = E.Shape(1, 16, 4, D, 0, 0), _cu([10])
+    q, k, v = _fused(gen, 10, 16, 4)
+    q_out, k_out = torch.empty(10, 16, D, dtype=torch.bfloat16, device=DEV), torch.empty(10, 4, D, dtype=torch.bfloat16, device=DEV)
+    ring = torch.empty(1, 4, 8, D, dtype=torch.bfloat16, device=DEV)
+    gain = torch.ones(D, device=DEV)
+    for bad in (dict(q_out=q), dict(k=k[:9]), dict(k_win=ring), dict(v_win=ring), dict(k_win=ring[:, :, :0], v_win=ring[:, :, :0]),
+                dict(pos0=cu), dict(k_win=ring, v_win=ring, v=v[:9])):
+        args = dict(cu_tokens=cu, pos0=None, q=q, k=k, v=v, q_out=q_out, k_out=k_out) | bad
+        with pytest.raises(ValueError):
+            E.embla_rope_qkv(shape, **args)
+    for bad in (dict(q_gain=gain), dict(norm_eps=-1.0), dict(rope_base=0.0)):
+        with pytest.raises(E.EmblaError) as err:
+            E.embla_rope_qkv(shape, cu, None, q, k, v, q_out, k_out, **bad)
+        assert err.value.status == 1
+    with pytest.raises(E.EmblaError) as err:
+        E.embla_window_decode_ragged(shape, q_out[:1].contiguous(), torch.empty(1, 4, 1025, D, dtype=torch.bfloat16, device=DEV),
+                                     torch.empty(1, 4, 1025, D, dtype=torch.bfloat16, device=DEV), cu[:1], torch.empty(1, 16, D, device=DEV))
+    assert err.value.status == 1
+
+
+@pytest.mark.parametrize("kind", ["window", "packed"])
+def test_prompts_of_thousands_of_sequences(kind):
+    """Many more sequences than CTAs, most of a token or none."""
+    lens, Hkv = [(7 * b * b) % 5 if b % 97 else 300 for b in range(1500)], 2
+    at = R.starts(lens)
+    q, k, v, out = _attention_inputs(33, lens, None, Hkv, 8, 0, 1.5)
+    _run_window(lens, None, Hkv, q, k, v, out, 128) if kind == "window" else _run_packed(lens, None, Hkv, q, k, v, out)
+    _checked()
+    some = [0, 1, 96, 97, 98, 700, 1455, 1499]
+    for b in some:
+        a, e = at[b], at[b + 1]
+        form = R.window_prefill(q[a:e], k[a:e], v[a:e], [0, e - a], [0, e - a], 128, D ** -0.5) if kind == "window" else \
+            R.prefill_packed(q[a:e], k[a:e], v[a:e], [0, e - a], [0, e - a], 1.0, 1.0, 1e-6)
+        R.assert_within(out[a:e], *form, f"sequence {b}")
+
+
 # ----------------------------------------------------------------------------- together
 
 @pytest.mark.parametrize("Hkv,window", [(4, 128), (2, 40)])
