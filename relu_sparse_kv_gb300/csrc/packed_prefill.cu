@@ -31,9 +31,12 @@
 // ReLU^2.  w' = max(dot rk_j, 0)^2, a2 = alpha^2 / (mean(q^2) + eps): out = a2 O' / (c + a2 sum w').
 //
 // A weight of zero times an infinite or NaN value would be NaN, and a tile holds rows that a query
-// must not see (later ones, older ones, other sequences').  An output that comes out infinite or NaN
-// is therefore computed again by its warp, key by key over the visible ones (slow_row); nothing
-// else pays for it.
+// must not see.  Value rows of other sequences, or behind the last (which nothing may have written), are
+// cleared in shared memory before the product.  Against its own later and older rows, an output that
+// comes out infinite or NaN is computed again by its warp, key by key over the visible ones (slow_row);
+// nothing else pays for it.  Measured: 16,300 tokens of a full layer with NaN behind them 0.63 ms (80 ms when
+// those rows were left to slow_row), with NaN in all of them 535 ms; 8 x 16,384 tokens of a window layer
+// 42 ms.  (Cleared by the weights' warps, or by the one that loads V, 4 to 20 % more on every call.)
 //
 // A block's sequence.  The host knows no lengths, so block numbers are spread with room to spare: sequence
 // b owns the numbers from floor(cu_q[b] / R) + b (R tokens to a block), which is enough for its blocks,
@@ -78,6 +81,7 @@ struct Block {
   int32_t k0;     // first key row of tile 0
   int32_t p0;     // the first token's newest key, less k0
   int32_t seq0;   // the sequence's first key, less k0
+  int32_t seqn;   // its last key, less k0
   int32_t tile0;  // tiles of the blocks before
 };
 
@@ -88,6 +92,7 @@ struct Layout {
   static constexpr int kWarpPV = 2 + TEAMS * kTeamWarps, kWarpV = kWarpPV + 1;
   static constexpr int kRingK = N < 128 ? 4 : 2;  // K stages
   static constexpr int kQ = 2;                    // blocks whose query rows are there
+  static_assert(kQ % TEAMS == 0, "a team's blocks have the same places");
   static constexpr int kColO = kRing * N;  // TEAMS times 128 columns
   static_assert(kColO + TEAMS * 128 <= kTmemCols, "tensor memory");
   static constexpr int kBoxKV = N * 128;  // [N rows][64 bf16]
@@ -103,6 +108,26 @@ struct Layout {
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) { return mbar_wait_long(bar, parity, kLimitNs); }
+
+// A place in a ring of R barriers and the parity of its phase.
+template <int R>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == R) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+  __device__ __forceinline__ Ring before() const { return at > 0 ? Ring{at - 1, phase} : Ring{R - 1, phase ^ 1u}; }
+};
+// The place before was completed (at once where there was none).
+template <int R>
+__device__ __forceinline__ bool wait_before(uint64_t *bars, Ring<R> r) {
+  const Ring<R> b = r.before();
+  return mbar_wait_long(&bars[b.at], b.phase, kLimitNs);
+}
 
 __device__ __forceinline__ void set_abort(volatile int *abort_flag, uint32_t *flags) {
   *abort_flag = 1;
@@ -179,13 +204,15 @@ struct BlockFinder {
       r.tiles = last < 0 ? 0 : (k_lo + last - r.k0) / N + 1;
       r.p0 = k_lo + newest - r.k0;
       r.seq0 = k_lo - r.k0;
+      r.seqn = k_hi - 1 - r.k0;
       return r;
     }
   }
 };
 
-// Row r of a block (token r / G, head r % G) computed key by key by one warp.  In two passes, so that no partial sum is larger than the result needs:
-// maximum and sum (ReLU^2: the sum), then the values by their normalised weights.
+// Row r of a block (token r / G, head r % G) computed key by key by one warp.  In two passes, so that no
+// partial sum is larger than the result needs: maximum and sum (ReLU^2: the sum), then the values by their
+// normalised weights.
 template <int MODE, int G>
 __device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block &b, int r, int lane) {
   const int i = r / G, h = b.g * G + r % G;
@@ -395,43 +422,48 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     }
     BlockFinder<MODE, N, G> finder(p, cta, P);
     Block b = finder.next(p, lane);
-    int g = 0;
+    Ring<kBlocksAhead> d;
+    Ring<L::kQ> q;
+    Ring<kRingK> r;
+    int issued = 0;
     bool ok = true;
     for (int k = 0, ends = 0; ok && ends < TEAMS; ++k) {  // (each team is told of the end)
-      const int s = k % L::kQ, d = k % kBlocksAhead;
-      b.tile0 = g;
+      // (a barrier's first wait, for the phase before its first, ends at once)
       if (lane == 0) {
-        ok = k < kBlocksAhead || wait_bar(&bempty[d], ((k / kBlocksAhead) - 1) & 1);
+        b.tile0 = issued;
+        ok = wait_bar(&bempty[d.at], d.phase ^ 1u);
         if (ok) {
-          sBlock[d] = b;
-          mbar_arrive(&bfull[d]);
+          sBlock[d.at] = b;
+          mbar_arrive(&bfull[d.at]);
         }
         // (blocks without tiles take their turn with the query rows, but load none)
-        if (ok && b.tiles >= 0) ok = k < L::kQ || wait_bar(&qempty[s], ((k / L::kQ) - 1) & 1);
+        if (ok && b.tiles >= 0) ok = wait_bar(&qempty[q.at], q.phase ^ 1u);
         if (ok && b.tiles >= 0) {
           if (b.tiles > 0) {
-            uint8_t *to = sQ + s * 2 * kBoxQ;
-            mbar_arrive_expect_tx(&qfull[s], 2 * kBoxQ);
-            tma_load_4d(to, &tm_q, &qfull[s], 0, 0, b.g, b.q0);
-            tma_load_4d(to + kBoxQ, &tm_q, &qfull[s], 64, 0, b.g, b.q0);
+            uint8_t *to = sQ + q.at * 2 * kBoxQ;
+            mbar_arrive_expect_tx(&qfull[q.at], 2 * kBoxQ);
+            tma_load_4d(to, &tm_q, &qfull[q.at], 0, 0, b.g, b.q0);
+            tma_load_4d(to + kBoxQ, &tm_q, &qfull[q.at], 64, 0, b.g, b.q0);
           } else {
-            mbar_arrive(&qfull[s]);
+            mbar_arrive(&qfull[q.at]);
           }
           s_issued[2] = k + 1;
-          for (int t = 0; t < b.tiles; ++t, ++g) {
-            const int r = g % kRingK;
-            ok = g < kRingK || wait_bar(&kempty[r], ((g / kRingK) - 1) & 1);
+          for (int t = 0, row = b.k0; t < b.tiles; ++t, row += N) {
+            ok = wait_bar(&kempty[r.at], r.phase ^ 1u);
             if (!ok) break;
-            mbar_arrive_expect_tx(&kfull[r], L::kStage);
-            tma_load_3d(sK + r * L::kStage, &tm_k, &kfull[r], 0, b.g, b.k0 + t * N);
-            tma_load_3d(sK + r * L::kStage + L::kBoxKV, &tm_k, &kfull[r], 64, b.g, b.k0 + t * N);
-            s_issued[0] = g + 1;
+            uint8_t *to = sK + r.at * L::kStage;
+            mbar_arrive_expect_tx(&kfull[r.at], L::kStage);
+            tma_load_3d(to, &tm_k, &kfull[r.at], 0, b.g, row);
+            tma_load_3d(to + L::kBoxKV, &tm_k, &kfull[r.at], 64, b.g, row);
+            s_issued[0] = ++issued;
+            r.next();
           }
         }
         if (!ok) set_abort(s_abort, p.flags);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      g = __shfl_sync(0xffffffffu, g, 0);
+      d.next();
+      q.next();
       if (b.tiles < 0)
         ++ends;
       else
@@ -442,112 +474,145 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       if (bad_sequence(p, p.cu_q[b], p.cu_q[b + 1], p.cu_k[b], p.cu_k[b + 1])) atomicOr(p.flags, kFlagIndexRange);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S issuer
-    if (lane == 0) {
-      const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
-      const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
-      int g = 0, blocks = 0, mine[TEAMS] = {};  // tiles, blocks, tiles of each team
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int s = k % TEAMS, d = k % kBlocksAhead;
-        ok = !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1);
+    // (the warp walks its loop together and one lane issues: descriptors stay in uniform registers)
+    const uint64_t qdesc = smem_desc_sw128(smem_u32(sQ));
+    const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
+    Ring<kBlocksAhead> d;
+    Ring<L::kQ> q;
+    Ring<kRing> sb, mine[TEAMS];  // mine: the tiles of the team whose turn it is, then the other's
+    Ring<kRingK> kb;
+    bool ok = true;
+    while (ok) {
+      ok = !*s_abort && wait_bar(&bfull[d.at], d.phase);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int tiles = sBlock[d.at].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bempty[d.at]);
+      d.next();
+      if (tiles < 0) break;
+      ok = __all_sync(0xffffffffu, wait_bar(&qfull[q.at], q.phase));
+      const int s = TEAMS > 1 ? q.at % TEAMS : 0;
+      for (int t = 0; ok && t < tiles; ++t) {
+        ok = wait_bar(&kfull[kb.at], kb.phase) && wait_bar(&pvdone[sb.at], sb.phase ^ 1u);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int tiles = sBlock[d].tiles;
-        mbar_arrive(&bempty[d]);
-        if (tiles < 0) break;
-        const int q = k % L::kQ;
-        ok = wait_bar(&qfull[q], (k / L::kQ) & 1);
-        int u = TEAMS > 1 && s ? mine[TEAMS - 1] : mine[0];
-        for (int t = 0; ok && t < tiles; ++t, ++g, ++u) {
-          const int sb = g % kRing, kb = g % kRingK;
-          ok = wait_bar(&kfull[kb], (g / kRingK) & 1) &&
-               (g < kRing || wait_bar(&pvdone[sb], ((g / kRing) - 1) & 1));
-          if (!ok) break;
-          tc_fence_after_sync();
+        tc_fence_after_sync();
+        if (elect_one()) {
+          const uint64_t qd = qdesc + static_cast<uint64_t>(q.at * (2 * kBoxQ >> 4));
+          const uint64_t kd = kdesc + static_cast<uint64_t>(kb.at * (L::kStage >> 4));
+          const uint32_t to = tmem + sb.at * N;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
+          for (int kk = 0; kk < 8; ++kk)
             // dims 16kk .. 16kk + 15: 32 bytes into a 128-byte row; dims 64.. start the second box
-            const uint64_t qo = static_cast<uint64_t>(((2 * q + (kk >> 2)) * kBoxQ + (kk & 3) * 32) >> 4);
-            const uint64_t ko = static_cast<uint64_t>((kb * L::kStage + (kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4);
-            tc_mma_bf16(tmem + sb * N, qdesc + qo, kdesc + ko, kIdescS, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&sfull[s * kRing + u % kRing]);
-          tc_commit(&kempty[kb]);
+            tc_mma_bf16(to, qd + (((kk >> 2) * kBoxQ + (kk & 3) * 32) >> 4),
+                        kd + (((kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
+          tc_commit(&sfull[s * kRing + mine[0].at]);
+          tc_commit(&kempty[kb.at]);
+          if (t + 1 == tiles) tc_commit(&qempty[q.at]);
         }
-        (TEAMS > 1 && s ? mine[TEAMS - 1] : mine[0]) = u;
-        if (ok) {
-          tc_commit(&qempty[q]);
-          blocks = k + 1;
-        }
+        __syncwarp();
+        sb.next();
+        kb.next();
+        mine[0].next();
       }
-      if (!ok) set_abort(s_abort, p.flags);
-      // every MMA of this thread has completed, and its last commits arrived, before the tensor
-      // memory is released and the CTA leaves (also when another role has given up)
-      for (int i = 0; i < TEAMS; ++i)
-        if (mine[i] > 0) wait_bar(&sfull[i * kRing + (mine[i] - 1) % kRing], ((mine[i] - 1) / kRing) & 1);
-      if (g > 0) wait_bar(&kempty[(g - 1) % kRingK], ((g - 1) / kRingK) & 1);
-      for (int k = blocks - 1; k >= 0 && k >= blocks - L::kQ; --k) wait_bar(&qempty[k % L::kQ], (k / L::kQ) & 1);
+      if (ok && tiles == 0 && lane == 0) mbar_arrive(&qempty[q.at]);
+      if (ok) q.next();
+      if (TEAMS > 1 && ok) {
+        const Ring<kRing> m = mine[0];
+        mine[0] = mine[TEAMS - 1];
+        mine[TEAMS - 1] = m;
+      }
     }
+    if (!ok && lane == 0) set_abort(s_abort, p.flags);
+    // every MMA of this warp has completed, and its last commits arrived, before the tensor memory is
+    // released and the CTA leaves (also when another role has given up)
+    const int s = TEAMS > 1 ? q.at % TEAMS : 0;  // the team of mine[0]
+    wait_before(sfull + s * kRing, mine[0]);
+    if (TEAMS > 1) wait_before(sfull + (s ^ 1) * kRing, mine[TEAMS - 1]);
+    wait_before(kempty, kb);
+    wait_before(qempty, q);
+    wait_before(qempty, q.before());
     __syncwarp();
   } else if (warp == L::kWarpPV) {
     // ------------------------------------------------------------------ P V issuer
-    if (lane == 0) {
-      int g = 0, blocks = 0;
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int s = k % TEAMS, d = k % kBlocksAhead;
-        ok = !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1);
+    const uint64_t vdesc = smem_desc_sw128_mn(smem_u32(sV), L::kBoxKV);
+    Ring<kBlocksAhead> d;
+    Ring<TEAMS> o;
+    Ring<kRing> pb;
+    bool ok = true;
+    while (ok) {
+      ok = !*s_abort && wait_bar(&bfull[d.at], d.phase);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int tiles = sBlock[d.at].tiles, seq0 = sBlock[d.at].seq0, seqn = sBlock[d.at].seqn;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bempty[d.at]);
+      d.next();
+      if (tiles < 0) break;
+      // the O of the team's block before has been read
+      ok = __all_sync(0xffffffffu, wait_bar(&ofree[o.at], o.phase ^ 1u));
+      for (int t = 0; ok && t < tiles; ++t) {
+        ok = __all_sync(0xffffffffu, wait_bar(&vfull[pb.at], pb.phase));
         if (!ok) break;
-        const int tiles = sBlock[d].tiles;
-        mbar_arrive(&bempty[d]);
-        if (tiles < 0) break;
-        // the O of the team's block before has been read
-        ok = k < TEAMS || wait_bar(&ofree[s], ((k / TEAMS) - 1) & 1);
-        const uint32_t o = tmem + L::kColO + s * 128;
-        for (int t = 0; ok && t < tiles; ++t, ++g) {
-          const int pb = g % kRing;
-          ok = wait_bar(&pfull[pb], (g / kRing) & 1) && wait_bar(&vfull[pb], (g / kRing) & 1);
-          if (!ok) break;
-          tc_fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < N / 16; ++kk) {
-            // keys 16kk .. 16kk + 15: eight columns of P, V rows 16kk .. (2 KB apart)
-            const uint64_t vd = smem_desc_sw128_mn(smem_u32(sV + pb * L::kStage + kk * 2048), L::kBoxKV);
-            tc_mma_bf16_tmem_a(o, tmem + pb * N + 8 * kk, vd, kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
+        if (t * N < seq0 || t * N + N - 1 > seqn) {  // value rows of other sequences, or behind the last
+          uint8_t *v = sV + pb.at * L::kStage;
+          for (int x = lane; x < 16 * N; x += 32) {
+            const int j = t * N + (x >> 3) % N;  // (a row's 128 bytes of a box stay together)
+            if (j < seq0 || j > seqn) *reinterpret_cast<uint4 *>(v + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
           }
-          tc_commit(&pvdone[pb]);
+          fence_proxy_async_smem();  // read by the tensor cores
+          __syncwarp();
         }
-        if (ok) {
-          tc_commit(&ofull[s]);
-          blocks = k + 1;
+        ok = __all_sync(0xffffffffu, wait_bar(&pfull[pb.at], pb.phase));
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          const uint64_t vd = vdesc + static_cast<uint64_t>(pb.at * (L::kStage >> 4));
+          const uint32_t to = tmem + L::kColO + o.at * 128, from = tmem + pb.at * N;
+#pragma unroll
+          for (int kk = 0; kk < N / 16; ++kk)
+            // keys 16kk .. 16kk + 15: eight columns of P, V rows 16kk .. (2 KB apart)
+            tc_mma_bf16_tmem_a(to, from + 8 * kk, vd + (kk * 2048 >> 4), kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(&pvdone[pb.at]);
+          if (t + 1 == tiles) tc_commit(&ofull[o.at]);
         }
+        __syncwarp();
+        pb.next();
       }
-      if (!ok) set_abort(s_abort, p.flags);
-      // every MMA of this thread has completed before the tensor memory is released
-      if (g > 0) wait_bar(&pvdone[(g - 1) % kRing], ((g - 1) / kRing) & 1);
-      for (int k = blocks - 1; k >= 0 && k >= blocks - TEAMS; --k) wait_bar(&ofull[k % TEAMS], (k / TEAMS) & 1);
+      if (ok && tiles == 0 && lane == 0) mbar_arrive(&ofull[o.at]);
+      if (ok) o.next();
     }
+    if (!ok && lane == 0) set_abort(s_abort, p.flags);
+    // every MMA of this warp has completed before the tensor memory is released
+    wait_before(pvdone, pb);
+    wait_before(ofull, o);
+    if (TEAMS > 1) wait_before(ofull, o.before());
     __syncwarp();
   } else if (warp == L::kWarpV) {
     // ------------------------------------------------------------------ V loads
     if (lane == 0) {
       tma_prefetch_desc(&tm_v);
-      int g = 0;
+      Ring<kBlocksAhead> d;
+      Ring<kRing> r;
+      int issued = 0;
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int d = k % kBlocksAhead;
-        ok = !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1);
+      while (ok) {
+        ok = !*s_abort && wait_bar(&bfull[d.at], d.phase);
         if (!ok) break;
-        const int tiles = sBlock[d].tiles, head = sBlock[d].g, k0 = sBlock[d].k0;
-        mbar_arrive(&bempty[d]);
+        const int tiles = sBlock[d.at].tiles, head = sBlock[d.at].g, k0 = sBlock[d.at].k0;
+        mbar_arrive(&bempty[d.at]);
+        d.next();
         if (tiles < 0) break;
-        for (int t = 0; t < tiles; ++t, ++g) {
-          const int r = g % kRing;
-          ok = g < kRing || wait_bar(&pvdone[r], ((g / kRing) - 1) & 1);
+        for (int t = 0, row = k0; t < tiles; ++t, row += N) {
+          ok = wait_bar(&pvdone[r.at], r.phase ^ 1u);
           if (!ok) break;
-          mbar_arrive_expect_tx(&vfull[r], L::kStage);
-          tma_load_3d(sV + r * L::kStage, &tm_v, &vfull[r], 0, head, k0 + t * N);
-          tma_load_3d(sV + r * L::kStage + L::kBoxKV, &tm_v, &vfull[r], 64, head, k0 + t * N);
-          s_issued[1] = g + 1;
+          uint8_t *to = sV + r.at * L::kStage;
+          mbar_arrive_expect_tx(&vfull[r.at], L::kStage);
+          tma_load_3d(to, &tm_v, &vfull[r.at], 0, head, row);
+          tma_load_3d(to + L::kBoxKV, &tm_v, &vfull[r.at], 64, head, row);
+          s_issued[1] = ++issued;
+          r.next();
         }
       }
       if (!ok) set_abort(s_abort, p.flags);
@@ -566,7 +631,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     const bool flip = MODE == kPackedSoftmax && p.tau2 < 0.0f;
     const float tau2 = fabsf(p.tau2);
     bool ok = true;
-    int u = 0;  // the team's tiles
+    Ring<kRing> mine;  // the team's tiles
     for (int k = team, n = 0; ok; k += TEAMS, ++n) {  // the team's n-th block
       // (every decision to go on is the warp's: what follows is warp-wide)
       const int d = k % kBlocksAhead;
@@ -575,6 +640,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       const Block b = sBlock[d];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bempty[d]);
+      Ring<kRing> tile{b.tile0 % kRing, static_cast<uint32_t>(b.tile0 / kRing) & 1u};
       if (b.tiles < 0) break;
       // a row sees the keys oldest .. oldest + span, relative to k0 (none: from far behind the last)
       int oldest[2];
@@ -603,14 +669,12 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           for (int j = 0; j < N / 8; ++j) rk[j] = *reinterpret_cast<const float2 *>(rkp + 8 * j);
         }
       }
-      for (int t = 0; t < b.tiles; ++t, ++u) {
-        const int g = b.tile0 + t;
-        const int sb = g % kRing;
+      for (int t = 0; t < b.tiles; ++t) {
         const int j0 = t * N;
-        ok = __all_sync(0xffffffffu, wait_bar(&sfull[team * kRing + u % kRing], (u / kRing) & 1));
+        ok = __all_sync(0xffffffffu, wait_bar(&sfull[team * kRing + mine.at], mine.phase));
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t cols = tmem + lanes16 + sb * N;
+        const uint32_t cols = tmem + lanes16 + tile.at * N;
         uint32_t acc[N / 2];
         load_scores<N>(cols, acc);
         uint32_t hi[N / 4];
@@ -656,7 +720,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           }
           if (t > 0 && __any_sync(0xffffffffu, grown)) {
             // O of these rows, once the products before this tile are done
-            ok = __all_sync(0xffffffffu, wait_bar(&pvdone[(g - 1) % kRing], ((g - 1) / kRing) & 1));
+            ok = __all_sync(0xffffffffu, wait_before(pvdone, tile));
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -721,7 +785,9 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
         tmem_wait_st();
         tc_fence_before_sync();  // P is read by the tensor cores
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[sb]);
+        if (lane == 0) mbar_arrive(&pfull[tile.at]);
+        mine.next();
+        tile.next();
       }
       if (!ok) break;
       // (late, so that it has the last products' time)
