@@ -107,7 +107,7 @@ struct Layout {
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
 };
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) { return mbar_wait_long(bar, parity, kLimitNs); }
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, kLimitNs); }
 
 // A place in a ring of R barriers and the parity of its phase.
 template <int R>
@@ -126,7 +126,7 @@ struct Ring {
 template <int R>
 __device__ __forceinline__ bool wait_before(uint64_t *bars, Ring<R> r) {
   const Ring<R> b = r.before();
-  return mbar_wait_long(&bars[b.at], b.phase, kLimitNs);
+  return mbar_wait(&bars[b.at], b.phase, kLimitNs);
 }
 
 __device__ __forceinline__ void set_abort(volatile int *abort_flag, uint32_t *flags) {

@@ -20,28 +20,6 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
-// mbar_wait whose polls let the hardware hold the thread for up to 20 us, so that a warp that waits long
-// leaves the issue slots to the others.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-  uint64_t t0 = 0;
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-    const uint64_t t = global_timer_ns();
-    if (t0 == 0)
-      t0 = t;
-    else if (t - t0 > limit_ns)
-      return false;
-  }
-}
-
 // End a group of this thread's cp.async copies; wait until all but the newest `left` groups have landed.
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int left>
