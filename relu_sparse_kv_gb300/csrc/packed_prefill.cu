@@ -43,12 +43,15 @@
 // and a number past them is skipped.  The owner is found by a 32-way search.
 //
 // What bounds it, and what was measured (16 query heads):
-//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 622 us, 1,765
-//     TFLOP/s of visible products (0.93 of the burst rate); softmax over all keys 1,490 (8,192 tokens), there
+//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 620 us, 1,770
+//     TFLOP/s of visible products (0.93 of the burst rate); softmax over all keys 1,480 (8,192 tokens), there
 //     the exponentials and the maximum add what the tensor cores cannot hide.
-//   - a window of 128 keys: memory.  8 x 16,384 tokens 246 us, 5.45 TB/s (0.80 of a copy's rate); a block is
+//   - a window of 128 keys: memory.  8 x 16,384 tokens 247 us, 5.43 TB/s (0.80 of a copy's rate); a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
 //     one team of eight warps on tiles of 128 took 480 us, two on tiles of 80 with a barrier per block 315.
+//     The issuers walk their loops as whole warps with places and phases counted on, so that a product's
+//     descriptor is two additions; every wait polls without a suspend hint (with one of 20 us: these 241, but
+//     18 ragged prompts of 6,200 tokens 20.6 against 19.4, a window of 1,024 218 against 215).
 //     With four warps of their own for the outputs beside one team 320 us (they take longer for a
 //     block than its weights do; the long prompt gained, 604 us).
 //   - short prompts: what a block costs beside its tiles, about 4,000 cycles.  Describing blocks earlier, a
@@ -948,8 +951,8 @@ cudaError_t launch_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_k, cons
 
 // A block of 128 / G tokens sees window + 128 / G - 1 keys at most.  Up to about a thousand, two teams on
 // tiles of 80 are faster than one on tiles of 128, which waits at each block's ends (2 x 16,384 tokens, 4 KV
-// heads, us: window 128 80 against 108, 256 91 and 130, 512 135 and 173, 1,024 248 and 247; 2 KV heads, 1,024
-// 226 and 242); for 2,048 keys 414 against 389.
+// heads, us: window 128 68 against 107, 256 87 and 127, 512 135 and 166, 1,024 244 and 240; 2 KV heads, 1,024
+// 217 and 239); for 2,048 keys 402 against 385.
 constexpr int64_t kShortSpan = 1100;
 int packed_tile_keys(int mode, int G, int64_t window) {
   return mode == kPackedSoftmax && window + 128 / G - 1 <= kShortSpan ? 80 : 128;
