@@ -411,7 +411,7 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  * shape->cache_stride are not used by these calls.  The lengths are read on the device: one captured
  * graph serves every batch that fits n_tokens and shape->batch.  Entries that do not ascend or lie outside
  * 0 .. n_tokens read and write nothing outside the arrays, but which rows then get an output is not
- * defined (the two attention calls report them, bit 0 of embla_device_check).  At most 2^30 tokens.
+ * defined (the two attention calls report them, bit 0 of embla_device_check).  At most 2^30 tokens and sequences.
  *
  * embla_rope_qkv — "Three kinds of attention" (Sliding window): queries and keys of the window
  * layers rotated at their positions, normed per head before if asked for, in one pass, and the rings

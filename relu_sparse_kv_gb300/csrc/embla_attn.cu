@@ -239,7 +239,7 @@ bool rows_in_cache(const embla_shape *s, int64_t pos, int64_t count) {
 bool token_stride_ok(int64_t stride, int32_t heads) {
   return stride >= static_cast<int64_t>(heads) * kHeadDim && stride % 8 == 0;
 }
-constexpr int64_t kMaxPackedTokens = static_cast<int64_t>(1) << 30;
+constexpr int64_t kMaxPackedTokens = static_cast<int64_t>(1) << 30;  // and sequences
 constexpr int64_t kMaxPackedStride = static_cast<int64_t>(1) << 38;  // TMA strides stay below 2^40 bytes
 
 embla_status cuda_status(cudaError_t e) { return e == cudaSuccess ? EMBLA_OK : EMBLA_ERR_CUDA; }
@@ -887,7 +887,8 @@ embla_status embla_rope_qkv(const embla_shape *shape, int64_t n_tokens, const in
       !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) || !aligned16(k_out) ||
       !aligned16(k_win) || !aligned16(v_win))
     return EMBLA_ERR_INVALID_ARG;
-  if (n_tokens > kMaxPackedTokens || n_tokens * shape->n_kv_heads > INT32_MAX) return EMBLA_ERR_UNSUPPORTED;
+  if (n_tokens > kMaxPackedTokens || shape->batch > kMaxPackedTokens || n_tokens * shape->n_kv_heads > INT32_MAX)
+    return EMBLA_ERR_UNSUPPORTED;
   if (q_stride > kMaxPackedStride || k_stride > kMaxPackedStride || (ring && v_stride > kMaxPackedStride))
     return EMBLA_ERR_UNSUPPORTED;
   RopeParams p = {};
@@ -935,7 +936,8 @@ embla_status packed_prefill_impl(int mode, const embla_shape *shape, int G, int6
   if (!aligned16(cu_tokens) || !aligned16(cu_keys) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
       !aligned16(out) || !aligned16(workspace))
     return EMBLA_ERR_INVALID_ARG;
-  if (n_tokens > kMaxPackedTokens || n_keys > kMaxPackedTokens || n_keys * shape->n_kv_heads > INT32_MAX)
+  if (n_tokens > kMaxPackedTokens || n_keys > kMaxPackedTokens || shape->batch > kMaxPackedTokens ||
+      n_keys * shape->n_kv_heads > INT32_MAX)
     return EMBLA_ERR_UNSUPPORTED;
   if (q_stride > kMaxPackedStride || (n_keys > 0 && (k_stride > kMaxPackedStride || v_stride > kMaxPackedStride)))
     return EMBLA_ERR_UNSUPPORTED;

@@ -40,18 +40,20 @@
 //
 // A block's sequence.  The host knows no lengths, so block numbers are spread with room to spare: sequence
 // b owns the numbers from floor(cu_q[b] / R) + b (R tokens to a block), which is enough for its blocks,
-// and a number past them is skipped.  The owner is found by a 32-way search.
+// and a number past them is skipped.  The owner is found by a 32-way search, whose first step needs no memory
+// (one of 32 sequences; reading each block's own took the warp that also loads Q and K 1,500 cycles more).
 //
 // What bounds it, and what was measured (16 query heads):
 //   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 620 us, 1,770
 //     TFLOP/s of visible products (0.93 of the burst rate); softmax over all keys 1,480 (8,192 tokens), there
 //     the exponentials and the maximum add what the tensor cores cannot hide.
-//   - a window of 128 keys: memory.  8 x 16,384 tokens 247 us, 5.43 TB/s (0.80 of a copy's rate); a block is
+//   - a window of 128 keys: memory.  8 x 16,384 tokens 237 us, 5.66 TB/s (0.83 of a copy's rate); a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
 //     one team of eight warps on tiles of 128 took 480 us, two on tiles of 80 with a barrier per block 315.
 //     The issuers walk their loops as whole warps with places and phases counted on, so that a product's
-//     descriptor is two additions; every wait polls without a suspend hint (with one of 20 us: these 241, but
-//     18 ragged prompts of 6,200 tokens 20.6 against 19.4, a window of 1,024 218 against 215).
+//     descriptor is two additions (one lane of each, with divisions: 247); every wait polls without a
+//     suspend hint (with one of 20 us 8 ragged prompts of 6,164 tokens took 20.6 against 19.4, a window of
+//     1,024 218 against 215).
 //     With four warps of their own for the outputs beside one team 320 us (they take longer for a
 //     block than its weights do; the long prompt gained, 604 us).
 //   - short prompts: what a block costs beside its tiles, about 4,000 cycles.  Describing blocks earlier, a
@@ -149,26 +151,42 @@ struct BlockFinder {
   static constexpr int R = 128 / G;
   uint32_t at, step, numbers;  // this CTA's place in the next round of numbers, and numbers per KV head
   bool draw = false;
+  // The first step of the search, kept in registers: the first number past lane's group of sequences; and
+  // where a group is one sequence, its queries and keys.
+  int past = INT32_MAX;
+  int seq_q0 = 0, seq_q1 = 0, seq_k0 = 0, seq_k1 = 0;
   // the sequence found last: its block numbers, queries and keys
   int first = 0, end = 0, q_lo = 0, q_hi = 0, k_lo = 0, k_hi = 0;
-  __device__ BlockFinder(const PackedPrefillParams &p, uint32_t cta, uint32_t ctas)
-      : at(cta), step(ctas), numbers(static_cast<uint32_t>(p.blocks) / static_cast<uint32_t>(p.Hkv)) {}
+  __device__ BlockFinder(const PackedPrefillParams &p, uint32_t cta, uint32_t ctas, int lane)
+      : at(cta), step(ctas), numbers(static_cast<uint32_t>(p.blocks) / static_cast<uint32_t>(p.Hkv)) {
+    const int w = (p.batch + 31) / 32, i = (lane + 1) * w;
+    if (i <= p.batch) past = p.cu_q[i] / R + i;
+    if (p.batch <= 32 && lane < p.batch) {
+      seq_q0 = p.cu_q[lane], seq_q1 = p.cu_q[lane + 1];
+      seq_k0 = p.cu_k[lane], seq_k1 = p.cu_k[lane + 1];
+    }
+  }
 
   // The sequence that owns block number v becomes the one found last; false where there is none.
   __device__ __forceinline__ bool find(const PackedPrefillParams &p, int v, int lane) {
     if (v >= first && v < end) return true;
-    int lo = 0, hi = p.batch;  // sequences whose successor's numbers begin at or before v
+    // sequences whose successor's numbers begin at or before v
+    int w = (p.batch + 31) / 32;
+    int lo = __popc(__ballot_sync(0xffffffffu, past <= v)) * w, hi = min(p.batch, lo + w - 1);
     while (hi > lo) {
-      const int w = (hi - lo + 31) / 32;
+      w = (hi - lo + 31) / 32;
       const int i = lo + (lane + 1) * w;
-      const bool past = i <= hi && p.cu_q[i] / R + i <= v;
-      const int n = __popc(__ballot_sync(0xffffffffu, past));
-      const int from = lo + n * w;
-      hi = min(hi, from + w - 1);
-      lo = from;
+      const int n = __popc(__ballot_sync(0xffffffffu, i <= hi && p.cu_q[i] / R + i <= v));
+      lo += n * w;
+      hi = min(hi, lo + w - 1);
     }
     if (lo >= p.batch) return false;
-    q_lo = p.cu_q[lo], q_hi = p.cu_q[lo + 1], k_lo = p.cu_k[lo], k_hi = p.cu_k[lo + 1];
+    if (p.batch <= 32) {
+      q_lo = __shfl_sync(0xffffffffu, seq_q0, lo), q_hi = __shfl_sync(0xffffffffu, seq_q1, lo);
+      k_lo = __shfl_sync(0xffffffffu, seq_k0, lo), k_hi = __shfl_sync(0xffffffffu, seq_k1, lo);
+    } else {
+      q_lo = p.cu_q[lo], q_hi = p.cu_q[lo + 1], k_lo = p.cu_k[lo], k_hi = p.cu_k[lo + 1];
+    }
     first = end = q_lo / R + lo;
     if (bad_sequence(p, q_lo, q_hi, k_lo, k_hi)) return false;
     end = first + (q_hi - q_lo + R - 1) / R;
@@ -423,7 +441,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
     }
-    BlockFinder<MODE, N, G> finder(p, cta, P);
+    BlockFinder<MODE, N, G> finder(p, cta, P, lane);
     Block b = finder.next(p, lane);
     Ring<kBlocksAhead> d;
     Ring<L::kQ> q;
@@ -432,46 +450,51 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     bool ok = true;
     for (int k = 0, ends = 0; ok && ends < TEAMS; ++k) {  // (each team is told of the end)
       // (a barrier's first wait, for the phase before its first, ends at once)
+      b.tile0 = issued;
+      ok = __all_sync(0xffffffffu, wait_bar(&bempty[d.at], d.phase ^ 1u));
+      if (!ok) break;
       if (lane == 0) {
-        b.tile0 = issued;
-        ok = wait_bar(&bempty[d.at], d.phase ^ 1u);
-        if (ok) {
-          sBlock[d.at] = b;
-          mbar_arrive(&bfull[d.at]);
-        }
-        // (blocks without tiles take their turn with the query rows, but load none)
-        if (ok && b.tiles >= 0) ok = wait_bar(&qempty[q.at], q.phase ^ 1u);
-        if (ok && b.tiles >= 0) {
-          if (b.tiles > 0) {
-            uint8_t *to = sQ + q.at * 2 * kBoxQ;
-            mbar_arrive_expect_tx(&qfull[q.at], 2 * kBoxQ);
-            tma_load_4d(to, &tm_q, &qfull[q.at], 0, 0, b.g, b.q0);
-            tma_load_4d(to + kBoxQ, &tm_q, &qfull[q.at], 64, 0, b.g, b.q0);
-          } else {
-            mbar_arrive(&qfull[q.at]);
-          }
-          s_issued[2] = k + 1;
-          for (int t = 0, row = b.k0; t < b.tiles; ++t, row += N) {
-            ok = wait_bar(&kempty[r.at], r.phase ^ 1u);
-            if (!ok) break;
-            uint8_t *to = sK + r.at * L::kStage;
-            mbar_arrive_expect_tx(&kfull[r.at], L::kStage);
-            tma_load_3d(to, &tm_k, &kfull[r.at], 0, b.g, row);
-            tma_load_3d(to + L::kBoxKV, &tm_k, &kfull[r.at], 64, b.g, row);
-            s_issued[0] = ++issued;
-            r.next();
-          }
-        }
-        if (!ok) set_abort(s_abort, p.flags);
+        sBlock[d.at] = b;
+        mbar_arrive(&bfull[d.at]);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       d.next();
-      q.next();
-      if (b.tiles < 0)
+      if (b.tiles < 0) {
         ++ends;
-      else
-        b = finder.next(p, lane);
+        continue;
+      }
+      // (blocks without tiles take their turn with the query rows, but load none)
+      ok = __all_sync(0xffffffffu, wait_bar(&qempty[q.at], q.phase ^ 1u));
+      if (!ok) break;
+      if (elect_one()) {
+        if (b.tiles > 0) {
+          uint8_t *to = sQ + q.at * 2 * kBoxQ;
+          mbar_arrive_expect_tx(&qfull[q.at], 2 * kBoxQ);
+          tma_load_4d(to, &tm_q, &qfull[q.at], 0, 0, b.g, b.q0);
+          tma_load_4d(to + kBoxQ, &tm_q, &qfull[q.at], 64, 0, b.g, b.q0);
+        } else {
+          mbar_arrive(&qfull[q.at]);
+        }
+        s_issued[2] = k + 1;
+      }
+      __syncwarp();
+      q.next();
+      for (int t = 0, row = b.k0; t < b.tiles; ++t, row += N) {
+        ok = __all_sync(0xffffffffu, wait_bar(&kempty[r.at], r.phase ^ 1u));
+        if (!ok) break;
+        ++issued;
+        if (elect_one()) {
+          uint8_t *to = sK + r.at * L::kStage;
+          mbar_arrive_expect_tx(&kfull[r.at], L::kStage);
+          tma_load_3d(to, &tm_k, &kfull[r.at], 0, b.g, row);
+          tma_load_3d(to + L::kBoxKV, &tm_k, &kfull[r.at], 64, b.g, row);
+          s_issued[0] = issued;
+        }
+        __syncwarp();
+        r.next();
+      }
+      if (ok) b = finder.next(p, lane);
     }
+    if (!ok && lane == 0) set_abort(s_abort, p.flags);
     // entries that no block could use are reported
     for (int64_t b = static_cast<int64_t>(cta) * 32 + lane; b < p.batch; b += static_cast<int64_t>(P) * 32)
       if (bad_sequence(p, p.cu_q[b], p.cu_q[b + 1], p.cu_k[b], p.cu_k[b + 1])) atomicOr(p.flags, kFlagIndexRange);

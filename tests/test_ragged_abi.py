@@ -122,6 +122,13 @@ def test_window_decode_ragged_refusals(lib, kw, status):
     assert _decode(lib, **kw) == status
 
 
+def test_packed_calls_refuse_more_than_a_billion_sequences(lib):
+    """(the searches' steps stay below 2^31)"""
+    many = dict(batch=(1 << 30) + 1, n_q_heads=4, n_kv_heads=1)
+    for call in (_rope, _window, _packed):
+        assert call(lib, shape=_shape(**many)) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("R", [16, 32])
 def test_block_numbers_cover_every_token_once(R):
     """Sequence b owns the numbers from floor(cu[b] / R) + b: every token of every sequence lies in exactly
