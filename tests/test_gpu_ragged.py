@@ -231,6 +231,36 @@ def test_infinite_and_nan_rows_stay_where_they_are_seen(kind):
     assert not torch.isfinite(out[at[1] + 71]).all()  # and those that see it show it
 
 
+@pytest.mark.parametrize("kind", ["window", "packed"])
+@pytest.mark.parametrize("Hkv,G", [(4, 4), (2, 8)])
+@pytest.mark.parametrize("before,n", [(0, 1), (1, 79), (2, 80), (3, 81), (130, 127), (5, 128), (7, 129), (38, 400)])
+def test_a_sequence_among_nan_rows(kind, Hkv, G, before, n):
+    """Every row of k and v but one sequence's is NaN or infinite, those behind the last sequence too."""
+    lens = [before, n, 50]
+    q, k, v, out = _attention_inputs(23 + n, lens, None, Hkv, G, 40, 1.0)
+    for x, bad in ((k, math.nan), (v, math.inf)):
+        x[:before] = bad
+        x[before + n:] = -bad
+    _run_window(lens, None, Hkv, q, k, v, out, 100) if kind == "window" else _run_packed(lens, None, Hkv, q, k, v, out)
+    _checked()
+    own = slice(before, before + n)
+    form = R.window_prefill(q[own], k[own], v[own], [0, n], [0, n], 100, D ** -0.5) if kind == "window" else \
+        R.prefill_packed(q[own], k[own], v[own], [0, n], [0, n], 1.0, 1.0, 1e-6)
+    R.assert_within(out[own], *form, "the sequence between")
+    assert (out[before + n + 50:] == 7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["window", "packed"])
+def test_queries_without_any_key(kind):
+    lens, Hkv = [3, 0, 40], 4
+    q, k, v, out = _attention_inputs(24, lens, [0, 0, 0], Hkv, 4, 0, 1.0)
+    assert k.shape[0] == 0
+    _run_window(lens, [0, 0, 0], Hkv, q, k, v, out, 100) if kind == "window" else \
+        _run_packed(lens, [0, 0, 0], Hkv, q, k, v, out)
+    _checked()
+    assert (out == 0.0).all()
+
+
 def test_zero_weight_keys_hide_their_values():
     """ReLU^2: a key whose score is not positive, or NaN, weighs nothing even where its value is NaN."""
     n, Hkv = 200, 4
