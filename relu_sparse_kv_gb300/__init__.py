@@ -29,6 +29,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import cached_property
 
 import torch
 
@@ -63,6 +64,10 @@ class Shape:
     cache_stride: int
 
     def c(self) -> _Shape:
+        return self._c
+
+    @cached_property
+    def _c(self) -> _Shape:  # (a shape does not change, and a loop calls with the same one)
         return _Shape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.ctx_len,
                       self.cache_stride)
 
@@ -676,11 +681,13 @@ def _packed_rows(t, heads: int, D: int, name: str) -> tuple[int, int, int]:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.is_contiguous():
-        return T, heads * D, dev
     step, head, dim = t.stride()
+    if T > 1 and head == D and dim == 1 and step >= heads * D:  # (most calls)
+        return T, step, dev
     if T > 1 and step < heads * D or heads > 1 and head != D or dim != 1:
-        raise ValueError(f"{name}: heads and dims must be dense, tokens apart")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: heads and dims must be dense, tokens apart")
+        step = heads * D
     return T, step if T > 1 else heads * D, dev
 
 
@@ -718,14 +725,13 @@ def embla_rope_qkv(shape: Shape, cu_tokens, pos0, q, k, v, q_out, k_out, rope_ba
     Tk, k_step, dev_k = _packed_rows(k, Hkv, D, "k")
     if Tk != T:
         raise ValueError("q and k must have the same tokens")
-    _same_device(dev, dev_k)
     cu = _beside(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens")
     to_q = _beside(q_out, torch.bfloat16, (T, Hq, D), dev, "q_out")
     to_k = None if k_out is None else _beside(k_out, torch.bfloat16, (T, Hkv, D), dev, "k_out")
     first = None if pos0 is None else _beside(pos0, torch.int32, (B,), dev, "pos0")
     qg = None if q_gain is None else _beside(q_gain, torch.float32, (D,), dev, "q_gain")
     kg = None if k_gain is None else _beside(k_gain, torch.float32, (D,), dev, "k_gain")
-    window, at_v, v_step, ring_k, ring_v = 0, None, Hkv * D, None, None
+    window, at_v, v_step, dev_v, ring_k, ring_v = 0, None, Hkv * D, dev, None, None
     if k_win is not None or v_win is not None:
         if k_win is None or k_win.dim() != 4 or k_win.shape[2] < 1:
             raise ValueError("k_win must be [B, Hkv, window, D], window >= 1")
@@ -736,8 +742,8 @@ def embla_rope_qkv(shape: Shape, cu_tokens, pos0, q, k, v, q_out, k_out, rope_ba
         Tv, v_step, dev_v = _packed_rows(v, Hkv, D, "v")
         if Tv != T:
             raise ValueError("q and v must have the same tokens")
-        _same_device(dev, dev_v)
         at_v = v.data_ptr()
+    _same_device(dev, dev_k, dev_v)
     _status("embla_rope_qkv", library().embla_rope_qkv(
         ctypes.byref(shape.c()), T, cu, first, q.data_ptr(), q_step, k.data_ptr(), k_step, at_v, v_step, rope_base,
         norm_eps is not None, norm_eps or 0.0, qg, kg, to_q, to_k, window, ring_k, ring_v, _stream(stream, dev)))
