@@ -15,12 +15,14 @@
 //   warp 0     finds each block's sequence (below), hands the block's description to the others and
 //              loads by TMA the 128 query rows (two blocks' worth fit) and the tiles' K rows.
 //   warp 1     tcgen05 issuer of S = Q K^T (M 128 rows x N keys) into one of three tensor-memory
-//              buffers; S of tile t takes the buffer of tile t - 3 once its P V is done.
+//              buffers, S of tile t into that of tile t - 3 once its P V is done; full layers: of two
+//              buffers, once tile t - 2's is read.
 //   warps 2..  one team or two of eight warps: the weights.  A warp takes 16 rows, a row lies in the four
 //              lanes of a quad (the fragment layout of 16x256b loads), so a row's maximum is two
 //              shuffles and no other warp's business, and P, packed in pairs, goes back in 16x128b stores
-//              to the columns of its own rows.  At the end of a block they divide O and store it.
-//   then       the tcgen05 issuer of O += P V, P from tensor memory (over its S), V as it lies;
+//              over its S; full layers: into one of two buffers of its own.  At the end of a block they
+//              divide O and store it.
+//   then       the tcgen05 issuer of O += P V, P from tensor memory, V as it lies;
 //   and last   the loads of the tiles' V rows.
 //
 // Softmax.  With z = tau log2(e) s, P = exp2(z - m) for a running reference m per row and l = sum P.
@@ -44,16 +46,17 @@
 // (one of 32 sequences; reading each block's own took the warp that also loads Q and K 1,500 cycles more).
 //
 // What bounds it, and what was measured (16 query heads):
-//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 620 us, 1,770
-//     TFLOP/s of visible products (0.93 of the burst rate); softmax over all keys 1,480 (8,192 tokens), there
+//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 589 us, 1,870
+//     TFLOP/s of visible products (0.98 of the burst rate); softmax over all keys 1,480 (8,192 tokens), there
 //     the exponentials and the maximum add what the tensor cores cannot hide.
-//   - a window of 128 keys: memory.  8 x 16,384 tokens 237 us, 5.66 TB/s (0.83 of a copy's rate); a block is
+//   - a window of 128 keys: memory.  8 x 16,384 tokens 220 us, 6.09 TB/s (0.90 of a copy's rate); a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
 //     one team of eight warps on tiles of 128 took 480 us, two on tiles of 80 with a barrier per block 315.
 //     The issuers walk their loops as whole warps with places and phases counted on, so that a product's
 //     descriptor is two additions (one lane of each, with divisions: 247); every wait polls without a
 //     suspend hint (with one of 20 us 8 ragged prompts of 6,164 tokens took 20.6 against 19.4, a window of
-//     1,024 218 against 215).
+//     1,024 218 against 215).  What a block's end needs of its description is read then (in registers all
+//     along, the weights spilled: 237).
 //     With four warps of their own for the outputs beside one team 320 us (they take longer for a
 //     block than its weights do; the long prompt gained, 604 us).
 //   - short prompts: what a block costs beside its tiles, about 4,000 cycles.  Describing blocks earlier, a
@@ -68,7 +71,7 @@ namespace embla {
 namespace {
 
 constexpr int kTeamWarps = 8;      // warps that turn a block's scores into weights
-constexpr int kRing = 3;           // V stages and S/P buffers
+constexpr int kRing = 3;           // V stages
 constexpr int kBoxQ = 128 * 128;   // [128 rows][64 bf16]
 constexpr float kSlack = 8.0f;     // P stays below 2^kSlack
 constexpr uint64_t kLimitNs = 10000000000ull;  // 10 s: a row computed key by key holds the others up
@@ -90,15 +93,21 @@ struct Block {
   int32_t tile0;  // tiles of the blocks before
 };
 
-// TEAMS sets of kTeamWarps warps take blocks in turn; each has an O of its own.
-template <int N, int TEAMS>
+// TEAMS sets of kTeamWarps warps take blocks in turn; each has an O of its own.  P is written over its S, and
+// three such buffers go round.  For ReLU^2 it has two buffers apart, and S two that are free once they are
+// read: the tensor cores wait less for a tile's weights (16,384 tokens 622 us over S, 589 apart), but a weights
+// warp waits for P's buffer, which softmax, the longer work, does not gain from (window 128 220 over, 245 apart).
+template <int MODE, int N, int TEAMS>
 struct Layout {
+  static constexpr bool kApart = MODE == kPackedRelu2;
+  static constexpr int kBuffers = kApart ? 2 : kRing;
   static constexpr int kThreads = (4 + TEAMS * kTeamWarps) * 32;
   static constexpr int kWarpPV = 2 + TEAMS * kTeamWarps, kWarpV = kWarpPV + 1;
   static constexpr int kRingK = N < 128 ? 4 : 2;  // K stages
   static constexpr int kQ = 2;                    // blocks whose query rows are there
   static_assert(kQ % TEAMS == 0, "a team's blocks have the same places");
-  static constexpr int kColO = kRing * N;  // TEAMS times 128 columns
+  static constexpr int kColP = kApart ? kBuffers * N : 0, kStepP = kApart ? N / 2 : N;  // columns
+  static constexpr int kColO = 3 * N;  // TEAMS times 128
   static_assert(kColO + TEAMS * 128 <= kTmemCols, "tensor memory");
   static constexpr int kBoxKV = N * 128;  // [N rows][64 bf16]
   static constexpr int kStage = 2 * kBoxKV;
@@ -106,7 +115,8 @@ struct Layout {
   static constexpr int kOffV = kOffK + kRingK * kStage;
   static constexpr int kOffBlock = kOffV + kRing * kStage;
   static constexpr int kOffBar = kOffBlock + kBlocksAhead * static_cast<int>(sizeof(Block));
-  static constexpr int kNBars = 2 * kRingK + (3 + TEAMS) * kRing + 2 * kBlocksAhead + 2 * kQ + 2 * TEAMS;
+  static constexpr int kNBars = 2 * kRingK + 2 * kRing + (1 + TEAMS + kApart) * kBuffers + 2 * kBlocksAhead + 2 * kQ +
+                                2 * TEAMS;
   static constexpr int kOffMisc = kOffBar + kNBars * 8;
   static constexpr int kBytes = kOffMisc + 32 + 1024;  // + room to align the base to 1024
   static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
@@ -362,30 +372,32 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[8], int lane) {
 }
 
 template <int MODE, int N, int G, int TEAMS>
-__global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
+__global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
     packed_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedPrefillParams p) {
-  using L = Layout<N, TEAMS>;
+  using L = Layout<MODE, N, TEAMS>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *sQ = smem, *sK = smem + L::kOffK, *sV = smem + L::kOffV;
   Block *sBlock = reinterpret_cast<Block *>(smem + L::kOffBlock);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
-  // Tile g has V stage and S/P buffer g % kRing in phase (g / kRing) & 1 and K stage g % kRingK in
-  // phase (g / kRingK) & 1.  Block k has the description k % kBlocksAhead, the query rows k % kQ
+  // Tile g has V stage g % kRing in phase (g / kRing) & 1, K stage g % kRingK in phase (g / kRingK) & 1, and
+  // S and P buffers g % kBuffers in phase (g / kBuffers) & 1.  Block k has the description k % kBlocksAhead, the
+  // query rows k % kQ
   // and the O of team k % TEAMS.
-  constexpr int kRingK = L::kRingK;
+  constexpr int kRingK = L::kRingK, kBuffers = L::kBuffers;
   uint64_t *kfull = bars, *kempty = kfull + kRingK, *vfull = kempty + kRingK;
   // S of a tile in tensor memory: a team's tiles by its own count, so that it sees every phase
   uint64_t *sfull = vfull + kRing;
-  uint64_t *pfull = sfull + TEAMS * kRing;  // its P written over it
-  uint64_t *pvdone = pfull + kRing;  // its P V done: the S/P buffer and the V stage are free
+  uint64_t *pfull = sfull + TEAMS * kBuffers;  // its P there
+  uint64_t *pvdone = pfull + kBuffers;         // its P V done: the P buffer and the V stage are free
   uint64_t *bfull = pvdone + kRing;  // a block's description is there
   uint64_t *bempty = bfull + kBlocksAhead;  // and has been read by everyone
   uint64_t *qfull = bempty + kBlocksAhead, *qempty = qfull + L::kQ;  // its query rows are there, and used
   uint64_t *ofull = qempty + L::kQ;  // a block's P V all done
   uint64_t *ofree = ofull + TEAMS;   // its O read out of tensor memory
+  uint64_t *sempty = ofree + TEAMS;  // apart: an S has been read out of it
   uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   uint32_t *s_tmem = misc;
   volatile int *s_abort = reinterpret_cast<volatile int *>(misc + 1);
@@ -398,9 +410,12 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
   if (warp == 0) {
     if (lane < kRing) {
       mbar_init(&vfull[lane], 1);
-      for (int i = 0; i < TEAMS; ++i) mbar_init(&sfull[i * kRing + lane], 1);
-      mbar_init(&pfull[lane], kTeamWarps);
       mbar_init(&pvdone[lane], 1);
+    }
+    if (lane < kBuffers) {
+      for (int i = 0; i < TEAMS; ++i) mbar_init(&sfull[i * kBuffers + lane], 1);
+      if (L::kApart) mbar_init(&sempty[lane], kTeamWarps);
+      mbar_init(&pfull[lane], kTeamWarps);
     }
     if (lane < kRingK) {
       mbar_init(&kfull[lane], 1);
@@ -505,7 +520,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     const uint64_t kdesc = smem_desc_sw128(smem_u32(sK));
     Ring<kBlocksAhead> d;
     Ring<L::kQ> q;
-    Ring<kRing> sb, mine[TEAMS];  // mine: the tiles of the team whose turn it is, then the other's
+    Ring<kBuffers> sb, mine[TEAMS];  // mine: the tiles of the team whose turn it is, then the other's
     Ring<kRingK> kb;
     bool ok = true;
     while (ok) {
@@ -520,7 +535,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       ok = __all_sync(0xffffffffu, wait_bar(&qfull[q.at], q.phase));
       const int s = TEAMS > 1 ? q.at % TEAMS : 0;
       for (int t = 0; ok && t < tiles; ++t) {
-        ok = wait_bar(&kfull[kb.at], kb.phase) && wait_bar(&pvdone[sb.at], sb.phase ^ 1u);
+        ok = wait_bar(&kfull[kb.at], kb.phase) && wait_bar(&(L::kApart ? sempty : pvdone)[sb.at], sb.phase ^ 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
@@ -533,7 +548,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
             // dims 16kk .. 16kk + 15: 32 bytes into a 128-byte row; dims 64.. start the second box
             tc_mma_bf16(to, qd + (((kk >> 2) * kBoxQ + (kk & 3) * 32) >> 4),
                         kd + (((kk >> 2) * L::kBoxKV + (kk & 3) * 32) >> 4), kIdescS, kk > 0 ? 1u : 0u);
-          tc_commit(&sfull[s * kRing + mine[0].at]);
+          tc_commit(&sfull[s * kBuffers + mine[0].at]);
           tc_commit(&kempty[kb.at]);
           if (t + 1 == tiles) tc_commit(&qempty[q.at]);
         }
@@ -545,7 +560,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       if (ok && tiles == 0 && lane == 0) mbar_arrive(&qempty[q.at]);
       if (ok) q.next();
       if (TEAMS > 1 && ok) {
-        const Ring<kRing> m = mine[0];
+        const Ring<kBuffers> m = mine[0];
         mine[0] = mine[TEAMS - 1];
         mine[TEAMS - 1] = m;
       }
@@ -554,8 +569,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     // every MMA of this warp has completed, and its last commits arrived, before the tensor memory is
     // released and the CTA leaves (also when another role has given up)
     const int s = TEAMS > 1 ? q.at % TEAMS : 0;  // the team of mine[0]
-    wait_before(sfull + s * kRing, mine[0]);
-    if (TEAMS > 1) wait_before(sfull + (s ^ 1) * kRing, mine[TEAMS - 1]);
+    wait_before(sfull + s * kBuffers, mine[0]);
+    if (TEAMS > 1) wait_before(sfull + (s ^ 1) * kBuffers, mine[TEAMS - 1]);
     wait_before(kempty, kb);
     wait_before(qempty, q);
     wait_before(qempty, q.before());
@@ -565,7 +580,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     const uint64_t vdesc = smem_desc_sw128_mn(smem_u32(sV), L::kBoxKV);
     Ring<kBlocksAhead> d;
     Ring<TEAMS> o;
-    Ring<kRing> pb;
+    Ring<kRing> vb;
+    Ring<2> pair;  // apart: the P buffers
     bool ok = true;
     while (ok) {
       ok = !*s_abort && wait_bar(&bfull[d.at], d.phase);
@@ -579,10 +595,10 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       // the O of the team's block before has been read
       ok = __all_sync(0xffffffffu, wait_bar(&ofree[o.at], o.phase ^ 1u));
       for (int t = 0; ok && t < tiles; ++t) {
-        ok = __all_sync(0xffffffffu, wait_bar(&vfull[pb.at], pb.phase));
+        ok = __all_sync(0xffffffffu, wait_bar(&vfull[vb.at], vb.phase));
         if (!ok) break;
         if (t * N < seq0 || t * N + N - 1 > seqn) {  // value rows of other sequences, or behind the last
-          uint8_t *v = sV + pb.at * L::kStage;
+          uint8_t *v = sV + vb.at * L::kStage;
           for (int x = lane; x < 16 * N; x += 32) {
             const int j = t * N + (x >> 3) % N;  // (a row's 128 bytes of a box stay together)
             if (j < seq0 || j > seqn) *reinterpret_cast<uint4 *>(v + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
@@ -590,28 +606,30 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           fence_proxy_async_smem();  // read by the tensor cores
           __syncwarp();
         }
-        ok = __all_sync(0xffffffffu, wait_bar(&pfull[pb.at], pb.phase));
+        const int pb = L::kApart ? pair.at : vb.at;
+        ok = __all_sync(0xffffffffu, wait_bar(&pfull[pb], L::kApart ? pair.phase : vb.phase));
         if (!ok) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          const uint64_t vd = vdesc + static_cast<uint64_t>(pb.at * (L::kStage >> 4));
-          const uint32_t to = tmem + L::kColO + o.at * 128, from = tmem + pb.at * N;
+          const uint64_t vd = vdesc + static_cast<uint64_t>(vb.at * (L::kStage >> 4));
+          const uint32_t to = tmem + L::kColO + o.at * 128, from = tmem + L::kColP + pb * L::kStepP;
 #pragma unroll
           for (int kk = 0; kk < N / 16; ++kk)
             // keys 16kk .. 16kk + 15: eight columns of P, V rows 16kk .. (2 KB apart)
             tc_mma_bf16_tmem_a(to, from + 8 * kk, vd + (kk * 2048 >> 4), kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(&pvdone[pb.at]);
+          tc_commit(&pvdone[vb.at]);
           if (t + 1 == tiles) tc_commit(&ofull[o.at]);
         }
         __syncwarp();
-        pb.next();
+        vb.next();
+        pair.next();
       }
       if (ok && tiles == 0 && lane == 0) mbar_arrive(&ofull[o.at]);
       if (ok) o.next();
     }
     if (!ok && lane == 0) set_abort(s_abort, p.flags);
     // every MMA of this warp has completed before the tensor memory is released
-    wait_before(pvdone, pb);
+    wait_before(pvdone, vb);
     wait_before(ofull, o);
     if (TEAMS > 1) wait_before(ofull, o.before());
     __syncwarp();
@@ -657,24 +675,25 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
     const bool flip = MODE == kPackedSoftmax && p.tau2 < 0.0f;
     const float tau2 = fabsf(p.tau2);
     bool ok = true;
-    Ring<kRing> mine;  // the team's tiles
+    Ring<kBuffers> mine;  // the team's tiles
     for (int k = team, n = 0; ok; k += TEAMS, ++n) {  // the team's n-th block
       // (every decision to go on is the warp's: what follows is warp-wide)
       const int d = k % kBlocksAhead;
       ok = __all_sync(0xffffffffu, !*s_abort && wait_bar(&bfull[d], (k / kBlocksAhead) & 1));
       if (!ok) break;
-      const Block b = sBlock[d];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bempty[d]);
+      // (the description stays until the block is done: what its end needs is read then)
+      const Block &b = sBlock[d];
+      const int tiles = b.tiles, window = p.window;
+      if (tiles < 0) break;
       Ring<kRing> tile{b.tile0 % kRing, static_cast<uint32_t>(b.tile0 / kRing) & 1u};
-      if (b.tiles < 0) break;
+      int pair = b.tile0 & 1;  // apart: the tile's buffers
       // a row sees the keys oldest .. oldest + span, relative to k0 (none: from far behind the last)
       int oldest[2];
       uint32_t span[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int newest = b.p0 + (row0 + 8 * i) / G;
-        oldest[i] = max(b.seq0, newest - p.window + 1);
+        oldest[i] = max(b.seq0, newest - window + 1);
         span[i] = static_cast<uint32_t>(newest - oldest[i]);
         if (newest < oldest[i]) {
           oldest[i] = 1 << 30;
@@ -682,7 +701,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
         }
       }
       // every row of the warp sees the keys between these two
-      const int whole0 = max(b.seq0, b.p0 + (rowa + 15) / G - p.window + 1), whole1 = b.p0 + rowa / G;
+      const int whole0 = max(b.seq0, b.p0 + (rowa + 15) / G - window + 1), whole1 = b.p0 + rowa / G;
       float m[2] = {-INFINITY, -INFINITY};    // reference of each row (base 2)
       float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // sums of its weights in this lane, two chains per row
       // ReLU^2: the norms of this lane's keys, each read again for the next tile once it is used
@@ -690,19 +709,24 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
       const float *rkp = nullptr;
       if constexpr (MODE == kPackedRelu2) {
         rkp = p.rk + b.g * p.rk_stride + b.k0 + q2;
-        if (b.tiles > 0) {
+        if (tiles > 0) {
 #pragma unroll
           for (int j = 0; j < N / 8; ++j) rk[j] = *reinterpret_cast<const float2 *>(rkp + 8 * j);
         }
       }
-      for (int t = 0; t < b.tiles; ++t) {
+      for (int t = 0; t < tiles; ++t) {
         const int j0 = t * N;
-        ok = __all_sync(0xffffffffu, wait_bar(&sfull[team * kRing + mine.at], mine.phase));
+        ok = __all_sync(0xffffffffu, wait_bar(&sfull[team * kBuffers + mine.at], mine.phase));
         if (!ok) break;
         tc_fence_after_sync();
-        const uint32_t cols = tmem + lanes16 + tile.at * N;
         uint32_t acc[N / 2];
-        load_scores<N>(cols, acc);
+        const int buffer = L::kApart ? pair : tile.at;
+        load_scores<N>(tmem + lanes16 + buffer * N, acc);
+        if constexpr (L::kApart) {
+          tc_fence_before_sync();  // the buffer is free for another S
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[buffer]);
+        }
         uint32_t hi[N / 4];
         if constexpr (MODE == kPackedSoftmax) {
           if (flip) {
@@ -774,7 +798,7 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
               hi[2 * j + i] = pack_bf16x2(e0, e1);
             }
         } else {
-          const bool next = t + 1 < b.tiles;
+          const bool next = t + 1 < tiles;
           rkp += N;
           auto weights = [&](auto with_mask) {
             const int lo[2] = {oldest[0] - j0 - q2, oldest[1] - j0 - q2};
@@ -807,13 +831,20 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           else
             weights(std::false_type{});
         }
-        store_weights<N>(cols, hi);
+        if constexpr (L::kApart) {
+          // the product that read the P buffer's last weights is done
+          ok = __all_sync(0xffffffffu, wait_before(pvdone, tile.before()));
+          if (!ok) break;
+          tc_fence_after_sync();
+        }
+        store_weights<N>(tmem + lanes16 + L::kColP + buffer * L::kStepP, hi);
         tmem_wait_st();
         tc_fence_before_sync();  // P is read by the tensor cores
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[tile.at]);
+        if (lane == 0) mbar_arrive(&pfull[buffer]);
         mine.next();
         tile.next();
+        pair ^= 1;
       }
       if (!ok) break;
       // (late, so that it has the last products' time)
@@ -907,6 +938,8 @@ __global__ void __launch_bounds__(Layout<N, TEAMS>::kThreads, 1)
           slow_row<MODE, G>(p, b, rowa + (at >> 2) + 8 * i, lane);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bempty[d]);
     }
     if (!ok) set_abort(s_abort, p.flags);
   }
@@ -961,7 +994,7 @@ __global__ void __launch_bounds__(256) packed_knorm_kernel(const PackedPrefillPa
 template <int MODE, int N, int G, int TEAMS>
 cudaError_t launch_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                           const PackedPrefillParams &p, const LaunchDevice &dev, cudaStream_t stream) {
-  using L = Layout<N, TEAMS>;
+  using L = Layout<MODE, N, TEAMS>;
   constexpr auto kernel = packed_prefill_kernel<MODE, N, G, TEAMS>;
   const cudaError_t e = allow_smem_once<kernel>(dev, L::kBytes);
   if (e != cudaSuccess) return e;
