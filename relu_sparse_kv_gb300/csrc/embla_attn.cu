@@ -949,7 +949,7 @@ embla_status packed_prefill_impl(int mode, const embla_shape *shape, int G, int6
   p.flags = flags_ptr();
   if (dev.sms <= 0 || !p.flags) return EMBLA_ERR_CUDA;
   if (window > kMaxPackedTokens) window = kMaxPackedTokens;  // more than any sequence has
-  const uint32_t rows = static_cast<uint32_t>(packed_tile_keys(mode, G, window));
+  const uint32_t rows = static_cast<uint32_t>(packed_tile_keys(mode, G, window, n_keys, shape->batch));
   CUtensorMap tm_q, tm_k, tm_v;
   // (without keys no tile is loaded, and the maps of K and V stand in for nothing)
   if (n_keys == 0) {

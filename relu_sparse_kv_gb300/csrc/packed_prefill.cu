@@ -94,12 +94,12 @@ struct Block {
 };
 
 // TEAMS sets of kTeamWarps warps take blocks in turn; each has an O of its own.  P is written over its S, and
-// three such buffers go round.  For ReLU^2 it has two buffers apart, and S two that are free once they are
-// read: the tensor cores wait less for a tile's weights (16,384 tokens 622 us over S, 589 apart), but a weights
+// three such buffers go round.  For ReLU^2 and one team it has two buffers apart, and S two that are free once
+// they are read: the tensor cores wait less for a tile's weights (16,384 tokens 622 us over S, 589 apart), but a weights
 // warp waits for P's buffer, which softmax, the longer work, does not gain from (window 128 220 over, 245 apart).
 template <int MODE, int N, int TEAMS>
 struct Layout {
-  static constexpr bool kApart = MODE == kPackedRelu2;
+  static constexpr bool kApart = MODE == kPackedRelu2 && TEAMS == 1;
   static constexpr int kBuffers = kApart ? 2 : kRing;
   static constexpr int kThreads = (4 + TEAMS * kTeamWarps) * 32;
   static constexpr int kWarpPV = 2 + TEAMS * kTeamWarps, kWarpV = kWarpPV + 1;
@@ -714,6 +714,29 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
           for (int j = 0; j < N / 8; ++j) rk[j] = *reinterpret_cast<const float2 *>(rkp + 8 * j);
         }
       }
+      float a2[2] = {0.0f, 0.0f};  // ReLU^2: alpha^2 / (mean(q^2) + eps) of this lane's rows
+      auto query_norms = [&]() {
+        if constexpr (MODE == kPackedRelu2) {
+          const int q = k % L::kQ;
+          ok = __all_sync(0xffffffffu, wait_bar(&qfull[q], (k / L::kQ) & 1));
+          if (!ok) return false;
+          // two lanes to a row, a box each
+          const int r = rowa + (lane >> 1);
+          float ss = box_square_sum(sQ + (2 * q + (lane & 1)) * kBoxQ, r, (r & 7) ^ (4 * (lane & 1)));
+          ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+          const float a = (p.alpha * p.alpha) / (ss * (1.0f / kHeadDim) + p.eps);
+          a2[0] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2));
+          a2[1] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2) + 16);
+          // the query rows are read: these depend on every lane's sum
+          const float used = __shfl_sync(0xffffffffu, a2[0], 0) + a2[1];
+          __syncwarp();
+          if (lane == 0) mbar_arrive_after(&qempty[q], used);
+        }
+        return true;
+      };
+      if constexpr (TEAMS > 1) {  // (early, so that the rows of the team's next block may come)
+        if (!query_norms()) break;
+      }
       for (int t = 0; t < tiles; ++t) {
         const int j0 = t * N;
         ok = __all_sync(0xffffffffu, wait_bar(&sfull[team * kBuffers + mine.at], mine.phase));
@@ -847,23 +870,8 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
         pair ^= 1;
       }
       if (!ok) break;
-      // (late, so that it has the last products' time)
-      float a2[2] = {0.0f, 0.0f};  // ReLU^2: alpha^2 / (mean(q^2) + eps) of this lane's rows
-      if constexpr (MODE == kPackedRelu2) {
-        const int q = k % L::kQ;
-        ok = __all_sync(0xffffffffu, wait_bar(&qfull[q], (k / L::kQ) & 1));
-        if (!ok) break;
-        // two lanes to a row, a box each
-        const int r = rowa + (lane >> 1);
-        float ss = box_square_sum(sQ + (2 * q + (lane & 1)) * kBoxQ, r, (r & 7) ^ (4 * (lane & 1)));
-        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-        const float a = (p.alpha * p.alpha) / (ss * (1.0f / kHeadDim) + p.eps);
-        a2[0] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2));
-        a2[1] = __shfl_sync(0xffffffffu, a, 2 * (lane >> 2) + 16);
-        // the query rows are read: these depend on every lane's sum
-        const float used = __shfl_sync(0xffffffffu, a2[0], 0) + a2[1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive_after(&qempty[q], used);
+      if constexpr (TEAMS == 1) {  // (late, so that it has the last products' time)
+        if (!query_norms()) break;
       }
       float f[2];  // what O is multiplied with; 0 where no key weighs anything
 #pragma unroll
@@ -1003,15 +1011,24 @@ cudaError_t launch_packed(const CUtensorMap &tm_q, const CUtensorMap &tm_k, cons
                     stream, 0u, tm_q, tm_k, tm_v, p);
 }
 
+template <int G, int N, int TEAMS>
+cudaError_t launch_kind(int mode, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                        const PackedPrefillParams &p, const LaunchDevice &dev, cudaStream_t stream) {
+  if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, N, G, TEAMS>(tm_q, tm_k, tm_v, p, dev, stream);
+  return launch_packed<kPackedSoftmax, N, G, TEAMS>(tm_q, tm_k, tm_v, p, dev, stream);
+}
+
 }  // namespace
 
-// A block of 128 / G tokens sees window + 128 / G - 1 keys at most.  Up to about a thousand, two teams on
-// tiles of 80 are faster than one on tiles of 128, which waits at each block's ends (2 x 16,384 tokens, 4 KV
-// heads, us: window 128 68 against 107, 256 87 and 127, 512 135 and 166, 1,024 244 and 240; 2 KV heads, 1,024
-// 217 and 239); for 2,048 keys 402 against 385.
-constexpr int64_t kShortSpan = 1100;
-int packed_tile_keys(int mode, int G, int64_t window) {
-  return mode == kPackedSoftmax && window + 128 / G - 1 <= kShortSpan ? 80 : 128;
+// Two teams on tiles of 80 are faster than one on tiles of 128, which waits at each block's ends, where blocks
+// have few keys.  A block of 128 / G tokens sees window + 128 / G - 1 at most: up to about a thousand (2 x 16,384
+// tokens, 4 KV heads, us: window 128 62 against 107, 256 87 and 127, 512 135 and 166, 1,024 244 and 240; 2 KV
+// heads, 1,024 217 and 239; 2,048 402 against 385).  In a full layer it sees half of its sequence's on average:
+// up to 1,500 keys to a sequence (8,192 tokens in sequences of 256 28.2 against 31.0, 512 31.8 and 35.2, 1,024
+// 40.7 and 42.6, 2,048 58.9 and 58.6, 4,096 98.0 and 90.0).
+constexpr int64_t kShortSpan = 1100, kShortContext = 1500;
+int packed_tile_keys(int mode, int G, int64_t window, int64_t keys, int batch) {
+  return (mode == kPackedSoftmax ? window + 128 / G - 1 <= kShortSpan : keys <= kShortContext * batch) ? 80 : 128;
 }
 
 int64_t packed_rk_stride(int64_t keys) { return (keys + 3) & ~static_cast<int64_t>(3); }
@@ -1037,17 +1054,13 @@ cudaError_t launch_packed_prefill(int mode, int G, const CUtensorMap &tm_q, cons
                                0u, p, rk);
     if (e != cudaSuccess) return e;
   }
-  const bool shorter = packed_tile_keys(mode, G, p.window) == 80;
-  if (G == 4) {
-    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 4, 1>(tm_q, tm_k, tm_v, p, dev, stream);
-    if (shorter) return launch_packed<kPackedSoftmax, 80, 4, 2>(tm_q, tm_k, tm_v, p, dev, stream);
-    return launch_packed<kPackedSoftmax, 128, 4, 1>(tm_q, tm_k, tm_v, p, dev, stream);
-  }
-  if (G == 8) {
-    if (mode == kPackedRelu2) return launch_packed<kPackedRelu2, 128, 8, 1>(tm_q, tm_k, tm_v, p, dev, stream);
-    if (shorter) return launch_packed<kPackedSoftmax, 80, 8, 2>(tm_q, tm_k, tm_v, p, dev, stream);
-    return launch_packed<kPackedSoftmax, 128, 8, 1>(tm_q, tm_k, tm_v, p, dev, stream);
-  }
+  const bool shorter = packed_tile_keys(mode, G, p.window, p.keys, p.batch) == 80;
+  if (G == 4)
+    return shorter ? launch_kind<4, 80, 2>(mode, tm_q, tm_k, tm_v, p, dev, stream)
+                   : launch_kind<4, 128, 1>(mode, tm_q, tm_k, tm_v, p, dev, stream);
+  if (G == 8)
+    return shorter ? launch_kind<8, 80, 2>(mode, tm_q, tm_k, tm_v, p, dev, stream)
+                   : launch_kind<8, 128, 1>(mode, tm_q, tm_k, tm_v, p, dev, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -79,7 +79,7 @@ struct PackedPrefillParams {
   float alpha, c, eps;         // ReLU^2
 };
 // Keys per tile (the rows of the K and V maps' boxes) and block numbers to walk.
-int packed_tile_keys(int mode, int G, int64_t window);
+int packed_tile_keys(int mode, int G, int64_t window, int64_t keys, int batch);
 int64_t packed_blocks(int64_t tokens, int batch, int G, int Hkv);
 int64_t packed_rk_stride(int64_t keys);
 size_t packed_workspace_bytes(int64_t keys, int Hkv);

@@ -163,6 +163,27 @@ def test_prefill_packed(case, Hkv, G, alpha, c, eps):
     assert (out[T:] == 7.0).all(), "rows behind the last sequence"
 
 
+@pytest.mark.parametrize("case", [c for c in range(len(LENS)) if len(LENS[c][0]) < 10])
+@pytest.mark.parametrize("Hkv,G", [(4, 4), (2, 8), (3, 4)])
+def test_prefill_packed_with_many_rows_behind(case, Hkv, G):
+    """More rows than sequences fill have the call take the form for long ones; those rows hold NaN, and so
+    do the values of some keys of weight zero."""
+    lens, klens = LENS[case]
+    q, k, v, out = _attention_inputs(40 + case, lens, klens, Hkv, G, 1600 * len(lens), 3.0)
+    T, at = sum(lens), R.starts(klens or lens)
+    k[at[-1]:] = math.nan
+    v[at[-1]:] = math.inf
+    k[10:at[-1]:37] = 0.0  # no direction: scores of zero
+    clean = v[:at[-1]].clone()
+    clean[10::37] = 0.0
+    v[10:at[-1]:37] = math.nan
+    _run_packed(lens, klens, Hkv, q, k, v, out)
+    _checked()
+    want, tol = R.prefill_packed(q[:T], k[:at[-1]], clean, R.starts(lens), at, 1.0, 1.0, 1e-6)
+    R.assert_within(out[:T], want, tol, "rows behind")
+    assert (out[T:] == 7.0).all()
+
+
 def test_prefill_packed_equals_prefill_of_each():
     """The unpacked call, sequence by sequence, within both calls' precision."""
     lens, Hkv = [500, 129, 1, 258], 4
