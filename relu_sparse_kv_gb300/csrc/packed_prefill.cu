@@ -1022,8 +1022,8 @@ cudaError_t launch_kind(int mode, const CUtensorMap &tm_q, const CUtensorMap &tm
 
 // Two teams on tiles of 80 are faster than one on tiles of 128, which waits at each block's ends, where blocks
 // have few keys.  A block of 128 / G tokens sees window + 128 / G - 1 at most: up to about a thousand (2 x 16,384
-// tokens, 4 KV heads, us: window 128 62 against 107, 256 87 and 127, 512 135 and 166, 1,024 244 and 240; 2 KV
-// heads, 1,024 217 and 239; 2,048 402 against 385).  In a full layer it sees half of its sequence's on average:
+// tokens, 4 KV heads, us: window 128 61 against 105, 256 87 and 125, 512 133 and 165, 1,024 240 and 238; 2 KV
+// heads, 1,024 220 and 237; 2,048 393 against 380).  In a full layer it sees half of its sequence's on average:
 // up to 1,500 keys to a sequence (8,192 tokens in sequences of 256 28.2 against 31.0, 512 31.8 and 35.2, 1,024
 // 40.7 and 42.6, 2,048 58.9 and 58.6, 4,096 98.0 and 90.0).
 constexpr int64_t kShortSpan = 1100, kShortContext = 1500;

@@ -16,17 +16,17 @@
 // Sixteen lanes take the G query heads and the key head of one KV group of one token, 16 bytes of
 // each row per lane, so a lane works out its four angles once for G + 1 rows and has all of their
 // loads in flight together; nothing waits on another lane but the norms' sums.  Bound by HBM: 4 x 32,768
-// tokens of 16 + 4 heads, normed, in 214 us (6.3 TB/s, 0.92 of a copy's rate); a step of 8 tokens 2.5 us, the
+// tokens of 16 + 4 heads, normed, in 209 us (6.4 TB/s, 0.95 of a copy's rate); a step of 8 tokens 2.3 us, the
 // launch.  Blocks of tokens that shared their angles through shared memory took 242 us (a barrier and
-// fewer loads in flight), 48 and 80 registers (5 and 3 blocks to an SM) 211 and 257 us but 2.9 and 2.5
-// for the step.
+// fewer loads in flight).  Small blocks start and leave sooner: 64 threads 209, 128 210, 256 214, 512 235 us.
+// Registers: 56 (36 warps to an SM) 204 us, but 2,000 tokens 6.6 against 5.9 and the step 2.6.
 #include "ptx_blocks.cuh"
 #include "ragged.h"
 
 namespace embla {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 64;
 constexpr int kRopeLanes = 16;  // lanes per (token, KV group)
 constexpr int kRopePerBlock = kRopeThreads / kRopeLanes;
 
@@ -47,7 +47,7 @@ __device__ __forceinline__ int sequence_of(const PackedTokens &s, int64_t t, int
 }
 
 template <int G, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, G == 4 ? 4 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, G == 4 ? 16 : 12) rope_kernel(const __grid_constant__ RopeParams p) {
   pdl_wait_primary();  // the rows are written; whoever read the old outputs and rings is done
   pdl_launch_dependents();
   const int sl = threadIdx.x % kRopeLanes;
