@@ -12,8 +12,8 @@
 //
 // 96 sequences of 2 KV heads over rings of 1,024 keys (85 MB): 19.4 us, 4.4 TB/s; of 4 heads (200 MB) 33.2 us,
 // 6.0 TB/s, 0.89 of a copy's rate: the first microseconds, until rows arrive, and the merge do not shrink
-// with the rings.  96 of 4 over rings of 128 (26 MB) 5.4 us; 8 of 4, 3.0 us, the launch and two trips to
-// memory (position, then rows).
+// with the rings.  96 of 4 over rings of 128 (26 MB) 5.2 us; 8 of 4, 2.9 us, the launch and a trip to
+// memory (3.0 where the rows are asked for after the position).
 #include <cooperative_groups.h>
 
 #include "ptx_blocks.cuh"
@@ -82,7 +82,10 @@ __device__ __forceinline__ uint32_t rw_piece(int r, int c) {
 // memory; each warp then computes 16 of the 128 output dims over all the rows, O^T = V^T P^T, so no
 // warp's sums have to be added to another's.  Three CTAs fit an SM, so that one's arithmetic has the
 // others' copies beside it.
-template <int G, int CL>
+//
+// AHEAD: the CTA asks for every ring row that could be its own before it knows the position, which saves a
+// trip to memory and reads up to 64 KB of rows that hold nothing yet.
+template <int G, int CL, bool AHEAD>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
     window_step_kernel(const RaggedWindowParams p) {
   pdl_wait_primary();  // the query, the rings and the positions are complete
@@ -93,28 +96,34 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
   const int64_t u = blockIdx.x / CL;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int last = p.pos[u / p.Hkv];
-  const int nv = last < 0 ? 0 : (last >= p.window ? p.window : last + 1);  // valid rows of the ring
-  const int share = (nv + CL - 1) / CL;
-  const int r0 = min(nv, rank * share), rows = min(nv, r0 + share) - r0;  // of this CTA
-
-  // This warp's rows: an instruction moves two whole ones; rows past the share are zeros (they read
-  // nothing, from an address inside the ring).
-  const int wrow = warp * 16;
-  auto copy = [&](const uint8_t *ring, uint8_t *to) {
+  const int last = p.pos[static_cast<uint32_t>(u) / static_cast<uint32_t>(p.Hkv)];
+  // This warp's rows of the CTA's `count` from row `first` on: an instruction moves two whole ones; rows past
+  // them are zeros (they read nothing, from an address inside the ring).
+  const int wrow = warp * 16, piece = lane & 15;
+  auto copy = [&](const uint8_t *ring, uint8_t *to, int first, int count) {
     const uint8_t *from = ring + u * p.window * kRwRowBytes;
-    const int piece = lane & 15;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int r = wrow + 2 * k + (lane >> 4);
-      const bool live = r < rows;
+      const bool live = r < count;
       cp_async16_zfill(to + rw_piece(r, piece),
-                       from + (live ? static_cast<int64_t>(r0 + r) * kRwRowBytes : 0) + piece * 16, live ? 16u : 0u);
+                       from + (live ? static_cast<int64_t>(first + r) * kRwRowBytes : 0) + piece * 16, live ? 16u : 0u);
     }
     cp_async_commit();
   };
-  copy(p.K, smem);
-  copy(p.V, smem + kRwBuffer);
+  int r0 = rank * kRwRows;
+  if constexpr (AHEAD) {
+    copy(p.K, smem, r0, p.window - r0);
+    copy(p.V, smem + kRwBuffer, r0, p.window - r0);
+  }
+  const int nv = last < 0 ? 0 : (last >= p.window ? p.window : last + 1);  // valid rows of the ring
+  const int share = AHEAD ? kRwRows : (nv + CL - 1) / CL;
+  r0 = min(nv, rank * share);
+  const int rows = min(nv, r0 + share) - r0;  // of this CTA
+  if constexpr (!AHEAD) {
+    copy(p.K, smem, r0, rows);
+    copy(p.V, smem + kRwBuffer, r0, rows);
+  }
   // query as the A operand of S: row g (head g), dims 16ks + 2t, +1 and +8, +9
   uint32_t qa0[8], qa2[8];
   {
@@ -174,7 +183,17 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
   l += __shfl_xor_sync(0xffffffffu, l, 2);
   if (t == 0) sh.wl[warp][g] = l;
   cp_async_wait<0>();  // the V rows
-  __syncthreads();     // everyone's, P and the sums
+  if constexpr (AHEAD) {
+    // rows that hold nothing yet may hold anything: a weight of zero needs a value
+    if (rows < wrow + 16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = wrow + 2 * k + (lane >> 4);
+        if (r >= rows) *reinterpret_cast<uint4 *>(smem + kRwBuffer + rw_piece(r, piece)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  __syncthreads();  // everyone's, P and the sums
 
   // O^T of dims 16 warp .. + 15: A = V^T (16 dims x 16 rows per step), B = P^T
   float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // dims g (o[0], o[1]) and g + 8, heads 2t and 2t + 1
@@ -264,7 +283,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kWsThreads, 3)
   const int64_t u = blockIdx.x / CL;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int last = p.pos[u / p.Hkv];
+  const int last = p.pos[static_cast<uint32_t>(u) / static_cast<uint32_t>(p.Hkv)];
   const int nv = last < 0 ? 0 : (last >= p.window ? p.window : last + 1);  // valid rows of the ring
   const int blocks = (nv + kWsRows - 1) / kWsRows;
   uint8_t *rows = smem + warp * kWsStages * kWsBlock;
@@ -418,14 +437,23 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kWsThreads, 3)
   }
 }
 
-template <int G, int CL>
-cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
+template <int G, int CL, bool AHEAD>
+cudaError_t launch_step(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
   constexpr int bytes = 2 * kRwBuffer + static_cast<int>(sizeof(RwShared));
   static_assert(3 * (bytes + 1024) <= 228 * 1024, "three CTAs per SM");
-  constexpr auto kernel = window_step_kernel<G, CL>;
+  constexpr auto kernel = window_step_kernel<G, CL, AHEAD>;
   const cudaError_t e = allow_smem_once<kernel>(dev, bytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(units * CL)), dim3(kRwThreads), bytes, stream, 0u, p);
+}
+
+// Rows are asked for ahead where each CTA has an SM to itself: what that reads in vain is then at most 10 MB
+// (8 sequences of 4 KV heads 2.85 us against 3.05, rings of 1,024 of 2 5.2 and 5.5; 32 with 7 rows each 2.75
+// and 2.62).
+template <int G, int CL>
+cudaError_t launch_rw(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
+  return units * CL <= dev.sms ? launch_step<G, CL, true>(units, p, dev, stream)
+                               : launch_step<G, CL, false>(units, p, dev, stream);
 }
 
 template <int G, int CL>

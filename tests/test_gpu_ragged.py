@@ -492,6 +492,24 @@ def test_window_decode_ragged_of_many_sequences(B, Hkv, G, window):
     R.assert_within(out, *R.window_decode(q, k, v, pos, D ** -0.5), "ragged window decode")
 
 
+@pytest.mark.parametrize("B,Hkv,G,window", [(1, 1, 4, 128), (9, 4, 4, 128), (60, 4, 4, 128), (10, 2, 8, 300), (50, 2, 8, 300),
+                                            (3, 4, 4, 1024), (200, 2, 8, 700)])
+def test_window_decode_ragged_rows_that_hold_nothing_yet(B, Hkv, G, window):
+    """NaN and infinities in the ring's unwritten rows, for batches of every form; nothing changes by them."""
+    gen = _gen(window + B)
+    pos = [(b * b * 7) % (window + 20) - 1 for b in range(B)]
+    q, k, v = _bf(gen, B, G * Hkv, D), _bf(gen, B, Hkv, window, D), _bf(gen, B, Hkv, window, D)
+    want = R.window_decode(q, k, v, pos, D ** -0.5)
+    for b, p in enumerate(pos):
+        k[b, :, max(0, p + 1):] = math.nan
+        v[b, :, max(0, p + 1):] = -math.inf
+    out = torch.full((B, G * Hkv, D), math.nan, device=DEV)
+    E.embla_window_decode_ragged(E.Shape(B, G * Hkv, Hkv, D, 0, 0), q, k, v,
+                                 torch.tensor(pos, dtype=torch.int32, device=DEV), out)
+    _checked()
+    R.assert_within(out, *want, "unwritten rows")
+
+
 def test_window_decode_ragged_matches_window_decode():
     """All sequences at one position: the batch call with its own rotation of the query, and this one on
     the rotated query, agree within the rounding of that query to bf16 (2^-8 of each element, in the
