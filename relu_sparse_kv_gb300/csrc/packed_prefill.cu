@@ -35,10 +35,10 @@
 // A weight of zero times an infinite or NaN value would be NaN, and a tile holds rows that a query
 // must not see.  Value rows of other sequences, or behind the last (which nothing may have written), are
 // cleared in shared memory before the product.  Against its own later and older rows, an output that
-// comes out infinite or NaN is computed again by its warp, key by key over the visible ones (slow_row);
-// nothing else pays for it.  Measured: 16,300 tokens of a full layer with NaN behind them 0.63 ms (80 ms when
-// those rows were left to slow_row), with NaN in all of them 535 ms; 8 x 16,384 tokens of a window layer
-// 42 ms.  (Cleared by the weights' warps, or by the one that loads V, 4 to 20 % more on every call.)
+// comes out infinite or NaN is computed again by its warp over the visible keys (slow_rows); nothing else
+// pays for it.  Measured: 16,300 tokens of a full layer with NaN behind them 0.60 ms (80 ms when a sequence's
+// neighbours were left to a slow path too), with NaN in all of them 118 ms; 8 x 16,384 tokens of a window layer
+// 18 ms.  (Cleared by the weights' warps, or by the one that loads V, 4 to 20 % more on every call.)
 //
 // A block's sequence.  The host knows no lengths, so block numbers are spread with room to spare: sequence
 // b owns the numbers from floor(cu_q[b] / R) + b (R tokens to a block), which is enough for its blocks,
@@ -111,6 +111,7 @@ struct Layout {
   static_assert(kColO + TEAMS * 128 <= kTmemCols, "tensor memory");
   static constexpr int kBoxKV = N * 128;  // [N rows][64 bf16]
   static constexpr int kStage = 2 * kBoxKV;
+  static constexpr int kSlowCols = TEAMS == 1 ? 128 : (MODE == kPackedRelu2 ? 16 : 32);
   static constexpr int kOffK = kQ * 2 * kBoxQ;
   static constexpr int kOffV = kOffK + kRingK * kStage;
   static constexpr int kOffBlock = kOffV + kRing * kStage;
@@ -241,87 +242,157 @@ struct BlockFinder {
   }
 };
 
-// Row r of a block (token r / G, head r % G) computed key by key by one warp.  In two passes, so that no
-// partial sum is larger than the result needs: maximum and sum (ReLU^2: the sum), then the values by their
-// normalised weights.
-template <int MODE, int G>
-__device__ __noinline__ void slow_row(const PackedPrefillParams &p, const Block &b, int r, int lane) {
-  const int i = r / G, h = b.g * G + r % G;
-  const uint16_t *q = p.q.base + static_cast<int64_t>(b.q0 + i) * p.q.stride + h * kHeadDim;
-  const uint2 qw = *reinterpret_cast<const uint2 *>(q + 4 * lane);
-  const float qf[4] = {bf16lo(qw.x), bf16hi(qw.x), bf16lo(qw.y), bf16hi(qw.y)};
-  float scale = p.tau2;
+// The 16 rows of a warp from rowa on once more, from memory and by warp products, those of `bad` (bit r: row
+// rowa + r) stored.  In two passes, so that no partial sum is larger than the result needs: maximum and sum
+// (ReLU^2: the sum), then the values by their normalised weights, in two bf16 parts.  Infinite and NaN values are
+// zeros to the products, and are added to the rows that see them.  (COLS columns at a time, nothing kept that can
+// be read again: what does not fit beside the caller's registers makes those spill, 5 to 30 % on every call.)
+template <int MODE, int G, int COLS>
+__device__ __noinline__ void slow_rows(const PackedPrefillParams &p, const Block &b, int rowa, uint32_t bad, int lane) {
+  const int g = lane >> 2, t = lane & 3;  // this lane's rows: g and g + 8; its keys of eight: 2t and 2t + 1
+  const int tokens = b.nq - 1;
+  const int low = max(b.seq0, b.p0 + min(rowa / G, tokens) - p.window + 1), high = b.p0 + min((rowa + 15) / G, tokens);
+  const int newest0 = b.p0 + min((rowa + g) / G, tokens), newest1 = b.p0 + min((rowa + g + 8) / G, tokens);
+  auto row = [&](int i) {  // of the query, [token][head]
+    const int r = rowa + g + 8 * i;
+    return p.q.base + static_cast<int64_t>(b.q0 + min(r / G, tokens)) * p.q.stride + (b.g * G + r % G) * kHeadDim;
+  };
+  float scale0 = p.tau2, scale1 = p.tau2;
   if (MODE == kPackedRelu2) {
-    float ss = (qf[0] * qf[0] + qf[1] * qf[1]) + (qf[2] * qf[2] + qf[3] * qf[3]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    scale = p.alpha / sqrtf(ss * (1.0f / kHeadDim) + p.eps);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t *q = reinterpret_cast<const uint32_t *>(row(i)) + t;
+      float ss = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < 16; ++k) ss = fmaf(bf16lo(q[4 * k]), bf16lo(q[4 * k]), fmaf(bf16hi(q[4 * k]), bf16hi(q[4 * k]), ss));
+      ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+      ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+      (i ? scale1 : scale0) = p.alpha / sqrtf(ss * (1.0f / kHeadDim) + p.eps);
+    }
   }
-  const int64_t newest = b.p0 + i;
-  const int64_t oldest = newest - p.window + 1 > b.seq0 ? newest - p.window + 1 : b.seq0;
-  // the score of key j for lane (j - first key of the step)
-  auto score = [&](int64_t j) {
-    const bool live = j <= newest;
-    const uint16_t *k = p.k.base + (b.k0 + (live ? j : newest)) * p.k.stride + b.g * kHeadDim;
-    float s = 0.0f;
-    for (int d = 0; d < kHeadDim; d += 8) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(k + d);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // keys j0 .. j0 + 7: elements 2i + e are row g + 8i, key j0 + 2t + e; ReLU^2: their weights
+  auto scores = [&](int j0, float (&s)[4]) {
+    const uint32_t *k = reinterpret_cast<const uint32_t *>(
+        p.k.base + static_cast<int64_t>(b.k0 + min(j0 + g, high)) * p.k.stride + b.g * kHeadDim) + t;
+    const uint32_t *q0 = reinterpret_cast<const uint32_t *>(row(0)) + t, *q1 = reinterpret_cast<const uint32_t *>(row(1)) + t;
+    s[0] = s[1] = s[2] = s[3] = 0.0f;
+#pragma unroll (COLS > 32 ? 4 : 2)
+    for (int ks = 0; ks < 64; ks += 8) mma_16816_bf16(s, q0[ks], q1[ks], q0[ks + 4], q1[ks + 4], k[ks], k[ks + 4]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s = fmaf(__shfl_sync(0xffffffffu, qf[(2 * e) & 3], (d + 2 * e) / 4), bf16lo(w[e]), s);
-        s = fmaf(__shfl_sync(0xffffffffu, qf[(2 * e + 1) & 3], (d + 2 * e) / 4), bf16hi(w[e]), s);
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + 2 * t + (e & 1), newest = e < 2 ? newest0 : newest1;
+      const bool live = j >= b.seq0 && j > newest - p.window && j <= newest;
+      s[e] *= e < 2 ? scale0 : scale1;
+      if (MODE == kPackedRelu2) {
+        const float w = live ? fmaxf(s[e] * p.rk[b.g * p.rk_stride + b.k0 + j], 0.0f) : 0.0f;
+        s[e] = w * w;
+      } else if (!live) {
+        s[e] = -INFINITY;
       }
     }
-    s *= scale;
-    if (MODE == kPackedRelu2) {
-      const float w = live ? fmaxf(s * p.rk[b.g * p.rk_stride + b.k0 + j], 0.0f) : 0.0f;
-      return w * w;
-    }
-    return live ? s : -INFINITY;
   };
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j0 = oldest; j0 <= newest; j0 += 32) {
-    const float s = score(j0 + lane);
-    if (MODE == kPackedRelu2) {
-      l += s;
-    } else {
-      const float mn = fmaxf(m, s);
-      l = l * (m == mn ? 1.0f : exp2f(m - mn)) + (s == -INFINITY ? 0.0f : exp2f(s - mn));
-      m = mn;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  auto join = [&](int i, float m2, float l2) {
+    const float mn = fmaxf(m[i], m2);
+    l[i] = l[i] * (m[i] == mn ? 1.0f : exp2f(m[i] - mn)) + l2 * (m2 == mn ? 1.0f : exp2f(m2 - mn));
+    m[i] = mn;
+  };
+#pragma unroll 1
+  for (int j0 = low; j0 <= high; j0 += 8) {
+    float s[4];
+    scores(j0, s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (MODE == kPackedRelu2)
+        l[e >> 1] += s[e];
+      else if (s[e] != -INFINITY)
+        join(e >> 1, s[e], 1.0f);
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-    if (MODE == kPackedRelu2) {
-      l += l2;
-    } else {
-      const float mn = fmaxf(m, m2);
-      l = l * (m == mn ? 1.0f : exp2f(m - mn)) + l2 * (m2 == mn ? 1.0f : exp2f(m2 - mn));
-      m = mn;
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m[i], o), l2 = __shfl_xor_sync(0xffffffffu, l[i], o);
+      if (MODE == kPackedRelu2)
+        l[i] += l2;
+      else
+        join(i, m2, l2);
+    }
+    const float z = MODE == kPackedRelu2 ? p.c + l[i] : l[i];
+    l[i] = z == 0.0f ? 0.0f : 1.0f / z;
+  }
+#pragma unroll 1
+  for (int c = 0; c < kHeadDim; c += COLS) {
+    float o[COLS / 8][4];  // columns c + 8n + 2t and the next of rows g and g + 8
+#pragma unroll
+    for (int n = 0; n < COLS / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+#pragma unroll 1
+    for (int j0 = low; j0 <= high; j0 += 16) {
+      uint32_t a[3][4];  // the weights' two parts, and ones where the row sees the key
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float s[4];
+        scores(j0 + 8 * h, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float w[2];
+          uint32_t seen = 0u;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = s[2 * i + e];
+            w[e] = MODE == kPackedRelu2 ? x * l[i] : (x == -INFINITY ? 0.0f : exp2f(x - m[i]) * l[i]);
+            if (MODE == kPackedRelu2 ? x > 0.0f : x != -INFINITY) seen |= 0x3F80u << (16 * e);
+          }
+          const uint32_t hi = pack_bf16x2(w[0], w[1]);
+          a[0][2 * h + i] = hi;
+          a[1][2 * h + i] = pack_bf16x2(w[0] - bf16lo(hi), w[1] - bf16hi(hi));
+          a[2][2 * h + i] = seen;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < COLS / 8; ++n) {
+        uint32_t x[4], clean[4];  // keys 2t, 2t + 1, 2t + 8 and 2t + 9
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = min(j0 + 2 * t + (e & 1) + 8 * (e >> 1), high);
+          x[e] = p.v.base[static_cast<int64_t>(b.k0 + j) * p.v.stride + b.g * kHeadDim + c + 8 * n + g];
+          const bool broken = (x[e] & 0x7F80u) == 0x7F80u;
+          odd |= broken;
+          clean[e] = broken ? 0u : x[e];
+        }
+#pragma unroll
+        for (int part = 1; part >= 0; --part)
+          mma_16816_bf16(o[n], a[part][0], a[part][1], a[part][2], a[part][3], clean[0] | clean[1] << 16,
+                         clean[2] | clean[3] << 16);
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+          for (int kind = 0; kind < 3; ++kind) {  // NaN, +infinity, -infinity: how many of them each row sees
+            uint32_t is[4];
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              is[e] = (kind == 0 ? (x[e] & 0x7FFFu) > 0x7F80u : x[e] == (kind == 1 ? 0x7F80u : 0xFF80u)) ? 0x3F80u : 0u;
+            mma_16816_bf16(d, a[2][0], a[2][1], a[2][2], a[2][3], is[0] | is[1] << 16, is[2] | is[3] << 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (d[e] > 0.0f) o[n][e] += kind == 0 ? NAN : (kind == 1 ? INFINITY : -INFINITY);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rowa + g + 8 * i;
+      if (bad >> (g + 8 * i) & 1u) {
+        uint16_t *to = p.out + (static_cast<int64_t>(b.q0 + r / G) * p.Hkv * G + b.g * G + r % G) * kHeadDim + c + 2 * t;
+#pragma unroll
+        for (int n = 0; n < COLS / 8; ++n)
+          *reinterpret_cast<uint32_t *>(to + 8 * n) = pack_bf16x2(o[n][2 * i], o[n][2 * i + 1]);
+      }
     }
   }
-  const float z = MODE == kPackedRelu2 ? p.c + l : l;
-  const float f = z == 0.0f ? 0.0f : 1.0f / z;
-  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // columns 4 lane .. + 3
-  for (int64_t j0 = oldest; j0 <= newest; j0 += 32) {
-    const float s = score(j0 + lane);
-    const float w = MODE == kPackedRelu2 ? s * f : (s == -INFINITY ? 0.0f : exp2f(s - m) * f);
-    const int n = static_cast<int>(newest - j0 + 1 < 32 ? newest - j0 + 1 : 32);
-    for (int c = 0; c < n; ++c) {
-      const float wc = __shfl_sync(0xffffffffu, w, c);
-      if (MODE == kPackedRelu2 && wc == 0.0f) continue;  // weighs nothing, whatever its value holds
-      const uint2 x = *reinterpret_cast<const uint2 *>(p.v.base + (b.k0 + j0 + c) * p.v.stride + b.g * kHeadDim +
-                                                       4 * lane);
-      a[0] = fmaf(wc, bf16lo(x.x), a[0]);
-      a[1] = fmaf(wc, bf16hi(x.x), a[1]);
-      a[2] = fmaf(wc, bf16lo(x.y), a[2]);
-      a[3] = fmaf(wc, bf16hi(x.y), a[3]);
-    }
-  }
-  *reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(b.q0 + i) * p.Hkv * G + h) * kHeadDim + 4 * lane) =
-      make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
 }
 
 // Scores of 16 rows x N keys to registers: element 4j + 2i + e is row l / 4 + 8i, key 8j + 2(l % 4) + e; and
@@ -841,7 +912,7 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 // max(x, 0)^2 = max(x |x|, 0); the denominator sums the weights the numerator multiplies.
-                // (A NaN score makes the row NaN here, and slow_row gives the key no weight.)
+                // (A NaN score makes the row NaN here, and slow_rows gives the key no weight.)
                 const uint32_t h = pack_relu_bf16x2(e[2 * i] * fabsf(e[2 * i]), e[2 * i + 1] * fabsf(e[2 * i + 1]));
                 hi[2 * j + i] = h;
                 add_bf16x2(h, l[2 * i], l[2 * i + 1]);
@@ -935,16 +1006,18 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
         }
         __syncwarp();
       }
+      uint32_t bad = 0u;  // bit r: row rowa + r
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint32_t bad = __ballot_sync(0xffffffffu, live[i] && f[i] != 0.0f && chk[2 * i] + chk[2 * i + 1] != 0.0f);
-        bad = (bad | bad >> 1 | bad >> 2 | bad >> 3) & 0x11111111u;  // of the quad's four lanes
-        while (bad) {
-          const int at = __ffs(bad) - 1;
-          bad &= bad - 1;
-          __syncwarp();
-          slow_row<MODE, G>(p, b, rowa + (at >> 2) + 8 * i, lane);
-        }
+        const uint32_t lanes = __ballot_sync(0xffffffffu, live[i] && f[i] != 0.0f && chk[2 * i] + chk[2 * i + 1] != 0.0f);
+        if (lanes == 0u) continue;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (lanes >> (4 * r) & 15u) bad |= 1u << (r + 8 * i);
+      }
+      if (bad != 0u) {
+        __syncwarp();
+        slow_rows<MODE, G, L::kSlowCols>(p, b, rowa, bad, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bempty[d]);
