@@ -47,7 +47,7 @@
 //
 // What bounds it, and what was measured (16 query heads):
 //   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 589 us, 1,870
-//     TFLOP/s of visible products (0.98 of the burst rate); softmax over all keys 1,480 (8,192 tokens), there
+//     TFLOP/s of visible products (0.98 of the burst rate); softmax over all keys 1,520 (8,192 tokens), there
 //     the exponentials and the maximum add what the tensor cores cannot hide.
 //   - a window of 128 keys: memory.  8 x 16,384 tokens 220 us, 6.09 TB/s (0.90 of a copy's rate); a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:

@@ -252,6 +252,38 @@ def test_infinite_and_nan_rows_stay_where_they_are_seen(kind):
     assert not torch.isfinite(out[at[1] + 71]).all()  # and those that see it show it
 
 
+@pytest.mark.parametrize("behind", [0, 5000])  # (many rows behind: the full layers' form for long contexts)
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("Hkv,G", [(4, 4), (3, 8)])
+def test_a_broken_value_reaches_one_column_of_the_rows_that_weigh_it(Hkv, G, value, behind):
+    lens, W, col = [70, 300, 5], 100, 37
+    n, at = sum(lens), R.starts(lens)
+    q, k, v, window_out = _attention_inputs(50, lens, None, Hkv, G, behind, 1.0)
+    full_out, clean = window_out.clone(), v.clone()
+    broken = [(0, 69), (1, 0), (1, 150), (2, 2)]
+    for b, j in broken:
+        v[at[b] + j, :, col], clean[at[b] + j, :, col] = value, 0.0
+    _run_window(lens, None, Hkv, q, k, v, window_out, W)
+    _run_packed(lens, None, Hkv, q, k, v, full_out)
+    _checked()
+    others = [d for d in range(D) if d != col]
+    for out, form in ((window_out, R.window_prefill(q[:n], k[:n], clean[:n], at, at, W, D ** -0.5)),
+                      (full_out, R.prefill_packed(q[:n], k[:n], clean[:n], at, at, 1.0, 1.0, 1e-6))):
+        want, tol = (x.expand(n, G * Hkv, D) for x in form)
+        R.assert_within(out[:n][..., others], want[..., others], tol[..., others], "the other columns")
+    unit = lambda x: x.double() / x.double().square().mean(-1, keepdim=True).sqrt()
+    sees = torch.zeros(n, dtype=torch.bool, device=DEV)
+    for b, j in broken:
+        sees[at[b] + j:min(at[b + 1], at[b] + j + W)] = True
+        dot = (unit(q[at[b] + j:at[b + 1]]) * unit(k[at[b] + j]).repeat_interleave(G, 0)).sum(-1)
+        assert not torch.isfinite(full_out[at[b] + j:at[b + 1]][..., col])[dot > 0.1].any()
+    finite = torch.isfinite(window_out[:n][..., col])
+    assert finite[~sees].all() and not finite[sees].any()
+    # one broken value: the rows of the other sign's scores do not weigh it
+    dot = (unit(q[:70]) * unit(k[69]).repeat_interleave(G, 0)).sum(-1)
+    assert torch.isfinite(full_out[:69][..., col]).all() and torch.isfinite(full_out[69][..., col])[dot[69] < -0.1].all()
+
+
 @pytest.mark.parametrize("kind", ["window", "packed"])
 @pytest.mark.parametrize("Hkv,G", [(4, 4), (2, 8)])
 @pytest.mark.parametrize("before,n", [(0, 1), (1, 79), (2, 80), (3, 81), (130, 127), (5, 128), (7, 129), (38, 400)])
