@@ -446,7 +446,7 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  * of one sign lose up to 6e-7 more per 80 or 128 keys, 6e-4 at 131,072).  A key that a query does not see
  * contributes nothing, whatever its rows hold.  Infinite or NaN values among a sequence's own v rows have the
  * outputs of the queries near them and behind them computed by a slow path (whole prompts of them 80 times
- * the usual time at a window of 128, 200 times in a full layer of 16,384); other sequences do not pay for them.
+ * the usual time at a window of 128, 220 times in a full layer of 16,384); other sequences do not pay for them.
  *
  * embla_prefill_packed — embla_prefill for packed prompts ("Sevren Sparse Attention learns to be sparse"):
  * the same queries and keys as embla_window_prefill's, no window, ReLU^2 weights of RMS-normalised

@@ -37,7 +37,7 @@
 // cleared in shared memory before the product.  Against its own later and older rows, an output that
 // comes out infinite or NaN is computed again by its warp over the visible keys (slow_rows); nothing else
 // pays for it.  Measured: 16,300 tokens of a full layer with NaN behind them 0.60 ms (80 ms when a sequence's
-// neighbours were left to a slow path too), with NaN in all of them 118 ms; 8 x 16,384 tokens of a window layer
+// neighbours were left to a slow path too), with NaN in all of them 133 ms; 8 x 16,384 tokens of a window layer
 // 18 ms.  (Cleared by the weights' warps, or by the one that loads V, 4 to 20 % more on every call.)
 //
 // A block's sequence.  The host knows no lengths, so block numbers are spread with room to spare: sequence
@@ -46,8 +46,8 @@
 // (one of 32 sequences; reading each block's own took the warp that also loads Q and K 1,500 cycles more).
 //
 // What bounds it, and what was measured (16 query heads):
-//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 589 us, 1,870
-//     TFLOP/s of visible products (0.98 of the burst rate); softmax over all keys 1,520 (8,192 tokens), there
+//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 564 to 606 us,
+//     1,950 to 1,815 TFLOP/s of visible products (boards differ; 0.96 to 1.03 of the burst rate); softmax over all keys 1,520 (8,192 tokens), there
 //     the exponentials and the maximum add what the tensor cores cannot hide.
 //   - a window of 128 keys: memory.  8 x 16,384 tokens 220 us, 6.09 TB/s (0.90 of a copy's rate); a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
@@ -111,7 +111,7 @@ struct Layout {
   static_assert(kColO + TEAMS * 128 <= kTmemCols, "tensor memory");
   static constexpr int kBoxKV = N * 128;  // [N rows][64 bf16]
   static constexpr int kStage = 2 * kBoxKV;
-  static constexpr int kSlowCols = TEAMS == 1 ? 128 : (MODE == kPackedRelu2 ? 16 : 32);
+  static constexpr int kSlowCols = TEAMS == 1 ? 64 : (MODE == kPackedRelu2 ? 16 : 32);
   static constexpr int kOffK = kQ * 2 * kBoxQ;
   static constexpr int kOffV = kOffK + kRingK * kStage;
   static constexpr int kOffBlock = kOffV + kRing * kStage;
