@@ -47,8 +47,9 @@
 //
 // What bounds it, and what was measured (16 query heads):
 //   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 564 to 606 us,
-//     1,950 to 1,815 TFLOP/s of visible products (boards differ; 0.96 to 1.03 of the burst rate); softmax over all keys 1,520 (8,192 tokens), there
-//     the exponentials and the maximum add what the tensor cores cannot hide.
+//     1,950 to 1,815 TFLOP/s of visible products (boards differ; 0.96 to 1.03 of the burst rate); softmax over
+//     all keys 1,520 (8,192 tokens), there the exponentials and the maximum add what the tensor cores cannot
+//     hide.
 //   - a window of 128 keys: memory.  8 x 16,384 tokens 220 us, 6.09 TB/s (0.90 of a copy's rate); a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
 //     one team of eight warps on tiles of 128 took 480 us, two on tiles of 80 with a barrier per block 315.
@@ -74,7 +75,7 @@ constexpr int kTeamWarps = 8;      // warps that turn a block's scores into weig
 constexpr int kRing = 3;           // V stages
 constexpr int kBoxQ = 128 * 128;   // [128 rows][64 bf16]
 constexpr float kSlack = 8.0f;     // P stays below 2^kSlack
-constexpr uint64_t kLimitNs = 10000000000ull;  // 10 s: a row computed key by key holds the others up
+constexpr uint64_t kLimitNs = 10000000000ull;  // 10 s: rows computed again (slow_rows) hold the others up
 constexpr int kBlocksAhead = 4;    // descriptions of blocks in flight
 constexpr int kTmemCols = 512;
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128) | (1u << 16);  // B (V) MN-major
@@ -95,8 +96,9 @@ struct Block {
 
 // TEAMS sets of kTeamWarps warps take blocks in turn; each has an O of its own.  P is written over its S, and
 // three such buffers go round.  For ReLU^2 and one team it has two buffers apart, and S two that are free once
-// they are read: the tensor cores wait less for a tile's weights (16,384 tokens 622 us over S, 589 apart), but a weights
-// warp waits for P's buffer, which softmax, the longer work, does not gain from (window 128 220 over, 245 apart).
+// they are read: the tensor cores wait less for a tile's weights (16,384 tokens 622 us over S, 589 apart), but
+// a weights warp waits for P's buffer, and softmax, the longer work, does not gain (window 128 220 us over S, 245
+// apart).  Sixteen warps on half rows each: 148 us for 14,496 tokens in four sequences, eight 140.
 template <int MODE, int N, int TEAMS>
 struct Layout {
   static constexpr bool kApart = MODE == kPackedRelu2 && TEAMS == 1;
@@ -264,7 +266,10 @@ __device__ __noinline__ void slow_rows(const PackedPrefillParams &p, const Block
       const uint32_t *q = reinterpret_cast<const uint32_t *>(row(i)) + t;
       float ss = 0.0f;
 #pragma unroll 4
-      for (int k = 0; k < 16; ++k) ss = fmaf(bf16lo(q[4 * k]), bf16lo(q[4 * k]), fmaf(bf16hi(q[4 * k]), bf16hi(q[4 * k]), ss));
+      for (int k = 0; k < 16; ++k) {
+        const float x = bf16lo(q[4 * k]), y = bf16hi(q[4 * k]);
+        ss = fmaf(x, x, fmaf(y, y, ss));
+      }
       ss += __shfl_xor_sync(0xffffffffu, ss, 1);
       ss += __shfl_xor_sync(0xffffffffu, ss, 2);
       (i ? scale1 : scale0) = p.alpha / sqrtf(ss * (1.0f / kHeadDim) + p.eps);
@@ -274,7 +279,8 @@ __device__ __noinline__ void slow_rows(const PackedPrefillParams &p, const Block
   auto scores = [&](int j0, float (&s)[4]) {
     const uint32_t *k = reinterpret_cast<const uint32_t *>(
         p.k.base + static_cast<int64_t>(b.k0 + min(j0 + g, high)) * p.k.stride + b.g * kHeadDim) + t;
-    const uint32_t *q0 = reinterpret_cast<const uint32_t *>(row(0)) + t, *q1 = reinterpret_cast<const uint32_t *>(row(1)) + t;
+    const uint32_t *q0 = reinterpret_cast<const uint32_t *>(row(0)) + t;
+    const uint32_t *q1 = reinterpret_cast<const uint32_t *>(row(1)) + t;
     s[0] = s[1] = s[2] = s[3] = 0.0f;
 #pragma unroll (COLS > 32 ? 4 : 2)
     for (int ks = 0; ks < 64; ks += 8) mma_16816_bf16(s, q0[ks], q1[ks], q0[ks + 4], q1[ks + 4], k[ks], k[ks + 4]);
