@@ -59,9 +59,9 @@ __device__ __forceinline__ void finish_outputs(const RwReceived<G, CL> &in, int 
     float L = 0.0f, A = 0.0f;
 #pragma unroll
     for (int c = 0; c < CL; ++c) {
-      // (a CTA without keys has nothing to add)
-      const float f = in.m[c][h] == -INFINITY ? 0.0f : exp2f(in.m[c][h] - M);
-      if (f != 0.0f) {
+      // (a CTA without keys has nothing to add, which its sum tells: NaN scores leave the maximum at minus infinity)
+      if (in.l[c][h] != 0.0f) {
+        const float f = exp2f(in.m[c][h] - M);
         L = fmaf(in.l[c][h], f, L);
         A = fmaf(in.o[c][li], f, A);
       }
@@ -410,9 +410,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kWsThreads, 3)
     float L = 0.0f, A = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWsWarps; ++w) {
-      // (a warp without rows has nothing to add)
-      const float f = mg.m[w][h] == -INFINITY ? 0.0f : exp2f(mg.m[w][h] - M);
-      if (f != 0.0f) {
+      // (a warp without rows has nothing to add, which its sum tells: as in finish_outputs)
+      if (mg.l[w][h] != 0.0f) {
+        const float f = exp2f(mg.m[w][h] - M);
         L = fmaf(mg.l[w][h], f, L);
         A = fmaf(mg.o[w][h][threadIdx.x], f, A);
       }
