@@ -10,7 +10,7 @@
 // reading each other's took a third of the kernel's time).  P is fp32 in three bf16 parts (hi + mid +
 // lo, all 24 bits), because the output is fp32.
 //
-// 96 sequences of 2 KV heads over rings of 1,024 keys (85 MB): 19.4 us, 4.4 TB/s; of 4 heads (200 MB) 33.2 us,
+// 96 sequences of 2 KV heads over rings of 1,024 keys (84 MB): 18.7 us, 4.5 TB/s; of 4 heads (200 MB) 33.2 us,
 // 6.0 TB/s, 0.89 of a copy's rate: the first microseconds, until rows arrive, and the merge do not shrink
 // with the rings.  96 of 4 over rings of 128 (26 MB) 5.2 us; 8 of 4, 2.9 us, the launch and a trip to
 // memory (3.0 where the rows are asked for after the position).
@@ -46,13 +46,78 @@ struct RwReceived {
   float o[CL][G * kHeadDim / CL];
 };
 
-// This CTA's share of a unit's outputs from what every CTA of the cluster sent.
+// An output that came out infinite or NaN though its sum of weights did not: a value is, or the products' sum
+// passed the largest float before it was divided.  P's three parts make NaN of an infinite value (its second
+// part may be zero or negative), so the output is computed once more.  (Nothing else pays for it: rings without
+// such values take what they took.  One infinite value to a ring: 8 sequences of 4 KV heads 69 us instead of 2.9 over
+// 128 keys, 141 instead of 6.5 over 1,024; 96 of 2 over 1,024 536 instead of 16.)
+__device__ __forceinline__ bool is_broken(float y, float l) { return !(fabsf(y) <= 3.402823466e38f) && l == l; }
+
+// Dim `dim` of a head (each lane's own) over the first `nv` rows of its unit's ring, from memory, by one warp: a key
+// weighs nothing only where its score is minus infinity, weights are divided before the sum, and an infinite or NaN
+// value enters as it is.
+__device__ __noinline__ float output_again(const uint16_t *q, const uint8_t *K, const uint8_t *V, int nv, float tau2,
+                                           int dim) {
+  const int lane = threadIdx.x & 31;
+  auto score = [&](int j) {
+    if (j >= nv) return -INFINITY;
+    const uint4 *k = reinterpret_cast<const uint4 *>(K + static_cast<int64_t>(j) * kRwRowBytes);
+    const uint4 *x = reinterpret_cast<const uint4 *>(q);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int c = 0; c < kRwRowBytes / 16; ++c) {
+      const uint4 a = k[c], b = x[c];
+      s[0] = fmaf(bf16lo(a.x), bf16lo(b.x), fmaf(bf16hi(a.x), bf16hi(b.x), s[0]));
+      s[1] = fmaf(bf16lo(a.y), bf16lo(b.y), fmaf(bf16hi(a.y), bf16hi(b.y), s[1]));
+      s[2] = fmaf(bf16lo(a.z), bf16lo(b.z), fmaf(bf16hi(a.z), bf16hi(b.z), s[2]));
+      s[3] = fmaf(bf16lo(a.w), bf16lo(b.w), fmaf(bf16hi(a.w), bf16hi(b.w), s[3]));
+    }
+    return tau2 * ((s[0] + s[1]) + (s[2] + s[3]));
+  };
+  float m = -INFINITY, l = 0.0f;
+  auto join = [&](float m2, float l2) {
+    const float mn = fmaxf(m, m2);
+    l = l * (m == mn ? 1.0f : exp2f(m - mn)) + l2 * (m2 == mn ? 1.0f : exp2f(m2 - mn));
+    m = mn;
+  };
+#pragma unroll 1
+  for (int j = lane; j < nv; j += 32) {
+    const float z = score(j);
+    if (z != -INFINITY) join(z, 1.0f);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, l, o));
+  if (l == 0.0f) return 0.0f;
+  float y = 0.0f;
+#pragma unroll 1
+  for (int j0 = 0; j0 < nv; j0 += 32) {
+    const float z = score(j0 + lane);
+    const float mine = z == -INFINITY ? -1.0f : exp2f(z - m) / l;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 32; i0 += 16) {
+      uint32_t x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        x[i] = *reinterpret_cast<const uint16_t *>(V + static_cast<int64_t>(min(j0 + i0 + i, nv - 1)) * kRwRowBytes + 2 * dim);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float w = __shfl_sync(0xffffffffu, mine, i0 + i), v = __uint_as_float(x[i] << 16);
+        if (w != -1.0f) y = (x[i] & 0x7F80u) == 0x7F80u ? y + v : fmaf(w, v, y);
+      }
+    }
+  }
+  return y;
+}
+
+// This CTA's share of a unit's outputs (nv keys) from what every CTA of the cluster sent.
 template <int G, int CL>
-__device__ __forceinline__ void finish_outputs(const RwReceived<G, CL> &in, int rank, int64_t u, float *out,
-                                               int threads) {
+__device__ __forceinline__ void finish_outputs(const RwReceived<G, CL> &in, int rank, int64_t u, int nv,
+                                               const RaggedWindowParams &p, int threads) {
   constexpr int per = G * kHeadDim / CL;
+  static_assert(per % 32 == 0, "a warp's outputs are one head's");
   for (int li = threadIdx.x; li < per; li += threads) {
-    const int h = (rank * per + li) / kHeadDim;
+    const int at = rank * per + li, h = at / kHeadDim;
     float M = -INFINITY;
 #pragma unroll
     for (int c = 0; c < CL; ++c) M = fmaxf(M, in.m[c][h]);
@@ -66,7 +131,13 @@ __device__ __forceinline__ void finish_outputs(const RwReceived<G, CL> &in, int 
         A = fmaf(in.o[c][li], f, A);
       }
     }
-    out[u * G * kHeadDim + rank * per + li] = L > 0.0f || L != L ? A / L : 0.0f;
+    float y = L > 0.0f || L != L ? A / L : 0.0f;
+    if (__any_sync(0xffffffffu, is_broken(y, L))) {
+      const int64_t ring = u * p.window * kRwRowBytes;
+      const float z = output_again(p.q + (u * G + h) * kHeadDim, p.K + ring, p.V + ring, nv, p.tau2, at % kHeadDim);
+      if (is_broken(y, L)) y = z;
+    }
+    p.out[u * G * kHeadDim + at] = y;
   }
 }
 
@@ -216,13 +287,27 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
       sh.l[lane] = ls;
     }
     __syncthreads();
+    bool broken = false;
+    float *out = p.out + u * G * kHeadDim + 16 * warp;
     if (2 * t < G) {
-      float *out = p.out + u * G * kHeadDim + 16 * warp + g;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int h = 2 * t + (i & 1);
-        const float lh = sh.l[h];
-        out[h * kHeadDim + 8 * (i >> 1)] = lh > 0.0f || lh != lh ? o[i] / lh : 0.0f;
+        const float lh = sh.l[h], y = lh > 0.0f || lh != lh ? o[i] / lh : 0.0f;
+        out[h * kHeadDim + g + 8 * (i >> 1)] = y;
+        broken |= is_broken(y, lh);
+      }
+    }
+    if (__any_sync(0xffffffffu, broken)) {
+      __syncwarp();  // the warp's outputs are written
+      const int64_t ring = u * p.window * kRwRowBytes;
+      const int d = lane & 15;
+#pragma unroll 1
+      for (int h = 0; h < G; ++h) {
+        const bool mine = is_broken(out[h * kHeadDim + d], sh.l[h]);
+        if (!__any_sync(0xffffffffu, mine)) continue;
+        const float y = output_again(p.q + (u * G + h) * kHeadDim, p.K + ring, p.V + ring, nv, p.tau2, 16 * warp + d);
+        if (mine && lane < 16) out[h * kHeadDim + d] = y;
       }
     }
   } else {
@@ -250,7 +335,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRwThreads, 3)
     }
     cluster_arrive();
     cluster_wait();  // everything is here, and nobody reads or writes another's shared memory any more
-    finish_outputs<G, CL>(*mine, rank, u, p.out, kRwThreads);
+    finish_outputs<G, CL>(*mine, rank, u, nv, p, kRwThreads);
   }
 }
 
@@ -418,7 +503,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kWsThreads, 3)
       }
     }
     if constexpr (CL == 1) {
-      p.out[(u * G + h) * kHeadDim + threadIdx.x] = L > 0.0f || L != L ? A / L : 0.0f;
+      float y = L > 0.0f || L != L ? A / L : 0.0f;
+      if (__any_sync(0xffffffffu, is_broken(y, L))) {
+        const int64_t ring = u * p.window * kRwRowBytes;
+        const float z = output_again(p.q + (u * G + h) * kHeadDim, p.K + ring, p.V + ring, nv, p.tau2, threadIdx.x);
+        if (is_broken(y, L)) y = z;
+      }
+      p.out[(u * G + h) * kHeadDim + threadIdx.x] = y;
     } else {
       const int at = h * kHeadDim + threadIdx.x;
       Received *to = cg::this_cluster().map_shared_rank(mine, at / per);
@@ -433,7 +524,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kWsThreads, 3)
   if constexpr (CL > 1) {
     cluster_arrive();
     cluster_wait();  // everything is here, and nobody writes another's shared memory any more
-    finish_outputs<G, CL>(*mine, rank, u, p.out, kWsThreads);
+    finish_outputs<G, CL>(*mine, rank, u, nv, p, kWsThreads);
   }
 }
 

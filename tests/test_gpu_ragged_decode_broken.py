@@ -72,3 +72,64 @@ def test_nan_keys_make_their_heads_nan(B, Hkv, G, W, rows):
     broken = broken.repeat_interleave(G, 1)
     assert torch.isnan(out[broken]).all()
     R.assert_within(out[~broken], want[~broken], tol[~broken], "the other heads")
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("B,Hkv,G,W", FORMS)
+def test_a_broken_value_reaches_its_column(B, Hkv, G, W, value):
+    """The column of a value that is infinite or NaN takes that value in every head of its group, whatever the
+    weights; with infinities of both signs it is NaN."""
+    q, k, v, pos = _inputs(B, Hkv, G, W)
+    clean = v.clone()
+    expect = torch.zeros(B, Hkv, D, dtype=torch.float64, device=DEV)
+    for b, n in enumerate(_rows(pos, W)):
+        for g in range(Hkv):
+            for col, at in ((3, [0]), (70, [n - 1]), (90, [0, n // 2])):
+                for i, j in enumerate(at):
+                    x = -value if i else value
+                    if n > 0:
+                        v[b, g, j, col], clean[b, g, j, col] = x, 0.0
+                        expect[b, g, col] += x if n > 1 or not i else -x
+                    if n == 1:
+                        v[b, g, 0, col], expect[b, g, col] = value, value
+    want, tol = R.window_decode(q, k, clean, pos, D ** -0.5)
+    expect = expect.repeat_interleave(G, 1)
+    out = _run(q, k, v, pos).double()
+    finite = torch.isfinite(expect)
+    R.assert_within(out[finite], want[finite], tol[finite], "the other columns")
+    got, x = out[~finite], expect[~finite]
+    assert ((got == x) | (torch.isnan(got) & torch.isnan(x))).all()
+
+
+@pytest.mark.parametrize("B,Hkv,G,W", FORMS)
+def test_weights_that_vanish(B, Hkv, G, W):
+    """A key whose weight is too small for a float still passes an infinite value on; one whose score is minus infinity
+    contributes nothing."""
+    q, k, v, pos = _inputs(B, Hkv, G, W)
+    q[..., 0], k[..., 0] = 64.0, 0.0
+    clean, low = v.clone(), k.clone()
+    rows = _rows(pos, W)
+    for b, n in enumerate(rows):
+        if n > 1:
+            k[b, :, 1, 0] = low[b, :, 1, 0] = -64.0  # tau 64^2 = 362 below the others
+            v[b, :, 1, 5], clean[b, :, 1, 5] = math.inf, 0.0
+        if n > 2:
+            k[b, :, n - 1, 0], low[b, :, n - 1, 0] = -math.inf, -128.0  # (weighs less than 64 bits tell from nothing)
+            v[b, :, n - 1, 9], clean[b, :, n - 1, 9] = math.nan, 0.0
+    want, tol = R.window_decode(q, low, clean, pos, D ** -0.5)
+    out = _run(q, k, v, pos)
+    hit = torch.zeros(out.shape, dtype=torch.bool, device=DEV)
+    hit[[b for b, n in enumerate(rows) if n > 1], :, 5] = True
+    assert (out[hit] == math.inf).all()
+    R.assert_within(out[~hit], want[~hit], tol[~hit], "the rest")
+
+
+@pytest.mark.parametrize("B,Hkv,G,W", FORMS)
+def test_values_whose_sum_overflows(B, Hkv, G, W):
+    """The mean of values near the largest finite one is finite, though their sum is not."""
+    q, k, v, pos = _inputs(B, Hkv, G, W)
+    v.copy_((3e38 * torch.sign(v.float())).bfloat16())
+    v[..., :40] = 3e38
+    out = _run(q, k, v, pos)
+    assert torch.isfinite(out).all()
+    R.assert_within(out, *R.window_decode(q, k, v, pos, D ** -0.5), "large values")
