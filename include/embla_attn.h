@@ -454,7 +454,8 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  *   alpha, c, eps   as for embla_full_decode
  *   workspace  the keys' norms: embla_prefill_packed_workspace_size(shape, n_keys) bytes, 16-byte aligned
  *   every other argument as for embla_window_prefill
- * Precision as for embla_window_prefill.  A NaN score weighs nothing; a key of weight zero contributes
+ * Precision as for embla_window_prefill; the rows' mean squares are fp32, and rows of q and k whose root mean square lies
+ * between 2^-48 and 2^59 come out as defined.  A NaN score weighs nothing; a key of weight zero contributes
  * nothing, whatever its value row holds (by the slow path where that is infinite or NaN).
  *
  * embla_window_decode_ragged — embla_window_decode for sequences at positions of their own.

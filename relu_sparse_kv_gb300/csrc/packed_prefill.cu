@@ -950,14 +950,16 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
       if constexpr (TEAMS == 1) {  // (late, so that it has the last products' time)
         if (!query_norms()) break;
       }
-      float f[2];  // what O is multiplied with; 0 where no key weighs anything
+      // What O is multiplied with: 0 where no key weighs anything, NaN (for slow_rows) where the weights' sum is too
+      // large for a float, as the squares of scores that wait for their query's norm may be.
+      float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = l[2 * i] + l[2 * i + 1];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         const float z = MODE == kPackedRelu2 ? p.c + a2[i] * x : x;
-        f[i] = x != 0.0f && z != 0.0f ? (MODE == kPackedRelu2 ? a2[i] / z : 1.0f / z) : 0.0f;
+        f[i] = x != 0.0f && z != 0.0f ? (MODE == kPackedRelu2 ? a2[i] / z : 1.0f / z) + (z - z) : 0.0f;
       }
       ok = __all_sync(0xffffffffu, !*s_abort && wait_bar(&ofull[team], n & 1));
       if (!ok) break;
