@@ -447,6 +447,8 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  * contributes nothing, whatever its rows hold.  Infinite or NaN values among a sequence's own v rows have the
  * outputs of the queries near them and behind them computed by a slow path (whole prompts of them 80 times
  * the usual time at a window of 128, 220 times in a full layer of 16,384); other sequences do not pay for them.
+ * A softmax row whose largest score lies so far from zero (2^30 and more) that its rounding moves the weights
+ * out of the floats' range takes that path too.
  *
  * embla_prefill_packed — embla_prefill for packed prompts ("Sevren Sparse Attention learns to be sparse"):
  * the same queries and keys as embla_window_prefill's, no window, ReLU^2 weights of RMS-normalised

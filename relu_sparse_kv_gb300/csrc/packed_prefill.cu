@@ -75,6 +75,7 @@ constexpr int kTeamWarps = 8;      // warps that turn a block's scores into weig
 constexpr int kRing = 3;           // V stages
 constexpr int kBoxQ = 128 * 128;   // [128 rows][64 bf16]
 constexpr float kSlack = 8.0f;     // P stays below 2^kSlack
+constexpr uint32_t kSumExp = 27, kSumExps = 200;  // a sum of weights, 2^-100 .. 2^100, has lost none of them (biased)
 constexpr uint64_t kLimitNs = 10000000000ull;  // 10 s: rows computed again (slow_rows) hold the others up
 constexpr int kBlocksAhead = 4;    // descriptions of blocks in flight
 constexpr int kTmemCols = 512;
@@ -950,16 +951,22 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
       if constexpr (TEAMS == 1) {  // (late, so that it has the last products' time)
         if (!query_norms()) break;
       }
-      // What O is multiplied with: 0 where no key weighs anything, NaN (for slow_rows) where the weights' sum is too
-      // large for a float, as the squares of scores that wait for their query's norm may be.
+      // What O is multiplied with; NaN sends the row to slow_rows.  ReLU^2: 0 where no key weighs anything, NaN where the
+      // sum is too large for a float, as the squares of scores that wait for their query's norm may be.  Softmax:
+      // the largest weight is about 1 but where the reference is so far from zero (2^30) that its rounding
+      // moves the exponents out of the floats' range; rows without keys come along, which costs them little.
       float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float x = l[2 * i] + l[2 * i + 1];
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
-        const float z = MODE == kPackedRelu2 ? p.c + a2[i] * x : x;
-        f[i] = x != 0.0f && z != 0.0f ? (MODE == kPackedRelu2 ? a2[i] / z : 1.0f / z) + (z - z) : 0.0f;
+        if constexpr (MODE == kPackedRelu2) {
+          const float z = p.c + a2[i] * x;
+          f[i] = x != 0.0f && z != 0.0f ? a2[i] / z + (z - z) : 0.0f;
+        } else {
+          f[i] = __float_as_uint(x) - (kSumExp << 23) <= kSumExps << 23 ? 1.0f / x : NAN;
+        }
       }
       ok = __all_sync(0xffffffffu, !*s_abort && wait_bar(&ofull[team], n & 1));
       if (!ok) break;
@@ -997,7 +1004,7 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
           // the quad's lanes hold columns 2l, 2l + 1 of eight groups of eight; lane l takes the groups
           // 2l and 2l + 1, 32 bytes, so that the quad stores 128 bytes at once
           quad_transpose(y[i], lane);
-          if (f[i] == 0.0f) {
+          if (MODE == kPackedRelu2 && f[i] == 0.0f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[i][j] = 0u;
           }
@@ -1017,7 +1024,8 @@ __global__ void __launch_bounds__(Layout<MODE, N, TEAMS>::kThreads, 1)
       uint32_t bad = 0u;  // bit r: row rowa + r
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t lanes = __ballot_sync(0xffffffffu, live[i] && f[i] != 0.0f && chk[2 * i] + chk[2 * i + 1] != 0.0f);
+        const bool weighs = MODE == kPackedSoftmax || f[i] != 0.0f;
+        const uint32_t lanes = __ballot_sync(0xffffffffu, live[i] && weighs && chk[2 * i] + chk[2 * i + 1] != 0.0f);
         if (lanes == 0u) continue;
 #pragma unroll
         for (int r = 0; r < 8; ++r)

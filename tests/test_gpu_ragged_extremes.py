@@ -48,3 +48,27 @@ def test_full_layers_do_not_ask_how_long_the_rows_are(Hkv, G, q_size, k_size, c,
     _checked()
     R.assert_within(out[:n], *R.prefill_packed(q[:n], k[:n], v[:n], at, at, 1.0, c, eps), "long and short rows")
     assert (out[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("window", [1, 100, 1 << 30])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [10, 14, 16, 20, 40, 60])
+@pytest.mark.parametrize("n", [100, 300])
+def test_window_prefill_of_scores_far_from_zero(n, size, sign, window):
+    """Scores that fp32 holds exactly, tau q . k = sign 2^(2 size - 3) (1 + r / 128): the largest ones take all of the
+    weight where their distance from the next does, also where the scores' own unit in the last place is more than the
+    exponential can reach.  (Tolerance: weights and outputs rounded to bf16; the exponents, tau log2(e) (s - max), are
+    off by 2^-22 of the distance, and a weight counts below 150 of them.)"""
+    Hkv, G = 2, 8
+    q = torch.zeros(n, G * Hkv, D, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(n, Hkv, D, dtype=torch.bfloat16, device=DEV)
+    v = _bf(_gen(61), n, Hkv, D)
+    r = (torch.arange(n, device=DEV) * 37) % 128
+    q[..., 5] = sign * 2.0 ** size
+    k[..., 5] = (2.0 ** size * (1 + r[:, None] / 128)).bfloat16()
+    out = torch.full_like(q, 7.0)
+    E.embla_window_prefill(E.Shape(1, G * Hkv, Hkv, D, 0, 0), _cu([n]), q, k, v, out, window=window, tau=0.125)
+    _checked()
+    want, _ = R.window_prefill(q, k, v, [0, n], [0, n], window, 0.125)
+    mean, _ = R.window_prefill(q, k, v.abs(), [0, n], [0, n], window, 0.125)
+    R.assert_within(out, want, R.BF16 * want.abs() + (R.BF16 + 150 * 2.0 ** -22) * mean * 1.02, f"scores of 2^{2 * size - 3}")
