@@ -422,7 +422,8 @@ embla_status embla_window_decode(const embla_shape *shape, const void *q, const 
  *   q, k, v    bf16 [n_tokens, Hq | Hkv | Hkv, 128]; v is read for the rings only
  *   norm       0: rows as they are; else each row of q and k first becomes
  *              x / sqrt(mean(x^2) + eps) * gain (eps finite and >= 0; a row of zeros with eps == 0
- *              becomes NaN)
+ *              becomes NaN).  Mean squares are fp32: rows whose root mean square lies between 2^-48 and 2^59
+ *              come out as defined, and shorter ones where eps is 2^-96 or more
  *   q_gain, k_gain  fp32 [128] or NULL (1); NULL without norm
  *   rope_base  > 0: pair (2i, 2i+1) is turned by position * rope_base^(-2i/128)
  *   q_out      bf16 [n_tokens, Hq, 128] (dense);  k_out  bf16 [n_tokens, Hkv, 128] or NULL: the rows,

@@ -72,3 +72,24 @@ def test_window_prefill_of_scores_far_from_zero(n, size, sign, window):
     want, _ = R.window_prefill(q, k, v, [0, n], [0, n], window, 0.125)
     mean, _ = R.window_prefill(q, k, v.abs(), [0, n], [0, n], window, 0.125)
     R.assert_within(out, want, R.BF16 * want.abs() + (R.BF16 + 150 * 2.0 ** -22) * mean * 1.02, f"scores of 2^{2 * size - 3}")
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+@pytest.mark.parametrize("Hkv,G", [(4, 4), (2, 8)])
+def test_rotation_norms_long_and_short_rows(Hkv, G, eps):
+    """Rows whose root mean square lies between 2^-48 and 2^59, as the call is defined for."""
+    gen, n = _gen(62), 160
+    shape = E.Shape(1, G * Hkv, Hkv, D, 0, 0)
+    q, k = _bf(gen, n, G * Hkv, D), _bf(gen, n, Hkv, D)
+    sizes = torch.tensor([-47, -46, -45, -44, -40, -30, -20, -8, 0, 0, 9, 17, 30, 45, 57, 58], device=DEV)
+    turn = torch.arange(n, device=DEV)[:, None]
+    for x in (q, k):
+        x.mul_(torch.pow(2.0, sizes[(turn + torch.arange(x.shape[1], device=DEV)) % 16].double())[..., None].float())
+    qg, kg = (1 + 0.3 * torch.randn(D, generator=gen, device=DEV) for _ in range(2))
+    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+    E.embla_rope_qkv(shape, _cu([n]), None, q, k, None, q_out, k_out, norm_eps=eps, q_gain=qg, k_gain=kg)
+    _checked()
+    pos = torch.arange(n, device=DEV)
+    for got, x, g, what in ((q_out, q, qg, "q_out"), (k_out, k, kg, "k_out")):
+        want, tol = R.rope(x, pos, 10000.0, g, eps)
+        R.assert_within(got, want, tol, what)
