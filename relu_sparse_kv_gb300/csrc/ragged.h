@@ -41,7 +41,7 @@ struct RopeParams {
   PackedTokens seqs;
   const int32_t *pos0;  // position of each sequence's first token; null: 0
   TokenRows q, k, v;
-  uint16_t *q_out, *k_out;  // either may be null: not written
+  uint16_t *q_out, *k_out;  // k_out null: not written
   uint16_t *k_win, *v_win;  // both null: no rings
   const float *q_gain, *k_gain;
   float eps;

@@ -19,8 +19,9 @@
 // tokens of 16 + 4 heads, normed, in 209 us (6.4 TB/s, 0.95 of a copy's rate); a step of 8 tokens 2.3 us, the
 // launch.  Blocks of tokens that shared their angles through shared memory took 242 us (a barrier and
 // fewer loads in flight).  Small blocks start and leave sooner: 64 threads 209, 128 210, 256 214, 512 235 us.
-// Rows whose squares leave the floats' range are not looked for: times a power of two first, in a branch that no other
-// row takes, they cost every call with norms 1.5 to 6 % (4 x 32,768 tokens 213 to 222 us, 5,072 ragged ones 11.2 to 11.7).
+// Each query is stored as it is done (all of them at the end: 210 to 217 us by how the stores are ordered).
+// Rows whose squares leave the floats' range are not looked for: times a power of two first, in a branch
+// that no other row takes, they cost every call with norms 1.5 to 6 % (213 to 222 us; 5,072 ragged tokens 11.2 to 11.7).
 // Registers: 56 (36 warps to an SM) 204 us, but 2,000 tokens 6.6 against 5.9 and the step 2.6.
 #include "ptx_blocks.cuh"
 #include "ragged.h"
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kRopeThreads, G == 4 ? 16 : 12) rope_kernel(co
     for (int h = 0; h <= G; ++h) rs[h] = rsqrtf(rs[h] * (1.0f / kHeadDim) + p.eps);
   }
   float gain[8];
+  uint16_t *to = p.q_out + (t * p.Hkv + g) * G * kHeadDim + d;
 #pragma unroll
   for (int h = 0; h <= G; ++h) {
     if constexpr (NORM) {
@@ -124,18 +126,14 @@ __global__ void __launch_bounds__(kRopeThreads, G == 4 ? 16 : 12) rope_kernel(co
       y[i] = pack_bf16x2(u, v2);
     }
     x[h] = make_uint4(y[0], y[1], y[2], y[3]);
+    if (h < G) *reinterpret_cast<uint4 *>(to + h * kHeadDim) = x[h];
   }
-  if (p.q_out) {
-    uint16_t *to = p.q_out + (t * p.Hkv + g) * G * kHeadDim + d;
-#pragma unroll
-    for (int h = 0; h < G; ++h) *reinterpret_cast<uint4 *>(to + h * kHeadDim) = x[h];
-  }
-  if (p.k_out) *reinterpret_cast<uint4 *>(p.k_out + (t * p.Hkv + g) * kHeadDim + d) = x[G];
   if (ring) {
     const int64_t row = (static_cast<int64_t>(b) * p.Hkv + g) * p.window + pos % static_cast<uint32_t>(p.window);
     *reinterpret_cast<uint4 *>(p.k_win + row * kHeadDim + d) = x[G];
     *reinterpret_cast<uint4 *>(p.v_win + row * kHeadDim + d) = v;
   }
+  if (p.k_out) *reinterpret_cast<uint4 *>(p.k_out + (t * p.Hkv + g) * kHeadDim + d) = x[G];
 }
 
 template <int G>
