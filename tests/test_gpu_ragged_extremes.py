@@ -93,3 +93,39 @@ def test_rotation_norms_long_and_short_rows(Hkv, G, eps):
     for got, x, g, what in ((q_out, q, qg, "q_out"), (k_out, k, kg, "k_out")):
         want, tol = R.rope(x, pos, 10000.0, g, eps)
         R.assert_within(got, want, tol, what)
+
+
+def test_rope_and_decode_on_a_stream_of_the_caller():
+    """A rotation into the rings, and a decode that reads them, on a stream that is busy when they are called: both
+    wait for what is before them there, and what they write is the reference's."""
+    gen = _gen(63)
+    lens, first, Hkv, W = [1, 30, 7], [5, 3, 100], 4, 16
+    B, n, at = len(lens), sum(lens), R.starts(lens)
+    shape, cu = E.Shape(B, 16, Hkv, D, 0, 0), _cu(lens)
+    pos0 = torch.tensor(first, dtype=torch.int32, device=DEV)
+    last = [f + m - 1 for f, m in zip(first, lens)]
+    pos1 = torch.tensor(last, dtype=torch.int32, device=DEV)
+    q, k, v, qb = _bf(gen, n, 16, D), _bf(gen, n, Hkv, D), _bf(gen, n, Hkv, D), _bf(gen, B, 16, D)
+    late = [torch.zeros_like(x) for x in (q, k, v)]
+    old = [_bf(gen, B, Hkv, W, D) for _ in range(2)]
+    rings = [torch.zeros_like(x) for x in old]
+    q_out, k_out, out = torch.zeros_like(q), torch.zeros_like(k), torch.full((B, 16, D), 7.0, device=DEV)
+    busy = torch.zeros(1 << 28, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(8):
+            busy.add_(1.0)
+        for to, x in zip(late + rings, [q, k, v] + old):
+            to.copy_(x)
+    E.embla_rope_qkv(shape, cu, pos0, *late, q_out, k_out, k_win=rings[0], v_win=rings[1], stream=side)
+    E.embla_window_decode_ragged(shape, qb, *rings, pos1, out, stream=side)
+    _checked()
+    pos = torch.cat([torch.arange(f, f + m, device=DEV) for f, m in zip(first, lens)])
+    R.assert_within(q_out, *R.rope(q, pos, 10000.0), "queries")
+    R.assert_within(k_out, *R.rope(k, pos, 10000.0), "keys")
+    for b, m in enumerate(lens):
+        for t in range(max(0, m - W), m):
+            old[0][b, :, (first[b] + t) % W], old[1][b, :, (first[b] + t) % W] = k_out[at[b] + t], v[at[b] + t]
+    assert torch.equal(rings[0], old[0]) and torch.equal(rings[1], old[1])
+    R.assert_within(out, *R.window_decode(qb, *old, last, D ** -0.5), "decode")
