@@ -46,11 +46,12 @@
 // (one of 32 sequences; reading each block's own took the warp that also loads Q and K 1,500 cycles more).
 //
 // What bounds it, and what was measured (16 query heads):
-//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 564 to 606 us,
-//     1,950 to 1,815 TFLOP/s of visible products (boards differ; 0.96 to 1.03 of the burst rate); softmax over
-//     all keys 1,520 (8,192 tokens), there the exponentials and the maximum add what the tensor cores cannot
-//     hide.
-//   - a window of 128 keys: memory.  8 x 16,384 tokens 220 us, 6.09 TB/s (0.90 of a copy's rate); a block is
+//   - long prompts: the tensor cores.  One prompt of 16,384 tokens through a full layer 564 to 630 us from a graph,
+//     1,950 to 1,745 TFLOP/s of visible products (boards differ; 0.92 to 1.03 of the burst rate), 660 us in a loop
+//     of calls under the power cap (1,670, 0.97 of the sustained rate); softmax over all keys 1,520 (8,192
+//     tokens), there the exponentials and the maximum add what the tensor cores cannot hide.
+//   - a window of 128 keys: memory.  8 x 16,384 tokens 213 us from a graph, 6.3 TB/s (0.93 of a copy's rate),
+//     230 in a loop of calls; a block is
 //     two tiles of 80 keys, so most of a warp's time is a chain of short waits.  Two teams hide each other's:
 //     one team of eight warps on tiles of 128 took 480 us, two on tiles of 80 with a barrier per block 315.
 //     The issuers walk their loops as whole warps with places and phases counted on, so that a product's
@@ -98,8 +99,8 @@ struct Block {
 // TEAMS sets of kTeamWarps warps take blocks in turn; each has an O of its own.  P is written over its S, and
 // three such buffers go round.  For ReLU^2 and one team it has two buffers apart, and S two that are free once
 // they are read: the tensor cores wait less for a tile's weights (16,384 tokens 622 us over S, 589 apart), but
-// a weights warp waits for P's buffer, and softmax, the longer work, does not gain (window 128 220 us over S, 245
-// apart).  Sixteen warps on half rows each: 148 us for 14,496 tokens in four sequences, eight 140.
+// a weights warp waits for P's buffer, and softmax, the longer work, does not gain (window 128, when it was
+// tried, 220 us over S, 245 apart).  Sixteen warps on half rows each: 148 us for 14,496 tokens in four sequences, eight 140.
 template <int MODE, int N, int TEAMS>
 struct Layout {
   static constexpr bool kApart = MODE == kPackedRelu2 && TEAMS == 1;

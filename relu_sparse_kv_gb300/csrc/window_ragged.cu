@@ -10,9 +10,9 @@
 // reading each other's took a third of the kernel's time).  P is fp32 in three bf16 parts (hi + mid +
 // lo, all 24 bits), because the output is fp32.
 //
-// 96 sequences of 2 KV heads over rings of 1,024 keys (84 MB): 18.7 us, 4.5 TB/s; of 4 heads (200 MB) 33.2 us,
-// 6.0 TB/s, 0.89 of a copy's rate: the first microseconds, until rows arrive, and the merge do not shrink
-// with the rings.  96 of 4 over rings of 128 (26 MB) 5.2 us; 8 of 4, 2.9 us, the launch and a trip to
+// 96 sequences of 2 KV heads over rings of 1,024 keys (84 MB): 18.7 to 20.6 us (boards differ), 4.5 to 4.1 TB/s; of
+// 4 heads (200 MB) 33.2 us, 6.0 TB/s, 0.89 of a copy's rate: the first microseconds, until rows arrive,
+// and the merge do not shrink with the rings.  96 of 4 over rings of 128 (26 MB) 5.2 us; 8 of 4, 2.9 us, the launch and a trip to
 // memory (3.0 where the rows are asked for after the position).
 #include <cooperative_groups.h>
 
@@ -99,7 +99,7 @@ __device__ __noinline__ float output_again(const uint16_t *q, const uint8_t *K, 
       uint32_t x[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        x[i] = *reinterpret_cast<const uint16_t *>(V + static_cast<int64_t>(min(j0 + i0 + i, nv - 1)) * kRwRowBytes + 2 * dim);
+        x[i] = reinterpret_cast<const uint16_t *>(V + static_cast<int64_t>(min(j0 + i0 + i, nv - 1)) * kRwRowBytes)[dim];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float w = __shfl_sync(0xffffffffu, mine, i0 + i), v = __uint_as_float(x[i] << 16);
@@ -559,7 +559,7 @@ cudaError_t launch_ws(int64_t units, const RaggedWindowParams &p, const LaunchDe
 
 // One step of up to 128 rows per CTA where all CTAs are resident at once, or a ring has no more; else as
 // many CTAs of four warps to a unit as are resident at once.  (64 sequences of 4 KV heads with rings of 512
-// keys: 19.0 us in steps, 14.6 streamed; 96 of 2 with 1,024: 27.9 and 19.4; 8 of 4 with 1,024, which fit: 6.3.)
+// keys: 19.0 us in steps, 14.6 streamed; 96 of 2 with 1,024: 27.9 and 18.7; 8 of 4 with 1,024, which fit: 6.3.)
 template <int G>
 cudaError_t launch_rw_g(int64_t units, const RaggedWindowParams &p, const LaunchDevice &dev, cudaStream_t stream) {
   const int64_t resident = 3ll * dev.sms;
